@@ -31,7 +31,10 @@ __all__ = [
     "STREAMK_NEVER", "gemm_streamk_plan", "gemm_set_tail_split", "gemm_tail_split_plan",
     "gemm_set_edge_last", "gemm_bf16_fused", "gemm_mxfp8_fused", "GemmEpilogue",
     "make_epilogue", "matmul_fused", "DTYPE_BF16", "DTYPE_F32", "ACT_NONE", "ACT_RELU", "ACT_GELU", "matmul_bf16",
-    "matmul_mxfp8",
+    "matmul_mxfp8", "MAX_GROUPS", "gemm_bf16_grouped", "gemm_bf16_grouped_dgrad",
+    "gemm_bf16_grouped_wgrad", "matmul_grouped", "matmul_grouped_dgrad", "matmul_grouped_wgrad",
+    "NEWTON_SCHULZ_COEFFICIENTS", "gemm_newton_schulz", "gemm_newton_schulz_workspace_bytes",
+    "newton_schulz", "newton_schulz_workspace",
 ]
 
 GEMM_OK = 0
@@ -59,7 +62,8 @@ EXPORTED_SYMBOLS = (
     "gemm_last_schedule", "gemm_bf16_streamk_noalloc", "gemm_set_streamk_mode",
     "gemm_streamk_plan", "gemm_bf16_fused", "gemm_mxfp8_fused", "gemm_mxfp8_tiled",
     "gemm_mxfp8_quantize_tiled", "gemm_set_tail_split", "gemm_tail_split_plan",
-    "gemm_set_edge_last",
+    "gemm_set_edge_last", "gemm_bf16_grouped", "gemm_bf16_grouped_dgrad", "gemm_bf16_grouped_wgrad",
+    "gemm_newton_schulz", "gemm_newton_schulz_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -148,6 +152,17 @@ def load() -> ctypes.CDLL:
             L.gemm_mxfp8_quantize.restype = ctypes.c_int
             L.gemm_mxfp8_quantize_tiled.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _vp]
             L.gemm_mxfp8_quantize_tiled.restype = ctypes.c_int
+            for name in ("gemm_bf16_grouped", "gemm_bf16_grouped_dgrad"):
+                getattr(L, name).argtypes = [_vp, _vp, _vp, _vp, *[_i64] * 8, ctypes.c_int, _vp]
+                getattr(L, name).restype = ctypes.c_int
+            L.gemm_bf16_grouped_wgrad.argtypes = [_vp, _vp, _vp, _vp, *[_i64] * 8, ctypes.c_int,
+                                                  ctypes.c_int, _vp]
+            L.gemm_bf16_grouped_wgrad.restype = ctypes.c_int
+            L.gemm_newton_schulz_workspace_bytes.argtypes = [_i64, _i64, _i64]
+            L.gemm_newton_schulz_workspace_bytes.restype = _i64
+            L.gemm_newton_schulz.argtypes = [_vp, _vp, *[_i64] * 7, *[ctypes.c_int] * 3,
+                                             *[ctypes.c_float] * 4, _vp, _i64, _vp]
+            L.gemm_newton_schulz.restype = ctypes.c_int
             L.gemm_last_status.argtypes = [_vp]
             L.gemm_last_status.restype = ctypes.c_int
             L.gemm_last_status_word.argtypes = [_vp]
@@ -352,6 +367,48 @@ def gemm_mxfp8_quantize_tiled(X: int, rows: int, K: int, ldx: int, Q: int, ldq: 
     return load().gemm_mxfp8_quantize_tiled(X, rows, K, ldx, Q, ldq, SF, stream)
 
 
+MAX_GROUPS = 1024
+
+
+def gemm_bf16_grouped(A: int, B: int, D: int, offsets: int, groups: int, M: int, N: int, K: int,
+                      lda: int, ldb: int, stride_b: int, ldd: int, out_dtype: int = DTYPE_BF16,
+                      stream: int = 0) -> int:
+    return load().gemm_bf16_grouped(A, B, D, offsets, groups, M, N, K, lda, ldb, stride_b, ldd,
+                                    out_dtype, stream)
+
+
+def gemm_bf16_grouped_dgrad(dD: int, B: int, dA: int, offsets: int, groups: int, M: int, N: int,
+                            K: int, ldd: int, ldb: int, stride_b: int, lda: int,
+                            out_dtype: int = DTYPE_BF16, stream: int = 0) -> int:
+    return load().gemm_bf16_grouped_dgrad(dD, B, dA, offsets, groups, M, N, K, ldd, ldb, stride_b,
+                                          lda, out_dtype, stream)
+
+
+def gemm_bf16_grouped_wgrad(dD: int, A: int, dB: int, offsets: int, groups: int, M: int, N: int,
+                            K: int, ldd: int, lda: int, ldb: int, stride_b: int,
+                            out_dtype: int = DTYPE_BF16, accumulate: int = 0,
+                            stream: int = 0) -> int:
+    return load().gemm_bf16_grouped_wgrad(dD, A, dB, offsets, groups, M, N, K, ldd, lda, ldb,
+                                          stride_b, out_dtype, accumulate, stream)
+
+
+# The quintic whose steps bring singular values of [0.003, 1] to about [0.7, 1.2] in five.
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def gemm_newton_schulz_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    return int(load().gemm_newton_schulz_workspace_bytes(batch, rows, cols))
+
+
+def gemm_newton_schulz(G: int, O: int, batch: int, rows: int, cols: int, ldg: int, stride_g: int,
+                       ldo: int, stride_o: int, in_dtype: int, out_dtype: int, steps: int,
+                       a: float, b: float, c: float, eps: float, workspace: int,
+                       workspace_bytes: int, stream: int = 0) -> int:
+    return load().gemm_newton_schulz(G, O, batch, rows, cols, ldg, stride_g, ldo, stride_o,
+                                     in_dtype, out_dtype, steps, a, b, c, eps, workspace,
+                                     workspace_bytes, stream)
+
+
 def gemm_last_status(stream: int = 0) -> int:
     return load().gemm_last_status(stream)
 
@@ -527,3 +584,160 @@ def quantize_mxfp8(X, stream=None):
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_mxfp8_quantize")
     return Q, SF
+
+
+# --------------------------------------------------- expert-training operators
+
+def _out_code(dtype):
+    import torch
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("the output dtype must be bfloat16 or float32")
+    return DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16
+
+
+def _check_3d(t, name):
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a 3-D tensor with unit column stride")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _check_bf16(*named):
+    import torch
+    for t, name in named:
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16")
+
+
+def _check_offsets(offsets, groups):
+    import torch
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
+        raise TypeError("offsets must be a contiguous 1-D int32 tensor")
+    if not offsets.is_cuda:
+        raise ValueError("offsets must be a CUDA tensor")
+    if groups is not None and offsets.numel() != groups + 1:
+        raise ValueError("offsets must hold one value more than there are groups")
+
+
+def _output(out, shape, dtype, device, name):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if dtype is not None and out.dtype != dtype:
+        raise TypeError(f"{name} must have out_dtype")
+    return out
+
+
+def matmul_grouped(A, B, offsets, out=None, out_dtype=None, stream=None):
+    """D[r] = A[r] @ B[e].T for the rows offsets[e] <= r < offsets[e + 1] of
+    A [M,K] bf16, B [groups,N,K] bf16, offsets [groups+1] int32, all on the
+    GPU; returns D [M,N] of out_dtype (bfloat16 or float32).  Rows that belong
+    to no group are not written."""
+    _check_2d(A, "A")
+    _check_3d(B, "B")
+    _check_bf16((A, "A"), (B, "B"))
+    groups, N, K = B.shape
+    _check_offsets(offsets, groups)
+    M = A.shape[0]
+    if A.shape[1] != K:
+        raise ValueError("A and B disagree on K")
+    out = _output(out, (M, N), out_dtype, A.device, "out")
+    _check_2d(out, "out")
+    rc = gemm_bf16_grouped(A.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups,
+                           M, N, K, A.stride(0), B.stride(1), B.stride(0), out.stride(0),
+                           _out_code(out.dtype), _stream_handle(stream))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_grouped")
+    return out
+
+
+def matmul_grouped_dgrad(dD, B, offsets, out=None, out_dtype=None, stream=None):
+    """The gradient of matmul_grouped to A: dA[r] = dD[r] @ B[e], dD [M,N]
+    bf16; returns dA [M,K] of out_dtype (bfloat16 or float32)."""
+    _check_2d(dD, "dD")
+    _check_3d(B, "B")
+    _check_bf16((dD, "dD"), (B, "B"))
+    groups, N, K = B.shape
+    _check_offsets(offsets, groups)
+    M = dD.shape[0]
+    if dD.shape[1] != N:
+        raise ValueError("dD and B disagree on N")
+    out = _output(out, (M, K), out_dtype, dD.device, "out")
+    _check_2d(out, "out")
+    rc = gemm_bf16_grouped_dgrad(dD.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(),
+                                 groups, M, N, K, dD.stride(0), B.stride(1), B.stride(0),
+                                 out.stride(0), _out_code(out.dtype), _stream_handle(stream))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_grouped_dgrad")
+    return out
+
+
+def matmul_grouped_wgrad(dD, A, offsets, out=None, out_dtype=None, accumulate=False, stream=None):
+    """The gradient of matmul_grouped to B: dB[e] = dD[rows of e].T @ A[rows of
+    e]; returns dB [groups,N,K] of out_dtype (bfloat16 or float32).  With
+    accumulate, adds to `out` instead."""
+    _check_2d(dD, "dD")
+    _check_2d(A, "A")
+    _check_bf16((dD, "dD"), (A, "A"))
+    M, N = dD.shape
+    K = A.shape[1]
+    if A.shape[0] != M:
+        raise ValueError("dD and A disagree on M")
+    _check_offsets(offsets, None)
+    groups = offsets.numel() - 1
+    if groups < 0:
+        raise ValueError("offsets must hold one value more than there are groups")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    out = _output(out, (groups, N, K), out_dtype, A.device, "out")
+    _check_3d(out, "out")
+    rc = gemm_bf16_grouped_wgrad(dD.data_ptr(), A.data_ptr(), out.data_ptr(), offsets.data_ptr(),
+                                 groups, M, N, K, dD.stride(0), A.stride(0), out.stride(1),
+                                 out.stride(0), _out_code(out.dtype), int(bool(accumulate)),
+                                 _stream_handle(stream))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_grouped_wgrad")
+    return out
+
+
+def newton_schulz_workspace(batch: int, rows: int, cols: int, device=None):
+    """A workspace for newton_schulz on a batch of rows x cols matrices (one
+    per stream: calls sharing a workspace must not overlap on the GPU)."""
+    import torch
+    n = gemm_newton_schulz_workspace_bytes(batch, rows, cols)
+    if n < 0:
+        raise GemmError(n, "gemm_newton_schulz_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7,
+                  out=None, out_dtype=None, workspace=None, stream=None):
+    """Newton-Schulz orthogonalisation of a matrix [rows,cols] or a batch
+    [batch,rows,cols] (bfloat16 or float32): X = G / (|G| + eps), then `steps`
+    times X <- a X + b (X X^T) X + c (X X^T)^2 X on the smaller side; returns X
+    in out_dtype (bfloat16 or float32).  Without `workspace` (from
+    newton_schulz_workspace) one is allocated for the call on torch's current
+    stream."""
+    import torch
+    batched = G if G.dim() == 3 else G.unsqueeze(0)
+    _check_3d(batched, "G")
+    if G.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("G must be bfloat16 or float32")
+    batch, rows, cols = batched.shape
+    out = _output(out, G.shape, out_dtype, G.device, "out")
+    o = out if out.dim() == 3 else out.unsqueeze(0)
+    _check_3d(o, "out")
+    a, b, c = coefficients
+    if workspace is None:
+        if stream is not None and stream != torch.cuda.current_stream():
+            raise ValueError("a call on another stream needs its own workspace")
+        workspace = newton_schulz_workspace(batch, rows, cols, G.device)
+    rc = gemm_newton_schulz(batched.data_ptr(), o.data_ptr(), batch, rows, cols, batched.stride(1),
+                            batched.stride(0), o.stride(1), o.stride(0), _out_code(G.dtype),
+                            _out_code(out.dtype), steps, a, b, c, eps, workspace.data_ptr(),
+                            workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_newton_schulz")
+    return out

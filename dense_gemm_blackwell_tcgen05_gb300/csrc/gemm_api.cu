@@ -209,6 +209,16 @@ int parse_epilogue(const gemm_epilogue_t* e, int64_t N, const void* D, int64_t l
 
 void note_cuda_error(cudaError_t e) { t_last_cuda_error = static_cast<int>(e); }
 
+int launch_context(int64_t K, LaunchCtx* ctx) {
+  const int rc = current_device(ctx);
+  if (rc == GEMM_OK) ctx->timeout_ns = static_cast<unsigned long long>(timeout_ns_for(K));
+  return rc;
+}
+
+bool device_pointer_ok(const void* p, const LaunchCtx& ctx) { return is_device_pointer(p, ctx.device); }
+
+uint32_t take_stall_request() { return take_stall(); }
+
 int streamk_mode() { return g_streamk_mode.load(); }
 
 uint32_t plan_tail_split(uint64_t tiles, uint64_t resident) {
@@ -301,10 +311,11 @@ bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
 }
 
 bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                   const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
+                   const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3],
+                   CUtensorMapSwizzle swizzle) {
   if (g_encode == nullptr) return false;
   MapKey key{base, dims[0], dims[1], strides[0], box[0], box[1], static_cast<int>(dtype),
-             static_cast<int>(CU_TENSOR_MAP_SWIZZLE_NONE)};
+             static_cast<int>(swizzle)};
   key.dim2 = dims[2];
   key.pitch2 = strides[1];
   key.box2 = box[2];
@@ -318,7 +329,7 @@ bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
   const cuuint32_t bx[3] = {box[0], box[1], box[2]};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = g_encode(map, dtype, 3, const_cast<void*>(base), d, st, bx, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     t_last_cuda_error = 100000 + static_cast<int>(r);

@@ -1,0 +1,759 @@
+// Grouped (ragged) and symmetric bf16/fp16 products on the tensor cores:
+//
+//     out[c, l] = sum_k P[l, k] Q[c, k]          fp32 accumulation in TMEM
+//
+// l runs along the contiguous dimension of the output and sits in the TMEM
+// lanes (the MMA's M), c is the output row and sits in the TMEM columns (the
+// MMA's N).  Each operand is K-major (its rows hold k contiguously) or
+// MN-major (k runs over its rows), as it lies in memory: nothing is
+// transposed beforehand.  The products built on it:
+//
+//   Op::Rows   rows sorted by group times the group's matrix.  c = the row,
+//              so a group's ragged last tile costs what its rows need: the
+//              MMA's N is those rows rounded up to 16 (32 for a CTA pair).
+//                D[r, n]  = sum_k B[e][n, k] A[r, k]    P = B[e] K-major
+//                dA[r, k] = sum_n B[e][n, k] dD[r, n]   P = B[e] MN-major
+//   Op::Sum    each group's rows summed: dB[e][n, k] = sum_r A[r, k] dD[r, n],
+//              P = A and Q = dD, both MN-major; the reduction is ragged.
+//   Op::Sym    a symmetric product (P and Q the same matrix): only the tiles
+//              on and below the diagonal are computed and each is stored
+//              twice.  out = alpha P P^T, or b R + c R R^T with R symmetric.
+//              With R the diagonal goes to fp32 values of its own, and zeros
+//              to the matrix.
+//   Op::Apply  X' = (a + d) X + B X (B symmetric without its diagonal d; P_MN),
+//              or X (a + d) + X B (P K-major), X held as two halves hi + lo
+//              of which hi feeds the tensor cores.
+//
+// Persistent, warp-specialised: warp 0 lane 0 loads operand tiles of 64 k by
+// TMA (128-byte swizzle) into a ring of stages, warp 1 lane 0 issues the MMAs
+// into one of two TMEM accumulators, eight epilogue warps (two per lane
+// quarter, alternating 32-column chunks) drain the other one straight to
+// global memory: with l in the lanes, a warp's store covers 32 consecutive
+// elements of an output row and needs no staging.  Op::Sum adds a warp that
+// clears the operand rows of the next group at the end of a ragged reduction.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "gemm_kernels.cuh"
+
+namespace gb300 {
+
+enum class Op { Rows, Sum, Sym, Apply };
+
+// Groups a launch can hold: the offsets and the tile table sit in shared memory.
+constexpr uint32_t kMaxGroups = 1024;
+// Up to this many groups, Op::Sum deals groups out by falling size.
+constexpr uint32_t kMaxSortedGroups = 256;
+
+struct GroupedArgs {
+  uint32_t L;                  // output columns (lanes)
+  uint32_t C;                  // output rows: in all (Rows), per group (Sum), per matrix (Sym, Apply)
+  uint32_t K;                  // reduction length (Rows, Sym, Apply); rows in all (Sum)
+  uint32_t groups;             // groups (Rows, Sum) or matrices (Sym, Apply)
+  const int32_t* offsets;      // [groups + 1] first row of each group (Rows, Sum)
+  void* out;                   // bf16 / fp32 (Rows, Sum), fp16 (Sym), fp16 hi or the result (Apply)
+  uint64_t ldo, stride_o;      // pitch and matrix stride of `out` in elements
+  uint32_t accumulate;         // Sum: out += instead of out =
+  uint32_t fmt;                // operand type: 1 bf16, 0 fp16
+  uint32_t pdl;                // launched while its predecessor runs: wait for it before touching memory
+  // Sym: out = alpha acc + beta R[l, c].   Apply: v = (alpha + diag) X + acc
+  float alpha, beta;
+  float* diag;                 // [matrix][C]: written by Sym with R, read by Apply
+  uint32_t diag_n;             // values of diag per matrix
+  const __half* R;             // Sym: the symmetric matrix of the beta term (nullptr: none)
+  const __half* x_hi;          // Apply: X as hi + lo (pitch ldx, stride stride_x)
+  const __half* x_lo;
+  uint64_t ldx, stride_x;      // also R's pitch and stride
+  __half* out_lo;              // Apply: the lo half of X'; nullptr: `out` is the result
+  float out_scale;             // Apply, result: factor on the way out
+  uint32_t out_f32;            // Apply, result: fp32 (else bf16)
+  unsigned long long* status;
+  unsigned long long timeout_ns;
+  uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
+};
+
+// One tile of work.  P rows l0.., Q rows c0.. of group / matrix z; Rows: Q's
+// rows start at memory row row0 + c0; Sum: the reduction covers memory rows
+// row0 .. row0 + k_len - 1.
+struct TileItem {
+  uint32_t z, l0, c0, live, row0, k_len;
+  bool mirror;
+};
+
+// Columns [c0, c0 + live) of the tile as the MMA's N: CTA pairs take
+// multiples of 32 (16 rows of Q from each CTA), one CTA multiples of 16.
+template <int CG>
+__device__ __forceinline__ uint32_t mma_n(uint32_t live) {
+  constexpr uint32_t g = 16u * CG;
+  return live == 0 ? g : (live + g - 1) / g * g;
+}
+
+template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32>
+struct GroupedCfg {
+  static_assert(CG == 1 || CG == 2, "cta_group is 1 or 2");
+  static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
+  static constexpr uint32_t LT = 128 * CG;               // lanes (output columns) per tile
+  static constexpr uint32_t Q_ROWS = NT / CG;            // Q rows staged by one CTA
+  static_assert(!Q_MN || Q_ROWS == 128, "an MN-major Q tile is two 64-wide boxes");
+  static_assert(Q_ROWS % 16 == 0 && Q_ROWS <= 256 && NT <= 256, "tile width");
+  static constexpr uint32_t P_BYTES = 128 * 128;
+  static constexpr uint32_t Q_BYTES = Q_ROWS * 128;
+  static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
+  static constexpr bool TAIL = OP == Op::Sum;            // a warp clears ragged reduction ends
+  static constexpr uint32_t kEpiWarps = 8;
+  static constexpr uint32_t kTailWarp = 2 + kEpiWarps;
+  static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps + (TAIL ? 1 : 0));
+  // fp32 outputs: the tensor core adds each MMA to the accumulator with
+  // truncation, a bias of about 1.1e-9 of the result per k (measured: 2e-6 at
+  // 2048).  Every SEG_TILES stages (512 k, 5e-7) the epilogue takes the
+  // accumulator over into registers, where the segments are added rounded to
+  // nearest.  bf16 and fp16 outputs round far above that and take one segment.
+  static constexpr uint32_t SEG_TILES = OUT32 ? 8u : 0xFFFFFFFFu;
+  static constexpr uint32_t NCH = (NT + 63) / 64;        // 32-column chunks per epilogue warp
+  static constexpr bool GROUPED = OP == Op::Rows || OP == Op::Sum;
+  static constexpr uint32_t TABLE_BYTES = GROUPED ? 2 * 4 * (kMaxGroups + 8) : 0;
+  static constexpr uint32_t BAR_BYTES = 512;
+  static constexpr uint32_t SMEM_LIMIT = 232448;
+  static constexpr uint32_t ALIGN_SLACK = 1024;
+  static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - TABLE_BYTES) / STAGE_BYTES;
+  static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
+  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + BAR_BYTES + TABLE_BYTES;
+  static_assert((3 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t ACC_COLS = 256;              // second accumulator's first column
+};
+
+// Shared-memory descriptor of an MN-major operand tile as SWIZZLE_128B boxes
+// of 64 (mn) x 64 (k) elements leave it: k rows of 128 bytes in 8-row atoms
+// (stride byte offset 1024 along k), 64-element blocks along mn one box
+// (leading byte offset 8192) apart.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// idesc_bf16 with the operand type (fmt: 1 bf16, 0 fp16) and majors chosen.
+__device__ __forceinline__ uint32_t idesc_f16(uint32_t M, uint32_t N, uint32_t fmt, bool p_mn, bool q_mn) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(p_mn) << 15) |
+         (static_cast<uint32_t>(q_mn) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The wi-th tile of cluster c among G; false past the last.  Every role of
+// every CTA walks the same sequence.  offs: the clamped offsets; tab: first
+// tile of each group (Rows), or the groups by falling size (Sum).
+template <class C, int CG, Op OP, uint32_t NT>
+__device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* offs, const uint32_t* tab,
+                                          uint32_t c, uint32_t G, uint32_t wi, TileItem& w) {
+  const uint32_t lt = (a.L + C::LT - 1) / C::LT;
+  w.mirror = false;
+  w.row0 = 0;
+  w.k_len = a.K;
+  if constexpr (OP == Op::Rows) {
+    const uint32_t t = c + wi * G;
+    if (t >= tab[a.groups]) return false;
+    uint32_t lo = 0, hi = a.groups;        // tab[lo] <= t < tab[hi]
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (tab[mid] <= t) lo = mid; else hi = mid;
+    }
+    const uint32_t rows = offs[lo + 1] - offs[lo];
+    uint32_t cb, lb;
+    tile_coords(t - tab[lo], (rows + NT - 1) / NT, lt, 8u, cb, lb);
+    w.z = lo;
+    w.row0 = offs[lo];
+    w.c0 = cb * NT;
+    w.l0 = lb * C::LT;
+    w.live = w.c0 < rows ? min(NT, rows - w.c0) : 0u;
+    return true;
+  } else if constexpr (OP == Op::Sum) {
+    // groups by falling size, rounds dealt in alternating directions: the
+    // clusters end within about the smallest tile of each other
+    const uint32_t ct = (a.C + NT - 1) / NT, per = lt * ct;
+    const uint32_t t = wi * G + ((wi & 1u) ? G - 1u - c : c);
+    if (t >= per * a.groups) return false;
+    const uint32_t g = t / per;
+    w.z = tab[g];
+    w.row0 = offs[w.z];
+    w.k_len = offs[w.z + 1] - w.row0;
+    uint32_t cb, lb;
+    tile_coords(t - g * per, ct, lt, 8u, cb, lb);
+    w.c0 = cb * NT;
+    w.l0 = lb * C::LT;
+    w.live = min(NT, a.C - w.c0);
+    return true;
+  } else if constexpr (OP == Op::Sym) {
+    // tiles on and below the diagonal, row by row (LT == NT)
+    static_assert(C::LT == NT || OP != Op::Sym, "square tiles");
+    const uint32_t per = lt * (lt + 1) / 2;
+    const uint32_t t = c + wi * G;
+    if (t >= per * a.groups) return false;
+    w.z = t / per;
+    const uint32_t r = t - w.z * per;
+    uint32_t i = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > r) --i;
+    while ((i + 1) * (i + 2) / 2 <= r) ++i;
+    const uint32_t j = r - i * (i + 1) / 2;
+    w.l0 = i * C::LT;
+    w.c0 = j * NT;
+    w.live = min(NT, a.C - w.c0);
+    w.mirror = i != j;
+    return true;
+  } else {
+    const uint32_t ct = (a.C + NT - 1) / NT, per = lt * ct;
+    const uint32_t t = c + wi * G;
+    if (t >= per * a.groups) return false;
+    w.z = t / per;
+    uint32_t cb, lb;
+    tile_coords(t - w.z * per, ct, lt, 8u, cb, lb);
+    w.c0 = cb * NT;
+    w.l0 = lb * C::LT;
+    w.live = min(NT, a.C - w.c0);
+    return true;
+  }
+}
+
+// Two neighbouring output columns of one row per lane instead of two rows of
+// one column: lanes 2j and 2j + 1 hold columns 2j, 2j + 1 of rows 2i (v0) and
+// 2i + 1 (v1); afterwards lane 2j has row 2i's pair, lane 2j + 1 row 2i + 1's.
+__device__ __forceinline__ void pair_columns(uint32_t v0, uint32_t v1, uint32_t odd, float& x0, float& x1) {
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+  x0 = __uint_as_float(odd ? got : v0);
+  x1 = __uint_as_float(odd ? v1 : got);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Stores the 16-bit pair `p` at columns col, col + 1 of row pointer `dst`.
+__device__ __forceinline__ void store_pair16(uint16_t* dst, uint32_t col, uint32_t L, bool vec, uint32_t p) {
+  if (vec && col + 1 < L) {
+    *reinterpret_cast<uint32_t*>(dst + col) = p;
+  } else {
+    if (col < L) dst[col] = static_cast<uint16_t>(p & 0xFFFFu);
+    if (col + 1 < L) dst[col + 1] = static_cast<uint16_t>(p >> 16);
+  }
+}
+
+template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32>
+__global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                   const GroupedArgs args) {
+  using C = GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bar0 = base + C::STAGES * C::STAGE_BYTES;
+  const auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
+  const auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (C::STAGES + s); };
+  const auto tail_bar = [&](uint32_t s) { return bar0 + 8 * (2 * C::STAGES + s); };
+  constexpr uint32_t kAccBar0 = 3 * C::STAGES;
+  const auto accf_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + b); };
+  const auto acce_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8 * (kAccBar0 + 4);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (kAccBar0 + 5));
+  volatile uint32_t* const abort_flag = tmem_slot + 1;
+  uint32_t* const offs = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
+  uint32_t* const tab = offs + kMaxGroups + 8;
+
+  const uint32_t warp = warp_idx_sync();
+  const uint32_t lane = lane_idx();
+  const uint32_t rank = (CG == 2) ? cluster_cta_rank() : 0u;
+  const bool leader = rank == 0;
+  const uint32_t cluster_id = blockIdx.x / CG;
+  const uint32_t G = gridDim.x / CG;
+  const Watchdog wd{args.status, args.timeout_ns, abort_flag};
+
+  // ---- set-up ------------------------------------------------------------------
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmP);
+      tma_prefetch_desc(&tmQ);
+      *abort_flag = 0u;
+    }
+    // arrivals: a full barrier gets the producer's expect_tx, or, with a tail
+    // warp, one arrival from each CTA (its producer, or its tail warp on a
+    // ragged tile); an accumulator is handed back by every epilogue warp
+    for (uint32_t i = lane; i < kAccBar0 + 5; i += 32) {
+      uint32_t count = 1;
+      if (C::TAIL && i < C::STAGES) count = CG;
+      if (i == kAccBar0 + 2 || i == kAccBar0 + 3) count = C::kEpiWarps * CG;
+      mbar_init(bar0 + 8 * i, count);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_addr(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish<CG>();
+  }
+  if (args.pdl) {
+    grid_dependents_launch();
+    grid_dependency_wait();
+  }
+  if constexpr (C::GROUPED) {
+    // offsets clamped into [0, rows] and made to rise: whatever they hold, no
+    // access leaves the operands and the groups do not overlap
+    const int32_t rows = static_cast<int32_t>(OP == Op::Rows ? args.C : args.K);
+    if (warp == 0) {
+      int32_t top = 0;
+      for (uint32_t e0 = 0; e0 <= args.groups; e0 += 32) {
+        const uint32_t e = e0 + lane;
+        int32_t v = e <= args.groups ? min(max(__ldg(args.offsets + e), 0), rows) : 0;
+#pragma unroll
+        for (uint32_t d = 1; d < 32; d *= 2) {
+          const int32_t up = __shfl_up_sync(0xffffffffu, v, d);
+          if (lane >= d) v = max(v, up);
+        }
+        v = max(v, top);
+        if (e <= args.groups) offs[e] = static_cast<uint32_t>(v);
+        top = __shfl_sync(0xffffffffu, v, 31);
+      }
+      __syncwarp();
+    }
+    if constexpr (OP == Op::Rows) {
+      // first tile of each group: an exclusive sum by warp 0
+      if (warp == 0) {
+        const uint32_t lt = (args.L + C::LT - 1) / C::LT;
+        uint32_t sum = 0;
+        for (uint32_t e0 = 0; e0 < args.groups; e0 += 32) {
+          const uint32_t e = e0 + lane;
+          uint32_t n = 0;
+          if (e < args.groups) n = (offs[e + 1] - offs[e] + NT - 1) / NT * lt;
+          uint32_t incl = n;
+#pragma unroll
+          for (uint32_t d = 1; d < 32; d *= 2) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += up;
+          }
+          if (e < args.groups) tab[e] = sum + incl - n;
+          sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) tab[args.groups] = sum;
+      }
+    } else {
+      __syncthreads();
+      for (uint32_t e = threadIdx.x; e < args.groups; e += C::kThreads) {
+        uint32_t place = e;
+        if (args.groups <= kMaxSortedGroups) {
+          const uint32_t n = offs[e + 1] - offs[e];
+          place = 0;
+          for (uint32_t f = 0; f < args.groups; ++f) {
+            const uint32_t m = offs[f + 1] - offs[f];
+            place += (m > n || (m == n && f < e)) ? 1u : 0u;
+          }
+        }
+        tab[place] = e;
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const auto item = [&](uint32_t wi, TileItem& w) {
+    return tile_item<C, CG, OP, NT>(args, offs, tab, cluster_id, G, wi, w);
+  };
+
+  if (warp == 0) {
+    // ==================== TMA producer: one thread ==============================
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_last();
+      uint32_t it = 0;
+      uint32_t tail_last = 0, tail_phase = 0;   // per stage: its last tile was ragged; its tail barrier's parity
+      bool ok = true;
+      TileItem w;
+      for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
+        const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
+        const uint32_t h = mma_n<CG>(w.live) / CG;     // Q rows this CTA contributes to the MMA
+        const int32_t px = static_cast<int32_t>(w.l0 + rank * 128);
+        const int32_t qy = static_cast<int32_t>(w.c0 + rank * h);
+        for (uint32_t kt = 0; kt < kt_n; ++kt, ++it) {
+          const uint32_t s = it % C::STAGES;
+          if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
+          if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = base + s * C::STAGE_BYTES;
+          const int32_t k0 = static_cast<int32_t>(kt * C::BK);
+          const bool ragged = C::TAIL && (kt + 1) * C::BK > w.k_len;
+          // a ragged tile lands on this CTA's own tail barrier; its tail warp
+          // passes it on to the leader's full barrier
+          uint32_t bar = full_bar(s);
+          bool pair = false;
+          if (ragged) {
+            bar = tail_bar(s);
+            mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+            tail_last |= 1u << s;
+            tail_phase ^= 1u << s;
+          } else {
+            tail_last &= ~(1u << s);
+            if constexpr (CG == 2) {
+              pair = true;
+              bar = mapa_shared(full_bar(s), 0);
+            }
+            if (leader) mbar_arrive_expect_tx(full_bar(s), CG * C::STAGE_BYTES);
+            else if (C::TAIL) mbar_arrive_cluster(bar);
+          }
+          const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, int32_t z) {
+            if (CG == 2 && pair) tma_load_3d_pair(dst, m, bar, x, y, z, pol);
+            else tma_load_3d(dst, m, bar, x, y, z, pol);
+          };
+          const int32_t pz = static_cast<int32_t>(OP == Op::Sum ? 0u : w.z);
+          const int32_t qz = static_cast<int32_t>(C::GROUPED ? 0u : w.z);
+          const int32_t kr = static_cast<int32_t>((OP == Op::Sum ? w.row0 : 0u)) + k0;
+          if constexpr (P_MN) {
+            load(sb, &tmP, px, kr, pz);
+            load(sb + 8192, &tmP, px + 64, kr, pz);
+          } else {
+            load(sb, &tmP, k0, px, pz);
+          }
+          if constexpr (Q_MN) {
+            load(sb + C::P_BYTES, &tmQ, qy, kr, qz);
+            load(sb + C::P_BYTES + 8192, &tmQ, qy + 64, kr, qz);
+          } else {
+            load(sb + C::P_BYTES, &tmQ, k0, static_cast<int32_t>(OP == Op::Rows ? w.row0 : 0u) + qy, qz);
+          }
+        }
+      }
+      // Exit path after a give-up: let this CTA's issued loads land first.
+      if (*abort_flag) {
+        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
+        for (uint32_t i = first; i < it; ++i) {
+          const uint32_t s = i % C::STAGES;
+          if (i == args.stall_iter) continue;
+          if ((tail_last >> s) & 1u) drain_wait(tail_bar(s), ((tail_phase >> s) & 1u) ^ 1u, wd, kSiteProducerDrain);
+          else if (leader) drain_wait(full_bar(s), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ==================== MMA issuer: one thread of the leader CTA ==============
+    if (leader && lane == 0) {
+      uint32_t it = 0, j = 0;
+      bool ok = true, issued = false;
+      TileItem w;
+      for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
+        const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
+        const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(w.live), args.fmt, P_MN, Q_MN);
+        for (uint32_t k_begin = 0; ok && k_begin < kt_n; ++j) {
+          const uint32_t k_end = kt_n - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : kt_n;
+          const uint32_t b = j & 1u;
+          // accumulator b must have been drained by every epilogue warp
+          if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
+          for (uint32_t kt = k_begin; kt < k_end; ++kt, ++it) {
+            const uint32_t s = it % C::STAGES;
+            if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t sb = base + s * C::STAGE_BYTES;
+            const uint64_t pd = P_MN ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
+            const uint64_t qd = Q_MN ? smem_desc_mn_sw128(sb + C::P_BYTES) : smem_desc_sw128(sb + C::P_BYTES);
+            // 16 k per MMA: 32 bytes along a K-major row, 16 rows of an MN-major tile
+            constexpr uint32_t kPStep = P_MN ? 128 : 2, kQStep = Q_MN ? 128 : 2;
+            const uint32_t left = w.k_len - kt * C::BK;
+            const uint32_t steps = C::TAIL && left < C::BK ? (left + 15) / 16 : 4u;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+              if (!C::TAIL || k < steps)
+                mma_bf16<CG>(d_tmem, pd + kPStep * k, qd + kQStep * k, idesc, (kt != k_begin || k != 0u));
+            commit_to<CG>(empty_bar(s));   // frees the stage once these MMAs finish
+            issued = true;
+          }
+          if (!ok) break;
+          commit_to<CG>(accf_bar(b));
+          k_begin = k_end;
+        }
+      }
+      // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
+      if (issued) {
+        if constexpr (CG == 1)
+          tc_commit(drain_bar);
+        else
+          tc_commit_pair_multicast(drain_bar, 0x1);
+        drain_wait(drain_bar, 0, wd, kSiteMmaDrain);
+      }
+    }
+  } else if (C::TAIL && warp == C::kTailWarp) {
+    // ==================== ragged reduction ends (Op::Sum) ========================
+    // The last tile of a group's reduction also holds rows of the next group
+    // (or nothing): those up to the next multiple of 16 k, which the MMA
+    // reads, are cleared in both operands, so that not even an Inf or NaN of
+    // another group's rows reaches this one.
+    uint32_t it = 0, phase = 0;
+    bool ok = true;
+    TileItem w;
+    for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
+      const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
+      const uint32_t tail = w.k_len % C::BK;
+      it += kt_n;
+      if (tail == 0) continue;
+      const uint32_t s = (it - 1) % C::STAGES;
+      if (!warp_wait(tail_bar(s), (phase >> s) & 1u, wd, kSiteTail, lane)) {
+        ok = false;
+        break;
+      }
+      phase ^= 1u << s;
+      uint8_t* const sp = base_ptr + s * C::STAGE_BYTES;
+      const uint32_t end = (tail + 15) / 16 * 16;
+      // 4 boxes (two 64-wide blocks of each operand), rows tail .. end - 1, 8 pieces of 16 bytes
+      const uint32_t n = (end - tail) * 32;
+      for (uint32_t i = lane; i < n; i += 32) {
+        const uint32_t r = tail + i / 32, box = (i / 8) & 3u, piece = i & 7u;
+        *reinterpret_cast<uint4*>(sp + box * 8192 + r * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 1) mbar_arrive(full_bar(s));
+        else mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
+      }
+    }
+  } else {
+    // ==================== epilogue: eight warps, two per TMEM lane quarter =======
+    const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
+    const uint32_t eg = (warp - 2u) / 4u;      // chunks eg, eg + 2, ...
+    const uint32_t odd = lane & 1u;
+    uint32_t j = 0;
+    bool ok = true;
+    TileItem w;
+    for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
+      const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
+      const uint32_t lbase = w.l0 + rank * 128 + q * 32;   // this warp's first output column
+      const uint32_t col = lbase + lane;
+      const uint32_t nch = (w.live + 31) / 32;
+      // output row of tile column c: matrix z, row c0 + c (Rows: memory row row0 + c0 + c)
+      const uint64_t out0 = OP == Op::Rows
+                                ? static_cast<uint64_t>(w.row0 + w.c0) * args.ldo
+                                : w.z * args.stride_o + static_cast<uint64_t>(w.c0) * args.ldo;
+      const auto release = [&](uint32_t b) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) mbar_arrive(acce_bar(b));
+          else mbar_arrive_cluster(mapa_shared(acce_bar(b), 0));
+        }
+      };
+      if constexpr (OUT32) {
+        float acc[C::NCH][32];
+#pragma unroll
+        for (uint32_t i = 0; i < C::NCH; ++i)
+#pragma unroll
+          for (uint32_t t = 0; t < 32; ++t) acc[i][t] = 0.0f;
+        for (uint32_t k = 0; k < kt_n; k += C::SEG_TILES, ++j) {
+          const uint32_t b = j & 1u;
+          if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t t_addr = tmem_base + ((q * 32u) << 16) + b * C::ACC_COLS;
+#pragma unroll
+          for (uint32_t i = 0; i < C::NCH; ++i) {
+            if (2 * i + eg < nch) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32_sync(t_addr + (2 * i + eg) * 32, v);
+#pragma unroll
+              for (uint32_t t = 0; t < 32; ++t) acc[i][t] += __uint_as_float(v[t]);
+            }
+          }
+          release(b);
+        }
+        if (!ok) break;
+        float* const o = static_cast<float*>(args.out) + out0 + col;
+#pragma unroll
+        for (uint32_t i = 0; i < C::NCH; ++i) {
+          const uint32_t c0 = (2 * i + eg) * 32;
+          if (col < args.L) {
+#pragma unroll
+            for (uint32_t t = 0; t < 32; ++t)
+              if (c0 + t < w.live) {
+                float* p = o + static_cast<uint64_t>(c0 + t) * args.ldo;
+                *p = (OP == Op::Sum && args.accumulate) ? *p + acc[i][t] : acc[i][t];
+              }
+          }
+        }
+      } else {
+        const bool summed = kt_n != 0;     // an empty reduction leaves no accumulator: zeros
+        const uint32_t b = j & 1u;
+        if (summed) {
+          if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          ++j;
+        }
+        const uint32_t t_addr = tmem_base + ((q * 32u) << 16) + b * C::ACC_COLS;
+        const bool vec = ((reinterpret_cast<uintptr_t>(args.out) & 3u) == 0) && (args.ldo & 1u) == 0 &&
+                         (args.stride_o & 1u) == 0;
+        const uint32_t pcol = lbase + (lane & ~1u);   // this lane's column pair
+#pragma unroll 1
+        for (uint32_t ch = eg; ch < nch; ch += 2) {
+          uint32_t v[32];
+          if (summed) {
+            tmem_ld_32x32b_x32_sync(t_addr + ch * 32, v);
+          } else {
+#pragma unroll
+            for (uint32_t t = 0; t < 32; ++t) v[t] = 0u;
+          }
+          const uint32_t c0 = ch * 32;
+          if constexpr (OP == Op::Rows || OP == Op::Sum) {
+            uint16_t* const o = static_cast<uint16_t*>(args.out) + out0;
+#pragma unroll
+            for (uint32_t t = 0; t < 16; ++t) {
+              float x0, x1;
+              pair_columns(v[2 * t], v[2 * t + 1], odd, x0, x1);
+              const uint32_t c = c0 + 2 * t + odd;
+              if (c < w.live) {
+                uint16_t* const row = o + static_cast<uint64_t>(c) * args.ldo;
+                if (OP == Op::Sum && args.accumulate) {
+                  if (pcol < args.L) x0 += bf16_bits_to_f32(row[pcol]);
+                  if (pcol + 1 < args.L) x1 += bf16_bits_to_f32(row[pcol + 1]);
+                }
+                store_pair16(row, pcol, args.L, vec, pack_bf16x2(x0, x1));
+              }
+            }
+          } else if constexpr (OP == Op::Sym) {
+            // row `col` of the matrix holds the same 32 values (symmetry):
+            // R is read and the mirrored tile written there, 64 bytes a lane;
+            // the pitch is a multiple of 8, so a 16-byte piece that starts
+            // inside it ends inside it
+            const bool row_ok = col < args.L;
+            const uint64_t at = w.z * args.stride_o + static_cast<uint64_t>(col) * args.ldo + w.c0 + c0;
+            const uint32_t pitch_left =
+                static_cast<uint32_t>(args.ldo) > w.c0 + c0 ? static_cast<uint32_t>(args.ldo) - (w.c0 + c0) : 0u;
+            float x[32];
+#pragma unroll
+            for (uint32_t t = 0; t < 32; ++t) x[t] = args.alpha * __uint_as_float(v[t]);
+            if (args.R != nullptr && row_ok) {
+#pragma unroll
+              for (uint32_t p = 0; p < 4; ++p) {
+                if (8 * p < pitch_left) {
+                  const uint4 r = *reinterpret_cast<const uint4*>(args.R + at + 8 * p);
+                  const __half2* h = reinterpret_cast<const __half2*>(&r);
+#pragma unroll
+                  for (uint32_t t = 0; t < 4; ++t) {
+                    const float2 f = __half22float2(h[t]);
+                    x[8 * p + 2 * t] = fmaf(args.beta, f.x, x[8 * p + 2 * t]);
+                    x[8 * p + 2 * t + 1] = fmaf(args.beta, f.y, x[8 * p + 2 * t + 1]);
+                  }
+                }
+              }
+              if (!w.mirror) {
+#pragma unroll
+                for (uint32_t t = 0; t < 32; ++t)
+                  if (w.c0 + c0 + t == col) {
+                    args.diag[static_cast<uint64_t>(w.z) * args.diag_n + col] = x[t];
+                    x[t] = 0.0f;
+                  }
+              }
+            }
+            if (w.mirror && row_ok) {
+#pragma unroll
+              for (uint32_t p = 0; p < 4; ++p)
+                if (8 * p < pitch_left)
+                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + at + 8 * p) =
+                      make_uint4(pack_f16x2(x[8 * p], x[8 * p + 1]), pack_f16x2(x[8 * p + 2], x[8 * p + 3]),
+                                 pack_f16x2(x[8 * p + 4], x[8 * p + 5]), pack_f16x2(x[8 * p + 6], x[8 * p + 7]));
+            }
+            uint16_t* const o = static_cast<uint16_t*>(args.out) + out0;
+#pragma unroll
+            for (uint32_t t = 0; t < 16; ++t) {
+              float x0, x1;
+              pair_columns(__float_as_uint(x[2 * t]), __float_as_uint(x[2 * t + 1]), odd, x0, x1);
+              const uint32_t c = c0 + 2 * t + odd;
+              if (c < w.live)
+                store_pair16(o + static_cast<uint64_t>(c) * args.ldo, pcol, args.L, true, pack_f16x2(x0, x1));
+            }
+          } else {
+            // v = (alpha + diag) (hi + lo) + acc, split again into hi + lo, or
+            // scaled out; diag goes by the row (Y X) or the column (X Y)
+            const float* const dg = args.diag + static_cast<uint64_t>(w.z) * args.diag_n;
+            const float f0 = P_MN ? 0.0f : args.alpha + (pcol < args.L ? dg[pcol] : 0.0f);
+            const float f1 = P_MN ? 0.0f : args.alpha + (pcol + 1 < args.L ? dg[pcol + 1] : 0.0f);
+            const uint64_t x_at = w.z * args.stride_x + static_cast<uint64_t>(w.c0 + c0) * args.ldx + pcol;
+#pragma unroll
+            for (uint32_t t0 = 0; t0 < 16; t0 += 8) {
+              uint32_t hi[8], lo[8];
+              float dr[8];
+#pragma unroll
+              for (uint32_t t = 0; t < 8; ++t) {
+                const uint32_t r = 2 * (t0 + t) + odd;
+                const bool live = c0 + r < w.live && pcol < args.L;
+                const uint64_t at = x_at + static_cast<uint64_t>(r) * args.ldx;
+                hi[t] = live ? *reinterpret_cast<const uint32_t*>(args.x_hi + at) : 0u;
+                lo[t] = live ? *reinterpret_cast<const uint32_t*>(args.x_lo + at) : 0u;
+                dr[t] = P_MN && c0 + r < w.live ? dg[w.c0 + c0 + r] : 0.0f;
+              }
+#pragma unroll
+              for (uint32_t t = 0; t < 8; ++t) {
+                const uint32_t r = 2 * (t0 + t) + odd;
+                float x0, x1;
+                pair_columns(v[2 * (t0 + t)], v[2 * (t0 + t) + 1], odd, x0, x1);
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[t]));
+                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo[t]));
+                x0 = fmaf(P_MN ? args.alpha + dr[t] : f0, h.x + l.x, x0);
+                x1 = fmaf(P_MN ? args.alpha + dr[t] : f1, h.y + l.y, x1);
+                if (c0 + r >= w.live) continue;
+                const uint64_t row = out0 + static_cast<uint64_t>(c0 + r) * args.ldo;
+                if (args.out_lo != nullptr) {
+                  const uint32_t p = pack_f16x2(x0, x1);
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+                  store_pair16(static_cast<uint16_t*>(args.out) + row, pcol, args.L, true, p);
+                  store_pair16(reinterpret_cast<uint16_t*>(args.out_lo) + row, pcol, args.L, true,
+                               pack_f16x2(x0 - f.x, x1 - f.y));
+                } else if (args.out_f32) {
+                  float* const o = static_cast<float*>(args.out) + row;
+                  if (pcol < args.L) o[pcol] = x0 * args.out_scale;
+                  if (pcol + 1 < args.L) o[pcol + 1] = x1 * args.out_scale;
+                } else {
+                  store_pair16(static_cast<uint16_t*>(args.out) + row, pcol, args.L, vec,
+                               pack_bf16x2(x0 * args.out_scale, x1 * args.out_scale));
+                }
+              }
+            }
+          }
+        }
+        if (summed) release(b);
+      }
+    }
+  }
+
+  // ---- teardown: every role is done with TMEM and with the peer's barriers ----
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace gb300

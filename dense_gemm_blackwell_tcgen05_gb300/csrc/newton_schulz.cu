@@ -1,0 +1,317 @@
+// Newton-Schulz orthogonalisation of a batch of matrices:
+//
+//     X = G / (|G|_F + eps);  steps times:  P = X X^T,  X <- a X + (b P + c P^2) X
+//
+// on the smaller side m of each rows x cols matrix (P = X^T X and
+// X <- a X + X (b P + c P^2) where rows > cols), as three products a step:
+// the Gram matrix P, the polynomial Y = b P + c P P -- both symmetric, so only
+// the tiles on and below the diagonal are computed -- and X' = a X + Y X.
+// Every operand lies as the tensor cores can take it, so neither orientation
+// is transposed.
+//
+// Precision.  The operands are fp16: at the same rate as bf16 their rounding
+// is 8 times finer, and the range fits, because X is held scaled by a power of
+// two that brings its entries near 1 and P and Y have norms of a few units.
+// X itself is held as hi + lo, two fp16 halves, and only the terms outside
+// the products see lo.  Directions with small singular values grow by a = 3.4
+// a step through a X, and so would its rounding errors.  Y's diagonal, about
+// -2.7 once singular values are near 1 and then most of Y, stays in fp32 and
+// is applied outside the product as well: (a + d_i) X_i + (Y - diag d) X.
+// Relative error of five steps against 64 bits, random 256 x 256 / rank 8,
+// 512 x 1024: bf16 operands 1.0e-2 / 0.34, fp16 1.3e-3 / 4.2e-2, X as hi + lo
+// 1.6e-3 / 3.3e-4, and with the diagonal apart 8.6e-4 / 5.8e-4.
+#include <cmath>
+
+#include "launch_grouped.cuh"
+
+namespace gb300 {
+namespace {
+
+constexpr uint32_t kSegment = 1024;      // columns a warp takes at a time
+constexpr uint32_t kMaxPartials = 1024;  // partial sums per matrix
+
+template <class T>
+__device__ __forceinline__ float load_as_f32(const T* p);
+template <>
+__device__ __forceinline__ float load_as_f32<float>(const float* p) { return __ldg(p); }
+template <>
+__device__ __forceinline__ float load_as_f32<uint16_t>(const uint16_t* p) { return bf16_bits_to_f32(__ldg(p)); }
+
+// Four consecutive elements at column col (those >= cols read as 0).
+template <class T>
+__device__ __forceinline__ float4 load4(const T* row, uint32_t col, uint32_t cols, bool vec) {
+  if (vec && col + 4 <= cols) {
+    if constexpr (sizeof(T) == 4) {
+      return __ldg(reinterpret_cast<const float4*>(row + col));
+    } else {
+      const uint2 t = __ldg(reinterpret_cast<const uint2*>(row + col));
+      return make_float4(bf16_bits_to_f32(t.x & 0xFFFFu), bf16_bits_to_f32(t.x >> 16),
+                         bf16_bits_to_f32(t.y & 0xFFFFu), bf16_bits_to_f32(t.y >> 16));
+    }
+  }
+  float4 v;
+  v.x = col < cols ? load_as_f32<T>(row + col) : 0.0f;
+  v.y = col + 1 < cols ? load_as_f32<T>(row + col + 1) : 0.0f;
+  v.z = col + 2 < cols ? load_as_f32<T>(row + col + 2) : 0.0f;
+  v.w = col + 3 < cols ? load_as_f32<T>(row + col + 3) : 0.0f;
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (uint32_t d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// Sum over the 8 warps of the block, in a fixed order; every thread gets it.
+__device__ __forceinline__ float block_sum(float v, float* slots) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31u) == 0) slots[threadIdx.x / 32] = v;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i) t += slots[i];
+  return t;
+}
+
+// partials[z][block]: sum of squares of this block's share of matrix z.  One
+// warp takes a row segment of kSegment columns at a time.  A read of G.
+template <class T>
+__global__ void __launch_bounds__(256) ns_square_sum_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
+                                                            uint64_t stride_g, float* partials) {
+  __shared__ float slots[8];
+  grid_dependents_launch();
+  const uint32_t lane = lane_idx();
+  const T* const g = G + blockIdx.y * stride_g;
+  const bool vec = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(T) - 1)) == 0 && ldg % 4 == 0;
+  const uint32_t segs = (cols + kSegment - 1) / kSegment;
+  const uint64_t units = static_cast<uint64_t>(rows) * segs;
+  float sum = 0.0f;
+  for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
+    const uint64_t r = u / segs;
+    const uint32_t c0 = static_cast<uint32_t>(u - r * segs) * kSegment;
+    float4 v[kSegment / 128];
+#pragma unroll
+    for (uint32_t i = 0; i < kSegment / 128; ++i) v[i] = load4<T>(g + r * ldg, c0 + i * 128 + lane * 4, cols, vec);
+#pragma unroll
+    for (uint32_t i = 0; i < kSegment / 128; ++i)
+      sum += v[i].x * v[i].x + v[i].y * v[i].y + (v[i].z * v[i].z + v[i].w * v[i].w);
+  }
+  sum = block_sum(sum, slots);
+  if (threadIdx.x == 0) partials[blockIdx.y * kMaxPartials + blockIdx.x] = sum;
+}
+
+// X = G * scale / (|G| + eps) as fp16 halves hi + lo.  A read of G, a write of X.
+template <class T>
+__global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
+                                                           uint64_t stride_g, const float* partials,
+                                                           uint32_t num_partials, float scale, float eps,
+                                                           __half* hi, __half* lo, uint64_t ldx, uint64_t stride_x) {
+  __shared__ float slots[8];
+  grid_dependents_launch();
+  grid_dependency_wait();
+  const uint32_t lane = lane_idx();
+  float sum = 0.0f;
+  for (uint32_t i = threadIdx.x; i < num_partials; i += 256) sum += partials[blockIdx.y * kMaxPartials + i];
+  const float f = scale / (sqrtf(block_sum(sum, slots)) + eps);
+  const T* const g = G + blockIdx.y * stride_g;
+  const bool vec = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(T) - 1)) == 0 && ldg % 4 == 0;
+  const uint32_t segs = (cols + kSegment - 1) / kSegment;
+  const uint64_t units = static_cast<uint64_t>(rows) * segs;
+  for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
+    const uint64_t r = u / segs;
+    const uint32_t c0 = static_cast<uint32_t>(u - r * segs) * kSegment;
+    float4 v[kSegment / 128];
+#pragma unroll
+    for (uint32_t i = 0; i < kSegment / 128; ++i) v[i] = load4<T>(g + r * ldg, c0 + i * 128 + lane * 4, cols, vec);
+#pragma unroll
+    for (uint32_t i = 0; i < kSegment / 128; ++i) {
+      const uint32_t c = c0 + i * 128 + lane * 4;
+      if (c >= ldx) continue;   // the pitch is a multiple of 8: four columns from c < ldx fit
+      const float x[4] = {v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f};
+      const uint2 h = make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
+      const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+      const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+      const uint64_t at = blockIdx.y * stride_x + r * ldx + c;
+      *reinterpret_cast<uint2*>(hi + at) = h;
+      *reinterpret_cast<uint2*>(lo + at) =
+          make_uint2(pack_f16x2(x[0] - h0.x, x[1] - h0.y), pack_f16x2(x[2] - h1.x, x[3] - h1.y));
+    }
+  }
+}
+
+uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
+
+// Where the parts of the workspace start, in bytes.
+struct Layout {
+  uint64_t ldx, stride_x, ldp, stride_p;   // elements
+  uint64_t hi[2], lo[2], gram, poly, diag, partials, bytes;
+};
+
+Layout layout_of(uint64_t batch, uint64_t rows, uint64_t cols) {
+  Layout w;
+  const uint64_t m = rows < cols ? rows : cols;
+  w.ldx = round_up(cols, 8);
+  w.stride_x = rows * w.ldx;
+  w.ldp = round_up(m, 8);
+  w.stride_p = m * w.ldp;
+  uint64_t at = 0;
+  const auto take = [&](uint64_t bytes) {
+    const uint64_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  for (int i = 0; i < 2; ++i) {
+    w.hi[i] = take(batch * w.stride_x * 2);
+    w.lo[i] = take(batch * w.stride_x * 2);
+  }
+  w.gram = take(batch * w.stride_p * 2);
+  w.poly = take(batch * w.stride_p * 2);
+  w.diag = take(batch * m * 4);
+  w.partials = take(batch * kMaxPartials * 4);
+  w.bytes = at;
+  return w;
+}
+
+int last_launch() {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return GEMM_OK;
+  note_cuda_error(e);
+  return GEMM_ERR_LAUNCH;
+}
+
+// hi + lo of the normalised matrices into the workspace.
+template <class T>
+int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
+  uint8_t* const ws = static_cast<uint8_t*>(p.workspace);
+  const uint64_t units = static_cast<uint64_t>(p.rows) * ceil_div_u64(p.cols, kSegment);
+  uint64_t blocks = ceil_div_u64(units, 8);
+  const uint64_t share = ceil_div_u64(8ull * static_cast<uint64_t>(ctx.num_sms), p.batch);
+  if (blocks > share) blocks = share;
+  if (blocks > kMaxPartials) blocks = kMaxPartials;
+  float* const partials = reinterpret_cast<float*>(ws + w.partials);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), p.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 0;
+  const T* const g = static_cast<const T*>(p.G);
+  if (cudaLaunchKernelEx(&cfg, ns_square_sum_kernel<T>, g, p.rows, p.cols, p.ldg, p.stride_g, partials) != cudaSuccess)
+    return last_launch();
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, ns_normalise_kernel<T>, g, p.rows, p.cols, p.ldg, p.stride_g,
+                     static_cast<const float*>(partials), static_cast<uint32_t>(blocks), scale, p.eps,
+                     reinterpret_cast<__half*>(ws + w.hi[0]), reinterpret_cast<__half*>(ws + w.lo[0]), w.ldx,
+                     w.stride_x);
+  return last_launch();
+}
+
+template <int CG, uint32_t NT>
+int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
+  using SymK = GroupedCfg<CG, Op::Sym, false, false, NT, false>;
+  uint8_t* const ws = static_cast<uint8_t*>(p.workspace);
+  const bool tall = p.rows > p.cols;
+  const uint32_t m = tall ? p.cols : p.rows;
+  __half* const gram = reinterpret_cast<__half*>(ws + w.gram);
+  __half* const poly = reinterpret_cast<__half*>(ws + w.poly);
+  const uint64_t lt = ceil_div_u64(m, SymK::LT);
+  const uint64_t sym_tiles = lt * (lt + 1) / 2 * p.batch;
+  const uint64_t all_tiles = ceil_div_u64(p.cols, SymK::LT) * ceil_div_u64(p.rows, NT) * p.batch;
+  if (sym_tiles > 0x7FFFFFFFull || all_tiles > 0x7FFFFFFFull) return GEMM_ERR_INVALID_ARG;
+
+  GroupedArgs base = {};
+  base.groups = p.batch;
+  base.pdl = 1;
+  base.status = ctx.status;
+  base.timeout_ns = ctx.timeout_ns;
+  base.stall_iter = 0xFFFFFFFFu;
+  base.diag = reinterpret_cast<float*>(ws + w.diag);
+  base.diag_n = m;
+
+  // Y as an operand: K-major P or Q; P as both operands of its square
+  CUtensorMap gramP, gramQ, polyP, polyQ;
+  if (!operand_map(&gramP, gram, m, m, p.batch, w.ldp, w.stride_p, p_box_rows<SymK, false>()) ||
+      !operand_map(&gramQ, gram, m, m, p.batch, w.ldp, w.stride_p, q_box_rows<SymK, false>()) ||
+      !operand_map(&polyP, poly, m, m, p.batch, w.ldp, w.stride_p, p_box_rows<SymK, false>()) ||
+      !operand_map(&polyQ, poly, m, m, p.batch, w.ldp, w.stride_p, q_box_rows<SymK, false>()))
+    return GEMM_ERR_LAUNCH;
+
+  for (int step = 0; step < p.steps; ++step) {
+    const int cur = step & 1;
+    const bool last = step + 1 == p.steps;
+    __half* const hi = reinterpret_cast<__half*>(ws + w.hi[cur]);
+    CUtensorMap xK, xKq, xMN;   // X by its rows (as P, as Q) and by its columns
+    if (!operand_map(&xK, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, p_box_rows<SymK, false>()) ||
+        !operand_map(&xKq, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, q_box_rows<SymK, false>()) ||
+        !operand_map(&xMN, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, 64))
+      return GEMM_ERR_LAUNCH;
+
+    GroupedArgs s = base;   // P = X X^T (or X^T X), the scale taken out
+    s.L = s.C = m;
+    s.K = tall ? p.rows : p.cols;
+    s.out = gram;
+    s.ldo = w.ldp;
+    s.stride_o = w.stride_p;
+    s.alpha = 1.0f / (scale * scale);
+    int rc = tall ? launch_grouped<CG, Op::Sym, true, true, NT, false>(xMN, xMN, s, sym_tiles, ctx, stream)
+                  : launch_grouped<CG, Op::Sym, false, false, NT, false>(xK, xKq, s, sym_tiles, ctx, stream);
+    if (rc != GEMM_OK) return rc;
+
+    s.K = m;                // Y = b P + c P P, its diagonal apart
+    s.out = poly;
+    s.alpha = p.c;
+    s.beta = p.b;
+    s.R = gram;
+    if ((rc = launch_grouped<CG, Op::Sym, false, false, NT, false>(gramP, gramQ, s, sym_tiles, ctx, stream)) != GEMM_OK)
+      return rc;
+
+    GroupedArgs t = base;   // X' = (a + d) X + Y X (or X (a + d) + X Y)
+    t.L = p.cols;
+    t.C = p.rows;
+    t.K = m;
+    t.alpha = p.a;
+    t.x_hi = hi;
+    t.x_lo = reinterpret_cast<const __half*>(ws + w.lo[cur]);
+    t.ldx = w.ldx;
+    t.stride_x = w.stride_x;
+    if (last) {
+      t.out = p.out;
+      t.ldo = p.ldo;
+      t.stride_o = p.stride_o;
+      t.out_scale = 1.0f / scale;
+      t.out_f32 = p.out_f32 ? 1u : 0u;
+    } else {
+      t.out = ws + w.hi[cur ^ 1];
+      t.out_lo = reinterpret_cast<__half*>(ws + w.lo[cur ^ 1]);
+      t.ldo = w.ldx;
+      t.stride_o = w.stride_x;
+    }
+    rc = tall ? launch_grouped<CG, Op::Apply, false, false, NT, false>(polyP, xKq, t, all_tiles, ctx, stream)
+              : launch_grouped<CG, Op::Apply, true, false, NT, false>(xMN, polyQ, t, all_tiles, ctx, stream);
+    if (rc != GEMM_OK) return rc;
+  }
+  return GEMM_OK;
+}
+
+}  // namespace
+
+uint64_t newton_schulz_bytes(uint64_t batch, uint64_t rows, uint64_t cols) {
+  return layout_of(batch, rows, cols).bytes;
+}
+
+int launch_newton_schulz(const NewtonSchulzProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
+  const Layout w = layout_of(p.batch, p.rows, p.cols);
+  // X is held times 2^k, near the square root of its longer side: its entries
+  // are then near 1 once its singular values are, and the fp16 halves far
+  // from their range's ends
+  const uint32_t n = p.rows > p.cols ? p.rows : p.cols;
+  const float scale = std::ldexp(1.0f, static_cast<int>(std::floor(0.5 * std::log2(static_cast<double>(n)))));
+  const int rc = p.g_f32 ? normalise<float>(p, w, scale, ctx, stream) : normalise<uint16_t>(p, w, scale, ctx, stream);
+  return rc != GEMM_OK ? rc : iterate<1, 128>(p, w, scale, ctx, stream);
+}
+
+}  // namespace gb300

@@ -320,6 +320,79 @@ int gemm_mxfp8_quantize_tiled(const float* X, int64_t rows, int64_t K, int64_t l
                               int64_t ldq, void* SF, cudaStream_t stream);
 
 /*
+ * Grouped products: rows sorted by group (a router's expert), each group's
+ * rows times its own matrix, and the two gradients.
+ *     gemm_bf16_grouped         D[r]  = A[r] * B[e]^T        offsets[e] <= r < offsets[e+1]
+ *     gemm_bf16_grouped_dgrad   dA[r] = dD[r] * B[e]
+ *     gemm_bf16_grouped_wgrad   dB[e] (+)= sum over e's rows r of dD[r]^T * A[r]
+ * A, dA [M, K]; D, dD [M, N]; B, dB [groups, N, K], matrix e at e * stride_b
+ * elements (stride_b >= N * ldb; ignored for one group); all row-major with
+ * pitches in elements.  offsets: groups + 1 int32 values on the DEVICE, rising,
+ * in [0, M]: the call reads them on the GPU, so a routing computed there needs
+ * no synchronisation.  (Values outside are clamped and falling ones raised: no
+ * access leaves the operands.)  Groups may be empty.  Rows before offsets[0]
+ * and from offsets[groups] on belong to no group: D and dA are not written
+ * there, and no value of another group's row, not even an Inf or NaN, reaches
+ * a group's result.
+ * Operands are bf16, sums fp32.  out_dtype: GEMM_DTYPE_BF16 or GEMM_DTYPE_F32
+ * (rounded once; fp32 results are added up from sums over 512 terms, which
+ * keeps the tensor core's truncating additions below 1e-6 of the result).
+ * accumulate (0 or 1): dB += instead of dB =, added in fp32; an empty group's
+ * dB is then left alone, and zeroed otherwise.  An empty reduction gives zeros
+ * in the rows of the groups.  groups == 0 or an empty output is a no-op.
+ * groups <= GEMM_MAX_GROUPS.  Operands must be 16-byte aligned with pitches
+ * (and B's stride, as an operand) that are multiples of 8; outputs sit at
+ * their element alignment with any pitch.  Outputs must not overlap operands.
+ * Calls are asynchronous on `stream`, allocate nothing and can be captured.
+ * Results do not depend on timing: the same call gives the same bits.  Errors
+ * as gemm_bf16.
+ */
+#define GEMM_MAX_GROUPS 1024
+int gemm_bf16_grouped(const void* A, const void* B, void* D, const int32_t* offsets, int64_t groups,
+                      int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t stride_b,
+                      int64_t ldd, int out_dtype, cudaStream_t stream);
+int gemm_bf16_grouped_dgrad(const void* dD, const void* B, void* dA, const int32_t* offsets,
+                            int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldd,
+                            int64_t ldb, int64_t stride_b, int64_t lda, int out_dtype,
+                            cudaStream_t stream);
+int gemm_bf16_grouped_wgrad(const void* dD, const void* A, void* dB, const int32_t* offsets,
+                            int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldd,
+                            int64_t lda, int64_t ldb, int64_t stride_b, int out_dtype,
+                            int accumulate, cudaStream_t stream);
+
+/*
+ * Newton-Schulz orthogonalisation of a batch of matrices, as the Muon
+ * optimiser applies it to a weight matrix's momentum:
+ *     X = G / (|G|_F + eps);  `steps` times, on the smaller side,
+ *     X <- a X + b (X X^T) X + c (X X^T)^2 X          (rows <= cols)
+ *     X <- a X + b X (X^T X) + c X (X^T X)^2          (rows > cols)
+ *     O = X
+ * which drives the singular values of G towards 1 and keeps its singular
+ * vectors.  G, O [batch, rows, cols] row-major, matrix i at i * stride
+ * elements (ignored for one matrix), any pitch, element alignment; in_dtype
+ * and out_dtype GEMM_DTYPE_BF16 or GEMM_DTYPE_F32.  1 <= steps <= 64; a, b, c
+ * finite; eps >= 0 finite.  The products run on the tensor cores with fp16
+ * operands and fp32 sums, X between steps in two fp16 halves, the norm in
+ * fp32: the result is within about 2e-3 of the 64-bit one (2-norm).  Steps
+ * whose coefficients drive X far beyond singular values of a few units
+ * overflow fp16.  A zero matrix gives zeros with eps > 0; a matrix with an Inf
+ * or NaN gives NaN, the others of the batch are not affected.
+ * workspace: 256-byte aligned device memory of at least
+ * gemm_newton_schulz_workspace_bytes(batch, rows, cols) bytes, uninitialised;
+ * calls that share one must not overlap on the GPU.  G is not written and must
+ * not overlap O or the workspace.  batch <= 65535, rows and cols <=
+ * GEMM_NEWTON_SCHULZ_MAX_DIM.  An empty batch or matrix is a no-op.
+ * Asynchronous on `stream`, allocates nothing, can be captured, the same bits
+ * every time.  Errors as gemm_bf16.
+ */
+#define GEMM_NEWTON_SCHULZ_MAX_DIM 65536
+int64_t gemm_newton_schulz_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int64_t cols,
+                       int64_t ldg, int64_t stride_g, int64_t ldo, int64_t stride_o, int in_dtype,
+                       int out_dtype, int steps, float a, float b, float c, float eps,
+                       void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status
  * word: GEMM_OK, GEMM_ERR_TIMEOUT when a kernel's bounded barrier wait gave up
  * (the kernel released its TMEM and returned; D is undefined), or

@@ -1,0 +1,379 @@
+"""Grouped products (matmul_grouped and its two gradients) against a plain
+implementation in 64 bits.
+
+Most cases use small integers: every product and partial sum is then exact in
+fp32, so the result must be the exact one rounded once to the output type, bit
+for bit -- at sizes around the tile edges (128 and 256 outputs, 64 and 16 of
+the reduction), with empty groups, rows outside every group, pitches and
+unaligned outputs.  Real-valued cases are held to
+
+    |err| <= u |ref| + n 2^-19 S,     S = sum_k |a_k b_k|,
+
+u = 2^-8 (bf16) or 2^-24 (fp32) for the one rounding, and for the sums n
+tensor-core steps of 16 terms (17 addends each cut off below 2^-23 of the
+largest: under 2^-18.9, halved on average by the sign of what is cut): n =
+ceil(K / 16), and for fp32 results, which are added up from segments of 512
+terms, 32 + K / 512."""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_blackwell_tcgen05_gb300 as g
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def ok():
+    assert g.gemm_last_status(stream()) == g.GEMM_OK
+
+
+def offsets_of(per, first=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(per)]) + first, dtype=torch.int32, device="cuda")
+
+
+def ints(gen, *shape, hi=3, pad=8, fill=1000.0):
+    """Integers in [-hi, hi] as bf16 in a buffer whose pitch is a multiple of
+    8 and whose padding columns hold `fill`."""
+    cols = (shape[-1] + 7) // 8 * 8 + (pad if shape[-1] % 3 == 0 else 0)
+    x = torch.full((*shape[:-1], cols), fill, dtype=torch.bfloat16, device="cuda")
+    x[..., :shape[-1]] = torch.randint(-hi, hi + 1, shape, generator=gen, device="cuda").to(torch.bfloat16)
+    return x[..., :shape[-1]]
+
+
+def gen(seed):
+    return torch.Generator("cuda").manual_seed(seed)
+
+
+def forward64(A, B, o):
+    D = torch.full((A.shape[0], B.shape[1]), float("nan"), dtype=torch.float64, device="cuda")
+    for e in range(B.shape[0]):
+        lo, hi = int(o[e]), int(o[e + 1])
+        D[lo:hi] = A[lo:hi].double() @ B[e].double().T
+    return D
+
+
+def dgrad64(dD, B, o):
+    return forward64(dD, B.transpose(1, 2), o)
+
+
+def wgrad64(dD, A, o, groups):
+    return torch.stack([dD[int(o[e]):int(o[e + 1])].double().T @ A[int(o[e]):int(o[e + 1])].double()
+                        for e in range(groups)])
+
+
+def marked(shape, dtype, pad=0, shift=0):
+    """A NaN-filled output view of pitch cols + pad starting `shift` elements in."""
+    n = int(np.prod(shape[:-1])) * (shape[-1] + pad) + shift
+    buf = torch.full((n,), float("nan"), dtype=dtype, device="cuda")
+    return buf, buf[shift:].view(*shape[:-1], shape[-1] + pad)[..., :shape[-1]]
+
+
+def equal_bits(got, want64):
+    want = want64.to(got.dtype)
+    bad = ~((got == want) | (got.isnan() & want.isnan()))
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} differ, first at {bad.nonzero()[0].tolist()}"
+
+
+# rows per group, N, K
+SHAPES = [
+    ([1], 1, 8),
+    ([1, 0, 2], 16, 64),
+    ([0, 0, 0], 24, 40),
+    ([127, 1, 128, 129, 0, 3], 128, 64),
+    ([16, 15, 17, 32, 33, 31, 48, 64, 65, 63], 136, 72),
+    ([300, 5, 260], 257, 200),
+    ([256, 512, 255, 257], 300, 520),
+    ([2, 700, 0, 1, 90], 1040, 328),
+    ([40] * 33, 64, 128),
+    ([3, 0] * 100, 72, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("per, N, K", SHAPES)
+def test_exact(per, N, K, dtype):
+    r = gen(N + K)
+    groups, first, after = len(per), 3 * (N % 2), 5 * (K % 3)
+    o = offsets_of(per, first)
+    M = first + sum(per) + after
+    A, dD = ints(r, M, K), ints(r, M, N)
+    B = ints(r, groups, N, K)
+    # fp32 sums of these integers are exact below 2^24; bf16 pads odd pitches too
+    for pad, shift in ((0, 0), (1, 0), (6, 1)):
+        buf, D = marked((M, N), dtype, pad, shift)
+        assert g.matmul_grouped(A, B, o, out=D) is D
+        ok()
+        equal_bits(D, forward64(A, B, o))
+        buf2, dA = marked((M, K), dtype, pad, shift)
+        g.matmul_grouped_dgrad(dD, B, o, out=dA)
+        ok()
+        equal_bits(dA, dgrad64(dD, B, o))
+        buf3, dB = marked((groups, N, K), dtype, pad, shift)
+        g.matmul_grouped_wgrad(dD, A, o, out=dB)
+        ok()
+        equal_bits(dB, wgrad64(dD, A, o, groups))
+        for b, view in ((buf, D), (buf2, dA), (buf3, dB)):
+            view.fill_(float("nan"))
+            assert b.isnan().all(), "wrote outside the output"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_random_shapes_exact(dtype):
+    rng = np.random.default_rng(11)
+    for i in range(24):
+        groups = int(rng.integers(1, 40))
+        per = rng.multinomial(int(2 ** rng.uniform(0, 11)), rng.dirichlet([0.4] * groups))
+        N, K = int(rng.integers(1, 700)), int(rng.integers(1, 700))
+        r = gen(i)
+        o = offsets_of(per)
+        M = int(per.sum())
+        A, dD, B = ints(r, M, K), ints(r, M, N), ints(r, groups, N, K)
+        what = f"{per.tolist()} N={N} K={K}"
+        for name, got, want in (
+                ("forward", g.matmul_grouped(A, B, o, out_dtype=dtype), lambda: forward64(A, B, o)),
+                ("dgrad", g.matmul_grouped_dgrad(dD, B, o, out_dtype=dtype), lambda: dgrad64(dD, B, o)),
+                ("wgrad", g.matmul_grouped_wgrad(dD, A, o, out_dtype=dtype), lambda: wgrad64(dD, A, o, groups))):
+            ok()
+            assert torch.equal(got, want().to(dtype)), f"{name} {what}"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("per, N, K", [([100, 0, 333, 70], 264, 1000), ([1100, 2500], 200, 136),
+                                       ([8] * 16, 512, 2048)])
+def test_real_values(per, N, K, dtype):
+    r = gen(5)
+    o, M, groups = offsets_of(per), sum(per), len(per)
+    A = torch.randn(M, K, device="cuda", generator=r).bfloat16()
+    dD = torch.randn(M, N, device="cuda", generator=r).bfloat16()
+    B = torch.randn(groups, N, K, device="cuda", generator=r).bfloat16()
+
+    def check(got, ref, S, red):
+        n = 32 + red / 512 if dtype == torch.float32 and red > 512 else -(-red // 16)
+        u = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+        bound = u * ref.abs() + n * 2.0 ** -19 * S
+        assert ((got.double() - ref).abs() <= bound).all()
+        if dtype == torch.float32:
+            # the segments keep the truncating additions' bias down
+            assert (got.double() - ref).norm() <= 1e-6 * ref.norm()
+
+    check(g.matmul_grouped(A, B, o, out_dtype=dtype), forward64(A, B, o), forward64(A.abs(), B.abs(), o), K)
+    check(g.matmul_grouped_dgrad(dD, B, o, out_dtype=dtype), dgrad64(dD, B, o), dgrad64(dD.abs(), B.abs(), o), N)
+    check(g.matmul_grouped_wgrad(dD, A, o, out_dtype=dtype), wgrad64(dD, A, o, groups),
+          wgrad64(dD.abs(), A.abs(), o, groups), max(per))
+    ok()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_accumulate(dtype):
+    per, N, K = [70, 0, 130, 1], 136, 264
+    r = gen(7)
+    o, M = offsets_of(per), sum(per)
+    A, dD = ints(r, M, K), ints(r, M, N)
+    old = torch.randint(-9, 10, (4, N, K), generator=r, device="cuda").to(dtype)
+    out = old.clone()
+    g.matmul_grouped_wgrad(dD, A, o, out=out, accumulate=True)
+    ok()
+    equal_bits(out, old.double() + wgrad64(dD, A, o, 4))
+    assert torch.equal(out[1], old[1])
+    out = old.clone()
+    g.matmul_grouped_wgrad(dD[:0], A[:0], torch.zeros_like(o), out=out, accumulate=True)
+    assert torch.equal(out, old)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_other_groups_values_stay_out(dtype):
+    """NaN and Inf in another group's rows, in rows of no group and in the
+    matrices of other groups: a group's result does not see them."""
+    per, N, K = [37, 5, 0, 91], 200, 136
+    r = gen(9)
+    o = offsets_of(per, 2)
+    M = sum(per) + 6
+    A, dD, B = ints(r, M, K), ints(r, M, N), ints(r, 4, N, K)
+    lo, hi = 2, 2 + 37
+    cA, cD, cB = A.clone(), dD.clone(), B.clone()
+    for t in (A, dD):
+        t[:lo] = float("inf")
+        t[hi:] = float("nan")
+    B[1:] = float("nan")
+    D, dA, dB = (g.matmul_grouped(A, B, o, out_dtype=dtype), g.matmul_grouped_dgrad(dD, B, o, out_dtype=dtype),
+                 g.matmul_grouped_wgrad(dD, A, o, out_dtype=dtype))
+    ok()
+    assert torch.equal(D[lo:hi], (cA[lo:hi].double() @ cB[0].double().T).to(dtype))
+    assert torch.equal(dA[lo:hi], (cD[lo:hi].double() @ cB[0].double()).to(dtype))
+    assert torch.equal(dB[0], (cD[lo:hi].double().T @ cA[lo:hi].double()).to(dtype))
+    assert (dB[2] == 0).all()
+    assert D[hi:hi + 5].isnan().all() and dB[1].isnan().all() and dB[3].isnan().all()
+    # inside a group they propagate
+    cA[lo, 3] = float("nan")
+    D = g.matmul_grouped(cA, cB, o, out_dtype=dtype)
+    assert D[lo].isnan().all() and not D[lo + 1:hi].isnan().any()
+
+
+def test_gradients_are_the_differences():
+    """<R, D(A + E, B) - D(A, B)> = <dA(R), E> and the same for B: exact in
+    integers, D being linear in each operand."""
+    per, N, K = [33, 0, 150], 136, 200
+    r = gen(3)
+    o, M = offsets_of(per), sum(per)
+    A, B, R = ints(r, M, K), ints(r, 3, N, K), ints(r, M, N)
+    E, F = ints(r, M, K, hi=1), ints(r, 3, N, K, hi=1)
+    f = lambda a, b: g.matmul_grouped(a, b, o, out_dtype=torch.float32).double()
+    dA = g.matmul_grouped_dgrad(R, B, o, out_dtype=torch.float32).double()
+    dB = g.matmul_grouped_wgrad(R, A, o, out_dtype=torch.float32).double()
+    base = f(A, B)
+    pad = lambda t: torch.nn.functional.pad(t, (0, -t.shape[-1] % 8))[..., :t.shape[-1]]
+    assert (R.double() * (f(pad(A + E), B) - base)).sum() == (dA * E.double()).sum()
+    assert (R.double() * (f(A, pad(B + F)) - base)).sum() == (dB * F.double()).sum()
+
+
+def test_bad_offsets_stay_inside():
+    """Offsets out of range or falling: clamped and raised, nothing written
+    outside the rows they then name."""
+    r = gen(4)
+    M, N, K = 100, 72, 64
+    A, B = ints(r, M, K), ints(r, 4, N, K)
+    o = torch.tensor([-5, 40, 20, 60, 1 << 30], dtype=torch.int32, device="cuda")
+    want = torch.tensor([0, 40, 40, 60, 100])
+    D = g.matmul_grouped(A, B, o)
+    ok()
+    equal_bits(D, forward64(A, B, want))
+    dB = g.matmul_grouped_wgrad(D := ints(r, M, N), A, o)
+    ok()
+    equal_bits(dB, wgrad64(D, A, want, 4))
+
+
+def test_empty_sizes():
+    o = torch.zeros(3, dtype=torch.int32, device="cuda")
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    assert g.matmul_grouped(z(0, 8), z(2, 5, 8), o).shape == (0, 5)
+    assert (g.matmul_grouped_wgrad(z(0, 8), z(0, 16), o) == 0).all()
+    assert g.matmul_grouped(z(4, 8), z(0, 5, 8), o[:1]).shape == (4, 5)
+    # an empty reduction: zeros in the groups' rows, the others left alone
+    o = torch.tensor([1, 2, 3], dtype=torch.int32, device="cuda")
+    out = torch.ones(4, 5, dtype=torch.bfloat16, device="cuda")
+    g.matmul_grouped(z(4, 0), z(2, 5, 0), o, out=out)
+    assert out[:, 0].tolist() == [1, 0, 0, 1] and (out[1:3] == 0).all()
+    out = torch.ones(4, 6, dtype=torch.float32, device="cuda")
+    g.matmul_grouped_dgrad(z(4, 0), z(2, 0, 6), o, out=out)
+    assert out[:, 5].tolist() == [1, 0, 0, 1]
+    ok()
+
+
+def test_stream_and_graph():
+    """On a side stream, and captured: a replay reads the offsets anew."""
+    r = gen(6)
+    per, N, K = [50, 14, 200], 264, 136
+    M = sum(per)
+    A, dD, B = ints(r, M, K), ints(r, M, N), ints(r, 3, N, K)
+    o = offsets_of(per)
+    D = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    dB = torch.zeros(3, N, K, dtype=torch.float32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g.matmul_grouped(A, B, o, out=D, stream=s)
+    g.matmul_grouped_wgrad(dD, A, o, out=dB, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    equal_bits(D, forward64(A, B, o))
+    equal_bits(dB, wgrad64(dD, A, o, 3))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.matmul_grouped(A, B, o, out=D)
+        g.matmul_grouped_wgrad(dD, A, o, out=dB)
+    o.copy_(offsets_of([7, 257, 0]))
+    graph.replay()
+    ok()
+    equal_bits(D, forward64(A, B, o))
+    equal_bits(dB, wgrad64(dD, A, o, 3))
+
+
+def test_same_bits_every_time():
+    r = gen(8)
+    o = offsets_of([400, 0, 37, 900])
+    A = torch.randn(1337, 520, device="cuda", generator=r).bfloat16()
+    dD = torch.randn(1337, 264, device="cuda", generator=r).bfloat16()
+    B = torch.randn(4, 264, 520, device="cuda", generator=r).bfloat16()
+    calls = (lambda: g.matmul_grouped(A, B, o, out_dtype=torch.float32),
+             lambda: g.matmul_grouped_dgrad(dD, B, o, out_dtype=torch.float32),
+             lambda: g.matmul_grouped_wgrad(dD, A, o, out_dtype=torch.float32))
+    for f in calls:
+        x = f()
+        assert all(torch.equal(x, f()) for _ in range(3))
+
+
+def test_large_offsets():
+    """Element offsets past 2^31 in B (its stride) and in D (its pitch)."""
+    r = gen(12)
+    N, K = 24, 64
+    big = torch.empty((1 << 31) + 8 + N * K, dtype=torch.bfloat16, device="cuda")
+    B = big.as_strided((2, N, K), ((1 << 31) + 8, K, 1))
+    B.copy_(ints(r, 2, N, K))
+    A, o = ints(r, 5, K), offsets_of([2, 3])
+    out = torch.empty(4 * (1 << 29) + N, dtype=torch.float32, device="cuda").as_strided((5, N), (1 << 29, 1))
+    g.matmul_grouped(A, B, o, out=out)
+    ok()
+    equal_bits(out, forward64(A, B, o))
+    dD = ints(r, 5, N)
+    dB = big.as_strided((2, N, K), ((1 << 31) + 8, K, 1))
+    g.matmul_grouped_wgrad(dD, A, o, out=dB)
+    ok()
+    equal_bits(dB, wgrad64(dD, A, o, 2))
+
+
+@pytest.mark.parametrize("stall", [0, 1])
+def test_stalled_load_times_out_then_recovers(stall):
+    r = gen(13)
+    per, N, K = [300, 41, 77], 520, 328
+    o, M = offsets_of(per), sum(per)
+    A, dD, B = ints(r, M, K), ints(r, M, N), ints(r, 3, N, K)
+    old = g.gemm_set_watchdog_ms(100)
+    try:
+        for f, want in ((lambda: g.matmul_grouped(A, B, o), lambda: forward64(A, B, o)),
+                        (lambda: g.matmul_grouped_dgrad(dD, B, o), lambda: dgrad64(dD, B, o)),
+                        (lambda: g.matmul_grouped_wgrad(dD, A, o), lambda: wgrad64(dD, A, o, 3))):
+            assert g.gemm_debug_stall_next_launch(stall) == g.GEMM_OK
+            f()
+            assert g.gemm_last_status(stream()) == g.GEMM_ERR_TIMEOUT
+            got = f()
+            ok()
+            equal_bits(got, want())
+    finally:
+        g.gemm_set_watchdog_ms(old)
+
+
+def test_tensor_refusals():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")
+    A, B, o = z(8, 16), z(2, 24, 16), torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        g.matmul_grouped(z(8, 24), B, o)
+    with pytest.raises(ValueError):
+        g.matmul_grouped(A, B, o[:2])
+    with pytest.raises(TypeError):
+        g.matmul_grouped(A, B, o.long())
+    with pytest.raises(TypeError):
+        g.matmul_grouped(A.float(), B, o)
+    with pytest.raises(TypeError):
+        g.matmul_grouped(A, B, o, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        g.matmul_grouped(A, B, o, out=z(8, 25))
+    with pytest.raises(ValueError):
+        g.matmul_grouped(A.cpu(), B, o)
+    with pytest.raises(ValueError):
+        g.matmul_grouped(A, B, o.cpu())
+    with pytest.raises(ValueError):
+        g.matmul_grouped(A.T, B, o)
+    with pytest.raises(ValueError):
+        g.matmul_grouped_wgrad(z(8, 24), A, o, accumulate=True)
+    with pytest.raises(ValueError):
+        g.matmul_grouped_wgrad(z(9, 24), A, o)
+    with pytest.raises(g.GemmError) as e:
+        g.matmul_grouped(z(8, 12), z(2, 24, 12), o)       # a 24-byte pitch
+    assert e.value.status == g.GEMM_ERR_ALIGNMENT
+    host = torch.zeros(8, 24, dtype=torch.bfloat16)
+    assert g.gemm_bf16_grouped(A.data_ptr(), B.data_ptr(), host.data_ptr(), o.data_ptr(), 2, 8, 24, 16, 16, 16,
+                               24 * 16, 24, g.DTYPE_BF16, stream()) == g.GEMM_ERR_INVALID_ARG

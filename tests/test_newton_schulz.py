@@ -1,0 +1,168 @@
+"""newton_schulz against the formula in 64 bits.
+
+Tolerance, on the 2-norm of the difference over that of the result.  A step
+rounds three operands to fp16 (unit 2^-11): X, which meets Y = b P + c P^2, and
+P and Y themselves.  With singular values near 1, |Y| is up to 2.8 against a
+result of at least 0.68, so a rounding enters up to 4 times larger; rounding
+errors of opposite sign cancel over a product's terms, so that the three
+together stay within 4 * 2^-11 a step.  Rounding the result adds 2^-9 (bf16).
+Directions of small singular values grow by up to 3.4445 a step: that they
+carry no more than this is what the low-rank case is for."""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_blackwell_tcgen05_gb300 as g
+
+pytestmark = pytest.mark.gpu
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def tolerance(steps, dtype):
+    return steps * 4 * 2.0 ** -11 + (2.0 ** -9 if dtype == torch.bfloat16 else 0.0)
+
+
+def reference(G, steps=5, coefficients=g.NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7):
+    a, b, c = coefficients
+    X = G.double()
+    tall = X.shape[-2] > X.shape[-1]
+    X = X.mT if tall else X
+    X = X / (X.square().sum((-2, -1), keepdim=True).sqrt() + eps)
+    for _ in range(steps):
+        P = X @ X.mT
+        X = a * X + b * (P @ X) + c * (P @ (P @ X))
+    return X.mT if tall else X
+
+
+def close(got, want, tol):
+    want = want.reshape(-1, *want.shape[-2:])
+    got = got.double().reshape(want.shape)
+    for i in range(want.shape[0]):
+        err = ((got[i] - want[i]).norm() / want[i].norm()).item()
+        assert err <= tol, f"matrix {i}: {err:.2e} > {tol:.2e}"
+
+
+SIZES = [(1, 1), (1, 9), (9, 1), (7, 5), (64, 64), (128, 128), (127, 300), (129, 128), (256, 256), (255, 513),
+         (300, 100), (640, 384), (520, 1040), (1041, 257)]
+
+
+@pytest.mark.parametrize("rows, cols", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_random(rows, cols, dtype, out_dtype):
+    gen = torch.Generator("cuda").manual_seed(rows + cols)
+    G = torch.randn(rows, cols, device="cuda", generator=gen).to(dtype)
+    for steps in (1, 5):
+        O = g.newton_schulz(G, steps=steps, out_dtype=out_dtype)
+        assert g.gemm_last_status(stream()) == g.GEMM_OK
+        close(O, reference(G, steps), tolerance(steps, out_dtype))
+
+
+@pytest.mark.parametrize("batch, rows, cols", [(3, 64, 200), (5, 200, 72), (2, 384, 384), (40, 16, 24)])
+def test_batch_pitches(batch, rows, cols):
+    """Batches with padded and odd pitches, an output that starts off any
+    vector's alignment, and scales apart by 1e6."""
+    gen = torch.Generator("cuda").manual_seed(batch)
+    buf = torch.full((batch, rows + 1, cols + 3), float("nan"), device="cuda")
+    G = buf[:, :rows, :cols]
+    G.copy_(torch.randn(batch, rows, cols, device="cuda", generator=gen) *
+            10.0 ** torch.linspace(-3, 3, batch, device="cuda")[:, None, None])
+    want = reference(G)
+    for pad, shift in ((0, 0), (1, 1), (4, 3)):
+        flat = torch.full((batch * rows * (cols + pad) + shift,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        O = flat[shift:].view(batch, rows, cols + pad)[..., :cols]
+        g.newton_schulz(G, out=O)
+        assert g.gemm_last_status(stream()) == g.GEMM_OK
+        close(O, want, tolerance(5, torch.bfloat16))
+        O.fill_(float("nan"))
+        assert flat.isnan().all(), "wrote outside the output"
+
+
+@pytest.mark.parametrize("rows, cols", [(512, 640), (640, 512), (96, 96)])
+@pytest.mark.parametrize("kind", ["rank8", "decay"])
+def test_small_singular_values(rows, cols, kind):
+    gen = torch.Generator("cuda").manual_seed(1)
+    if kind == "rank8":
+        G = torch.randn(rows, 8, device="cuda", generator=gen) @ torch.randn(8, cols, device="cuda", generator=gen)
+    else:
+        m = min(rows, cols)
+        q = lambda n: torch.linalg.qr(torch.randn(n, m, device="cuda", generator=gen))[0]
+        G = (q(rows) / torch.arange(1, m + 1, device="cuda") ** 1.5) @ q(cols).T
+    O = g.newton_schulz(G, out_dtype=torch.float32)
+    close(O, reference(G), tolerance(5, torch.float32))
+
+
+def test_other_coefficients():
+    """The cubic Newton-Schulz iteration (1.5, -0.5, 0), which converges to
+    the orthogonal factor itself."""
+    gen = torch.Generator("cuda").manual_seed(2)
+    G = torch.randn(96, 320, device="cuda", generator=gen)
+    O = g.newton_schulz(G, steps=24, coefficients=(1.5, -0.5, 0.0), out_dtype=torch.float32)
+    U, _, V = torch.linalg.svd(G.double(), full_matrices=False)
+    # at the fixed point |Y| = 0.5 and the errors of earlier steps die out: one step's remain
+    close(O, U @ V, tolerance(1, torch.float32))
+
+
+def test_zero_and_nonfinite_matrices():
+    gen = torch.Generator("cuda").manual_seed(3)
+    G = torch.randn(5, 160, 96, device="cuda", generator=gen)
+    G[1] = 0.0
+    G[2, 5, 7] = float("nan")
+    G[3, 9, 1] = float("inf")
+    O = g.newton_schulz(G, out_dtype=torch.float32)
+    assert g.gemm_last_status(stream()) == g.GEMM_OK
+    assert (O[1] == 0).all()
+    assert O[2].isnan().any() and O[3].isnan().any()
+    close(O[[0, 4]], reference(G[[0, 4]]), tolerance(5, torch.float32))
+
+
+def test_empty():
+    for shape in ((0, 4, 4), (2, 0, 5), (2, 5, 0)):
+        assert g.newton_schulz(torch.zeros(shape, device="cuda")).shape == shape
+
+
+def test_stream_graph_and_repeat():
+    gen = torch.Generator("cuda").manual_seed(4)
+    G = torch.randn(2, 300, 520, device="cuda", generator=gen)
+    ws = g.newton_schulz_workspace(2, 300, 520)
+    O = torch.empty(2, 300, 520, dtype=torch.float32, device="cuda")
+    first = g.newton_schulz(G, out=O, workspace=ws).clone()
+    for _ in range(3):
+        ws.fill_(255)      # NaN in every half: the workspace needs no clearing
+        assert torch.equal(g.newton_schulz(G, out=O, workspace=ws), first)
+    s = torch.cuda.Stream()
+    O.zero_()
+    s.wait_stream(torch.cuda.current_stream())
+    g.newton_schulz(G, out=O, workspace=ws, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(O, first)
+    with pytest.raises(ValueError):
+        g.newton_schulz(G, out=O, stream=s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.newton_schulz(G, out=O, workspace=ws)
+    G.mul_(3.0)            # the same directions
+    G[0] = G[1]
+    graph.replay()
+    assert g.gemm_last_status(stream()) == g.GEMM_OK
+    close(O, reference(G), tolerance(5, torch.float32))
+
+
+def test_tensor_refusals():
+    G = torch.zeros(4, 8, device="cuda")
+    with pytest.raises(TypeError):
+        g.newton_schulz(G.half())
+    with pytest.raises(ValueError):
+        g.newton_schulz(G.T)
+    with pytest.raises(ValueError):
+        g.newton_schulz(G.cpu())
+    with pytest.raises(ValueError):
+        g.newton_schulz(G, out=torch.zeros(4, 9, device="cuda"))
+    for kw in ({"steps": 0}, {"steps": 65}, {"eps": -1.0}, {"coefficients": (float("nan"), 0.0, 0.0)},
+               {"workspace": torch.empty(256, dtype=torch.uint8, device="cuda")}):
+        with pytest.raises(g.GemmError) as e:
+            g.newton_schulz(G, **kw)
+        assert e.value.status == g.GEMM_ERR_INVALID_ARG
