@@ -587,12 +587,25 @@ def quantize_mxfp8(X, stream=None):
 
 
 # --------------------------------------------------- expert-training operators
+#
+# A decoding step makes these calls with a few microseconds of GPU work each,
+# so the checks are one expression on the way to the call; what was wrong is
+# worked out only once something is.
+
+def _raw_stream(stream, device_index) -> int:
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return int(stream.cuda_stream)
+
 
 def _out_code(dtype):
     import torch
-    if dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("the output dtype must be bfloat16 or float32")
-    return DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16
+    if dtype is torch.bfloat16:
+        return DTYPE_BF16
+    if dtype is torch.float32:
+        return DTYPE_F32
+    raise TypeError("the output dtype must be bfloat16 or float32")
 
 
 def _check_3d(t, name):
@@ -602,31 +615,54 @@ def _check_3d(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _check_bf16(*named):
+def _refuse_grouped(x, x_name, B, offsets, groups):
+    """Raises for what is wrong with a grouped product's operands."""
     import torch
-    for t, name in named:
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bfloat16")
-
-
-def _check_offsets(offsets, groups):
-    import torch
+    _check_2d(x, x_name)
+    _check_3d(B, "B") if B.dim() == 3 else _check_2d(B, "A")
+    if x.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
+        raise TypeError("the operands must be bfloat16")
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise TypeError("offsets must be a contiguous 1-D int32 tensor")
     if not offsets.is_cuda:
         raise ValueError("offsets must be a CUDA tensor")
-    if groups is not None and offsets.numel() != groups + 1:
-        raise ValueError("offsets must hold one value more than there are groups")
+    raise ValueError(f"offsets must hold one value more than the {groups} groups")
 
 
 def _output(out, shape, dtype, device, name):
     import torch
     if out is None:
         return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
-    if tuple(out.shape) != tuple(shape):
+    if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     if dtype is not None and out.dtype != dtype:
         raise TypeError(f"{name} must have out_dtype")
+    return out
+
+
+def _grouped_rows(entry, x, x_name, B, offsets, dgrad, out, out_dtype, stream):
+    import torch
+    bf16 = torch.bfloat16
+    if not (x.dtype is bf16 and B.dtype is bf16 and offsets.dtype is torch.int32 and x.dim() == 2
+            and B.dim() == 3 and offsets.dim() == 1 and x.is_cuda and B.is_cuda
+            and offsets.is_cuda and x.stride(1) == 1 and B.stride(2) == 1
+            and offsets.shape[0] == B.shape[0] + 1 and offsets.is_contiguous()):
+        _check_3d(B, "B")
+        _refuse_grouped(x, x_name, B, offsets, B.shape[0])
+    groups, N, K = B.shape
+    M, reduced = x.shape
+    if reduced != (N if dgrad else K):
+        raise ValueError(f"{x_name} and B disagree on {'N' if dgrad else 'K'}")
+    out = _output(out, (M, K if dgrad else N), out_dtype, x.device, "out")
+    if out.dim() != 2 or out.stride(1) != 1 or not out.is_cuda:
+        _check_2d(out, "out")
+    sb, ldb, _ = B.stride()
+    rc = getattr(_lib or load(), entry)(
+        x.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups, M, N, K,
+        x.stride(0), ldb, sb, out.stride(0), _out_code(out.dtype),
+        _raw_stream(stream, x.get_device()))
+    if rc != GEMM_OK:
+        raise GemmError(rc, entry)
     return out
 
 
@@ -635,68 +671,42 @@ def matmul_grouped(A, B, offsets, out=None, out_dtype=None, stream=None):
     A [M,K] bf16, B [groups,N,K] bf16, offsets [groups+1] int32, all on the
     GPU; returns D [M,N] of out_dtype (bfloat16 or float32).  Rows that belong
     to no group are not written."""
-    _check_2d(A, "A")
-    _check_3d(B, "B")
-    _check_bf16((A, "A"), (B, "B"))
-    groups, N, K = B.shape
-    _check_offsets(offsets, groups)
-    M = A.shape[0]
-    if A.shape[1] != K:
-        raise ValueError("A and B disagree on K")
-    out = _output(out, (M, N), out_dtype, A.device, "out")
-    _check_2d(out, "out")
-    rc = gemm_bf16_grouped(A.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups,
-                           M, N, K, A.stride(0), B.stride(1), B.stride(0), out.stride(0),
-                           _out_code(out.dtype), _stream_handle(stream))
-    if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_grouped")
-    return out
+    return _grouped_rows("gemm_bf16_grouped", A, "A", B, offsets, False, out, out_dtype, stream)
 
 
 def matmul_grouped_dgrad(dD, B, offsets, out=None, out_dtype=None, stream=None):
     """The gradient of matmul_grouped to A: dA[r] = dD[r] @ B[e], dD [M,N]
     bf16; returns dA [M,K] of out_dtype (bfloat16 or float32)."""
-    _check_2d(dD, "dD")
-    _check_3d(B, "B")
-    _check_bf16((dD, "dD"), (B, "B"))
-    groups, N, K = B.shape
-    _check_offsets(offsets, groups)
-    M = dD.shape[0]
-    if dD.shape[1] != N:
-        raise ValueError("dD and B disagree on N")
-    out = _output(out, (M, K), out_dtype, dD.device, "out")
-    _check_2d(out, "out")
-    rc = gemm_bf16_grouped_dgrad(dD.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(),
-                                 groups, M, N, K, dD.stride(0), B.stride(1), B.stride(0),
-                                 out.stride(0), _out_code(out.dtype), _stream_handle(stream))
-    if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_grouped_dgrad")
-    return out
+    return _grouped_rows("gemm_bf16_grouped_dgrad", dD, "dD", B, offsets, True, out, out_dtype,
+                         stream)
 
 
 def matmul_grouped_wgrad(dD, A, offsets, out=None, out_dtype=None, accumulate=False, stream=None):
     """The gradient of matmul_grouped to B: dB[e] = dD[rows of e].T @ A[rows of
     e]; returns dB [groups,N,K] of out_dtype (bfloat16 or float32).  With
     accumulate, adds to `out` instead."""
-    _check_2d(dD, "dD")
-    _check_2d(A, "A")
-    _check_bf16((dD, "dD"), (A, "A"))
+    import torch
+    bf16 = torch.bfloat16
+    if not (dD.dtype is bf16 and A.dtype is bf16 and offsets.dtype is torch.int32 and dD.dim() == 2
+            and A.dim() == 2 and offsets.dim() == 1 and dD.is_cuda and A.is_cuda
+            and offsets.is_cuda and dD.stride(1) == 1 and A.stride(1) == 1
+            and offsets.shape[0] > 0 and offsets.is_contiguous()):
+        _refuse_grouped(dD, "dD", A, offsets, 0)
     M, N = dD.shape
     K = A.shape[1]
     if A.shape[0] != M:
         raise ValueError("dD and A disagree on M")
-    _check_offsets(offsets, None)
-    groups = offsets.numel() - 1
-    if groups < 0:
-        raise ValueError("offsets must hold one value more than there are groups")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
+    groups = offsets.shape[0] - 1
     out = _output(out, (groups, N, K), out_dtype, A.device, "out")
-    _check_3d(out, "out")
-    rc = gemm_bf16_grouped_wgrad(dD.data_ptr(), A.data_ptr(), out.data_ptr(), offsets.data_ptr(),
-                                 groups, M, N, K, dD.stride(0), A.stride(0), out.stride(1),
-                                 out.stride(0), _out_code(out.dtype), int(bool(accumulate)),
-                                 _stream_handle(stream))
+    if out.dim() != 3 or out.stride(2) != 1 or not out.is_cuda:
+        _check_3d(out, "out")
+    sb, ldb, _ = out.stride()
+    rc = (_lib or load()).gemm_bf16_grouped_wgrad(
+        dD.data_ptr(), A.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups, M, N, K,
+        dD.stride(0), A.stride(0), ldb, sb, _out_code(out.dtype), 1 if accumulate else 0,
+        _raw_stream(stream, A.get_device()))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_bf16_grouped_wgrad")
     return out
@@ -737,7 +747,8 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     rc = gemm_newton_schulz(batched.data_ptr(), o.data_ptr(), batch, rows, cols, batched.stride(1),
                             batched.stride(0), o.stride(1), o.stride(0), _out_code(G.dtype),
                             _out_code(out.dtype), steps, a, b, c, eps, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                            workspace.numel() * workspace.element_size(),
+                            _raw_stream(stream, G.get_device()))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_newton_schulz")
     return out

@@ -22,7 +22,9 @@
 //              to the matrix.
 //   Op::Apply  X' = (a + d) X + B X (B symmetric without its diagonal d; P_MN),
 //              or X (a + d) + X B (P K-major), X held as two halves hi + lo
-//              of which hi feeds the tensor cores.
+//              of which hi feeds the tensor cores.  ApplyOut: the last one,
+//              whose X' is rounded once to the result's type.
+//   Op::SumAdd is Op::Sum added to what the output holds.
 //
 // Persistent, warp-specialised: warp 0 lane 0 loads operand tiles of 64 k by
 // TMA (128-byte swizzle) into a ring of stages, warp 1 lane 0 issues the MMAs
@@ -41,11 +43,11 @@
 
 namespace gb300 {
 
-enum class Op { Rows, Sum, Sym, Apply };
+enum class Op { Rows, Sum, SumAdd, Sym, Apply, ApplyOut };
 
 // Groups a launch can hold: the offsets and the tile table sit in shared memory.
 constexpr uint32_t kMaxGroups = 1024;
-// Up to this many groups, Op::Sum deals groups out by falling size.
+// Up to this many groups, they are sorted by size before they are dealt out.
 constexpr uint32_t kMaxSortedGroups = 256;
 
 struct GroupedArgs {
@@ -56,7 +58,6 @@ struct GroupedArgs {
   const int32_t* offsets;      // [groups + 1] first row of each group (Rows, Sum)
   void* out;                   // bf16 / fp32 (Rows, Sum), fp16 (Sym), fp16 hi or the result (Apply)
   uint64_t ldo, stride_o;      // pitch and matrix stride of `out` in elements
-  uint32_t accumulate;         // Sum: out += instead of out =
   uint32_t fmt;                // operand type: 1 bf16, 0 fp16
   uint32_t pdl;                // launched while its predecessor runs: wait for it before touching memory
   // Sym: out = alpha acc + beta R[l, c].   Apply: v = (alpha + diag) X + acc
@@ -67,9 +68,9 @@ struct GroupedArgs {
   const __half* x_hi;          // Apply: X as hi + lo (pitch ldx, stride stride_x)
   const __half* x_lo;
   uint64_t ldx, stride_x;      // also R's pitch and stride
-  __half* out_lo;              // Apply: the lo half of X'; nullptr: `out` is the result
-  float out_scale;             // Apply, result: factor on the way out
-  uint32_t out_f32;            // Apply, result: fp32 (else bf16)
+  __half* out_lo;              // Apply: the lo half of X'
+  float out_scale;             // ApplyOut: factor on the way out
+  uint32_t out_f32;            // ApplyOut: fp32 (else bf16)
   unsigned long long* status;
   unsigned long long timeout_ns;
   uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
@@ -78,10 +79,16 @@ struct GroupedArgs {
 // One tile of work.  P rows l0.., Q rows c0.. of group / matrix z; Rows: Q's
 // rows start at memory row row0 + c0; Sum: the reduction covers memory rows
 // row0 .. row0 + k_len - 1.
-struct TileItem {
+struct __align__(16) TileItem {
   uint32_t z, l0, c0, live, row0, k_len;
-  bool mirror;
+  uint32_t mirror;   // Sym: store the tile's mirror image too
+  uint32_t valid;    // 0: past the cluster's last tile
 };
+
+// A cluster's first tiles are worked out ahead by all threads at once; the
+// division-heavy arithmetic (0.5 us of one thread's time) would otherwise
+// stand between two tiles' MMAs.
+constexpr uint32_t kAheadItems = 128;
 
 // Columns [c0, c0 + live) of the tile as the MMA's N: CTA pairs take
 // multiples of 32 (16 rows of Q from each CTA), one CTA multiples of 16.
@@ -97,12 +104,16 @@ struct GroupedCfg {
   static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
   static constexpr uint32_t LT = 128 * CG;               // lanes (output columns) per tile
   static constexpr uint32_t Q_ROWS = NT / CG;            // Q rows staged by one CTA
-  static_assert(!Q_MN || Q_ROWS == 128, "an MN-major Q tile is two 64-wide boxes");
+  static_assert(!Q_MN || Q_ROWS == 128 || (Q_ROWS == 64 && OP == Op::Sym), "an MN-major Q tile is 64-wide boxes");
   static_assert(Q_ROWS % 16 == 0 && Q_ROWS <= 256 && NT <= 256, "tile width");
+  static constexpr uint32_t Q_BOX = Q_ROWS < 32 ? Q_ROWS : 32;   // rows per load of a K-major Q
   static constexpr uint32_t P_BYTES = 128 * 128;
   static constexpr uint32_t Q_BYTES = Q_ROWS * 128;
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr bool TAIL = OP == Op::Sum;            // a warp clears ragged reduction ends
+  static constexpr bool ADD = OP == Op::SumAdd;          // out += instead of out =
+  static constexpr bool SUM = OP == Op::Sum || ADD;
+  static constexpr bool APPLY = OP == Op::Apply || OP == Op::ApplyOut;
+  static constexpr bool TAIL = SUM;                      // a warp clears ragged reduction ends
   static constexpr uint32_t kEpiWarps = 8;
   static constexpr uint32_t kTailWarp = 2 + kEpiWarps;
   static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps + (TAIL ? 1 : 0));
@@ -113,15 +124,16 @@ struct GroupedCfg {
   // nearest.  bf16 and fp16 outputs round far above that and take one segment.
   static constexpr uint32_t SEG_TILES = OUT32 ? 8u : 0xFFFFFFFFu;
   static constexpr uint32_t NCH = (NT + 63) / 64;        // 32-column chunks per epilogue warp
-  static constexpr bool GROUPED = OP == Op::Rows || OP == Op::Sum;
-  static constexpr uint32_t TABLE_BYTES = GROUPED ? 2 * 4 * (kMaxGroups + 8) : 0;
+  static constexpr bool GROUPED = OP == Op::Rows || SUM;
+  static constexpr uint32_t ITEM_BYTES = kAheadItems * sizeof(TileItem);
+  static constexpr uint32_t TABLE_BYTES = ITEM_BYTES + (GROUPED ? 2 * 4 * (kMaxGroups + 8) : 0);
   static constexpr uint32_t BAR_BYTES = 512;
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;
   static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - TABLE_BYTES) / STAGE_BYTES;
   static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
   static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + BAR_BYTES + TABLE_BYTES;
-  static_assert((3 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
+  static_assert((3 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = 256;              // second accumulator's first column
 };
@@ -154,64 +166,74 @@ __device__ __forceinline__ void grid_dependents_launch() {
 }
 
 // The wi-th tile of cluster c among G; false past the last.  Every role of
-// every CTA walks the same sequence.  offs: the clamped offsets; tab: first
-// tile of each group (Rows), or the groups by falling size (Sum).
+// every CTA walks the same sequence.  offs: the clamped offsets; tab: the
+// first tile of each group and their number (Rows), or the groups in the order
+// they are walked (Sum).
 template <class C, int CG, Op OP, uint32_t NT>
 __device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* offs, const uint32_t* tab,
                                           uint32_t c, uint32_t G, uint32_t wi, TileItem& w) {
   const uint32_t lt = (a.L + C::LT - 1) / C::LT;
-  w.mirror = false;
+  w.mirror = 0u;
   w.row0 = 0;
   w.k_len = a.K;
   if constexpr (OP == Op::Rows) {
-    const uint32_t t = c + wi * G;
-    if (t >= tab[a.groups]) return false;
-    uint32_t lo = 0, hi = a.groups;        // tab[lo] <= t < tab[hi]
+    // Group by group, dealt round-robin: a group's matrix is read by all
+    // clusters at about the same time.  (Groups by falling tile width, equal
+    // tiles within a group and alternating directions measured the same on
+    // uneven groups of 512 rows: what is left to even out is the power limit's.)
+    const uint32_t x = c + wi * G;
+    if (x >= tab[a.groups]) return false;
+    uint32_t lo = 0, hi = a.groups;        // tab[lo] <= x < tab[hi]
     while (hi - lo > 1) {
       const uint32_t mid = (lo + hi) / 2;
-      if (tab[mid] <= t) lo = mid; else hi = mid;
+      if (tab[mid] <= x) lo = mid; else hi = mid;
     }
-    const uint32_t rows = offs[lo + 1] - offs[lo];
-    uint32_t cb, lb;
-    tile_coords(t - tab[lo], (rows + NT - 1) / NT, lt, 8u, cb, lb);
     w.z = lo;
     w.row0 = offs[lo];
+    const uint32_t rows = offs[lo + 1] - w.row0;
+    uint32_t cb, lb;
+    tile_coords(x - tab[lo], (rows + NT - 1) / NT, lt, 8u, cb, lb);
     w.c0 = cb * NT;
     w.l0 = lb * C::LT;
     w.live = w.c0 < rows ? min(NT, rows - w.c0) : 0u;
     return true;
-  } else if constexpr (OP == Op::Sum) {
-    // groups by falling size, rounds dealt in alternating directions: the
-    // clusters end within about the smallest tile of each other
+  } else if constexpr (C::SUM) {
+    // Large and small groups in turn, so that a tile bound by its MMAs runs
+    // beside one bound by its store; rounds in alternating directions.
     const uint32_t ct = (a.C + NT - 1) / NT, per = lt * ct;
     const uint32_t t = wi * G + ((wi & 1u) ? G - 1u - c : c);
     if (t >= per * a.groups) return false;
-    const uint32_t g = t / per;
+    // tiles of the groups 2p and 2p + 1 of the order alternate
+    const uint32_t pr = t / (2 * per), r = t - pr * 2 * per;
+    const bool both = 2 * pr + 1 < a.groups;
+    const uint32_t g = both ? 2 * pr + (r & 1u) : 2 * pr;
     w.z = tab[g];
     w.row0 = offs[w.z];
     w.k_len = offs[w.z + 1] - w.row0;
     uint32_t cb, lb;
-    tile_coords(t - g * per, ct, lt, 8u, cb, lb);
+    tile_coords(both ? r / 2 : r, ct, lt, 8u, cb, lb);
     w.c0 = cb * NT;
     w.l0 = lb * C::LT;
     w.live = min(NT, a.C - w.c0);
     return true;
   } else if constexpr (OP == Op::Sym) {
-    // tiles on and below the diagonal, row by row (LT == NT)
-    static_assert(C::LT == NT || OP != Op::Sym, "square tiles");
-    const uint32_t per = lt * (lt + 1) / 2;
+    // blocks of LT x LT on and below the diagonal, row by row, each as LT / NT
+    // tiles; those on it are stored as they are, the others twice
+    constexpr uint32_t kPer = C::LT / NT;
+    static_assert(OP != Op::Sym || C::LT % NT == 0, "tiles divide the diagonal's blocks");
+    const uint32_t per = kPer * (lt * (lt + 1) / 2);
     const uint32_t t = c + wi * G;
     if (t >= per * a.groups) return false;
     w.z = t / per;
-    const uint32_t r = t - w.z * per;
+    const uint32_t r = (t - w.z * per) / kPer;
     uint32_t i = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > r) --i;
     while ((i + 1) * (i + 2) / 2 <= r) ++i;
     const uint32_t j = r - i * (i + 1) / 2;
     w.l0 = i * C::LT;
-    w.c0 = j * NT;
-    w.live = min(NT, a.C - w.c0);
-    w.mirror = i != j;
+    w.c0 = j * C::LT + t % kPer * NT;      // (per is a multiple of kPer)
+    w.live = w.c0 < a.C ? min(NT, a.C - w.c0) : 0u;
+    w.mirror = i != j ? 1u : 0u;
     return true;
   } else {
     const uint32_t ct = (a.C + NT - 1) / NT, per = lt * ct;
@@ -230,25 +252,15 @@ __device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* 
 // Two neighbouring output columns of one row per lane instead of two rows of
 // one column: lanes 2j and 2j + 1 hold columns 2j, 2j + 1 of rows 2i (v0) and
 // 2i + 1 (v1); afterwards lane 2j has row 2i's pair, lane 2j + 1 row 2i + 1's.
-__device__ __forceinline__ void pair_columns(uint32_t v0, uint32_t v1, uint32_t odd, float& x0, float& x1) {
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-  x0 = __uint_as_float(odd ? got : v0);
-  x1 = __uint_as_float(odd ? v1 : got);
+__device__ __forceinline__ void pair_columns(float v0, float v1, uint32_t odd, float& x0, float& x1) {
+  const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+  x0 = odd ? got : v0;
+  x1 = odd ? v1 : got;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Stores the 16-bit pair `p` at columns col, col + 1 of row pointer `dst`.
-__device__ __forceinline__ void store_pair16(uint16_t* dst, uint32_t col, uint32_t L, bool vec, uint32_t p) {
-  if (vec && col + 1 < L) {
-    *reinterpret_cast<uint32_t*>(dst + col) = p;
-  } else {
-    if (col < L) dst[col] = static_cast<uint16_t>(p & 0xFFFFu);
-    if (col + 1 < L) dst[col + 1] = static_cast<uint16_t>(p >> 16);
-  }
 }
 
 template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32>
@@ -270,7 +282,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
   const uint32_t drain_bar = bar0 + 8 * (kAccBar0 + 4);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (kAccBar0 + 5));
   volatile uint32_t* const abort_flag = tmem_slot + 1;
-  uint32_t* const offs = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
+  TileItem* const ahead = reinterpret_cast<TileItem*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
+  uint32_t* const offs = reinterpret_cast<uint32_t*>(ahead + kAheadItems);
   uint32_t* const tab = offs + kMaxGroups + 8;
 
   const uint32_t warp = warp_idx_sync();
@@ -288,12 +301,11 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       tma_prefetch_desc(&tmQ);
       *abort_flag = 0u;
     }
-    // arrivals: a full barrier gets the producer's expect_tx, or, with a tail
-    // warp, one arrival from each CTA (its producer, or its tail warp on a
-    // ragged tile); an accumulator is handed back by every epilogue warp
+    // arrivals: a full barrier gets the leader's expect_tx (its producer's, or
+    // its tail warp's on a ragged tile); an accumulator is handed back by
+    // every epilogue warp
     for (uint32_t i = lane; i < kAccBar0 + 5; i += 32) {
       uint32_t count = 1;
-      if (C::TAIL && i < C::STAGES) count = CG;
       if (i == kAccBar0 + 2 || i == kAccBar0 + 3) count = C::kEpiWarps * CG;
       mbar_init(bar0 + 8 * i, count);
     }
@@ -303,15 +315,12 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
     tmem_alloc<CG>(smem_addr(tmem_slot), C::TMEM_COLS);
     tmem_relinquish<CG>();
   }
-  if (args.pdl) {
-    grid_dependents_launch();
-    grid_dependency_wait();
-  }
+  if (args.pdl) grid_dependents_launch();
   if constexpr (C::GROUPED) {
     // offsets clamped into [0, rows] and made to rise: whatever they hold, no
     // access leaves the operands and the groups do not overlap
     const int32_t rows = static_cast<int32_t>(OP == Op::Rows ? args.C : args.K);
-    if (warp == 0) {
+    if (warp == 2) {
       int32_t top = 0;
       for (uint32_t e0 = 0; e0 <= args.groups; e0 += 32) {
         const uint32_t e = e0 + lane;
@@ -328,14 +337,13 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       __syncwarp();
     }
     if constexpr (OP == Op::Rows) {
-      // first tile of each group: an exclusive sum by warp 0
-      if (warp == 0) {
+      // first tile of each group: an exclusive sum
+      if (warp == 2) {
         const uint32_t lt = (args.L + C::LT - 1) / C::LT;
         uint32_t sum = 0;
         for (uint32_t e0 = 0; e0 < args.groups; e0 += 32) {
           const uint32_t e = e0 + lane;
-          uint32_t n = 0;
-          if (e < args.groups) n = (offs[e + 1] - offs[e] + NT - 1) / NT * lt;
+          const uint32_t n = e < args.groups ? (offs[e + 1] - offs[e] + NT - 1) / NT * lt : 0u;
           uint32_t incl = n;
 #pragma unroll
           for (uint32_t d = 1; d < 32; d *= 2) {
@@ -348,6 +356,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
         if (lane == 0) tab[args.groups] = sum;
       }
     } else {
+      // the group with most rows, the one with fewest, the next, ...
       __syncthreads();
       for (uint32_t e = threadIdx.x; e < args.groups; e += C::kThreads) {
         uint32_t place = e;
@@ -358,10 +367,18 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
             const uint32_t m = offs[f + 1] - offs[f];
             place += (m > n || (m == n && f < e)) ? 1u : 0u;
           }
+          place = 2 * place < args.groups ? 2 * place : 2 * (args.groups - 1 - place) + 1;
         }
         tab[place] = e;
       }
     }
+    __syncthreads();
+  }
+  static_assert(kAheadItems <= C::kThreads, "one item per thread");
+  if (threadIdx.x < kAheadItems) {
+    TileItem w;
+    w.valid = tile_item<C, CG, OP, NT>(args, offs, tab, cluster_id, G, threadIdx.x, w) ? 1u : 0u;
+    ahead[threadIdx.x] = w;
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -369,12 +386,19 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const auto item = [&](uint32_t wi, TileItem& w) {
+    if (wi < kAheadItems) {
+      w = ahead[wi];
+      return w.valid != 0u;
+    }
     return tile_item<C, CG, OP, NT>(args, offs, tab, cluster_id, G, wi, w);
   };
 
   if (warp == 0) {
     // ==================== TMA producer: one thread ==============================
     if (lane == 0) {
+      // (the threads that touch memory wait for the predecessor; every CTA
+      // has some, so none ends before it)
+      if (args.pdl) grid_dependency_wait();
       const uint64_t pol = l2_policy_evict_last();
       uint32_t it = 0;
       uint32_t tail_last = 0, tail_phase = 0;   // per stage: its last tile was ragged; its tail barrier's parity
@@ -383,6 +407,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
         const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
         const uint32_t h = mma_n<CG>(w.live) / CG;     // Q rows this CTA contributes to the MMA
+        // a K-major Q arrives in boxes of Q_BOX rows, as many as the MMA reads
+        const uint32_t q_boxes = Q_MN ? 0u : (h + C::Q_BOX - 1) / C::Q_BOX;
+        const uint32_t tx = C::P_BYTES + (Q_MN ? C::Q_BYTES : q_boxes * C::Q_BOX * 128);
         const int32_t px = static_cast<int32_t>(w.l0 + rank * 128);
         const int32_t qy = static_cast<int32_t>(w.c0 + rank * h);
         for (uint32_t kt = 0; kt < kt_n; ++kt, ++it) {
@@ -401,7 +428,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           bool pair = false;
           if (ragged) {
             bar = tail_bar(s);
-            mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+            mbar_arrive_expect_tx(bar, tx);
             tail_last |= 1u << s;
             tail_phase ^= 1u << s;
           } else {
@@ -410,16 +437,15 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
               pair = true;
               bar = mapa_shared(full_bar(s), 0);
             }
-            if (leader) mbar_arrive_expect_tx(full_bar(s), CG * C::STAGE_BYTES);
-            else if (C::TAIL) mbar_arrive_cluster(bar);
+            if (leader) mbar_arrive_expect_tx(full_bar(s), CG * tx);
           }
           const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y, int32_t z) {
             if (CG == 2 && pair) tma_load_3d_pair(dst, m, bar, x, y, z, pol);
             else tma_load_3d(dst, m, bar, x, y, z, pol);
           };
-          const int32_t pz = static_cast<int32_t>(OP == Op::Sum ? 0u : w.z);
+          const int32_t pz = static_cast<int32_t>(C::SUM ? 0u : w.z);
           const int32_t qz = static_cast<int32_t>(C::GROUPED ? 0u : w.z);
-          const int32_t kr = static_cast<int32_t>((OP == Op::Sum ? w.row0 : 0u)) + k0;
+          const int32_t kr = static_cast<int32_t>((C::SUM ? w.row0 : 0u)) + k0;
           if constexpr (P_MN) {
             load(sb, &tmP, px, kr, pz);
             load(sb + 8192, &tmP, px + 64, kr, pz);
@@ -427,10 +453,13 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
             load(sb, &tmP, k0, px, pz);
           }
           if constexpr (Q_MN) {
-            load(sb + C::P_BYTES, &tmQ, qy, kr, qz);
-            load(sb + C::P_BYTES + 8192, &tmQ, qy + 64, kr, qz);
+#pragma unroll
+            for (uint32_t x = 0; x < C::Q_ROWS; x += 64)
+              load(sb + C::P_BYTES + x * 128, &tmQ, qy + static_cast<int32_t>(x), kr, qz);
           } else {
-            load(sb + C::P_BYTES, &tmQ, k0, static_cast<int32_t>(OP == Op::Rows ? w.row0 : 0u) + qy, qz);
+            const int32_t y = static_cast<int32_t>(OP == Op::Rows ? w.row0 : 0u) + qy;
+            for (uint32_t r = 0; r < q_boxes; ++r)
+              load(sb + C::P_BYTES + r * C::Q_BOX * 128, &tmQ, k0, y + static_cast<int32_t>(r * C::Q_BOX), qz);
           }
         }
       }
@@ -441,7 +470,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           const uint32_t s = i % C::STAGES;
           if (i == args.stall_iter) continue;
           if ((tail_last >> s) & 1u) drain_wait(tail_bar(s), ((tail_phase >> s) & 1u) ^ 1u, wd, kSiteProducerDrain);
-          else if (leader) drain_wait(full_bar(s), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
+          if (leader) drain_wait(full_bar(s), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
         }
       }
     }
@@ -530,8 +559,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (CG == 1) mbar_arrive(full_bar(s));
-        else mbar_arrive_cluster(mapa_shared(full_bar(s), 0));
+        // the leader's barrier: its own arrival, and 4 bytes from the peer CTA
+        if (leader) mbar_arrive_expect_tx(full_bar(s), CG == 2 ? 4u : 0u);
+        else st_async_u32(mapa_shared(smem_addr(tmem_slot + 2), 0), s, mapa_shared(full_bar(s), 0));
       }
     }
   } else {
@@ -542,6 +572,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
     uint32_t j = 0;
     bool ok = true;
     TileItem w;
+    if (args.pdl) grid_dependency_wait();
     for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
       const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
       const uint32_t lbase = w.l0 + rank * 128 + q * 32;   // this warp's first output column
@@ -551,13 +582,23 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       const uint64_t out0 = OP == Op::Rows
                                 ? static_cast<uint64_t>(w.row0 + w.c0) * args.ldo
                                 : w.z * args.stride_o + static_cast<uint64_t>(w.c0) * args.ldo;
+      // The hand-back of an accumulator whose reads are complete
+      // (tcgen05.wait::ld): it publishes nothing.
       const auto release = [&](uint32_t b) {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           if constexpr (CG == 1) mbar_arrive(acce_bar(b));
-          else mbar_arrive_cluster(mapa_shared(acce_bar(b), 0));
+          else mbar_arrive_cluster_relaxed(mapa_shared(acce_bar(b), 0));
         }
+      };
+      const auto t_addr = [&](uint32_t ch) {
+        return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + ch * 32;
+      };
+      const auto acc_wait = [&]() {
+        ok = warp_wait(accf_bar(j & 1u), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane);
+        tc_fence_after_sync();
+        return ok;
       };
       if constexpr (OUT32) {
         float acc[C::NCH][32];
@@ -566,181 +607,227 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
 #pragma unroll
           for (uint32_t t = 0; t < 32; ++t) acc[i][t] = 0.0f;
         for (uint32_t k = 0; k < kt_n; k += C::SEG_TILES, ++j) {
-          const uint32_t b = j & 1u;
-          if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t t_addr = tmem_base + ((q * 32u) << 16) + b * C::ACC_COLS;
+          if (!acc_wait()) break;
 #pragma unroll
           for (uint32_t i = 0; i < C::NCH; ++i) {
             if (2 * i + eg < nch) {
               uint32_t v[32];
-              tmem_ld_32x32b_x32_sync(t_addr + (2 * i + eg) * 32, v);
+              tmem_ld_32x32b_x32_sync(t_addr(2 * i + eg), v);
 #pragma unroll
               for (uint32_t t = 0; t < 32; ++t) acc[i][t] += __uint_as_float(v[t]);
             }
           }
-          release(b);
+          release(j & 1u);
         }
         if (!ok) break;
+        if (C::ADD && kt_n == 0) continue;
         float* const o = static_cast<float*>(args.out) + out0 + col;
 #pragma unroll
         for (uint32_t i = 0; i < C::NCH; ++i) {
           const uint32_t c0 = (2 * i + eg) * 32;
-          if (col < args.L) {
+          float* p = o + static_cast<uint64_t>(c0) * args.ldo;
+          if (c0 + 32 <= w.live && lbase + 32 <= args.L && !(C::ADD)) {
 #pragma unroll
-            for (uint32_t t = 0; t < 32; ++t)
-              if (c0 + t < w.live) {
-                float* p = o + static_cast<uint64_t>(c0 + t) * args.ldo;
-                *p = (OP == Op::Sum && args.accumulate) ? *p + acc[i][t] : acc[i][t];
-              }
+            for (uint32_t t = 0; t < 32; ++t, p += args.ldo) *p = acc[i][t];
+          } else if (col < args.L) {
+#pragma unroll
+            for (uint32_t t = 0; t < 32; ++t, p += args.ldo)
+              if (c0 + t < w.live) *p = C::ADD ? *p + acc[i][t] : acc[i][t];
           }
         }
       } else {
-        const bool summed = kt_n != 0;     // an empty reduction leaves no accumulator: zeros
-        const uint32_t b = j & 1u;
-        if (summed) {
-          if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          ++j;
-        }
-        const uint32_t t_addr = tmem_base + ((q * 32u) << 16) + b * C::ACC_COLS;
-        const bool vec = ((reinterpret_cast<uintptr_t>(args.out) & 3u) == 0) && (args.ldo & 1u) == 0 &&
-                         (args.stride_o & 1u) == 0;
+        // 16-bit outputs, one 32-column chunk at a time.  The code of a chunk is
+        // kept short and rolled: run once or twice a kernel, it costs what its
+        // instructions cost to fetch.
         const uint32_t pcol = lbase + (lane & ~1u);   // this lane's column pair
+        const bool summed = kt_n != 0;     // an empty reduction leaves no accumulator: zeros
+        // What the epilogue adds to a chunk is loaded a chunk ahead, the first
+        // chunk's before the accumulator is waited for.
+        //   Sym: row `col` of the symmetric R, whose 32 values from column
+        //     w.c0 + c0 on are the chunk's; the pitch is a multiple of 8, so a
+        //     16-byte piece that starts inside it ends inside it
+        //   Apply: X's halves at this lane's column pair, row 2 t + odd
+        const auto pitch_left = [&](uint32_t c0) {
+          const uint32_t p = static_cast<uint32_t>(args.ldo), c = w.c0 + c0;
+          return p > c ? p - c : 0u;
+        };
+        const auto sym_at = [&](uint32_t c0) {
+          return w.z * args.stride_o + static_cast<uint64_t>(col) * args.ldo + w.c0 + c0;
+        };
+        uint32_t add0[16], add1[16];         // Sym: R in add0; Apply: hi, lo
+        float rowf = 0.0f;                   // Apply, Y X: this lane's row's alpha + diag
+        const float* const dg = args.diag + static_cast<uint64_t>(w.z) * args.diag_n;
+        const auto fetch = [&](uint32_t ch) {
+          const uint32_t c0 = ch * 32;
+          if constexpr (OP == Op::Sym) {
+            const uint32_t left = pitch_left(c0);
+            const bool live = args.R != nullptr && ch < nch && col < args.L;
+            const uint4* const r = reinterpret_cast<const uint4*>(args.R + sym_at(c0));
+#pragma unroll
+            for (uint32_t p = 0; p < 4; ++p) {
+              const uint4 x = live && 8 * p < left ? r[p] : make_uint4(0, 0, 0, 0);
+              add0[4 * p] = x.x;
+              add0[4 * p + 1] = x.y;
+              add0[4 * p + 2] = x.z;
+              add0[4 * p + 3] = x.w;
+            }
+          } else if constexpr (C::APPLY) {
+            const uint64_t at =
+                w.z * args.stride_x + static_cast<uint64_t>(w.c0 + c0 + odd) * args.ldx + pcol;
+            const uint32_t* h = reinterpret_cast<const uint32_t*>(args.x_hi + at);
+            const uint32_t* l = reinterpret_cast<const uint32_t*>(args.x_lo + at);
+            const uint32_t left = pcol < args.L && c0 + odd < w.live ? w.live - c0 - odd : 0u;
+            if (P_MN) rowf = c0 + lane < w.live ? args.alpha + dg[w.c0 + c0 + lane] : 0.0f;
+#pragma unroll
+            for (uint32_t t = 0; t < 16; ++t, h += args.ldx, l += args.ldx) {
+              add0[t] = 2 * t < left ? *h : 0u;
+              add1[t] = 2 * t < left ? *l : 0u;
+            }
+          }
+        };
+        float colf0 = 0.0f, colf1 = 0.0f;    // Apply, X Y: this lane's columns' alpha + diag
+        if constexpr (C::APPLY && !P_MN) {
+          if (pcol < args.L) colf0 = args.alpha + dg[pcol];
+          if (pcol + 1 < args.L) colf1 = args.alpha + dg[pcol + 1];
+        }
+        fetch(eg);
+        if (summed && !acc_wait()) break;
+        const uint32_t b = j & 1u;
+        bool held = summed;
 #pragma unroll 1
         for (uint32_t ch = eg; ch < nch; ch += 2) {
+          const uint32_t c0 = ch * 32;
           uint32_t v[32];
           if (summed) {
-            tmem_ld_32x32b_x32_sync(t_addr + ch * 32, v);
+            tmem_ld_32x32b_x32_sync(t_addr(ch), v);
           } else {
 #pragma unroll
             for (uint32_t t = 0; t < 32; ++t) v[t] = 0u;
           }
-          const uint32_t c0 = ch * 32;
-          if constexpr (OP == Op::Rows || OP == Op::Sum) {
-            uint16_t* const o = static_cast<uint16_t*>(args.out) + out0;
+          if (held && ch + 2 >= nch) {   // all of it is in registers: hand it back before the last stores
+            release(b);
+            held = false;
+          }
+          if constexpr (OP == Op::Sym) {
 #pragma unroll
             for (uint32_t t = 0; t < 16; ++t) {
-              float x0, x1;
-              pair_columns(v[2 * t], v[2 * t + 1], odd, x0, x1);
-              const uint32_t c = c0 + 2 * t + odd;
-              if (c < w.live) {
-                uint16_t* const row = o + static_cast<uint64_t>(c) * args.ldo;
-                if (OP == Op::Sum && args.accumulate) {
-                  if (pcol < args.L) x0 += bf16_bits_to_f32(row[pcol]);
-                  if (pcol + 1 < args.L) x1 += bf16_bits_to_f32(row[pcol + 1]);
-                }
-                store_pair16(row, pcol, args.L, vec, pack_bf16x2(x0, x1));
-              }
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&add0[t]));
+              v[2 * t] = __float_as_uint(fmaf(args.beta, f.x, args.alpha * __uint_as_float(v[2 * t])));
+              v[2 * t + 1] = __float_as_uint(fmaf(args.beta, f.y, args.alpha * __uint_as_float(v[2 * t + 1])));
             }
-          } else if constexpr (OP == Op::Sym) {
-            // row `col` of the matrix holds the same 32 values (symmetry):
-            // R is read and the mirrored tile written there, 64 bytes a lane;
-            // the pitch is a multiple of 8, so a 16-byte piece that starts
-            // inside it ends inside it
-            const bool row_ok = col < args.L;
-            const uint64_t at = w.z * args.stride_o + static_cast<uint64_t>(col) * args.ldo + w.c0 + c0;
-            const uint32_t pitch_left =
-                static_cast<uint32_t>(args.ldo) > w.c0 + c0 ? static_cast<uint32_t>(args.ldo) - (w.c0 + c0) : 0u;
-            float x[32];
+            fetch(ch + 2);
+            if (args.R != nullptr && !w.mirror && col - w.c0 - c0 < 32u && col < args.L) {
+              // (an unrolled search: registers have no addresses)
 #pragma unroll
-            for (uint32_t t = 0; t < 32; ++t) x[t] = args.alpha * __uint_as_float(v[t]);
-            if (args.R != nullptr && row_ok) {
+              for (uint32_t t = 0; t < 32; ++t)
+                if (w.c0 + c0 + t == col) {
+                  args.diag[static_cast<uint64_t>(w.z) * args.diag_n + col] = __uint_as_float(v[t]);
+                  v[t] = 0u;
+                }
+            }
+            if (w.mirror && col < args.L) {
+              // the values also belong to row `col`: 64 bytes a lane
+              const uint32_t left = pitch_left(c0);
+              uint4* const m = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + sym_at(c0));
 #pragma unroll
               for (uint32_t p = 0; p < 4; ++p) {
-                if (8 * p < pitch_left) {
-                  const uint4 r = *reinterpret_cast<const uint4*>(args.R + at + 8 * p);
-                  const __half2* h = reinterpret_cast<const __half2*>(&r);
+                uint32_t h[4];
 #pragma unroll
-                  for (uint32_t t = 0; t < 4; ++t) {
-                    const float2 f = __half22float2(h[t]);
-                    x[8 * p + 2 * t] = fmaf(args.beta, f.x, x[8 * p + 2 * t]);
-                    x[8 * p + 2 * t + 1] = fmaf(args.beta, f.y, x[8 * p + 2 * t + 1]);
-                  }
-                }
-              }
-              if (!w.mirror) {
-#pragma unroll
-                for (uint32_t t = 0; t < 32; ++t)
-                  if (w.c0 + c0 + t == col) {
-                    args.diag[static_cast<uint64_t>(w.z) * args.diag_n + col] = x[t];
-                    x[t] = 0.0f;
-                  }
+                for (uint32_t t = 0; t < 4; ++t)
+                  h[t] = pack_f16x2(__uint_as_float(v[8 * p + 2 * t]), __uint_as_float(v[8 * p + 2 * t + 1]));
+                if (8 * p < left) m[p] = make_uint4(h[0], h[1], h[2], h[3]);
               }
             }
-            if (w.mirror && row_ok) {
+          }
+          // this lane's column pair of row 2 t + odd: rounded in st0 (Apply: and the
+          // lo halves in st1), or the two fp32 values
+          uint32_t st0[16], st1[16];
 #pragma unroll
-              for (uint32_t p = 0; p < 4; ++p)
-                if (8 * p < pitch_left)
-                  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + at + 8 * p) =
-                      make_uint4(pack_f16x2(x[8 * p], x[8 * p + 1]), pack_f16x2(x[8 * p + 2], x[8 * p + 3]),
-                                 pack_f16x2(x[8 * p + 4], x[8 * p + 5]), pack_f16x2(x[8 * p + 6], x[8 * p + 7]));
+          for (uint32_t t = 0; t < 16; ++t) {
+            float x0, x1;
+            pair_columns(__uint_as_float(v[2 * t]), __uint_as_float(v[2 * t + 1]), odd, x0, x1);
+            if constexpr (C::APPLY) {
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&add0[t]));
+              const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&add1[t]));
+              const float f = P_MN ? __shfl_sync(0xffffffffu, rowf, 2 * t + odd) : 0.0f;
+              x0 = fmaf(P_MN ? f : colf0, h.x + l.x, x0);
+              x1 = fmaf(P_MN ? f : colf1, h.y + l.y, x1);
             }
-            uint16_t* const o = static_cast<uint16_t*>(args.out) + out0;
+            if constexpr (OP == Op::Apply) {
+              const uint32_t p = pack_f16x2(x0, x1);
+              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&p));
+              st0[t] = p;
+              st1[t] = pack_f16x2(x0 - g.x, x1 - g.y);
+            } else if constexpr (OP == Op::ApplyOut) {
+              st0[t] = __float_as_uint(x0 * args.out_scale);
+              st1[t] = __float_as_uint(x1 * args.out_scale);
+            } else {
+              st0[t] = OP == Op::Sym ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+              if (C::ADD) {   // unrounded
+                st0[t] = __float_as_uint(x0);
+                st1[t] = __float_as_uint(x1);
+              }
+            }
+          }
+          if constexpr (C::APPLY) fetch(ch + 2);
+          const uint64_t at = out0 + static_cast<uint64_t>(c0 + odd) * args.ldo;
+          const uint32_t rows_left = c0 + odd < w.live ? w.live - c0 - odd : 0u;   // row 2 t is live: 2 t < rows_left
+          if constexpr (OP == Op::Sym || OP == Op::Apply) {
+            // the workspace: even pitches, and the column past an odd last one is padding
+            uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.out) + at + pcol);
+            uint32_t* p1 = reinterpret_cast<uint32_t*>(args.out_lo + at + pcol);
+            const uint32_t left = pcol < args.L ? rows_left : 0u;
 #pragma unroll
-            for (uint32_t t = 0; t < 16; ++t) {
-              float x0, x1;
-              pair_columns(__float_as_uint(x[2 * t]), __float_as_uint(x[2 * t + 1]), odd, x0, x1);
-              const uint32_t c = c0 + 2 * t + odd;
-              if (c < w.live)
-                store_pair16(o + static_cast<uint64_t>(c) * args.ldo, pcol, args.L, true, pack_f16x2(x0, x1));
-            }
+            for (uint32_t t = 0; t < 16; ++t, p += args.ldo, p1 += args.ldo)
+              if (2 * t < left) {
+                *p = st0[t];
+                if (OP == Op::Apply) *p1 = st1[t];
+              }
+          } else if (OP == Op::ApplyOut && args.out_f32) {
+            float* p = static_cast<float*>(args.out) + at + pcol;
+#pragma unroll
+            for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo)
+              if (2 * t < rows_left) {
+                if (pcol < args.L) p[0] = __uint_as_float(st0[t]);
+                if (pcol + 1 < args.L) p[1] = __uint_as_float(st1[t]);
+              }
           } else {
-            // v = (alpha + diag) (hi + lo) + acc, split again into hi + lo, or
-            // scaled out; diag goes by the row (Y X) or the column (X Y)
-            const float* const dg = args.diag + static_cast<uint64_t>(w.z) * args.diag_n;
-            const float f0 = P_MN ? 0.0f : args.alpha + (pcol < args.L ? dg[pcol] : 0.0f);
-            const float f1 = P_MN ? 0.0f : args.alpha + (pcol + 1 < args.L ? dg[pcol + 1] : 0.0f);
-            const uint64_t x_at = w.z * args.stride_x + static_cast<uint64_t>(w.c0 + c0) * args.ldx + pcol;
+            const bool vec = ((reinterpret_cast<uintptr_t>(args.out) & 3u) == 0) && (args.ldo & 1u) == 0 &&
+                             (args.stride_o & 1u) == 0;
+            uint16_t* p = static_cast<uint16_t*>(args.out) + at + pcol;
+            if (C::ADD) {
+              // += : a group without rows adds nothing and its output is not read
 #pragma unroll
-            for (uint32_t t0 = 0; t0 < 16; t0 += 8) {
-              uint32_t hi[8], lo[8];
-              float dr[8];
-#pragma unroll
-              for (uint32_t t = 0; t < 8; ++t) {
-                const uint32_t r = 2 * (t0 + t) + odd;
-                const bool live = c0 + r < w.live && pcol < args.L;
-                const uint64_t at = x_at + static_cast<uint64_t>(r) * args.ldx;
-                hi[t] = live ? *reinterpret_cast<const uint32_t*>(args.x_hi + at) : 0u;
-                lo[t] = live ? *reinterpret_cast<const uint32_t*>(args.x_lo + at) : 0u;
-                dr[t] = P_MN && c0 + r < w.live ? dg[w.c0 + c0 + r] : 0.0f;
+              for (uint32_t t = 0; t < 16; ++t) {
+                uint16_t* const o = p + static_cast<uint64_t>(2 * t) * args.ldo;
+                const bool live = summed && 2 * t < rows_left;
+                float x0 = __uint_as_float(st0[t]), x1 = __uint_as_float(st1[t]);
+                if (live && pcol < args.L) x0 += bf16_bits_to_f32(o[0]);
+                if (live && pcol + 1 < args.L) x1 += bf16_bits_to_f32(o[1]);
+                st0[t] = pack_bf16x2(x0, x1);
               }
+            }
+            if (OP == Op::ApplyOut) {
 #pragma unroll
-              for (uint32_t t = 0; t < 8; ++t) {
-                const uint32_t r = 2 * (t0 + t) + odd;
-                float x0, x1;
-                pair_columns(v[2 * (t0 + t)], v[2 * (t0 + t) + 1], odd, x0, x1);
-                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[t]));
-                const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&lo[t]));
-                x0 = fmaf(P_MN ? args.alpha + dr[t] : f0, h.x + l.x, x0);
-                x1 = fmaf(P_MN ? args.alpha + dr[t] : f1, h.y + l.y, x1);
-                if (c0 + r >= w.live) continue;
-                const uint64_t row = out0 + static_cast<uint64_t>(c0 + r) * args.ldo;
-                if (args.out_lo != nullptr) {
-                  const uint32_t p = pack_f16x2(x0, x1);
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
-                  store_pair16(static_cast<uint16_t*>(args.out) + row, pcol, args.L, true, p);
-                  store_pair16(reinterpret_cast<uint16_t*>(args.out_lo) + row, pcol, args.L, true,
-                               pack_f16x2(x0 - f.x, x1 - f.y));
-                } else if (args.out_f32) {
-                  float* const o = static_cast<float*>(args.out) + row;
-                  if (pcol < args.L) o[pcol] = x0 * args.out_scale;
-                  if (pcol + 1 < args.L) o[pcol + 1] = x1 * args.out_scale;
-                } else {
-                  store_pair16(static_cast<uint16_t*>(args.out) + row, pcol, args.L, vec,
-                               pack_bf16x2(x0 * args.out_scale, x1 * args.out_scale));
-                }
+              for (uint32_t t = 0; t < 16; ++t)
+                st0[t] = pack_bf16x2(__uint_as_float(st0[t]), __uint_as_float(st1[t]));
+            }
+            const uint32_t rows = C::ADD && !summed ? 0u : rows_left;
+            if (vec && lbase + 32 <= args.L) {
+#pragma unroll
+              for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo)
+                if (2 * t < rows) *reinterpret_cast<uint32_t*>(p) = st0[t];
+            } else {
+#pragma unroll
+              for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo) {
+                if (2 * t < rows && pcol < args.L) p[0] = static_cast<uint16_t>(st0[t] & 0xFFFFu);
+                if (2 * t < rows && pcol + 1 < args.L) p[1] = static_cast<uint16_t>(st0[t] >> 16);
               }
             }
           }
         }
-        if (summed) release(b);
+        if (held) release(b);   // (a warp without a chunk)
+        if (summed) ++j;
       }
     }
   }

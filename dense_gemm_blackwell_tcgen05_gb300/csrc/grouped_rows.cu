@@ -6,11 +6,9 @@ namespace gb300 {
 namespace {
 
 // X [M, K'] times each group's matrix; L output columns, K' reduced.
-template <bool P_MN, bool OUT32>
+template <int CG, uint32_t NT, bool P_MN, bool OUT32>
 int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
               const LaunchCtx& ctx, cudaStream_t stream) {
-  constexpr int CG = 1;
-  constexpr uint32_t NT = 128;
   using C = GroupedCfg<CG, Op::Rows, P_MN, false, NT, OUT32>;
   CUtensorMap tmP, tmQ;
   if (!operand_map(&tmP, p.B, p.K, p.N, p.groups, p.ldb, p.stride_b, p_box_rows<C, P_MN>()) ||
@@ -34,16 +32,46 @@ int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
   return launch_grouped<CG, Op::Rows, P_MN, false, NT, OUT32>(tmP, tmQ, a, tiles, ctx, stream);
 }
 
+// Which tiles.  With few rows a group the call reads its matrices and little
+// else: one CTA, 128 output columns, and a tile as narrow as the rows leave
+// more of shared memory to the matrices' loads.  Measured at 32 groups of
+// 4096 x 2048, us, 64 / 128 rows a tile on one CTA / 256 on a pair: 4 rows a
+// group 80 / 82 / 89, 16: 84 / 86 / 91, 32: 90 / 88 / 93, 64: 105 / 92 / 95.
+// With more rows the pair's tiles of 256 x 256 load half as much for each
+// product, but fill the device with a quarter as many tiles.  Time of either
+// from its rounds of tiles, 0.30 us for 64 k on a pair's tile and 0.22 on one
+// CTA's of 128 x 128, and 2 us for the cluster launch; e.g. (measured, one CTA
+// / pair) 8 groups of 1024 x 1024, 512 rows each: 13.4 / 17.0, 1024 rows: 20.3
+// / 19.2; 32 groups of 4096 x 2048, 256 rows each: 145 / 129.
+template <bool P_MN, bool OUT32>
+int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
+              const LaunchCtx& ctx, cudaStream_t stream) {
+  const uint64_t touched = p.M < p.groups ? p.M : p.groups;   // groups that can have rows
+  if (p.M <= 24 * touched) return rows_impl<1, 64, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
+  // a group's last tile is half full on average
+  const auto rounds = [&](uint64_t nt, uint64_t lt, uint64_t room) {
+    const uint64_t tiles = p.M / nt + touched / 2;
+    const double r = static_cast<double>((tiles > touched ? tiles : touched) * ceil_div_u64(L, lt)) / static_cast<double>(room);
+    return r > 1.0 ? r : 1.0;
+  };
+  const double kt = static_cast<double>(ceil_div_u64(K, 64));
+  const uint64_t sms = static_cast<uint64_t>(ctx.num_sms);
+  const double one = rounds(128, 128, sms) * kt * 0.22;
+  const double pair = rounds(256, 256, sms / 2) * kt * 0.30 + 2.0;
+  return pair < one ? rows_impl<2, 256, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream)
+                    : rows_impl<1, 128, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
+}
+
 }  // namespace
 
 int launch_grouped_forward(const GroupedProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
-  return p.out_f32 ? rows_impl<false, true>(p, p.A, p.lda, p.N, p.K, ctx, stream)
-                   : rows_impl<false, false>(p, p.A, p.lda, p.N, p.K, ctx, stream);
+  return p.out_f32 ? rows_pick<false, true>(p, p.A, p.lda, p.N, p.K, ctx, stream)
+                   : rows_pick<false, false>(p, p.A, p.lda, p.N, p.K, ctx, stream);
 }
 
 int launch_grouped_dgrad(const GroupedProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
-  return p.out_f32 ? rows_impl<true, true>(p, p.dD, p.ldd, p.K, p.N, ctx, stream)
-                   : rows_impl<true, false>(p, p.dD, p.ldd, p.K, p.N, ctx, stream);
+  return p.out_f32 ? rows_pick<true, true>(p, p.dD, p.ldd, p.K, p.N, ctx, stream)
+                   : rows_pick<true, false>(p, p.dD, p.ldd, p.K, p.N, ctx, stream);
 }
 
 }  // namespace gb300

@@ -24,11 +24,11 @@ inline bool operand_map(CUtensorMap* map, const void* base, uint64_t inner, uint
 }
 
 // Rows of the operand boxes of a kernel: 64 k rows of an MN-major operand;
-// 128 rows of a K-major P, the staged rows of a K-major Q.
+// 128 rows of a K-major P, Q_BOX of a K-major Q.
 template <class C, bool MN>
 constexpr uint32_t p_box_rows() { return MN ? 64u : 128u; }
 template <class C, bool MN>
-constexpr uint32_t q_box_rows() { return MN ? 64u : C::Q_ROWS; }
+constexpr uint32_t q_box_rows() { return MN ? 64u : C::Q_BOX; }
 
 template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32>
 int launch_grouped(const CUtensorMap& tmP, const CUtensorMap& tmQ, const GroupedArgs& a, uint64_t tiles,

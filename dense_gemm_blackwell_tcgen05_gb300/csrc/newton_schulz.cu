@@ -219,7 +219,7 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
   __half* const gram = reinterpret_cast<__half*>(ws + w.gram);
   __half* const poly = reinterpret_cast<__half*>(ws + w.poly);
   const uint64_t lt = ceil_div_u64(m, SymK::LT);
-  const uint64_t sym_tiles = lt * (lt + 1) / 2 * p.batch;
+  const uint64_t sym_tiles = SymK::LT / NT * (lt * (lt + 1) / 2) * p.batch;
   const uint64_t all_tiles = ceil_div_u64(p.cols, SymK::LT) * ceil_div_u64(p.rows, NT) * p.batch;
   if (sym_tiles > 0x7FFFFFFFull || all_tiles > 0x7FFFFFFFull) return GEMM_ERR_INVALID_ARG;
 
@@ -290,11 +290,33 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
       t.ldo = w.ldx;
       t.stride_o = w.stride_x;
     }
-    rc = tall ? launch_grouped<CG, Op::Apply, false, false, NT, false>(polyP, xKq, t, all_tiles, ctx, stream)
-              : launch_grouped<CG, Op::Apply, true, false, NT, false>(xMN, polyQ, t, all_tiles, ctx, stream);
+    if (last)
+      rc = tall ? launch_grouped<CG, Op::ApplyOut, false, false, NT, false>(polyP, xKq, t, all_tiles, ctx, stream)
+                : launch_grouped<CG, Op::ApplyOut, true, false, NT, false>(xMN, polyQ, t, all_tiles, ctx, stream);
+    else
+      rc = tall ? launch_grouped<CG, Op::Apply, false, false, NT, false>(polyP, xKq, t, all_tiles, ctx, stream)
+                : launch_grouped<CG, Op::Apply, true, false, NT, false>(xMN, polyQ, t, all_tiles, ctx, stream);
     if (rc != GEMM_OK) return rc;
   }
   return GEMM_OK;
+}
+
+// Which tiles.  A step is three dependent products; with few tiles in a
+// product, narrower ones spread it over more SMs, with many the pair's load
+// least.  Measured, us, 128 x 64 and 128 x 128 on one CTA / 256 x 256 on a
+// pair: one matrix of 512 x 512: 79 / 100 / 149, 1024 x 1024: 111 / 133 / 187,
+// 1536 x 1536: 229 / 178 / 239, 4096 x 4096: 2169 / 1390 / 978; 16 of 1024 x
+// 2048: 1167 / 799 / 755.
+int pick(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
+  const uint32_t m = p.rows < p.cols ? p.rows : p.cols;
+  const auto blocks = [&](uint64_t size) {   // of that size on and below the diagonals
+    const uint64_t n = ceil_div_u64(m, size);
+    return n * (n + 1) / 2 * p.batch;
+  };
+  const uint64_t sms = static_cast<uint64_t>(ctx.num_sms);
+  if (blocks(256) >= sms / 2) return iterate<2, 256>(p, w, scale, ctx, stream);
+  if (blocks(128) > sms / 3) return iterate<1, 128>(p, w, scale, ctx, stream);
+  return iterate<1, 64>(p, w, scale, ctx, stream);
 }
 
 }  // namespace
@@ -311,7 +333,7 @@ int launch_newton_schulz(const NewtonSchulzProblem& p, const LaunchCtx& ctx, cud
   const uint32_t n = p.rows > p.cols ? p.rows : p.cols;
   const float scale = std::ldexp(1.0f, static_cast<int>(std::floor(0.5 * std::log2(static_cast<double>(n)))));
   const int rc = p.g_f32 ? normalise<float>(p, w, scale, ctx, stream) : normalise<uint16_t>(p, w, scale, ctx, stream);
-  return rc != GEMM_OK ? rc : iterate<1, 128>(p, w, scale, ctx, stream);
+  return rc != GEMM_OK ? rc : pick(p, w, scale, ctx, stream);
 }
 
 }  // namespace gb300

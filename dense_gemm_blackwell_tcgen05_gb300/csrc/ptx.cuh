@@ -54,6 +54,25 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
+// The same without release semantics, for an arrival that hands back what this
+// thread has only read: a release at cluster scope first waits for the
+// thread's earlier global stores, which such a hand-back does not publish.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
+// Stores `value` at `cluster_addr` and then completes 4 transaction bytes on
+// `cluster_bar`, both in one CTA of the cluster (addresses from mapa),
+// asynchronously: the completion releases at cluster scope without making
+// this thread wait for its SM's outstanding stores, as an arrive.release
+// from another CTA does.
+__device__ __forceinline__ void st_async_u32(uint32_t cluster_addr, uint32_t value, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr),
+               "r"(value), "r"(cluster_bar)
+               : "memory");
+}
+
 // Sets the expected transaction byte count of the current phase and performs
 // the issuing thread's arrival (the ready-barrier protocol of a TMA stage).
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
