@@ -615,18 +615,20 @@ def _check_3d(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _refuse_grouped(x, x_name, B, offsets, groups):
-    """Raises for what is wrong with a grouped product's operands."""
+def _refuse_grouped(rc, entry, x, x_name, B, B_name, offsets, groups, out):
+    """Raises for what is wrong with a grouped product's tensors, else `rc`."""
     import torch
-    _check_2d(x, x_name)
-    _check_3d(B, "B") if B.dim() == 3 else _check_2d(B, "A")
+    for t, name in ((x, x_name), (B, B_name), (out, "out")):
+        (_check_3d if t.dim() == 3 else _check_2d)(t, name)
     if x.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
         raise TypeError("the operands must be bfloat16")
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous():
         raise TypeError("offsets must be a contiguous 1-D int32 tensor")
     if not offsets.is_cuda:
         raise ValueError("offsets must be a CUDA tensor")
-    raise ValueError(f"offsets must hold one value more than the {groups} groups")
+    if offsets.numel() != groups + 1:
+        raise ValueError(f"offsets must hold one value more than the {groups} groups")
+    raise GemmError(rc, entry)
 
 
 def _output(out, shape, dtype, device, name):
@@ -642,27 +644,24 @@ def _output(out, shape, dtype, device, name):
 
 def _grouped_rows(entry, x, x_name, B, offsets, dgrad, out, out_dtype, stream):
     import torch
-    bf16 = torch.bfloat16
-    if not (x.dtype is bf16 and B.dtype is bf16 and offsets.dtype is torch.int32 and x.dim() == 2
-            and B.dim() == 3 and offsets.dim() == 1 and x.is_cuda and B.is_cuda
-            and offsets.is_cuda and x.stride(1) == 1 and B.stride(2) == 1
-            and offsets.shape[0] == B.shape[0] + 1 and offsets.is_contiguous()):
-        _check_3d(B, "B")
-        _refuse_grouped(x, x_name, B, offsets, B.shape[0])
-    groups, N, K = B.shape
     M, reduced = x.shape
+    groups, N, K = B.shape
     if reduced != (N if dgrad else K):
         raise ValueError(f"{x_name} and B disagree on {'N' if dgrad else 'K'}")
     out = _output(out, (M, K if dgrad else N), out_dtype, x.device, "out")
-    if out.dim() != 2 or out.stride(1) != 1 or not out.is_cuda:
-        _check_2d(out, "out")
-    sb, ldb, _ = B.stride()
-    rc = getattr(_lib or load(), entry)(
-        x.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups, M, N, K,
-        x.stride(0), ldb, sb, out.stride(0), _out_code(out.dtype),
-        _raw_stream(stream, x.get_device()))
+    ldx, x1 = x.stride()
+    sb, ldb, b1 = B.stride()
+    ldo, o1 = out.stride()
+    bf16 = torch.bfloat16
+    rc = GEMM_ERR_INVALID_ARG
+    # (what is not on the GPU the call itself refuses)
+    if (x.dtype is bf16 and B.dtype is bf16 and offsets.dtype is torch.int32 and x1 == b1 == o1 == 1
+            and offsets.shape == (groups + 1,) and offsets.is_contiguous()):
+        rc = getattr(_lib or load(), entry)(
+            x.data_ptr(), B.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups, M, N, K,
+            ldx, ldb, sb, ldo, _out_code(out.dtype), _raw_stream(stream, x.get_device()))
     if rc != GEMM_OK:
-        raise GemmError(rc, entry)
+        _refuse_grouped(rc, entry, x, x_name, B, "B", offsets, groups, out)
     return out
 
 
@@ -686,29 +685,27 @@ def matmul_grouped_wgrad(dD, A, offsets, out=None, out_dtype=None, accumulate=Fa
     e]; returns dB [groups,N,K] of out_dtype (bfloat16 or float32).  With
     accumulate, adds to `out` instead."""
     import torch
-    bf16 = torch.bfloat16
-    if not (dD.dtype is bf16 and A.dtype is bf16 and offsets.dtype is torch.int32 and dD.dim() == 2
-            and A.dim() == 2 and offsets.dim() == 1 and dD.is_cuda and A.is_cuda
-            and offsets.is_cuda and dD.stride(1) == 1 and A.stride(1) == 1
-            and offsets.shape[0] > 0 and offsets.is_contiguous()):
-        _refuse_grouped(dD, "dD", A, offsets, 0)
     M, N = dD.shape
-    K = A.shape[1]
-    if A.shape[0] != M:
+    MA, K = A.shape
+    if MA != M:
         raise ValueError("dD and A disagree on M")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    groups = offsets.shape[0] - 1
+    groups = max(0, offsets.numel() - 1)
     out = _output(out, (groups, N, K), out_dtype, A.device, "out")
-    if out.dim() != 3 or out.stride(2) != 1 or not out.is_cuda:
-        _check_3d(out, "out")
-    sb, ldb, _ = out.stride()
-    rc = (_lib or load()).gemm_bf16_grouped_wgrad(
-        dD.data_ptr(), A.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups, M, N, K,
-        dD.stride(0), A.stride(0), ldb, sb, _out_code(out.dtype), 1 if accumulate else 0,
-        _raw_stream(stream, A.get_device()))
+    ldd, d1 = dD.stride()
+    lda, a1 = A.stride()
+    sb, ldb, o1 = out.stride()
+    bf16 = torch.bfloat16
+    rc = GEMM_ERR_INVALID_ARG
+    if (dD.dtype is bf16 and A.dtype is bf16 and offsets.dtype is torch.int32
+            and d1 == a1 == o1 == 1 and offsets.shape == (groups + 1,) and offsets.is_contiguous()):
+        rc = (_lib or load()).gemm_bf16_grouped_wgrad(
+            dD.data_ptr(), A.data_ptr(), out.data_ptr(), offsets.data_ptr(), groups, M, N, K,
+            ldd, lda, ldb, sb, _out_code(out.dtype), 1 if accumulate else 0,
+            _raw_stream(stream, A.get_device()))
     if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_grouped_wgrad")
+        _refuse_grouped(rc, "gemm_bf16_grouped_wgrad", dD, "dD", A, "A", offsets, groups, out)
     return out
 
 
