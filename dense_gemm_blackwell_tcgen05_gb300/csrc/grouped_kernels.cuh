@@ -38,6 +38,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "gemm_kernels.cuh"
 
@@ -246,6 +247,24 @@ __device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* 
     w.l0 = lb * C::LT;
     w.live = min(NT, a.C - w.c0);
     return true;
+  }
+}
+
+// Zeros in rows 0 .. rows - 1, columns 0 .. cols - 1 (cols <= 128) of a tile at
+// `out`, by 256 threads, 16 bytes a thread where `vec` says that every row starts
+// on such a boundary.
+template <class T>
+__device__ __forceinline__ void zero_tile(T* out, uint64_t ldo, uint32_t rows, uint32_t cols, bool vec,
+                                          uint32_t thread) {
+  constexpr uint32_t kPer = 16 / sizeof(T), kPieces = 128 / kPer;   // a row's elements a piece, pieces
+  const uint32_t c = thread % kPieces * kPer;
+  out += static_cast<uint64_t>(thread / kPieces) * ldo + c;
+  for (uint32_t r = thread / kPieces; r < rows; r += 256 / kPieces, out += 256 / kPieces * ldo) {
+    if (vec && c + kPer <= cols) {
+      *reinterpret_cast<uint4*>(out) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (uint32_t i = 0; i < kPer && c + i < cols; ++i) out[i] = T(0);
+    }
   }
 }
 
@@ -592,6 +611,19 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           else mbar_arrive_cluster_relaxed(mapa_shared(acce_bar(b), 0));
         }
       };
+      if (C::SUM && kt_n == 0) {
+        // a group without rows: no accumulator, zeros, or (+=) nothing at all
+        if (!C::ADD) {
+          using T = std::conditional_t<OUT32, uint32_t, uint16_t>;
+          const uint32_t l = w.l0 + rank * 128;
+          const bool vec = ((reinterpret_cast<uintptr_t>(args.out) | (args.ldo * sizeof(T)) |
+                             (args.stride_o * sizeof(T))) & 15u) == 0;
+          if (l < args.L)
+            zero_tile(static_cast<T*>(args.out) + out0 + l, args.ldo, w.live, min(128u, args.L - l), vec,
+                      threadIdx.x - 64);
+        }
+        continue;
+      }
       const auto t_addr = [&](uint32_t ch) {
         return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + ch * 32;
       };
@@ -620,7 +652,6 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           release(j & 1u);
         }
         if (!ok) break;
-        if (C::ADD && kt_n == 0) continue;
         float* const o = static_cast<float*>(args.out) + out0 + col;
 #pragma unroll
         for (uint32_t i = 0; i < C::NCH; ++i) {
@@ -640,7 +671,6 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
         // kept short and rolled: run once or twice a kernel, it costs what its
         // instructions cost to fetch.
         const uint32_t pcol = lbase + (lane & ~1u);   // this lane's column pair
-        const bool summed = kt_n != 0;     // an empty reduction leaves no accumulator: zeros
         // What the epilogue adds to a chunk is loaded a chunk ahead, the first
         // chunk's before the accumulator is waited for.
         //   Sym: row `col` of the symmetric R, whose 32 values from column
@@ -691,19 +721,14 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           if (pcol + 1 < args.L) colf1 = args.alpha + dg[pcol + 1];
         }
         fetch(eg);
-        if (summed && !acc_wait()) break;
+        if (!acc_wait()) break;
         const uint32_t b = j & 1u;
-        bool held = summed;
+        bool held = true;
 #pragma unroll 1
         for (uint32_t ch = eg; ch < nch; ch += 2) {
           const uint32_t c0 = ch * 32;
           uint32_t v[32];
-          if (summed) {
-            tmem_ld_32x32b_x32_sync(t_addr(ch), v);
-          } else {
-#pragma unroll
-            for (uint32_t t = 0; t < 32; ++t) v[t] = 0u;
-          }
+          tmem_ld_32x32b_x32_sync(t_addr(ch), v);
           if (held && ch + 2 >= nch) {   // all of it is in registers: hand it back before the last stores
             release(b);
             held = false;
@@ -796,11 +821,10 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
                              (args.stride_o & 1u) == 0;
             uint16_t* p = static_cast<uint16_t*>(args.out) + at + pcol;
             if (C::ADD) {
-              // += : a group without rows adds nothing and its output is not read
 #pragma unroll
               for (uint32_t t = 0; t < 16; ++t) {
                 uint16_t* const o = p + static_cast<uint64_t>(2 * t) * args.ldo;
-                const bool live = summed && 2 * t < rows_left;
+                const bool live = 2 * t < rows_left;
                 float x0 = __uint_as_float(st0[t]), x1 = __uint_as_float(st1[t]);
                 if (live && pcol < args.L) x0 += bf16_bits_to_f32(o[0]);
                 if (live && pcol + 1 < args.L) x1 += bf16_bits_to_f32(o[1]);
@@ -812,22 +836,21 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
               for (uint32_t t = 0; t < 16; ++t)
                 st0[t] = pack_bf16x2(__uint_as_float(st0[t]), __uint_as_float(st1[t]));
             }
-            const uint32_t rows = C::ADD && !summed ? 0u : rows_left;
             if (vec && lbase + 32 <= args.L) {
 #pragma unroll
               for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo)
-                if (2 * t < rows) *reinterpret_cast<uint32_t*>(p) = st0[t];
+                if (2 * t < rows_left) *reinterpret_cast<uint32_t*>(p) = st0[t];
             } else {
 #pragma unroll
               for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo) {
-                if (2 * t < rows && pcol < args.L) p[0] = static_cast<uint16_t>(st0[t] & 0xFFFFu);
-                if (2 * t < rows && pcol + 1 < args.L) p[1] = static_cast<uint16_t>(st0[t] >> 16);
+                if (2 * t < rows_left && pcol < args.L) p[0] = static_cast<uint16_t>(st0[t] & 0xFFFFu);
+                if (2 * t < rows_left && pcol + 1 < args.L) p[1] = static_cast<uint16_t>(st0[t] >> 16);
               }
             }
           }
         }
         if (held) release(b);   // (a warp without a chunk)
-        if (summed) ++j;
+        ++j;
       }
     }
   }
