@@ -99,7 +99,9 @@ __device__ __forceinline__ uint32_t mma_n(uint32_t live) {
   return live == 0 ? g : (live + g - 1) / g * g;
 }
 
-template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32>
+// SPLIT: a cluster of that many CTAs shares each tile's reduction (one tile a
+// cluster: the launcher splits only where there are clusters for all tiles).
+template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32, uint32_t SPLIT = 1>
 struct GroupedCfg {
   static_assert(CG == 1 || CG == 2, "cta_group is 1 or 2");
   static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
@@ -126,15 +128,21 @@ struct GroupedCfg {
   static constexpr uint32_t SEG_TILES = OUT32 ? 8u : 0xFFFFFFFFu;
   static constexpr uint32_t NCH = (NT + 63) / 64;        // 32-column chunks per epilogue warp
   static constexpr bool GROUPED = OP == Op::Rows || SUM;
+  static_assert(SPLIT == 1 || (CG == 1 && OP == Op::Rows && NT == 64), "split reductions");
+  static constexpr uint32_t kCluster = CG * SPLIT;       // CTAs a cluster
+  // the other CTAs' sums, fp32, in the first one: for each of them a tile of
+  // 128 lanes by NT columns, 16 bytes a lane after another
+  static constexpr uint32_t PART_BYTES = 128 * NT * 4;
+  static constexpr uint32_t SPLIT_BYTES = (SPLIT - 1) * PART_BYTES;
   static constexpr uint32_t ITEM_BYTES = kAheadItems * sizeof(TileItem);
   static constexpr uint32_t TABLE_BYTES = ITEM_BYTES + (GROUPED ? 2 * 4 * (kMaxGroups + 8) : 0);
   static constexpr uint32_t BAR_BYTES = 512;
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;
-  static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - TABLE_BYTES) / STAGE_BYTES;
+  static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - TABLE_BYTES - SPLIT_BYTES) / STAGE_BYTES;
   static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
-  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + BAR_BYTES + TABLE_BYTES;
-  static_assert((3 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
+  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + SPLIT_BYTES + BAR_BYTES + TABLE_BYTES;
+  static_assert((3 * STAGES + 6) * 8 + 16 <= BAR_BYTES, "barrier area");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = 256;              // second accumulator's first column
 };
@@ -282,16 +290,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32>
-__global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kThreads, 1)
+template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32, uint32_t SPLIT = 1>
+__global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLIT>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                    const GroupedArgs args) {
-  using C = GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>;
+  using C = GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLIT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bar0 = base + C::STAGES * C::STAGE_BYTES;
+  const uint32_t part0 = base + C::STAGES * C::STAGE_BYTES;
+  const uint32_t bar0 = part0 + C::SPLIT_BYTES;
   const auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
   const auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (C::STAGES + s); };
   const auto tail_bar = [&](uint32_t s) { return bar0 + 8 * (2 * C::STAGES + s); };
@@ -299,7 +308,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
   const auto accf_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + b); };
   const auto acce_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + 2 + b); };
   const uint32_t drain_bar = bar0 + 8 * (kAccBar0 + 4);
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (kAccBar0 + 5));
+  const uint32_t part_bar = bar0 + 8 * (kAccBar0 + 5);   // SPLIT: the other CTAs' sums are here
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (kAccBar0 + 6));
   volatile uint32_t* const abort_flag = tmem_slot + 1;
   TileItem* const ahead = reinterpret_cast<TileItem*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
   uint32_t* const offs = reinterpret_cast<uint32_t*>(ahead + kAheadItems);
@@ -309,8 +319,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
   const uint32_t lane = lane_idx();
   const uint32_t rank = (CG == 2) ? cluster_cta_rank() : 0u;
   const bool leader = rank == 0;
-  const uint32_t cluster_id = blockIdx.x / CG;
-  const uint32_t G = gridDim.x / CG;
+  const uint32_t k_rank = SPLIT > 1 ? cluster_cta_rank() : 0u;   // which part of the reduction
+  const uint32_t cluster_id = blockIdx.x / C::kCluster;
+  const uint32_t G = gridDim.x / C::kCluster;
   const Watchdog wd{args.status, args.timeout_ns, abort_flag};
 
   // ---- set-up ------------------------------------------------------------------
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
     // arrivals: a full barrier gets the leader's expect_tx (its producer's, or
     // its tail warp's on a ragged tile); an accumulator is handed back by
     // every epilogue warp
-    for (uint32_t i = lane; i < kAccBar0 + 5; i += 32) {
+    for (uint32_t i = lane; i < kAccBar0 + 6; i += 32) {
       uint32_t count = 1;
       if (i == kAccBar0 + 2 || i == kAccBar0 + 3) count = C::kEpiWarps * CG;
       mbar_init(bar0 + 8 * i, count);
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
   }
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  if constexpr (C::kCluster > 1) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   const auto item = [&](uint32_t wi, TileItem& w) {
@@ -411,6 +422,10 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
     }
     return tile_item<C, CG, OP, NT>(args, offs, tab, cluster_id, G, wi, w);
   };
+
+  // this CTA's stages of a reduction of kt_n: all of them, or its part
+  const auto k_first = [&](uint32_t kt_n) { return SPLIT > 1 ? kt_n * k_rank / SPLIT : 0u; };
+  const auto k_last = [&](uint32_t kt_n) { return SPLIT > 1 ? kt_n * (k_rank + 1) / SPLIT : kt_n; };
 
   if (warp == 0) {
     // ==================== TMA producer: one thread ==============================
@@ -431,7 +446,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
         const uint32_t tx = C::P_BYTES + (Q_MN ? C::Q_BYTES : q_boxes * C::Q_BOX * 128);
         const int32_t px = static_cast<int32_t>(w.l0 + rank * 128);
         const int32_t qy = static_cast<int32_t>(w.c0 + rank * h);
-        for (uint32_t kt = 0; kt < kt_n; ++kt, ++it) {
+        if (SPLIT > 1 && k_rank == 0)
+          mbar_arrive_expect_tx(part_bar, (SPLIT - 1) * ((w.live + 31) / 32) * (128 * 32 * 4));
+        for (uint32_t kt = k_first(kt_n); kt < k_last(kt_n); ++kt, ++it) {
           const uint32_t s = it % C::STAGES;
           if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
           if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
@@ -482,8 +499,10 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           }
         }
       }
-      // Exit path after a give-up: let this CTA's issued loads land first.
+      // Exit path after a give-up: let this CTA's issued loads, and sums on their
+      // way to it, land first.
       if (*abort_flag) {
+        if (SPLIT > 1 && k_rank == 0) drain_wait(part_bar, 0, wd, kSiteProducerDrain);
         const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
         for (uint32_t i = first; i < it; ++i) {
           const uint32_t s = i % C::STAGES;
@@ -502,8 +521,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       for (uint32_t wi = 0; ok && item(wi, w); ++wi) {
         const uint32_t kt_n = (w.k_len + C::BK - 1) / C::BK;
         const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(w.live), args.fmt, P_MN, Q_MN);
-        for (uint32_t k_begin = 0; ok && k_begin < kt_n; ++j) {
-          const uint32_t k_end = kt_n - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : kt_n;
+        const uint32_t k_stop = k_last(kt_n);
+        for (uint32_t k_begin = k_first(kt_n); ok && k_begin < k_stop; ++j) {
+          const uint32_t k_end = k_stop - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : k_stop;
           const uint32_t b = j & 1u;
           // accumulator b must have been drained by every epilogue warp
           if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) {
@@ -627,6 +647,36 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
       const auto t_addr = [&](uint32_t ch) {
         return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + ch * 32;
       };
+      // SPLIT: the first CTA adds the others' sums of a chunk in their order; the
+      // others send theirs and are done (true: the chunk is not theirs to store)
+      const auto combine = [&](uint32_t ch, uint32_t (&v)[32]) -> bool {
+        const uint32_t at = (ch * 4 + q) * 4096 + lane * 16;
+        if (k_rank != 0) {
+          const uint32_t dst = mapa_shared(part0 + (k_rank - 1) * C::PART_BYTES + at, 0);
+          const uint32_t bar = mapa_shared(part_bar, 0);
+#pragma unroll
+          for (uint32_t i = 0; i < 8; ++i)
+            st_async_v4(dst + i * 512, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], bar);
+          return true;
+        }
+        if (!warp_wait(part_bar, 0, wd, kSiteSplit, lane)) {
+          ok = false;
+          return true;
+        }
+#pragma unroll 1
+        for (uint32_t r = 0; r + 1 < SPLIT; ++r) {
+          const uint8_t* const src = base_ptr + (part0 - base) + r * C::PART_BYTES + at;
+#pragma unroll
+          for (uint32_t i = 0; i < 8; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(src + i * 512);
+            v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + x.x);
+            v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + x.y);
+            v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + x.z);
+            v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + x.w);
+          }
+        }
+        return false;
+      };
       const auto acc_wait = [&]() {
         ok = warp_wait(accf_bar(j & 1u), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane);
         tc_fence_after_sync();
@@ -638,7 +688,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
         for (uint32_t i = 0; i < C::NCH; ++i)
 #pragma unroll
           for (uint32_t t = 0; t < 32; ++t) acc[i][t] = 0.0f;
-        for (uint32_t k = 0; k < kt_n; k += C::SEG_TILES, ++j) {
+        for (uint32_t k = k_first(kt_n); k < k_last(kt_n); k += C::SEG_TILES, ++j) {
           if (!acc_wait()) break;
 #pragma unroll
           for (uint32_t i = 0; i < C::NCH; ++i) {
@@ -656,6 +706,14 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
 #pragma unroll
         for (uint32_t i = 0; i < C::NCH; ++i) {
           const uint32_t c0 = (2 * i + eg) * 32;
+          if constexpr (SPLIT > 1) {
+            uint32_t v[32];
+#pragma unroll
+            for (uint32_t t = 0; t < 32; ++t) v[t] = __float_as_uint(acc[i][t]);
+            if (2 * i + eg >= nch || combine(2 * i + eg, v)) continue;
+#pragma unroll
+            for (uint32_t t = 0; t < 32; ++t) acc[i][t] = __uint_as_float(v[t]);
+          }
           float* p = o + static_cast<uint64_t>(c0) * args.ldo;
           if (c0 + 32 <= w.live && lbase + 32 <= args.L && !(C::ADD)) {
 #pragma unroll
@@ -732,6 +790,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
           if (held && ch + 2 >= nch) {   // all of it is in registers: hand it back before the last stores
             release(b);
             held = false;
+          }
+          if constexpr (SPLIT > 1) {
+            if (combine(ch, v)) continue;
           }
           if constexpr (OP == Op::Sym) {
 #pragma unroll
@@ -859,7 +920,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32>::kTh
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();
+  if constexpr (C::kCluster > 1) cluster_sync();
   if (warp == 1) {
     tc_fence_after_sync();
     tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);

@@ -5,11 +5,19 @@
 namespace gb300 {
 namespace {
 
+// The most tiles a launch can have: M / NT full ones and a ragged one for each
+// group that can have rows.
+uint64_t most_tiles(const GroupedProblem& p, uint64_t nt, uint64_t lt, uint32_t L) {
+  const uint64_t touched = p.M < p.groups ? p.M : p.groups;
+  const uint64_t blocks = p.M / nt + touched;
+  return (blocks < p.M ? blocks : p.M) * ceil_div_u64(L, lt);
+}
+
 // X [M, K'] times each group's matrix; L output columns, K' reduced.
-template <int CG, uint32_t NT, bool P_MN, bool OUT32>
+template <int CG, uint32_t NT, bool P_MN, bool OUT32, uint32_t SPLIT = 1>
 int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
               const LaunchCtx& ctx, cudaStream_t stream) {
-  using C = GroupedCfg<CG, Op::Rows, P_MN, false, NT, OUT32>;
+  using C = GroupedCfg<CG, Op::Rows, P_MN, false, NT, OUT32, SPLIT>;
   CUtensorMap tmP, tmQ;
   if (!operand_map(&tmP, p.B, p.K, p.N, p.groups, p.ldb, p.stride_b, p_box_rows<C, P_MN>()) ||
       !operand_map(&tmQ, X, K, p.M, 1, ldx, 0, q_box_rows<C, false>()))
@@ -26,10 +34,8 @@ int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
   a.status = ctx.status;
   a.timeout_ns = ctx.timeout_ns;
   a.stall_iter = p.stall_iter;
-  // at most M / NT full tiles and one ragged one for each group with rows
-  const uint64_t touched = p.M < p.groups ? p.M : p.groups;
-  const uint64_t tiles = (p.M / NT + touched) * ceil_div_u64(L, C::LT);
-  return launch_grouped<CG, Op::Rows, P_MN, false, NT, OUT32>(tmP, tmQ, a, tiles, ctx, stream);
+  const uint64_t tiles = most_tiles(p, NT, C::LT, L);
+  return launch_grouped<CG, Op::Rows, P_MN, false, NT, OUT32, SPLIT>(tmP, tmQ, a, tiles, ctx, stream);
 }
 
 // Which tiles.  With few rows a group the call reads its matrices and little
@@ -47,6 +53,23 @@ template <bool P_MN, bool OUT32>
 int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
               const LaunchCtx& ctx, cudaStream_t stream) {
   const uint64_t touched = p.M < p.groups ? p.M : p.groups;   // groups that can have rows
+  // Few tiles and a long reduction: a cluster of CTAs shares it.  A cluster
+  // launch and the exchange cost 4.5 us, four CTAs save 0.14 us for each 64 k,
+  // two 0.09.  Measured, us, one CTA / two / four, 8 groups, one row in all: 1024
+  // x 1024: 6.9 / 9.5 / 9.3, 338 x 2360: 11.3 / 12.2 / 10.6, 256 x 4096: 16.1 /
+  // 14.6 / 12.0, 2048 x 4096: 16.8 / 15.4 / 13.4.
+  if (K >= 36 * 64) {
+    const uint64_t narrow = most_tiles(p, 64, 128, L);
+    uint64_t room = 0;
+    if (narrow <= static_cast<uint64_t>(ctx.num_sms / 4)) {
+      if (const int rc = grouped_room<1, Op::Rows, P_MN, false, 64, OUT32, 4>(ctx, &room); rc != GEMM_OK) return rc;
+      if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 4>(p, X, ldx, L, K, ctx, stream);
+    }
+    if (narrow <= static_cast<uint64_t>(ctx.num_sms / 2) && K >= 48 * 64) {
+      if (const int rc = grouped_room<1, Op::Rows, P_MN, false, 64, OUT32, 2>(ctx, &room); rc != GEMM_OK) return rc;
+      if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 2>(p, X, ldx, L, K, ctx, stream);
+    }
+  }
   if (p.M <= 24 * touched) return rows_impl<1, 64, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
   // a group's last tile is half full on average
   const auto rounds = [&](uint64_t nt, uint64_t lt, uint64_t room) {

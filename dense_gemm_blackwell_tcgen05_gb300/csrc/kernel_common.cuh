@@ -24,6 +24,7 @@ enum WaitSite : uint32_t {
   kSiteStreamKFlag = 9,     // stream-K owner waiting for a partial accumulator
   kSiteEpiC = 10,           // epilogue waiting for a TMA-loaded tile of C
   kSiteTail = 11,           // tail warp waiting for a ragged reduction end
+  kSiteSplit = 12,          // epilogue waiting for the other CTAs' parts of a reduction
 };
 
 // Fused-epilogue mode word (0: the plain bf16 store of the accumulator).

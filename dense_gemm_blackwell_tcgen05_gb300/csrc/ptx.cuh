@@ -73,6 +73,15 @@ __device__ __forceinline__ void st_async_u32(uint32_t cluster_addr, uint32_t val
                : "memory");
 }
 
+// Four words at once, 16 transaction bytes.
+__device__ __forceinline__ void st_async_v4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                            uint32_t cluster_bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(cluster_bar)
+      : "memory");
+}
+
 // Sets the expected transaction byte count of the current phase and performs
 // the issuing thread's arrival (the ready-barrier protocol of a TMA stage).
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {

@@ -124,6 +124,45 @@ def test_exact(per, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("per, N, K", [([1, 0, 2], 136, 2400), ([1, 3], 300, 4000), ([0, 5, 40, 64, 65, 1], 520, 2304),
+                                       ([100, 30], 1000, 3200), ([64] * 8, 264, 3080), ([3, 1], 8, 2311)])
+def test_long_reductions_exact(per, N, K, dtype):
+    """Few tiles and a long reduction, which clusters of two and four CTAs
+    share: one tile a cluster or two, ragged parts, groups without rows."""
+    r = gen(K)
+    o, M, groups = offsets_of(per, 1), sum(per) + 2, len(per)
+    A, B = ints(r, M, K, hi=2), ints(r, groups, N, K, hi=2)
+    buf, D = marked((M, N), dtype, 3, 1)
+    g.matmul_grouped(A, B, o, out=D)
+    ok()
+    equal_bits(D, forward64(A, B, o))
+    # the row gradient reduces over N: the matrices the other way round
+    Bt = ints(r, groups, K, N, hi=2)
+    buf2, dA = marked((M, N), dtype, 3, 1)
+    g.matmul_grouped_dgrad(A, Bt, o, out=dA)
+    ok()
+    equal_bits(dA, dgrad64(A, Bt, o))
+    for b, view in ((buf, D), (buf2, dA)):
+        view.fill_(float("nan"))
+        assert b.isnan().all(), "wrote outside the output"
+
+
+def test_long_reduction_stall_times_out_then_recovers():
+    r = gen(14)
+    o, A, B = offsets_of([1, 3]), ints(r, 4, 4000), ints(r, 2, 300, 4000)
+    old = g.gemm_set_watchdog_ms(100)
+    try:
+        assert g.gemm_debug_stall_next_launch(1) == g.GEMM_OK
+        g.matmul_grouped(A, B, o)
+        assert g.gemm_last_status(stream()) == g.GEMM_ERR_TIMEOUT
+        got = g.matmul_grouped(A, B, o)
+        ok()
+        equal_bits(got, forward64(A, B, o))
+    finally:
+        g.gemm_set_watchdog_ms(old)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_random_shapes_exact(dtype):
     rng = np.random.default_rng(11)
     for i in range(24):
