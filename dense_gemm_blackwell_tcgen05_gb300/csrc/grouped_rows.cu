@@ -38,17 +38,19 @@ int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
   return launch_grouped<CG, Op::Rows, P_MN, false, NT, OUT32, SPLIT>(tmP, tmQ, a, tiles, ctx, stream);
 }
 
-// Which tiles.  With few rows a group the call reads its matrices and little
-// else: one CTA, 128 output columns, and a tile as narrow as the rows leave
-// more of shared memory to the matrices' loads.  Measured at 32 groups of
-// 4096 x 2048, us, 64 / 128 rows a tile on one CTA / 256 on a pair: 4 rows a
-// group 80 / 82 / 89, 16: 84 / 86 / 91, 32: 90 / 88 / 93, 64: 105 / 92 / 95.
-// With more rows the pair's tiles of 256 x 256 load half as much for each
-// product, but fill the device with a quarter as many tiles.  Time of either
-// from its rounds of tiles, 0.30 us for 64 k on a pair's tile and 0.22 on one
-// CTA's of 128 x 128, and 2 us for the cluster launch; e.g. (measured, one CTA
-// / pair) 8 groups of 1024 x 1024, 512 rows each: 13.4 / 17.0, 1024 rows: 20.3
-// / 19.2; 32 groups of 4096 x 2048, 256 rows each: 145 / 129.
+// Which tiles.  A launch takes its rounds of tiles (those of all groups over
+// the CTAs or pairs that run at once), each as long as its loads: a stage of 64 k
+// is 24 KB for 64 rows and 128 columns, 32 KB for 128 rows, and 32 KB in each CTA
+// of a pair for 256 rows and 256 columns, at 64 bytes a clock from L2 into an SM
+// 0.20, 0.27 and 0.27 us.  So wide tiles move least for a product, narrow ones
+// leave least of a ragged group empty and spread over most SMs.  0.24, 0.27 and
+// 0.30 us and 2 us for a cluster launch fit best: over 365 draws (1 to 16384
+// rows, 4 to 128 groups, sides of 256 to 4096) the choice is 0.8 % slower in
+// the mean than the best of the three.  Measured, us, 64 rows / 128 / a pair:
+// 8 groups of 1024 x 1024, 256 rows each: 11.2 / 11.3 / 11.0, 512: 19.1 / 13.8 /
+// 16.0, 1024: 30.1 / 22.4 / 17.9; 32 groups of 4096 x 2048, 4 rows: 80 / 82 / 89,
+// 32: 90 / 88 / 93, 256: 215 / 141 / 114; 61 of 399 x 1736, 52 rows: 22.4 / 24.5
+// / 24.7.
 template <bool P_MN, bool OUT32>
 int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
               const LaunchCtx& ctx, cudaStream_t stream) {
@@ -65,24 +67,23 @@ int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
       if (const int rc = grouped_room<1, Op::Rows, P_MN, false, 64, OUT32, 4>(ctx, &room); rc != GEMM_OK) return rc;
       if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 4>(p, X, ldx, L, K, ctx, stream);
     }
-    if (narrow <= static_cast<uint64_t>(ctx.num_sms / 2) && K >= 48 * 64) {
+    if (narrow <= static_cast<uint64_t>(ctx.num_sms / 2) && K >= 50 * 64) {
       if (const int rc = grouped_room<1, Op::Rows, P_MN, false, 64, OUT32, 2>(ctx, &room); rc != GEMM_OK) return rc;
       if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 2>(p, X, ldx, L, K, ctx, stream);
     }
   }
-  if (p.M <= 24 * touched) return rows_impl<1, 64, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
-  // a group's last tile is half full on average
-  const auto rounds = [&](uint64_t nt, uint64_t lt, uint64_t room) {
-    const uint64_t tiles = p.M / nt + touched / 2;
-    const double r = static_cast<double>((tiles > touched ? tiles : touched) * ceil_div_u64(L, lt)) / static_cast<double>(room);
-    return r > 1.0 ? r : 1.0;
+  const auto time = [&](uint64_t nt, uint64_t lt, uint64_t clusters, double stage) {
+    // a group's last tile is half full on average
+    const uint64_t blocks = p.M / nt + touched / 2;
+    const uint64_t tiles = (blocks > touched ? blocks : touched) * ceil_div_u64(L, lt);
+    return static_cast<double>(ceil_div_u64(tiles, clusters) * ceil_div_u64(K, 64)) * stage;
   };
-  const double kt = static_cast<double>(ceil_div_u64(K, 64));
   const uint64_t sms = static_cast<uint64_t>(ctx.num_sms);
-  const double one = rounds(128, 128, sms) * kt * 0.22;
-  const double pair = rounds(256, 256, sms / 2) * kt * 0.30 + 2.0;
-  return pair < one ? rows_impl<2, 256, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream)
-                    : rows_impl<1, 128, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
+  const double narrow = time(64, 128, sms, 0.24), wide = time(128, 128, sms, 0.27),
+               pair = time(256, 256, sms / 2, 0.30) + 2.0;
+  if (pair < wide && pair < narrow) return rows_impl<2, 256, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
+  return wide < narrow ? rows_impl<1, 128, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream)
+                       : rows_impl<1, 64, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
 }
 
 }  // namespace
