@@ -25,6 +25,10 @@
 //              of which hi feeds the tensor cores.  ApplyOut: the last one,
 //              whose X' is rounded once to the result's type.
 //   Op::SumAdd is Op::Sum added to what the output holds.
+//   Op::SumLane, Op::SumLaneAdd are these with the operands' places exchanged:
+//              P = dD and Q = A, l the output row and c along its contiguous
+//              dimension, for 16-bit outputs whose rows hold whole pieces of 16
+//              bytes: a lane then stores its row's elements in whole sectors.
 //
 // Persistent, warp-specialised: warp 0 lane 0 loads operand tiles of 64 k by
 // TMA (128-byte swizzle) into a ring of stages, warp 1 lane 0 issues the MMAs
@@ -44,7 +48,7 @@
 
 namespace gb300 {
 
-enum class Op { Rows, Sum, SumAdd, Sym, Apply, ApplyOut };
+enum class Op { Rows, Sum, SumAdd, SumLane, SumLaneAdd, Sym, Apply, ApplyOut };
 
 // Groups a launch can hold: the offsets and the tile table sit in shared memory.
 constexpr uint32_t kMaxGroups = 1024;
@@ -113,8 +117,10 @@ struct GroupedCfg {
   static constexpr uint32_t P_BYTES = 128 * 128;
   static constexpr uint32_t Q_BYTES = Q_ROWS * 128;
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
-  static constexpr bool ADD = OP == Op::SumAdd;          // out += instead of out =
-  static constexpr bool SUM = OP == Op::Sum || ADD;
+  static constexpr bool ADD = OP == Op::SumAdd || OP == Op::SumLaneAdd;   // out += instead of out =
+  static constexpr bool LANE = OP == Op::SumLane || OP == Op::SumLaneAdd; // output rows in the lanes
+  static constexpr bool SUM = OP == Op::Sum || LANE || ADD;
+  static_assert(!LANE || !OUT32, "fp32 rows are stored as whole lines either way");
   static constexpr bool APPLY = OP == Op::Apply || OP == Op::ApplyOut;
   static constexpr bool TAIL = SUM;                      // a warp clears ragged reduction ends
   static constexpr uint32_t kEpiWarps = 8;
@@ -174,6 +180,14 @@ __device__ __forceinline__ void grid_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Tiles along the C columns of a Sum.  LANE: neighbours share 8 columns, so that
+// each row can pass from one to the next at a boundary of its sectors.
+template <class C, uint32_t NT>
+__host__ __device__ __forceinline__ uint32_t sum_column_tiles(uint32_t columns) {
+  if (!C::LANE) return (columns + NT - 1) / NT;
+  return columns <= NT ? 1u : (columns - 8 + NT - 9) / (NT - 8);
+}
+
 // The wi-th tile of cluster c among G; false past the last.  Every role of
 // every CTA walks the same sequence.  offs: the clamped offsets; tab: the
 // first tile of each group and their number (Rows), or the groups in the order
@@ -209,7 +223,7 @@ __device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* 
   } else if constexpr (C::SUM) {
     // Large and small groups in turn, so that a tile bound by its MMAs runs
     // beside one bound by its store; rounds in alternating directions.
-    const uint32_t ct = (a.C + NT - 1) / NT, per = lt * ct;
+    const uint32_t ct = sum_column_tiles<C, NT>(a.C), per = lt * ct;
     const uint32_t t = wi * G + ((wi & 1u) ? G - 1u - c : c);
     if (t >= per * a.groups) return false;
     // tiles of the groups 2p and 2p + 1 of the order alternate
@@ -221,7 +235,7 @@ __device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* 
     w.k_len = offs[w.z + 1] - w.row0;
     uint32_t cb, lb;
     tile_coords(both ? r / 2 : r, ct, lt, 8u, cb, lb);
-    w.c0 = cb * NT;
+    w.c0 = cb * (C::LANE ? NT - 8 : NT);
     w.l0 = lb * C::LT;
     w.live = min(NT, a.C - w.c0);
     return true;
@@ -283,6 +297,14 @@ __device__ __forceinline__ void pair_columns(float v0, float v1, uint32_t odd, f
   const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
   x0 = odd ? got : v0;
   x1 = odd ? v1 : got;
+}
+
+// The same with both rounded to bf16 first: one conversion, one exchange and one
+// permutation of bytes for two elements.
+__device__ __forceinline__ uint32_t pair_columns_bf16(float v0, float v1, uint32_t odd) {
+  const uint32_t own = pack_bf16x2(v0, v1);   // rows 2i, 2i + 1 of this lane's column
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
+  return __byte_perm(own, got, odd ? 0x3276u : 0x5410u);
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -638,9 +660,14 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           const uint32_t l = w.l0 + rank * 128;
           const bool vec = ((reinterpret_cast<uintptr_t>(args.out) | (args.ldo * sizeof(T)) |
                              (args.stride_o * sizeof(T))) & 15u) == 0;
-          if (l < args.L)
+          if (C::LANE && l < args.L) {
+            T* const o = static_cast<T*>(args.out) + w.z * args.stride_o + l * args.ldo + w.c0;
+            for (uint32_t c = 0; c < w.live; c += 128)
+              zero_tile(o + c, args.ldo, min(128u, args.L - l), min(128u, w.live - c), vec, threadIdx.x - 64);
+          } else if (l < args.L) {
             zero_tile(static_cast<T*>(args.out) + out0 + l, args.ldo, w.live, min(128u, args.L - l), vec,
                       threadIdx.x - 64);
+          }
         }
         continue;
       }
@@ -724,6 +751,70 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
               if (c0 + t < w.live) *p = C::ADD ? *p + acc[i][t] : acc[i][t];
           }
         }
+      } else if constexpr (C::LANE) {
+        // This lane's row as whole sectors of 32 bytes.  Rows start on 16 bytes and
+        // hold whole pieces of 8 columns.  Where the tile starts inside a sector of
+        // this row (`late`), its first piece is the tile before's, which shares 8
+        // columns, and a chunk's last piece waits for the next chunk (`kept`).
+        const uint32_t half = (nch + 1) / 2;
+        const uint32_t first = eg * half, last = min(nch, first + half);
+        uint16_t* const row = static_cast<uint16_t*>(args.out) + w.z * args.stride_o + col * args.ldo + w.c0;
+        const bool late = ((reinterpret_cast<uintptr_t>(row) >> 4) & 1u) != 0;
+        const bool row_end = w.c0 + NT >= args.C;
+        uint32_t kept[4] = {};
+        if (!acc_wait()) break;
+        const uint32_t b = j & 1u;
+        bool held = true;
+#pragma unroll 1
+        for (uint32_t ch = first == 0 ? 0 : first - 1; ch < last; ++ch) {   // (first - 1: for the piece kept)
+          uint16_t* const o = row + ch * 32;
+          const uint32_t pieces = col < args.L ? min(4u, (w.live - ch * 32) / 8) : 0u;
+          uint32_t v[32];
+          tmem_ld_32x32b_x32_sync(t_addr(ch), v);
+          if (ch + 1 == last) {
+            release(b);
+            held = false;
+          }
+          uint32_t h[16];
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            uint4 had = make_uint4(0, 0, 0, 0);   // what the output holds
+            if (C::ADD && i < pieces) had = *reinterpret_cast<const uint4*>(o + 8 * i);
+            const uint32_t had4[4] = {had.x, had.y, had.z, had.w};
+#pragma unroll
+            for (uint32_t t = 0; t < 4; ++t) {
+              float x0 = __uint_as_float(v[8 * i + 2 * t]), x1 = __uint_as_float(v[8 * i + 2 * t + 1]);
+              if (C::ADD) {
+                x0 += bf16_bits_to_f32(had4[t] & 0xFFFFu);
+                x1 += bf16_bits_to_f32(had4[t] >> 16);
+              }
+              h[4 * i + t] = pack_bf16x2(x0, x1);
+            }
+          }
+          // two sectors: pieces 0 1 2 3, or the one kept and 0 1 2
+          uint32_t x[16];
+#pragma unroll
+          for (uint32_t t = 0; t < 4; ++t) x[t] = late ? kept[t] : h[t];
+#pragma unroll
+          for (uint32_t t = 4; t < 16; ++t) x[t] = late ? h[t - 4] : h[t];
+#pragma unroll
+          for (uint32_t t = 0; t < 4; ++t) kept[t] = h[12 + t];
+          if (ch < first || pieces == 0) continue;
+          uint16_t* const at = o - (late ? 8 : 0);
+          const uint32_t have = pieces + (late ? 1u : 0u);
+          if (late && ch == 0) {
+            if (w.c0 == 0) st_global_v4(o, x + 4);   // the row's first piece
+          } else if (have >= 2) {
+            st_global_v8(at, x);
+          } else {
+            st_global_v4(at, x);
+          }
+          if (have >= 4) st_global_v8(at + 16, x + 8);
+          else if (have == 3) st_global_v4(at + 16, x + 8);
+          if (have == 5 && row_end && ch + 1 == nch) st_global_v4(o + 24, kept);
+        }
+        if (held) release(b);   // (a warp without a chunk)
+        ++j;
       } else {
         // 16-bit outputs, one 32-column chunk at a time.  The code of a chunk is
         // kept short and rolled: run once or twice a kernel, it costs what its
@@ -830,6 +921,10 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           uint32_t st0[16], st1[16];
 #pragma unroll
           for (uint32_t t = 0; t < 16; ++t) {
+            if constexpr (OP == Op::Rows || OP == Op::Sum) {
+              st0[t] = pair_columns_bf16(__uint_as_float(v[2 * t]), __uint_as_float(v[2 * t + 1]), odd);
+              continue;
+            }
             float x0, x1;
             pair_columns(__uint_as_float(v[2 * t]), __uint_as_float(v[2 * t + 1]), odd, x0, x1);
             if constexpr (C::APPLY) {
@@ -848,11 +943,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
               st0[t] = __float_as_uint(x0 * args.out_scale);
               st1[t] = __float_as_uint(x1 * args.out_scale);
             } else {
-              st0[t] = OP == Op::Sym ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
-              if (C::ADD) {   // unrounded
-                st0[t] = __float_as_uint(x0);
-                st1[t] = __float_as_uint(x1);
-              }
+              // (SumAdd: unrounded)
+              st0[t] = OP == Op::Sym ? pack_f16x2(x0, x1) : __float_as_uint(x0);
+              st1[t] = __float_as_uint(x1);
             }
           }
           if constexpr (C::APPLY) fetch(ch + 2);
@@ -897,7 +990,11 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
               for (uint32_t t = 0; t < 16; ++t)
                 st0[t] = pack_bf16x2(__uint_as_float(st0[t]), __uint_as_float(st1[t]));
             }
-            if (vec && lbase + 32 <= args.L) {
+            if (vec && lbase + 32 <= args.L && c0 + 32 <= w.live) {
+              uint32_t* o = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+              for (uint32_t t = 0; t < 16; ++t, o += args.ldo) *o = st0[t];
+            } else if (vec && lbase + 32 <= args.L) {
 #pragma unroll
               for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo)
                 if (2 * t < rows_left) *reinterpret_cast<uint32_t*>(p) = st0[t];

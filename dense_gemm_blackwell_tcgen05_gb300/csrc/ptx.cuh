@@ -62,6 +62,16 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar
                : "memory");
 }
 
+// 32 bytes at a 32-byte boundary of global memory.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+__device__ __forceinline__ void st_global_v4(void* p, const uint32_t* x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 // Stores `value` at `cluster_addr` and then completes 4 transaction bytes on
 // `cluster_bar`, both in one CTA of the cluster (addresses from mapa),
 // asynchronously: the completion releases at cluster scope without making

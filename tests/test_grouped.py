@@ -225,6 +225,31 @@ def test_accumulate(dtype):
     assert torch.equal(out, old)
 
 
+@pytest.mark.parametrize("per, N, K", [
+    ([70, 0, 130, 1, 17], 136, 8), ([33, 0, 64], 130, 120), ([5, 65, 0], 260, 128), ([16, 9], 40, 136),
+    ([1, 0, 2], 129, 248), ([7], 77, 256), ([90, 0, 3], 136, 376), ([3, 0, 40], 20, 1032),
+    ([i % 4 for i in range(40)], 1032, 1032), ([40 * (i % 3) for i in range(44)], 1000, 1040)])
+def test_wgrad_rows_inside_sectors_exact(per, N, K):
+    """bf16 weight gradients whose rows start on 16 bytes but not all on 32: every
+    width around the tiles' seams, with a bound on each side; also added."""
+    r = gen(N + 3 * K)
+    groups, o, M = len(per), offsets_of(per), sum(per)
+    A, dD = ints(r, M, K), ints(r, M, N)
+    want = wgrad64(dD, A, o, groups)
+    for pad, shift in ((0, 8 if K % 16 == 0 else 0), (8 if K % 16 == 0 else 16, 0), (16 if K % 16 == 0 else 8, 8)):
+        buf, dB = marked((groups, N, K), torch.bfloat16, pad, shift)
+        g.matmul_grouped_wgrad(dD, A, o, out=dB)
+        ok()
+        equal_bits(dB, want)
+        old = torch.randint(-9, 10, (groups, N, K), generator=r, device="cuda").to(torch.bfloat16)
+        dB.copy_(old)
+        g.matmul_grouped_wgrad(dD, A, o, out=dB, accumulate=True)
+        ok()
+        equal_bits(dB, old.double() + want)
+        dB.fill_(float("nan"))
+        assert buf.isnan().all(), "wrote outside the output"
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_other_groups_values_stay_out(dtype):
     """NaN and Inf in another group's rows, in rows of no group and in the
