@@ -134,7 +134,7 @@ struct GroupedCfg {
   static constexpr uint32_t SEG_TILES = OUT32 ? 8u : 0xFFFFFFFFu;
   static constexpr uint32_t NCH = (NT + 63) / 64;        // 32-column chunks per epilogue warp
   static constexpr bool GROUPED = OP == Op::Rows || SUM;
-  static_assert(SPLIT == 1 || (CG == 1 && OP == Op::Rows && NT == 64), "split reductions");
+  static_assert(SPLIT == 1 || (CG == 1 && (OP == Op::Rows || OP == Op::Sym) && NT == 64), "split reductions");
   static constexpr uint32_t kCluster = CG * SPLIT;       // CTAs a cluster
   // the other CTAs' sums, fp32, in the first one: for each of them a tile of
   // 128 lanes by NT columns, 16 bytes a lane after another

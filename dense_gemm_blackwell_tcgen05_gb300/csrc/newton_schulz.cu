@@ -210,18 +210,83 @@ int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const 
   return last_launch();
 }
 
-template <int CG, uint32_t NT>
+// Time of a product, us: rounds of tiles over the CTAs or pairs that run at once,
+// each as long as its kt stages of 64 k or its epilogue, whichever is longer (the
+// shorter one is seen once).  Fitted to 1100 measured chains (110 sizes: 1 to 32
+// matrices, sides of 64 to 8192; 10 choices of the three products' tiles); choosing
+// each product's tiles by it is 0.1 % behind the best choice, the same tiles for
+// all three 1.1 %.
+struct TileCost {
+  uint32_t lt, nt;                        // output columns and rows
+  double stage, sym, apply, launch;
+};
+constexpr TileCost kNarrow = {128, 64, 0.30, 0.0, 2.4, 2.2};
+constexpr TileCost kWide = {128, 128, 0.41, 0.1, 4.1, 2.0};
+constexpr TileCost kPair = {256, 256, 0.47, 1.5, 6.7, 0.8};
+
+double time_of(const TileCost& c, uint64_t tiles, uint32_t K, double epilogue, const LaunchCtx& ctx) {
+  const uint64_t clusters = static_cast<uint64_t>(ctx.num_sms) * 128 / c.lt;
+  const double load = static_cast<double>(ceil_div_u64(K, 64)) * c.stage;
+  const double rounds = static_cast<double>(ceil_div_u64(tiles, clusters));
+  return c.launch + (load > epilogue ? rounds * load + epilogue : rounds * epilogue + load);
+}
+
+// Tiles on and below the diagonal of m x m.
+uint64_t sym_tiles(uint64_t lt, uint64_t nt, uint64_t m, uint64_t batch) {
+  const uint64_t n = ceil_div_u64(m, lt);
+  return lt / nt * (n * (n + 1) / 2) * batch;
+}
+uint64_t all_tiles(uint64_t lt, uint64_t nt, const GroupedArgs& a) {
+  return ceil_div_u64(a.L, lt) * ceil_div_u64(a.C, nt) * a.groups;
+}
+
+// A symmetric product of P and Q, the same matrix; MN: by its columns.
+template <bool MN>
+int symmetric(const CUtensorMap& P, const CUtensorMap& Q, const GroupedArgs& a, const LaunchCtx& ctx,
+              cudaStream_t stream) {
+  const auto tiles = [&](const TileCost& c) { return sym_tiles(c.lt, c.nt, a.C, a.groups); };
+  const auto time = [&](const TileCost& c) { return time_of(c, tiles(c), a.K, c.sym, ctx); };
+  // Few tiles and a long reduction: a cluster of CTAs shares it.  Four cost 6.0 us more
+  // a launch than one and save 0.17 us for each 64 k, two cost 4.6 and save 0.11.
+  // Measured, five steps on a 64 x n matrix, us, one CTA / two / four: n = 1024:
+  // 64 / 77 / 80, 2048: 82 / 87 / 84, 4096: 118 / 105 / 94, 8192: 191 / 140 / 111; four
+  // matrices of 384 x 4096, whose tiles are too many for four: 194 / 179.
+  const uint64_t fine = tiles(kNarrow);
+  uint64_t room = 0;
+  if (a.K >= 36 * 64 && fine <= static_cast<uint64_t>(ctx.num_sms / 4)) {
+    if (const int rc = grouped_room<1, Op::Sym, MN, MN, 64, false, 4>(ctx, &room); rc != GEMM_OK) return rc;
+    if (fine <= room) return launch_grouped<1, Op::Sym, MN, MN, 64, false, 4>(P, Q, a, fine, ctx, stream);
+  }
+  if (a.K >= 42 * 64 && fine <= static_cast<uint64_t>(ctx.num_sms / 2)) {
+    if (const int rc = grouped_room<1, Op::Sym, MN, MN, 64, false, 2>(ctx, &room); rc != GEMM_OK) return rc;
+    if (fine <= room) return launch_grouped<1, Op::Sym, MN, MN, 64, false, 2>(P, Q, a, fine, ctx, stream);
+  }
+  const double narrow = time(kNarrow), wide = time(kWide), pair = time(kPair);
+  if (pair < wide && pair < narrow)
+    return launch_grouped<2, Op::Sym, MN, MN, 256, false>(P, Q, a, tiles(kPair), ctx, stream);
+  return wide < narrow ? launch_grouped<1, Op::Sym, MN, MN, 128, false>(P, Q, a, tiles(kWide), ctx, stream)
+                       : launch_grouped<1, Op::Sym, MN, MN, 64, false>(P, Q, a, tiles(kNarrow), ctx, stream);
+}
+
+// X' from Y as P (K-major) and X as Q, or, MN, X as P (by its columns) and Y as Q.
+template <Op OP, bool MN>
+int apply(const CUtensorMap& P, const CUtensorMap& Q, const GroupedArgs& a, const LaunchCtx& ctx,
+          cudaStream_t stream) {
+  const auto tiles = [&](const TileCost& c) { return all_tiles(c.lt, c.nt, a); };
+  const auto time = [&](const TileCost& c) { return time_of(c, tiles(c), a.K, c.apply, ctx); };
+  const double narrow = time(kNarrow), wide = time(kWide), pair = time(kPair);
+  if (pair < wide && pair < narrow)
+    return launch_grouped<2, OP, MN, false, 256, false>(P, Q, a, tiles(kPair), ctx, stream);
+  return wide < narrow ? launch_grouped<1, OP, MN, false, 128, false>(P, Q, a, tiles(kWide), ctx, stream)
+                       : launch_grouped<1, OP, MN, false, 64, false>(P, Q, a, tiles(kNarrow), ctx, stream);
+}
+
 int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
-  using SymK = GroupedCfg<CG, Op::Sym, false, false, NT, false>;
   uint8_t* const ws = static_cast<uint8_t*>(p.workspace);
   const bool tall = p.rows > p.cols;
   const uint32_t m = tall ? p.cols : p.rows;
   __half* const gram = reinterpret_cast<__half*>(ws + w.gram);
   __half* const poly = reinterpret_cast<__half*>(ws + w.poly);
-  const uint64_t lt = ceil_div_u64(m, SymK::LT);
-  const uint64_t sym_tiles = SymK::LT / NT * (lt * (lt + 1) / 2) * p.batch;
-  const uint64_t all_tiles = ceil_div_u64(p.cols, SymK::LT) * ceil_div_u64(p.rows, NT) * p.batch;
-  if (sym_tiles > 0x7FFFFFFFull || all_tiles > 0x7FFFFFFFull) return GEMM_ERR_INVALID_ARG;
 
   GroupedArgs base = {};
   base.groups = p.batch;
@@ -232,12 +297,18 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
   base.diag = reinterpret_cast<float*>(ws + w.diag);
   base.diag_n = m;
 
-  // Y as an operand: K-major P or Q; P as both operands of its square
+  // Y as an operand: K-major P or Q; P as both operands of its square.  The boxes
+  // are those of every tile size.
+  using Any = GroupedCfg<1, Op::Sym, false, false, 64, false>;
+  constexpr uint32_t kP = p_box_rows<Any, false>(), kQ = q_box_rows<Any, false>(), kMN = p_box_rows<Any, true>();
+  static_assert(kQ == GroupedCfg<1, Op::Sym, false, false, 128, false>::Q_BOX &&
+                    kQ == GroupedCfg<2, Op::Sym, false, false, 256, false>::Q_BOX,
+                "one tensor map for all tiles");
   CUtensorMap gramP, gramQ, polyP, polyQ;
-  if (!operand_map(&gramP, gram, m, m, p.batch, w.ldp, w.stride_p, p_box_rows<SymK, false>()) ||
-      !operand_map(&gramQ, gram, m, m, p.batch, w.ldp, w.stride_p, q_box_rows<SymK, false>()) ||
-      !operand_map(&polyP, poly, m, m, p.batch, w.ldp, w.stride_p, p_box_rows<SymK, false>()) ||
-      !operand_map(&polyQ, poly, m, m, p.batch, w.ldp, w.stride_p, q_box_rows<SymK, false>()))
+  if (!operand_map(&gramP, gram, m, m, p.batch, w.ldp, w.stride_p, kP) ||
+      !operand_map(&gramQ, gram, m, m, p.batch, w.ldp, w.stride_p, kQ) ||
+      !operand_map(&polyP, poly, m, m, p.batch, w.ldp, w.stride_p, kP) ||
+      !operand_map(&polyQ, poly, m, m, p.batch, w.ldp, w.stride_p, kQ))
     return GEMM_ERR_LAUNCH;
 
   for (int step = 0; step < p.steps; ++step) {
@@ -245,9 +316,9 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
     const bool last = step + 1 == p.steps;
     __half* const hi = reinterpret_cast<__half*>(ws + w.hi[cur]);
     CUtensorMap xK, xKq, xMN;   // X by its rows (as P, as Q) and by its columns
-    if (!operand_map(&xK, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, p_box_rows<SymK, false>()) ||
-        !operand_map(&xKq, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, q_box_rows<SymK, false>()) ||
-        !operand_map(&xMN, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, 64))
+    if (!operand_map(&xK, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kP) ||
+        !operand_map(&xKq, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kQ) ||
+        !operand_map(&xMN, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kMN))
       return GEMM_ERR_LAUNCH;
 
     GroupedArgs s = base;   // P = X X^T (or X^T X), the scale taken out
@@ -257,8 +328,7 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
     s.ldo = w.ldp;
     s.stride_o = w.stride_p;
     s.alpha = 1.0f / (scale * scale);
-    int rc = tall ? launch_grouped<CG, Op::Sym, true, true, NT, false>(xMN, xMN, s, sym_tiles, ctx, stream)
-                  : launch_grouped<CG, Op::Sym, false, false, NT, false>(xK, xKq, s, sym_tiles, ctx, stream);
+    int rc = tall ? symmetric<true>(xMN, xMN, s, ctx, stream) : symmetric<false>(xK, xKq, s, ctx, stream);
     if (rc != GEMM_OK) return rc;
 
     s.K = m;                // Y = b P + c P P, its diagonal apart
@@ -266,8 +336,7 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
     s.alpha = p.c;
     s.beta = p.b;
     s.R = gram;
-    if ((rc = launch_grouped<CG, Op::Sym, false, false, NT, false>(gramP, gramQ, s, sym_tiles, ctx, stream)) != GEMM_OK)
-      return rc;
+    if ((rc = symmetric<false>(gramP, gramQ, s, ctx, stream)) != GEMM_OK) return rc;
 
     GroupedArgs t = base;   // X' = (a + d) X + Y X (or X (a + d) + X Y)
     t.L = p.cols;
@@ -291,32 +360,14 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
       t.stride_o = w.stride_x;
     }
     if (last)
-      rc = tall ? launch_grouped<CG, Op::ApplyOut, false, false, NT, false>(polyP, xKq, t, all_tiles, ctx, stream)
-                : launch_grouped<CG, Op::ApplyOut, true, false, NT, false>(xMN, polyQ, t, all_tiles, ctx, stream);
+      rc = tall ? apply<Op::ApplyOut, false>(polyP, xKq, t, ctx, stream)
+                : apply<Op::ApplyOut, true>(xMN, polyQ, t, ctx, stream);
     else
-      rc = tall ? launch_grouped<CG, Op::Apply, false, false, NT, false>(polyP, xKq, t, all_tiles, ctx, stream)
-                : launch_grouped<CG, Op::Apply, true, false, NT, false>(xMN, polyQ, t, all_tiles, ctx, stream);
+      rc = tall ? apply<Op::Apply, false>(polyP, xKq, t, ctx, stream)
+                : apply<Op::Apply, true>(xMN, polyQ, t, ctx, stream);
     if (rc != GEMM_OK) return rc;
   }
   return GEMM_OK;
-}
-
-// Which tiles.  A step is three dependent products; with few tiles in a
-// product, narrower ones spread it over more SMs, with many the pair's load
-// least.  Measured, us, 128 x 64 and 128 x 128 on one CTA / 256 x 256 on a
-// pair: one matrix of 512 x 512: 79 / 100 / 149, 1024 x 1024: 111 / 133 / 187,
-// 1536 x 1536: 229 / 178 / 239, 4096 x 4096: 2169 / 1390 / 978; 16 of 1024 x
-// 2048: 1167 / 799 / 755.
-int pick(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
-  const uint32_t m = p.rows < p.cols ? p.rows : p.cols;
-  const auto blocks = [&](uint64_t size) {   // of that size on and below the diagonals
-    const uint64_t n = ceil_div_u64(m, size);
-    return n * (n + 1) / 2 * p.batch;
-  };
-  const uint64_t sms = static_cast<uint64_t>(ctx.num_sms);
-  if (blocks(256) >= sms / 2) return iterate<2, 256>(p, w, scale, ctx, stream);
-  if (blocks(128) > sms / 3) return iterate<1, 128>(p, w, scale, ctx, stream);
-  return iterate<1, 64>(p, w, scale, ctx, stream);
 }
 
 }  // namespace
@@ -327,13 +378,14 @@ uint64_t newton_schulz_bytes(uint64_t batch, uint64_t rows, uint64_t cols) {
 
 int launch_newton_schulz(const NewtonSchulzProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
   const Layout w = layout_of(p.batch, p.rows, p.cols);
+  if (ceil_div_u64(p.cols, 128) * ceil_div_u64(p.rows, 64) * p.batch > 0x7FFFFFFFull) return GEMM_ERR_INVALID_ARG;
   // X is held times 2^k, near the square root of its longer side: its entries
   // are then near 1 once its singular values are, and the fp16 halves far
   // from their range's ends
   const uint32_t n = p.rows > p.cols ? p.rows : p.cols;
   const float scale = std::ldexp(1.0f, static_cast<int>(std::floor(0.5 * std::log2(static_cast<double>(n)))));
   const int rc = p.g_f32 ? normalise<float>(p, w, scale, ctx, stream) : normalise<uint16_t>(p, w, scale, ctx, stream);
-  return rc != GEMM_OK ? rc : pick(p, w, scale, ctx, stream);
+  return rc != GEMM_OK ? rc : iterate(p, w, scale, ctx, stream);
 }
 
 }  // namespace gb300

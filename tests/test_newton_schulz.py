@@ -81,6 +81,20 @@ def test_batch_pitches(batch, rows, cols):
         assert flat.isnan().all(), "wrote outside the output"
 
 
+@pytest.mark.parametrize("batch, rows, cols", [
+    (1, 70, 2400), (1, 5000, 33), (2, 128, 2304), (1, 4100, 130), (4, 300, 2700), (3, 2900, 384), (5, 2047, 60),
+    (20, 138, 670), (30, 300, 900), (24, 1300, 72)])
+def test_long_sides(batch, rows, cols):
+    """Long reductions of few tiles, and products whose best tiles differ."""
+    gen = torch.Generator("cuda").manual_seed(rows - cols)
+    G = torch.randn(batch, rows, cols, device="cuda", generator=gen)
+    for dtype in (torch.float32, torch.bfloat16):
+        O = g.newton_schulz(G, out_dtype=dtype)
+        assert g.gemm_last_status(stream()) == g.GEMM_OK
+        close(O, reference(G), tolerance(5, dtype))
+        assert torch.equal(O, g.newton_schulz(G, out_dtype=dtype))
+
+
 @pytest.mark.parametrize("rows, cols", [(512, 640), (640, 512), (96, 96)])
 @pytest.mark.parametrize("kind", ["rank8", "decay"])
 def test_small_singular_values(rows, cols, kind):
