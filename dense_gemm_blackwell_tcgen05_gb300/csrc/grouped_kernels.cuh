@@ -70,9 +70,9 @@ struct GroupedArgs {
   float* diag;                 // [matrix][C]: written by Sym with R, read by Apply
   uint32_t diag_n;             // values of diag per matrix
   const __half* R;             // Sym: the symmetric matrix of the beta term (nullptr: none)
-  const __half* x_hi;          // Apply: X as hi + lo (pitch ldx, stride stride_x)
-  const __half* x_lo;
-  uint64_t ldx, stride_x;      // also R's pitch and stride
+  const __half* x_hi;          // Apply: X as hi + lo: hi by rows (pitch ldx, stride stride_x),
+  const __half* x_lo;          //   lo in blocks as the epilogue's lanes take it (lo_block)
+  uint64_t ldx, stride_x;
   __half* out_lo;              // Apply: the lo half of X'
   float out_scale;             // ApplyOut: factor on the way out
   uint32_t out_f32;            // ApplyOut: fp32 (else bf16)
@@ -310,6 +310,14 @@ __device__ __forceinline__ uint32_t pair_columns_bf16(float v0, float v1, uint32
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// First element of a 32 x 32 block of X's lo half, whose layout is private to the
+// kernels that write and read it: blocks of 1024 along the rows; in a block piece p
+// (of 4) of lane l is 8 elements at 256 p + 8 l: columns 2 (l / 2) and the next of
+// rows 2 t + l % 2, t = 4 p .. 4 p + 3.  Four 16-byte accesses a lane, all in order.
+__device__ __forceinline__ uint64_t lo_block(uint64_t z, uint32_t row, uint32_t col, uint32_t rows, uint32_t cols) {
+  return ((z * ((rows + 31) / 32) + row / 32) * ((cols + 31) / 32) + col / 32) * 1024;
 }
 
 template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32, uint32_t SPLIT = 1>
@@ -854,13 +862,21 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
             const uint64_t at =
                 w.z * args.stride_x + static_cast<uint64_t>(w.c0 + c0 + odd) * args.ldx + pcol;
             const uint32_t* h = reinterpret_cast<const uint32_t*>(args.x_hi + at);
-            const uint32_t* l = reinterpret_cast<const uint32_t*>(args.x_lo + at);
+            const uint4* l =
+                reinterpret_cast<const uint4*>(args.x_lo + lo_block(w.z, w.c0 + c0, lbase, args.C, args.L)) + lane;
             const uint32_t left = pcol < args.L && c0 + odd < w.live ? w.live - c0 - odd : 0u;
             if (P_MN) rowf = c0 + lane < w.live ? args.alpha + dg[w.c0 + c0 + lane] : 0.0f;
 #pragma unroll
-            for (uint32_t t = 0; t < 16; ++t, h += args.ldx, l += args.ldx) {
-              add0[t] = 2 * t < left ? *h : 0u;
-              add1[t] = 2 * t < left ? *l : 0u;
+            for (uint32_t t = 0; t < 16; ++t, h += args.ldx) add0[t] = 2 * t < left ? *h : 0u;
+            // (the block's rows and columns past the matrix's are never stored as hi)
+            const bool live = ch < nch && lbase < args.L;
+#pragma unroll
+            for (uint32_t p = 0; p < 4; ++p) {
+              const uint4 x = live ? l[32 * p] : make_uint4(0, 0, 0, 0);
+              add1[4 * p] = x.x;
+              add1[4 * p + 1] = x.y;
+              add1[4 * p + 2] = x.z;
+              add1[4 * p + 3] = x.w;
             }
           }
         };
@@ -954,14 +970,17 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           if constexpr (OP == Op::Sym || OP == Op::Apply) {
             // the workspace: even pitches, and the column past an odd last one is padding
             uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(args.out) + at + pcol);
-            uint32_t* p1 = reinterpret_cast<uint32_t*>(args.out_lo + at + pcol);
             const uint32_t left = pcol < args.L ? rows_left : 0u;
 #pragma unroll
-            for (uint32_t t = 0; t < 16; ++t, p += args.ldo, p1 += args.ldo)
-              if (2 * t < left) {
-                *p = st0[t];
-                if (OP == Op::Apply) *p1 = st1[t];
-              }
+            for (uint32_t t = 0; t < 16; ++t, p += args.ldo)
+              if (2 * t < left) *p = st0[t];
+            if (OP == Op::Apply && lbase < args.L) {
+              uint4* l =
+                  reinterpret_cast<uint4*>(args.out_lo + lo_block(w.z, w.c0 + c0, lbase, args.C, args.L)) + lane;
+#pragma unroll
+              for (uint32_t p = 0; p < 4; ++p)
+                l[32 * p] = make_uint4(st1[4 * p], st1[4 * p + 1], st1[4 * p + 2], st1[4 * p + 3]);
+            }
           } else if (OP == Op::ApplyOut && args.out_f32) {
             float* p = static_cast<float*>(args.out) + at + pcol;
 #pragma unroll

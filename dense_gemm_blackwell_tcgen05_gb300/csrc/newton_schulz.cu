@@ -101,7 +101,41 @@ __global__ void __launch_bounds__(256) ns_square_sum_kernel(const T* G, uint32_t
   if (threadIdx.x == 0) partials[blockIdx.y * kMaxPartials + blockIdx.x] = sum;
 }
 
-// X = G * scale / (|G| + eps) as fp16 halves hi + lo.  A read of G, a write of X.
+// A lane's 16 pairs of elements of a block: columns col, col + 1 of every second
+// row from row on (those outside the matrix read as 0).  PAIRS: as one load each.
+// All loads come before the first use.
+template <class T, bool PAIRS>
+__device__ __forceinline__ void load_pairs(const T* g, uint64_t ld, uint32_t row, uint32_t col, uint32_t rows,
+                                           uint32_t cols, float2 (&v)[16]) {
+  g += row * ld + col;
+  const bool in0 = col < cols, in1 = col + 1 < cols;
+  if constexpr (PAIRS) {
+    using P = std::conditional_t<sizeof(T) == 4, float2, uint32_t>;
+    P x[16];
+#pragma unroll
+    for (uint32_t t = 0; t < 16; ++t, g += 2 * ld) x[t] = row + 2 * t < rows ? __ldg(reinterpret_cast<const P*>(g)) : P{};
+#pragma unroll
+    for (uint32_t t = 0; t < 16; ++t) {
+      if constexpr (sizeof(T) == 4) v[t] = x[t];
+      else v[t] = make_float2(bf16_bits_to_f32(x[t] & 0xFFFFu), bf16_bits_to_f32(x[t] >> 16));
+    }
+  } else {
+    T x[16], y[16];
+#pragma unroll
+    for (uint32_t t = 0; t < 16; ++t, g += 2 * ld) {
+      x[t] = in0 && row + 2 * t < rows ? __ldg(g) : T(0);
+      y[t] = in1 && row + 2 * t < rows ? __ldg(g + 1) : T(0);
+    }
+#pragma unroll
+    for (uint32_t t = 0; t < 16; ++t) {
+      if constexpr (sizeof(T) == 4) v[t] = make_float2(x[t], y[t]);
+      else v[t] = make_float2(bf16_bits_to_f32(x[t]), bf16_bits_to_f32(y[t]));
+    }
+  }
+}
+
+// X = G * scale / (|G| + eps) as fp16 halves hi + lo, a 32 x 32 block at a time
+// with a lane's elements as lo_block has them.  A read of G, a write of X.
 template <class T>
 __global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
                                                            uint64_t stride_g, const float* partials,
@@ -115,28 +149,29 @@ __global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t 
   for (uint32_t i = threadIdx.x; i < num_partials; i += 256) sum += partials[blockIdx.y * kMaxPartials + i];
   const float f = scale / (sqrtf(block_sum(sum, slots)) + eps);
   const T* const g = G + blockIdx.y * stride_g;
-  const bool vec = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(T) - 1)) == 0 && ldg % 4 == 0;
-  const uint32_t segs = (cols + kSegment - 1) / kSegment;
-  const uint64_t units = static_cast<uint64_t>(rows) * segs;
+  const bool vec = (reinterpret_cast<uintptr_t>(g) & (2 * sizeof(T) - 1)) == 0 && ldg % 2 == 0;
+  const uint32_t across = (cols + 31) / 32;
+  const uint64_t units = static_cast<uint64_t>((rows + 31) / 32) * across;
   for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
-    const uint64_t r = u / segs;
-    const uint32_t c0 = static_cast<uint32_t>(u - r * segs) * kSegment;
-    float4 v[kSegment / 128];
+    const uint32_t rb = static_cast<uint32_t>(u / across);
+    const uint32_t c = (static_cast<uint32_t>(u) - rb * across) * 32 + (lane & ~1u), r = rb * 32 + (lane & 1u);
+    float2 v[16];
+    if (vec && (c & ~31u) + 32 <= cols) load_pairs<T, true>(g, ldg, r, c, rows, cols, v);
+    else load_pairs<T, false>(g, ldg, r, c, rows, cols, v);
+    uint32_t low[16];
 #pragma unroll
-    for (uint32_t i = 0; i < kSegment / 128; ++i) v[i] = load4<T>(g + r * ldg, c0 + i * 128 + lane * 4, cols, vec);
-#pragma unroll
-    for (uint32_t i = 0; i < kSegment / 128; ++i) {
-      const uint32_t c = c0 + i * 128 + lane * 4;
-      if (c >= ldx) continue;   // the pitch is a multiple of 8: four columns from c < ldx fit
-      const float x[4] = {v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f};
-      const uint2 h = make_uint2(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]));
-      const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
-      const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
-      const uint64_t at = blockIdx.y * stride_x + r * ldx + c;
-      *reinterpret_cast<uint2*>(hi + at) = h;
-      *reinterpret_cast<uint2*>(lo + at) =
-          make_uint2(pack_f16x2(x[0] - h0.x, x[1] - h0.y), pack_f16x2(x[2] - h1.x, x[3] - h1.y));
+    for (uint32_t t = 0; t < 16; ++t) {
+      const float x = v[t].x * f, y = v[t].y * f;
+      const uint32_t h = pack_f16x2(x, y);
+      const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      low[t] = pack_f16x2(x - got.x, y - got.y);
+      // the pitch is even: two columns from c < ldx fit
+      if (r + 2 * t < rows && c < ldx)
+        *reinterpret_cast<uint32_t*>(hi + blockIdx.y * stride_x + (r + 2 * t) * ldx + c) = h;
     }
+    uint4* const l = reinterpret_cast<uint4*>(lo + lo_block(blockIdx.y, rb * 32, c, rows, cols)) + lane;
+#pragma unroll
+    for (uint32_t p = 0; p < 4; ++p) l[32 * p] = make_uint4(low[4 * p], low[4 * p + 1], low[4 * p + 2], low[4 * p + 3]);
   }
 }
 
@@ -163,7 +198,7 @@ Layout layout_of(uint64_t batch, uint64_t rows, uint64_t cols) {
   };
   for (int i = 0; i < 2; ++i) {
     w.hi[i] = take(batch * w.stride_x * 2);
-    w.lo[i] = take(batch * w.stride_x * 2);
+    w.lo[i] = take(batch * round_up(rows, 32) * round_up(cols, 32) * 2);
   }
   w.gram = take(batch * w.stride_p * 2);
   w.poly = take(batch * w.stride_p * 2);
@@ -184,11 +219,12 @@ int last_launch() {
 template <class T>
 int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
   uint8_t* const ws = static_cast<uint8_t*>(p.workspace);
-  const uint64_t units = static_cast<uint64_t>(p.rows) * ceil_div_u64(p.cols, kSegment);
-  uint64_t blocks = ceil_div_u64(units, 8);
   const uint64_t share = ceil_div_u64(8ull * static_cast<uint64_t>(ctx.num_sms), p.batch);
-  if (blocks > share) blocks = share;
-  if (blocks > kMaxPartials) blocks = kMaxPartials;
+  const auto blocks_of = [&](uint64_t units) {   // eight warps a block, one unit a warp at a time
+    const uint64_t b = ceil_div_u64(units, 8), most = share < kMaxPartials ? share : kMaxPartials;
+    return b < most ? b : most;
+  };
+  const uint64_t blocks = blocks_of(static_cast<uint64_t>(p.rows) * ceil_div_u64(p.cols, kSegment));
   float* const partials = reinterpret_cast<float*>(ws + w.partials);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), p.batch);
@@ -203,6 +239,7 @@ int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const 
   if (cudaLaunchKernelEx(&cfg, ns_square_sum_kernel<T>, g, p.rows, p.cols, p.ldg, p.stride_g, partials) != cudaSuccess)
     return last_launch();
   cfg.numAttrs = 1;
+  cfg.gridDim.x = static_cast<unsigned>(blocks_of(ceil_div_u64(p.rows, 32) * ceil_div_u64(p.cols, 32)));
   cudaLaunchKernelEx(&cfg, ns_normalise_kernel<T>, g, p.rows, p.cols, p.ldg, p.stride_g,
                      static_cast<const float*>(partials), static_cast<uint32_t>(blocks), scale, p.eps,
                      reinterpret_cast<__half*>(ws + w.hi[0]), reinterpret_cast<__half*>(ws + w.lo[0]), w.ldx,
