@@ -30,31 +30,41 @@ namespace {
 constexpr uint32_t kSegment = 1024;      // columns a warp takes at a time
 constexpr uint32_t kMaxPartials = 1024;  // partial sums per matrix
 
-template <class T>
-__device__ __forceinline__ float load_as_f32(const T* p);
-template <>
-__device__ __forceinline__ float load_as_f32<float>(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load_as_f32<uint16_t>(const uint16_t* p) { return bf16_bits_to_f32(__ldg(p)); }
-
-// Four consecutive elements at column col (those >= cols read as 0).
-template <class T>
-__device__ __forceinline__ float4 load4(const T* row, uint32_t col, uint32_t cols, bool vec) {
-  if (vec && col + 4 <= cols) {
-    if constexpr (sizeof(T) == 4) {
-      return __ldg(reinterpret_cast<const float4*>(row + col));
-    } else {
-      const uint2 t = __ldg(reinterpret_cast<const uint2*>(row + col));
-      return make_float4(bf16_bits_to_f32(t.x & 0xFFFFu), bf16_bits_to_f32(t.x >> 16),
-                         bf16_bits_to_f32(t.y & 0xFFFFu), bf16_bits_to_f32(t.y >> 16));
+// Sum of squares of a lane's share of columns col .. of a row segment: four
+// consecutive columns out of each 128.  QUADS: as one load (rows of whole
+// quadruples).  All loads come before the first use.
+template <class T, bool QUADS>
+__device__ __forceinline__ float segment_square_sum(const T* row, uint32_t col, uint32_t cols) {
+  constexpr uint32_t kN = kSegment / 128;
+  float sum = 0.0f;
+  const auto add = [&](float x, float y, float z, float w) { sum += x * x + y * y + (z * z + w * w); };
+  row += col;
+  if constexpr (QUADS) {
+    using P = std::conditional_t<sizeof(T) == 4, float4, uint2>;
+    P x[kN];
+#pragma unroll
+    for (uint32_t i = 0; i < kN; ++i) x[i] = col + i * 128 < cols ? __ldg(reinterpret_cast<const P*>(row + i * 128)) : P{};
+#pragma unroll
+    for (uint32_t i = 0; i < kN; ++i) {
+      if constexpr (sizeof(T) == 4) add(x[i].x, x[i].y, x[i].z, x[i].w);
+      else add(bf16_bits_to_f32(x[i].x & 0xFFFFu), bf16_bits_to_f32(x[i].x >> 16), bf16_bits_to_f32(x[i].y & 0xFFFFu),
+               bf16_bits_to_f32(x[i].y >> 16));
+    }
+  } else {
+    T x[4 * kN];
+#pragma unroll
+    for (uint32_t i = 0; i < 4 * kN; ++i) {
+      const uint32_t at = i / 4 * 128 + i % 4;
+      x[i] = col + at < cols ? __ldg(row + at) : T(0);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kN; ++i) {
+      if constexpr (sizeof(T) == 4) add(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      else add(bf16_bits_to_f32(x[4 * i]), bf16_bits_to_f32(x[4 * i + 1]), bf16_bits_to_f32(x[4 * i + 2]),
+               bf16_bits_to_f32(x[4 * i + 3]));
     }
   }
-  float4 v;
-  v.x = col < cols ? load_as_f32<T>(row + col) : 0.0f;
-  v.y = col + 1 < cols ? load_as_f32<T>(row + col + 1) : 0.0f;
-  v.z = col + 2 < cols ? load_as_f32<T>(row + col + 2) : 0.0f;
-  v.w = col + 3 < cols ? load_as_f32<T>(row + col + 3) : 0.0f;
-  return v;
+  return sum;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -83,19 +93,16 @@ __global__ void __launch_bounds__(256) ns_square_sum_kernel(const T* G, uint32_t
   grid_dependents_launch();
   const uint32_t lane = lane_idx();
   const T* const g = G + blockIdx.y * stride_g;
-  const bool vec = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(T) - 1)) == 0 && ldg % 4 == 0;
+  const bool vec = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(T) - 1)) == 0 && ldg % 4 == 0 && cols % 4 == 0;
   const uint32_t segs = (cols + kSegment - 1) / kSegment;
   const uint64_t units = static_cast<uint64_t>(rows) * segs;
   float sum = 0.0f;
   for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
     const uint64_t r = u / segs;
     const uint32_t c0 = static_cast<uint32_t>(u - r * segs) * kSegment;
-    float4 v[kSegment / 128];
-#pragma unroll
-    for (uint32_t i = 0; i < kSegment / 128; ++i) v[i] = load4<T>(g + r * ldg, c0 + i * 128 + lane * 4, cols, vec);
-#pragma unroll
-    for (uint32_t i = 0; i < kSegment / 128; ++i)
-      sum += v[i].x * v[i].x + v[i].y * v[i].y + (v[i].z * v[i].z + v[i].w * v[i].w);
+    const T* const row = g + r * ldg;
+    sum += vec ? segment_square_sum<T, true>(row, c0 + lane * 4, cols)
+               : segment_square_sum<T, false>(row, c0 + lane * 4, cols);
   }
   sum = block_sum(sum, slots);
   if (threadIdx.x == 0) partials[blockIdx.y * kMaxPartials + blockIdx.x] = sum;
