@@ -312,6 +312,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// fp16 bits plus, or minus, an fp32 value, in fp32.
+__device__ __forceinline__ float f16_plus(uint32_t bits, float x) {
+  float r;
+  asm("add.f32.f16 %0, %1, %2;" : "=f"(r) : "h"(static_cast<uint16_t>(bits)), "f"(x));
+  return r;
+}
+__device__ __forceinline__ float f16_minus(uint32_t bits, float x) {
+  float r;
+  asm("sub.f32.f16 %0, %1, %2;" : "=f"(r) : "h"(static_cast<uint16_t>(bits)), "f"(x));
+  return r;
+}
+
 // First element of a 32 x 32 block of X's lo half, whose layout is private to the
 // kernels that write and read it: blocks of 1024 along the rows; in a block piece p
 // (of 4) of lane l is 8 elements at 256 p + 8 l: columns 2 (l / 2) and the next of
@@ -944,17 +956,15 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
             float x0, x1;
             pair_columns(__uint_as_float(v[2 * t]), __uint_as_float(v[2 * t + 1]), odd, x0, x1);
             if constexpr (C::APPLY) {
-              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&add0[t]));
               const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&add1[t]));
               const float f = P_MN ? __shfl_sync(0xffffffffu, rowf, 2 * t + odd) : 0.0f;
-              x0 = fmaf(P_MN ? f : colf0, h.x + l.x, x0);
-              x1 = fmaf(P_MN ? f : colf1, h.y + l.y, x1);
+              x0 = fmaf(P_MN ? f : colf0, f16_plus(add0[t] & 0xFFFFu, l.x), x0);
+              x1 = fmaf(P_MN ? f : colf1, f16_plus(add0[t] >> 16, l.y), x1);
             }
             if constexpr (OP == Op::Apply) {
               const uint32_t p = pack_f16x2(x0, x1);
-              const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&p));
               st0[t] = p;
-              st1[t] = pack_f16x2(x0 - g.x, x1 - g.y);
+              st1[t] = pack_f16x2(-f16_minus(p & 0xFFFFu, x0), -f16_minus(p >> 16, x1));
             } else if constexpr (OP == Op::ApplyOut) {
               st0[t] = __float_as_uint(x0 * args.out_scale);
               st1[t] = __float_as_uint(x1 * args.out_scale);
