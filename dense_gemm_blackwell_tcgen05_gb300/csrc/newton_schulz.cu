@@ -193,9 +193,9 @@ struct Layout {
 Layout layout_of(uint64_t batch, uint64_t rows, uint64_t cols) {
   Layout w;
   const uint64_t m = rows < cols ? rows : cols;
-  w.ldx = round_up(cols, 8);
+  w.ldx = round_up(cols, 64);   // rows on whole lines: no store leaves a part of a sector
   w.stride_x = rows * w.ldx;
-  w.ldp = round_up(m, 8);
+  w.ldp = round_up(m, 64);
   w.stride_p = m * w.ldp;
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes) {
