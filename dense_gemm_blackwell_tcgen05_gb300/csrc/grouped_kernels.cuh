@@ -843,13 +843,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
         // What the epilogue adds to a chunk is loaded a chunk ahead, the first
         // chunk's before the accumulator is waited for.
         //   Sym: row `col` of the symmetric R, whose 32 values from column
-        //     w.c0 + c0 on are the chunk's; the pitch is a multiple of 8, so a
-        //     16-byte piece that starts inside it ends inside it
+        //     w.c0 + c0 on are the chunk's (rows are whole lines of 64)
         //   Apply: X's halves at this lane's column pair, row 2 t + odd
-        const auto pitch_left = [&](uint32_t c0) {
-          const uint32_t p = static_cast<uint32_t>(args.ldo), c = w.c0 + c0;
-          return p > c ? p - c : 0u;
-        };
         const auto sym_at = [&](uint32_t c0) {
           return w.z * args.stride_o + static_cast<uint64_t>(col) * args.ldo + w.c0 + c0;
         };
@@ -859,12 +854,11 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
         const auto fetch = [&](uint32_t ch) {
           const uint32_t c0 = ch * 32;
           if constexpr (OP == Op::Sym) {
-            const uint32_t left = pitch_left(c0);
             const bool live = args.R != nullptr && ch < nch && col < args.L;
             const uint4* const r = reinterpret_cast<const uint4*>(args.R + sym_at(c0));
 #pragma unroll
             for (uint32_t p = 0; p < 4; ++p) {
-              const uint4 x = live && 8 * p < left ? r[p] : make_uint4(0, 0, 0, 0);
+              const uint4 x = live ? r[p] : make_uint4(0, 0, 0, 0);
               add0[4 * p] = x.x;
               add0[4 * p + 1] = x.y;
               add0[4 * p + 2] = x.z;
@@ -897,6 +891,9 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           if (pcol < args.L) colf0 = args.alpha + dg[pcol];
           if (pcol + 1 < args.L) colf1 = args.alpha + dg[pcol + 1];
         }
+        // a row's column pairs start on 4 bytes
+        const bool pairs = ((reinterpret_cast<uintptr_t>(args.out) & 3u) == 0) && (args.ldo & 1u) == 0 &&
+                           (args.stride_o & 1u) == 0;
         fetch(eg);
         if (!acc_wait()) break;
         const uint32_t b = j & 1u;
@@ -931,17 +928,29 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
                 }
             }
             if (w.mirror && col < args.L) {
-              // the values also belong to row `col`: 64 bytes a lane
-              const uint32_t left = pitch_left(c0);
-              uint4* const m = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.out) + sym_at(c0));
+              // the values also belong to row `col`: two sectors a lane
+              uint16_t* const m = static_cast<uint16_t*>(args.out) + sym_at(c0);
 #pragma unroll
-              for (uint32_t p = 0; p < 4; ++p) {
-                uint32_t h[4];
+              for (uint32_t p = 0; p < 2; ++p) {
+                uint32_t h[8];
 #pragma unroll
-                for (uint32_t t = 0; t < 4; ++t)
-                  h[t] = pack_f16x2(__uint_as_float(v[8 * p + 2 * t]), __uint_as_float(v[8 * p + 2 * t + 1]));
-                if (8 * p < left) m[p] = make_uint4(h[0], h[1], h[2], h[3]);
+                for (uint32_t t = 0; t < 8; ++t)
+                  h[t] = pack_f16x2(__uint_as_float(v[16 * p + 2 * t]), __uint_as_float(v[16 * p + 2 * t + 1]));
+                st_global_v8(m + 16 * p, h);
               }
+            }
+          }
+          if constexpr (OP == Op::Rows || OP == Op::Sum) {
+            if (!pairs) {
+              // rows that start on 2 bytes: this lane's column, row by row
+              uint16_t* p = static_cast<uint16_t*>(args.out) + out0 + static_cast<uint64_t>(c0) * args.ldo + col;
+#pragma unroll
+              for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo) {
+                const uint32_t h = pack_bf16x2(__uint_as_float(v[2 * t]), __uint_as_float(v[2 * t + 1]));
+                if (c0 + 2 * t < w.live && col < args.L) p[0] = static_cast<uint16_t>(h & 0xFFFFu);
+                if (c0 + 2 * t + 1 < w.live && col < args.L) p[args.ldo] = static_cast<uint16_t>(h >> 16);
+              }
+              continue;
             }
           }
           // this lane's column pair of row 2 t + odd: rounded in st0 (Apply: and the
@@ -1000,8 +1009,6 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
                 if (pcol + 1 < args.L) p[1] = __uint_as_float(st1[t]);
               }
           } else {
-            const bool vec = ((reinterpret_cast<uintptr_t>(args.out) & 3u) == 0) && (args.ldo & 1u) == 0 &&
-                             (args.stride_o & 1u) == 0;
             uint16_t* p = static_cast<uint16_t*>(args.out) + at + pcol;
             if (C::ADD) {
 #pragma unroll
@@ -1019,11 +1026,11 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
               for (uint32_t t = 0; t < 16; ++t)
                 st0[t] = pack_bf16x2(__uint_as_float(st0[t]), __uint_as_float(st1[t]));
             }
-            if (vec && lbase + 32 <= args.L && c0 + 32 <= w.live) {
+            if (pairs && lbase + 32 <= args.L && c0 + 32 <= w.live) {
               uint32_t* o = reinterpret_cast<uint32_t*>(p);
 #pragma unroll
               for (uint32_t t = 0; t < 16; ++t, o += args.ldo) *o = st0[t];
-            } else if (vec && lbase + 32 <= args.L) {
+            } else if (pairs && lbase + 32 <= args.L) {
 #pragma unroll
               for (uint32_t t = 0; t < 16; ++t, p += 2 * args.ldo)
                 if (2 * t < rows_left) *reinterpret_cast<uint32_t*>(p) = st0[t];
