@@ -256,17 +256,18 @@ int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const 
 
 // Time of a product, us: rounds of tiles over the CTAs or pairs that run at once,
 // each as long as its kt stages of 64 k or its epilogue, whichever is longer (the
-// shorter one is seen once).  Fitted to 1100 measured chains (110 sizes: 1 to 32
-// matrices, sides of 64 to 8192; 10 choices of the three products' tiles); choosing
-// each product's tiles by it is 0.1 % behind the best choice, the same tiles for
-// all three 1.1 %.
+// shorter one is seen once).  A stage is bound by its loads: 24, 32 and 32 KB into
+// each SM at 64 bytes a clock are 0.20, 0.27 and 0.27 us, and X and X' use the same
+// way.  Fitted to 1500 measured chains (101 sizes: 1 to 32 matrices, sides of 64 to
+// 8192; 14 choices of the three products' tiles): choosing each product's tiles by
+// it is 0.2 % behind the best choice, the same tiles for all three 1.1 %.
 struct TileCost {
   uint32_t lt, nt;                        // output columns and rows
   double stage, sym, apply, launch;
 };
-constexpr TileCost kNarrow = {128, 64, 0.30, 0.0, 2.4, 2.2};
-constexpr TileCost kWide = {128, 128, 0.41, 0.1, 4.1, 2.0};
-constexpr TileCost kPair = {256, 256, 0.47, 1.5, 6.7, 0.8};
+constexpr TileCost kNarrow = {128, 64, 0.26, 0.0, 2.3, 2.3};
+constexpr TileCost kWide = {128, 128, 0.31, 1.2, 3.9, 1.6};
+constexpr TileCost kPair = {256, 256, 0.42, 3.0, 6.5, 0.0};   // (less than the others' by this fit)
 
 double time_of(const TileCost& c, uint64_t tiles, uint32_t K, double epilogue, const LaunchCtx& ctx) {
   const uint64_t clusters = static_cast<uint64_t>(ctx.num_sms) * 128 / c.lt;
