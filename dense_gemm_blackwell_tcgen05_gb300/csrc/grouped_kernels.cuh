@@ -600,10 +600,10 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           };
           // Whole stages in a loop of their own, without a step's condition between two
           // MMAs.  A pair's MMAs of a stage take 512 clocks and the issuing thread nearly
-          // as long: unrolled, one group of 4096 x 4096 x 4096 takes 84 us to the weights
-          // instead of 92.  One CTA's narrower MMAs leave it time, and calls as short
+          // as long: unrolled, one group of 4096 x 4096 x 4096 takes 82 us to the weights
+          // instead of 92 (fp32: 98, 106).  One CTA's narrower MMAs leave it time, and calls as short
           // as those that use them wait for its instructions.
-          constexpr uint32_t kUnroll = CG == 2 && !OUT32 ? 4 : 1;
+          constexpr uint32_t kUnroll = CG == 2 ? 4 : 1;
           const uint32_t whole = C::TAIL && k_end == k_stop ? w.k_len / C::BK : k_end;
           uint32_t kt = k_begin;
 #pragma unroll kUnroll
