@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the GEMM runs in the CUDA library's
 own kernels.  The entry points keep the C names and arguments (raw device
 pointers as integers, sizes, leading dimensions in elements, a CUDA stream
-handle); ``matmul_bf16`` / ``matmul_mxfp8`` are conveniences that take torch
-CUDA tensors, call the same entry points on the current stream and raise on
+handle); ``matmul_bf16`` / ``matmul_mxfp8``, ``matmul_grouped`` with its two
+gradients and ``newton_schulz`` are conveniences that take torch CUDA
+tensors, call the same entry points on the current stream and raise on
 a non-zero status.  There is no CPU or library fallback: when the CUDA
 library cannot be built or loaded, every call raises.
 """

@@ -3,6 +3,10 @@
  *
  *     D[M,N] = A[M,K] * B[N,K]^T      fp32 accumulation, bf16 output
  *
+ * and of the products of a mixture of experts' training and serving: grouped
+ * (ragged) products with their gradients, and the Newton-Schulz products of
+ * the Muon optimiser.
+ *
  * The operation is the dense GEMM of b200-gemm-optimization-ladder ("E --
  * Executable steps", step 1: fix the math definition, layout and dtype; "A1 --
  * The nine-level route": data path GMEM -> SMEM -> tcgen05 -> TMEM ->
@@ -454,8 +458,8 @@ int gemm_set_edge_last(int enable);
 
 /* Test hook for the device watchdog (no counterpart on the pages: it exists to
  * exercise the failure path without faulting a GPU).  The calling thread's NEXT
- * persistent-kernel launch (gemm_bf16/gemm_mxfp8 variants 0-2) withholds the
- * operand loads of the given K-tile iteration in every CTA, so the consumers'
+ * persistent-kernel launch (gemm_bf16/gemm_mxfp8 variants 0-2, or a grouped
+ * product) withholds the operand loads of the given K-tile iteration in every CTA, so the consumers'
  * bounded waits run out: that launch then releases its TMEM, returns, leaves D
  * undefined, and gemm_last_status() reports GEMM_ERR_TIMEOUT.  Pair it with a
  * short gemm_set_watchdog_ms().  Returns GEMM_ERR_INVALID_ARG for a negative

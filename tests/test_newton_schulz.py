@@ -120,6 +120,20 @@ def test_other_coefficients():
     close(O, U @ V, tolerance(1, torch.float32))
 
 
+@pytest.mark.parametrize("batch, rows, cols", [(1, 33, 47), (3, 130, 70), (2, 257, 600), (1, 70, 2400), (1, 2401, 65)])
+def test_workspace_contents_do_not_matter(batch, rows, cols):
+    gen = torch.Generator("cuda").manual_seed(rows)
+    G = torch.randn(batch, rows, cols, device="cuda", generator=gen)
+    bits = []
+    for fill in (0, 0xFF, 0x7B):   # zeros, NaN, large numbers
+        ws = g.newton_schulz_workspace(batch, rows, cols)
+        ws.view(torch.uint8).fill_(fill)
+        bits.append(g.newton_schulz(G, out_dtype=torch.float32, workspace=ws))
+        assert g.gemm_last_status(stream()) == g.GEMM_OK
+    assert not bits[0].isnan().any()
+    assert torch.equal(bits[0], bits[1]) and torch.equal(bits[0], bits[2])
+
+
 def test_zero_and_nonfinite_matrices():
     gen = torch.Generator("cuda").manual_seed(3)
     G = torch.randn(5, 160, 96, device="cuda", generator=gen)
