@@ -12,6 +12,7 @@
 
 #include "gemm_gb300.h"
 #include "gemm_host.h"
+#include "grouped_host.h"
 #include "kernel_common.cuh"
 
 // The library's only device state: the watchdog status word (first error
@@ -308,6 +309,11 @@ bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
   slot.key = key;
   slot.map = *map;
   return true;
+}
+
+bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                   const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3]) {
+  return encode_map_3d(map, dtype, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,

@@ -134,18 +134,10 @@ bool edge_last_enabled();
 bool encode_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
                    uint64_t rows, uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_rows,
                    CUtensorMapSwizzle swizzle);
-// Encodes a 3-D tiled tensor map: extents dims[0..2]
+// Encodes a 3-D tiled tensor map without swizzle: extents dims[0..2]
 // (elements), strides of dimensions 1 and 2 in bytes, box extents box[0..2].
 bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
-                   const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3],
-                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
-
-// The current device's launch context with the watchdog limit for a
-// reduction of K set (a gemm_status_t), whether `p` is memory it can address,
-// and the calling thread's pending stall request (gemm_debug_stall_next_launch).
-int launch_context(int64_t K, LaunchCtx* ctx);
-bool device_pointer_ok(const void* p, const LaunchCtx& ctx);
-uint32_t take_stall_request();
+                   const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3]);
 
 // Kernel launchers; each returns a gemm_status_t value.
 int launch_bf16_ws(int cg, bool tma_store, const Problem& p, const LaunchCtx& ctx,

@@ -10,6 +10,18 @@
 
 namespace gb300 {
 
+// The current device's launch context with the watchdog limit for a
+// reduction of K set (a gemm_status_t), whether `p` is memory it can address,
+// and the calling thread's pending stall request (gemm_debug_stall_next_launch).
+int launch_context(int64_t K, LaunchCtx* ctx);
+bool device_pointer_ok(const void* p, const LaunchCtx& ctx);
+uint32_t take_stall_request();
+
+// encode_map_3d with the swizzle chosen.
+bool encode_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
+                   const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3],
+                   CUtensorMapSwizzle swizzle);
+
 // Rows of X sorted by group; W [groups, N, K] bf16.
 struct GroupedProblem {
   uint32_t M, N, K, groups;          // rows in all, the matrices' rows and columns, groups

@@ -46,8 +46,15 @@
 #include <type_traits>
 
 #include "gemm_kernels.cuh"
+#include "ptx_grouped.cuh"
 
 namespace gb300 {
+
+// Wait sites of the status word, after those that all kernels share.
+enum GroupedWaitSite : uint32_t {
+  kSiteTail = 11,           // tail warp waiting for a ragged reduction end
+  kSiteSplit = 12,          // epilogue waiting for the other CTAs' parts of a reduction
+};
 
 enum class Op { Rows, Sum, SumAdd, SumLane, SumLaneAdd, Sym, Apply, ApplyOut };
 

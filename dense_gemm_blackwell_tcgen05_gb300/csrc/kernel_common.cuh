@@ -23,8 +23,6 @@ enum WaitSite : uint32_t {
   kSiteSfFull = 8,          // scale-factor warp waiting for its scale bytes
   kSiteStreamKFlag = 9,     // stream-K owner waiting for a partial accumulator
   kSiteEpiC = 10,           // epilogue waiting for a TMA-loaded tile of C
-  kSiteTail = 11,           // tail warp waiting for a ragged reduction end
-  kSiteSplit = 12,          // epilogue waiting for the other CTAs' parts of a reduction
 };
 
 // Fused-epilogue mode word (0: the plain bf16 store of the accumulator).
