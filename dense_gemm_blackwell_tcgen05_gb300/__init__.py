@@ -616,6 +616,20 @@ def _check_3d(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _matrices(t, name):
+    """(batch, rows, cols, row pitch, matrix stride) of a matrix or a batch of them."""
+    if t.dim() == 2:
+        (rows, cols), (ld, unit) = t.shape, t.stride()
+        batch = stride = 1
+    elif t.dim() == 3:
+        (batch, rows, cols), (stride, ld, unit) = t.shape, t.stride()
+    else:
+        unit = 0
+    if unit != 1 or not t.is_cuda:
+        _check_3d(t if t.dim() == 3 else t.unsqueeze(0), name)
+    return batch, rows, cols, ld, stride
+
+
 def _refuse_grouped(rc, entry, x, x_name, B, B_name, offsets, groups, out):
     """Raises for what is wrong with a grouped product's tensors, else `rc`."""
     import torch
@@ -729,24 +743,19 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     newton_schulz_workspace) one is allocated for the call on torch's current
     stream."""
     import torch
-    batched = G if G.dim() == 3 else G.unsqueeze(0)
-    _check_3d(batched, "G")
+    batch, rows, cols, ldg, stride_g = _matrices(G, "G")
     if G.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("G must be bfloat16 or float32")
-    batch, rows, cols = batched.shape
     out = _output(out, G.shape, out_dtype, G.device, "out")
-    o = out if out.dim() == 3 else out.unsqueeze(0)
-    _check_3d(o, "out")
+    _, _, _, ldo, stride_o = _matrices(out, "out")
     a, b, c = coefficients
     if workspace is None:
         if stream is not None and stream != torch.cuda.current_stream():
             raise ValueError("a call on another stream needs its own workspace")
         workspace = newton_schulz_workspace(batch, rows, cols, G.device)
-    rc = gemm_newton_schulz(batched.data_ptr(), o.data_ptr(), batch, rows, cols, batched.stride(1),
-                            batched.stride(0), o.stride(1), o.stride(0), _out_code(G.dtype),
-                            _out_code(out.dtype), steps, a, b, c, eps, workspace.data_ptr(),
-                            workspace.numel() * workspace.element_size(),
-                            _raw_stream(stream, G.get_device()))
+    rc = gemm_newton_schulz(G.data_ptr(), out.data_ptr(), batch, rows, cols, ldg, stride_g, ldo, stride_o,
+                            _out_code(G.dtype), _out_code(out.dtype), steps, a, b, c, eps,
+                            workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, G.get_device()))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_newton_schulz")
     return out

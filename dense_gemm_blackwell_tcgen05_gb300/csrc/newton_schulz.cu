@@ -355,16 +355,20 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
       !operand_map(&polyP, poly, m, m, p.batch, w.ldp, w.stride_p, kP) ||
       !operand_map(&polyQ, poly, m, m, p.batch, w.ldp, w.stride_p, kQ))
     return GEMM_ERR_LAUNCH;
+  CUtensorMap byRows[2], byRowsQ[2], byCols[2];   // X, of either buffer, by its rows (as P, as Q) and by its columns
+  for (int i = 0; i < (p.steps > 1 ? 2 : 1); ++i) {
+    const void* const hi = ws + w.hi[i];
+    if ((!tall && !operand_map(&byRows[i], hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kP)) ||
+        !operand_map(&byRowsQ[i], hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kQ) ||
+        !operand_map(&byCols[i], hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kMN))
+      return GEMM_ERR_LAUNCH;
+  }
 
   for (int step = 0; step < p.steps; ++step) {
     const int cur = step & 1;
     const bool last = step + 1 == p.steps;
     __half* const hi = reinterpret_cast<__half*>(ws + w.hi[cur]);
-    CUtensorMap xK, xKq, xMN;   // X by its rows (as P, as Q) and by its columns
-    if (!operand_map(&xK, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kP) ||
-        !operand_map(&xKq, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kQ) ||
-        !operand_map(&xMN, hi, p.cols, p.rows, p.batch, w.ldx, w.stride_x, kMN))
-      return GEMM_ERR_LAUNCH;
+    const CUtensorMap &xK = byRows[cur], &xKq = byRowsQ[cur], &xMN = byCols[cur];
 
     GroupedArgs s = base;   // P = X X^T (or X^T X), the scale taken out
     s.L = s.C = m;
