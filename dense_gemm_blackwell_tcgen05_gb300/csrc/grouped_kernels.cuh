@@ -37,6 +37,15 @@
 // global memory: with l in the lanes, a warp's store covers 32 consecutive
 // elements of an output row and needs no staging.  Op::Sum adds a warp that
 // clears the operand rows of the next group at the end of a ragged reduction.
+//
+// What bounds it.  A stage of 64 k brings 32 KB into an SM, 512 clocks at 64 bytes
+// each; a pair's tile of 256 x 256 has MMAs of 512 clocks for it, one CTA's of 128 x
+// 128 of 256.  So large products run on pairs (32 groups of 4096 x 2048, 16384
+// rows: 177 us, 1.55 PFLOP/s at the power limit), few rows a group read the weights
+// and little else (64 groups of 2048 x 4096, 256 rows: 152 us, 7.1 TB/s), short
+// reductions write (79 groups of 1536 x 4096 in bf16, 427 rows: 166 us, 6.0 TB/s),
+// and Apply's X adds its traffic to the operands' (16 of 1024 x 2048: 64 us a
+// product, 36 without X).  Stores move whole sectors wherever the pitch allows it.
 #pragma once
 
 

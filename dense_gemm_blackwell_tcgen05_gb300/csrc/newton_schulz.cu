@@ -20,6 +20,10 @@
 // Relative error of five steps against 64 bits, random 256 x 256 / rank 8,
 // 512 x 1024: bf16 operands 1.0e-2 / 0.34, fp16 1.3e-3 / 4.2e-2, X as hi + lo
 // 1.6e-3 / 3.3e-4, and with the diagonal apart 8.6e-4 / 5.8e-4.
+//
+// Measured, five steps: 4096 x 4096 bf16 914 us (1.5 PFLOP/s, the power limit), 16 of
+// 1024 x 2048 fp32 662 us (X's traffic), 2053 x 1040 141 us and 256 x 256 59 us (the
+// latency of 15 dependent products and two launches before them).
 #include <cmath>
 
 #include "launch_grouped.cuh"
@@ -85,7 +89,8 @@ __device__ __forceinline__ float block_sum(float v, float* slots) {
 }
 
 // partials[z][block]: sum of squares of this block's share of matrix z.  One
-// warp takes a row segment of kSegment columns at a time.  A read of G.
+// warp takes a row segment of kSegment columns at a time.  A read of G: 16 of 1024
+// x 2048 fp32 in 22.5 us, 6.0 TB/s.
 template <class T>
 __global__ void __launch_bounds__(256) ns_square_sum_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
                                                             uint64_t stride_g, float* partials) {
@@ -142,7 +147,8 @@ __device__ __forceinline__ void load_pairs(const T* g, uint64_t ld, uint32_t row
 }
 
 // X = G * scale / (|G| + eps) as fp16 halves hi + lo, a 32 x 32 block at a time
-// with a lane's elements as lo_block has them.  A read of G, a write of X.
+// with a lane's elements as lo_block has them.  A read of G, a write of X: 16 of
+// 1024 x 2048 fp32 in 39 us, 6.9 TB/s.
 template <class T>
 __global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
                                                            uint64_t stride_g, const float* partials,
