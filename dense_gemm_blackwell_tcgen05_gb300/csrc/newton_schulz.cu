@@ -34,14 +34,19 @@ namespace {
 constexpr uint32_t kSegment = 1024;      // columns a warp takes at a time
 constexpr uint32_t kMaxPartials = 1024;  // partial sums per matrix
 
-// Sum of squares of a lane's share of columns col .. of a row segment: four
-// consecutive columns out of each 128.  QUADS: as one load (rows of whole
-// quadruples).  All loads come before the first use.
+// Sum of squares of a lane's share of columns col .. of a row segment, each times
+// `factor`: four consecutive columns out of each 128; and the largest magnitude seen.
+// QUADS: as one load (rows of whole quadruples).  All loads come before the first use.
 template <class T, bool QUADS>
-__device__ __forceinline__ float segment_square_sum(const T* row, uint32_t col, uint32_t cols) {
+__device__ __forceinline__ float segment_square_sum(const T* row, uint32_t col, uint32_t cols, float factor,
+                                                    float& top) {
   constexpr uint32_t kN = kSegment / 128;
   float sum = 0.0f;
-  const auto add = [&](float x, float y, float z, float w) { sum += x * x + y * y + (z * z + w * w); };
+  const auto add = [&](float x, float y, float z, float w) {
+    top = fmaxf(fmaxf(top, fmaxf(fabsf(x), fabsf(y))), fmaxf(fabsf(z), fabsf(w)));
+    x *= factor, y *= factor, z *= factor, w *= factor;
+    sum += x * x + y * y + (z * z + w * w);
+  };
   row += col;
   if constexpr (QUADS) {
     using P = std::conditional_t<sizeof(T) == 4, float4, uint2>;
@@ -88,12 +93,19 @@ __device__ __forceinline__ float block_sum(float v, float* slots) {
   return t;
 }
 
+// A sum of squares of any fp32 values: `sum` 2^(180 `range`), range -1, 0 or 1.  The
+// sum stays between 2^-80 and 2^100 (or is 0, Inf or NaN), far from where squares
+// and sums of 1024 such leave fp32.
+constexpr float kSumMost = 0x1p100f, kSumLeast = 0x1p-80f;
+__device__ __forceinline__ float range_factor(int range) { return range > 0 ? 0x1p-90f : range < 0 ? 0x1p90f : 1.0f; }
+
 // partials[z][block]: sum of squares of this block's share of matrix z.  One
-// warp takes a row segment of kSegment columns at a time.  A read of G: 16 of 1024
+// warp takes a row segment of kSegment columns at a time.  A share whose squares
+// leave the range is read once more with its values scaled.  A read of G: 16 of 1024
 // x 2048 fp32 in 22.5 us, 6.0 TB/s.
 template <class T>
 __global__ void __launch_bounds__(256) ns_square_sum_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
-                                                            uint64_t stride_g, float* partials) {
+                                                            uint64_t stride_g, float2* partials) {
   __shared__ float slots[8];
   grid_dependents_launch();
   const uint32_t lane = lane_idx();
@@ -101,16 +113,55 @@ __global__ void __launch_bounds__(256) ns_square_sum_kernel(const T* G, uint32_t
   const bool vec = (reinterpret_cast<uintptr_t>(g) & (4 * sizeof(T) - 1)) == 0 && ldg % 4 == 0 && cols % 4 == 0;
   const uint32_t segs = (cols + kSegment - 1) / kSegment;
   const uint64_t units = static_cast<uint64_t>(rows) * segs;
-  float sum = 0.0f;
-  for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
-    const uint64_t r = u / segs;
-    const uint32_t c0 = static_cast<uint32_t>(u - r * segs) * kSegment;
-    const T* const row = g + r * ldg;
-    sum += vec ? segment_square_sum<T, true>(row, c0 + lane * 4, cols)
-               : segment_square_sum<T, false>(row, c0 + lane * 4, cols);
+  float sum = 0.0f, top = 0.0f;
+  int range = 0;
+  for (;;) {   // (every thread of the block takes the same turns)
+    const float factor = range_factor(range);
+    sum = 0.0f;
+    for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
+      const uint64_t r = u / segs;
+      const uint32_t c0 = static_cast<uint32_t>(u - r * segs) * kSegment;
+      const T* const row = g + r * ldg;
+      sum += vec ? segment_square_sum<T, true>(row, c0 + lane * 4, cols, factor, top)
+                 : segment_square_sum<T, false>(row, c0 + lane * 4, cols, factor, top);
+    }
+    const bool any = __syncthreads_or(top > 0.0f) != 0;   // (also: the slots are free again)
+    sum = block_sum(sum, slots);
+    if (range != 0) break;
+    if (!(sum < kSumMost)) range = 1;
+    else if (any && sum < kSumLeast) range = -1;
+    else break;
   }
-  sum = block_sum(sum, slots);
-  if (threadIdx.x == 0) partials[blockIdx.y * kMaxPartials + blockIdx.x] = sum;
+  if (threadIdx.x == 0) partials[blockIdx.y * kMaxPartials + blockIdx.x] = make_float2(sum, static_cast<float>(range));
+}
+
+// The sum of a matrix's `count` partial sums; every thread of the block gets it.
+__device__ __forceinline__ float partial_sum(const float2* partials, uint32_t count, float* slots, int& range) {
+  constexpr uint32_t kN = kMaxPartials / 256;
+  float2 p[kN];
+  bool high = false, mid = false, low = false;
+#pragma unroll
+  for (uint32_t i = 0; i < kN; ++i) {
+    const uint32_t at = i * 256 + threadIdx.x;
+    p[i] = at < count ? partials[at] : make_float2(0.0f, 0.0f);
+    high |= p[i].y > 0.0f;
+    mid |= p[i].y == 0.0f && p[i].x > 0.0f;
+    low |= p[i].y < 0.0f;
+  }
+  range = 0;
+  if (__syncthreads_or(high || low)) {   // (rare: every partial to the largest one's range)
+    range = __syncthreads_or(high) ? 1 : __syncthreads_or(mid) ? 0 : -1;
+#pragma unroll
+    for (uint32_t i = 0; i < kN; ++i) {
+      const int below = range - static_cast<int>(p[i].y);   // 2^-180 for each range
+      if (below == 1) p[i].x = p[i].x * 0x1p-90f * 0x1p-90f;
+      if (below == 2) p[i].x = 0.0f;
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (uint32_t i = 0; i < kN; ++i) sum += p[i].x;
+  return block_sum(sum, slots);
 }
 
 // A lane's 16 pairs of elements of a block: columns col, col + 1 of every second
@@ -146,21 +197,39 @@ __device__ __forceinline__ void load_pairs(const T* g, uint64_t ld, uint32_t row
   }
 }
 
+// A factor that fp32 need not hold: mantissa 2^(e0 + e1).
+struct Factor {
+  float first, second;   // mantissa 2^e0, 2^e1
+  __device__ __forceinline__ float of(float x) const { return x * first * second; }
+};
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// scale / (|G| + eps), scale a power of two, |G| = root 2^(90 range): in 64 bits up
+// to its mantissa and exponent, as |G| of fp32 entries lies between 2^-149 and 2^144.
+__device__ __forceinline__ Factor normalising_factor(float root, int range, float scale, float eps) {
+  const double norm = static_cast<double>(root) * (range > 0 ? 0x1p90 : range < 0 ? 0x1p-90 : 1.0) + eps;
+  if (!(norm > 0.0) || isinf(norm)) return {scale / static_cast<float>(norm), 1.0f};   // Inf, NaN or 0
+  const int hi = __double2hiint(norm), e = (hi >> 20) - 1023;
+  const float mantissa = static_cast<float>(__hiloint2double(hi - e * (1 << 20), __double2loint(norm)));
+  const int e0 = -e / 2;
+  return {scale / mantissa * pow2(e0), pow2(-e - e0)};
+}
+
 // X = G * scale / (|G| + eps) as fp16 halves hi + lo, a 32 x 32 block at a time
 // with a lane's elements as lo_block has them.  A read of G, a write of X: 16 of
 // 1024 x 2048 fp32 in 39 us, 6.9 TB/s.
 template <class T>
 __global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
-                                                           uint64_t stride_g, const float* partials,
+                                                           uint64_t stride_g, const float2* partials,
                                                            uint32_t num_partials, float scale, float eps,
                                                            __half* hi, __half* lo, uint64_t ldx, uint64_t stride_x) {
   __shared__ float slots[8];
   grid_dependents_launch();
   grid_dependency_wait();
   const uint32_t lane = lane_idx();
-  float sum = 0.0f;
-  for (uint32_t i = threadIdx.x; i < num_partials; i += 256) sum += partials[blockIdx.y * kMaxPartials + i];
-  const float f = scale / (sqrtf(block_sum(sum, slots)) + eps);
+  int range;
+  const float root = sqrtf(partial_sum(partials + blockIdx.y * kMaxPartials, num_partials, slots, range));
+  const Factor f = normalising_factor(root, range, scale, eps);
   const T* const g = G + blockIdx.y * stride_g;
   const bool vec = (reinterpret_cast<uintptr_t>(g) & (2 * sizeof(T) - 1)) == 0 && ldg % 2 == 0;
   const uint32_t across = (cols + 31) / 32;
@@ -174,7 +243,7 @@ __global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t 
     uint32_t low[16];
 #pragma unroll
     for (uint32_t t = 0; t < 16; ++t) {
-      const float x = v[t].x * f, y = v[t].y * f;
+      const float x = f.of(v[t].x), y = f.of(v[t].y);
       const uint32_t h = pack_f16x2(x, y);
       const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&h));
       low[t] = pack_f16x2(x - got.x, y - got.y);
@@ -216,7 +285,7 @@ Layout layout_of(uint64_t batch, uint64_t rows, uint64_t cols) {
   w.gram = take(batch * w.stride_p * 2);
   w.poly = take(batch * w.stride_p * 2);
   w.diag = take(batch * m * 4);
-  w.partials = take(batch * kMaxPartials * 4);
+  w.partials = take(batch * kMaxPartials * sizeof(float2));
   w.bytes = at;
   return w;
 }
@@ -238,7 +307,7 @@ int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const 
     return b < most ? b : most;
   };
   const uint64_t blocks = blocks_of(static_cast<uint64_t>(p.rows) * ceil_div_u64(p.cols, kSegment));
-  float* const partials = reinterpret_cast<float*>(ws + w.partials);
+  float2* const partials = reinterpret_cast<float2*>(ws + w.partials);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), p.batch);
   cfg.blockDim = dim3(256);
@@ -254,7 +323,7 @@ int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const 
   cfg.numAttrs = 1;
   cfg.gridDim.x = static_cast<unsigned>(blocks_of(ceil_div_u64(p.rows, 32) * ceil_div_u64(p.cols, 32)));
   cudaLaunchKernelEx(&cfg, ns_normalise_kernel<T>, g, p.rows, p.cols, p.ldg, p.stride_g,
-                     static_cast<const float*>(partials), static_cast<uint32_t>(blocks), scale, p.eps,
+                     static_cast<const float2*>(partials), static_cast<uint32_t>(blocks), scale, p.eps,
                      reinterpret_cast<__half*>(ws + w.hi[0]), reinterpret_cast<__half*>(ws + w.lo[0]), w.ldx,
                      w.stride_x);
   return last_launch();

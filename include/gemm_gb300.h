@@ -376,8 +376,9 @@ int gemm_bf16_grouped_wgrad(const void* dD, const void* A, void* dB, const int32
  * elements (ignored for one matrix), any pitch, element alignment; in_dtype
  * and out_dtype GEMM_DTYPE_BF16 or GEMM_DTYPE_F32.  1 <= steps <= 64; a, b, c
  * finite; eps >= 0 finite.  The products run on the tensor cores with fp16
- * operands and fp32 sums, X between steps in two fp16 halves, the norm in
- * fp32: the result is within about 2e-3 of the 64-bit one (2-norm).  Steps
+ * operands and fp32 sums, X between steps in two fp16 halves, the norm from
+ * fp32 sums scaled so that no finite G overflows or vanishes: the result is
+ * within about 2e-3 of the 64-bit one (2-norm).  Steps
  * whose coefficients drive X far beyond singular values of a few units
  * overflow fp16.  A zero matrix gives zeros with eps > 0; a matrix with an Inf
  * or NaN gives NaN, the others of the batch are not affected.

@@ -194,3 +194,35 @@ def test_tensor_refusals():
         with pytest.raises(g.GemmError) as e:
             g.newton_schulz(G, **kw)
         assert e.value.status == g.GEMM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("rows, cols", [(96, 160), (300, 70), (64, 3000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [1e-39, 1e-37, 1e-30, 1e-23, 1e-19, 1e-13, 1e15, 1e19, 1e24, 4e37])
+def test_norms_whose_square_leaves_fp32(rows, cols, dtype, scale):
+    """The norm is taken of any finite values: their squares need not be fp32 numbers."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    G = (torch.randn(rows, cols, device="cuda", generator=gen).double() * scale).to(dtype)
+    assert G.isfinite().all() and (G != 0).any()
+    O = g.newton_schulz(G, eps=0.0, out_dtype=torch.float32)
+    assert g.gemm_last_status(stream()) == g.GEMM_OK
+    close(O, reference(G, eps=0.0), tolerance(5, torch.float32))
+
+
+def test_norms_of_mixed_magnitudes():
+    """Parts of one matrix whose squares lie in different ranges, and matrices
+    of a batch apart by 1e76; the default eps and none."""
+    gen = torch.Generator("cuda").manual_seed(6)
+    G = torch.randn(6, 130, 2100, device="cuda", generator=gen)
+    G[0, :100] *= 1e-30
+    G[1, 7:9] *= 1e25
+    G[2] *= 1e-37
+    G[2, 129] *= 1e17
+    G[3, 64:] *= 1e18
+    G[4] *= 1e38 / G[4].abs().max()
+    G[5] *= 1e-38
+    O = g.newton_schulz(G, eps=0.0, out_dtype=torch.float32)
+    assert g.gemm_last_status(stream()) == g.GEMM_OK
+    close(O, reference(G, eps=0.0), tolerance(5, torch.float32))
+    O = g.newton_schulz(G[:5], out_dtype=torch.float32)
+    close(O[[0, 1, 3, 4]], reference(G[[0, 1, 3, 4]]), tolerance(5, torch.float32))
