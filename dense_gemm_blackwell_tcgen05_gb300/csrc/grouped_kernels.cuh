@@ -84,6 +84,10 @@ struct GroupedArgs {
   uint32_t pdl;                // launched while its predecessor runs: wait for it before touching memory
   // Sym: out = alpha acc + beta R[l, c].   Apply: v = (alpha + diag) X + acc
   float alpha, beta;
+  // Sym, Apply: X is held times 2^now, now = max(lift[matrix] - spent, 0), X' times 2^next,
+  // from spent_next; P and, apart from the factor 2^(next - now) it brings to X', Y are not
+  const int32_t* lift;
+  int32_t spent, spent_next;
   float* diag;                 // [matrix][C]: written by Sym with R, read by Apply
   uint32_t diag_n;             // values of diag per matrix
   const __half* R;             // Sym: the symmetric matrix of the beta term (nullptr: none)
@@ -325,6 +329,9 @@ __device__ __forceinline__ uint32_t pair_columns_bf16(float v0, float v1, uint32
   const uint32_t got = __shfl_xor_sync(0xffffffffu, own, 1);
   return __byte_perm(own, got, odd ? 0x3276u : 0x5410u);
 }
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -878,6 +885,18 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
         const auto sym_at = [&](uint32_t c0) {
           return w.z * args.stride_o + static_cast<uint64_t>(col) * args.ldo + w.c0 + c0;
         };
+        // the arguments with this matrix's powers of two
+        float alpha = args.alpha, beta = args.beta, out_scale = args.out_scale;
+        if constexpr (OP == Op::Sym || C::APPLY) {
+          const int lift = args.lift[w.z], now = max(lift - args.spent, 0), next = max(lift - args.spent_next, 0);
+          if (OP == Op::Sym && args.R == nullptr) {
+            alpha = alpha * pow2(-now) * pow2(-now);
+          } else {
+            alpha *= pow2(next - now);
+            beta *= pow2(next - now);
+          }
+          out_scale *= pow2(-next);
+        }
         uint32_t add0[16], add1[16];         // Sym: R in add0; Apply: hi, lo
         float rowf = 0.0f;                   // Apply, Y X: this lane's row's alpha + diag
         const float* const dg = args.diag + static_cast<uint64_t>(w.z) * args.diag_n;
@@ -901,7 +920,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
             const uint4* l =
                 reinterpret_cast<const uint4*>(args.x_lo + lo_block(w.z, w.c0 + c0, lbase, args.C, args.L)) + lane;
             const uint32_t left = pcol < args.L && c0 + odd < w.live ? w.live - c0 - odd : 0u;
-            if (P_MN) rowf = c0 + lane < w.live ? args.alpha + dg[w.c0 + c0 + lane] : 0.0f;
+            if (P_MN) rowf = c0 + lane < w.live ? alpha + dg[w.c0 + c0 + lane] : 0.0f;
 #pragma unroll
             for (uint32_t t = 0; t < 16; ++t, h += args.ldx) add0[t] = 2 * t < left ? *h : 0u;
             // (the block's rows and columns past the matrix's are never stored as hi)
@@ -918,8 +937,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
         };
         float colf0 = 0.0f, colf1 = 0.0f;    // Apply, X Y: this lane's columns' alpha + diag
         if constexpr (C::APPLY && !P_MN) {
-          if (pcol < args.L) colf0 = args.alpha + dg[pcol];
-          if (pcol + 1 < args.L) colf1 = args.alpha + dg[pcol + 1];
+          if (pcol < args.L) colf0 = alpha + dg[pcol];
+          if (pcol + 1 < args.L) colf1 = alpha + dg[pcol + 1];
         }
         // a row's column pairs start on 4 bytes
         const bool pairs = ((reinterpret_cast<uintptr_t>(args.out) & 3u) == 0) && (args.ldo & 1u) == 0 &&
@@ -944,8 +963,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
 #pragma unroll
             for (uint32_t t = 0; t < 16; ++t) {
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&add0[t]));
-              v[2 * t] = __float_as_uint(fmaf(args.beta, f.x, args.alpha * __uint_as_float(v[2 * t])));
-              v[2 * t + 1] = __float_as_uint(fmaf(args.beta, f.y, args.alpha * __uint_as_float(v[2 * t + 1])));
+              v[2 * t] = __float_as_uint(fmaf(beta, f.x, alpha * __uint_as_float(v[2 * t])));
+              v[2 * t + 1] = __float_as_uint(fmaf(beta, f.y, alpha * __uint_as_float(v[2 * t + 1])));
             }
             fetch(ch + 2);
             if (args.R != nullptr && !w.mirror && col - w.c0 - c0 < 32u && col < args.L) {
@@ -1005,8 +1024,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
               st0[t] = p;
               st1[t] = pack_f16x2(-f16_minus(p & 0xFFFFu, x0), -f16_minus(p >> 16, x1));
             } else if constexpr (OP == Op::ApplyOut) {
-              st0[t] = __float_as_uint(x0 * args.out_scale);
-              st1[t] = __float_as_uint(x1 * args.out_scale);
+              st0[t] = __float_as_uint(x0 * out_scale);
+              st1[t] = __float_as_uint(x1 * out_scale);
             } else {
               // (SumAdd: unrounded)
               st0[t] = OP == Op::Sym ? pack_f16x2(x0, x1) : __float_as_uint(x0);

@@ -11,7 +11,10 @@
 //
 // Precision.  The operands are fp16: at the same rate as bf16 their rounding
 // is 8 times finer, and the range fits, because X is held scaled by a power of
-// two that brings its entries near 1 and P and Y have norms of a few units.
+// two that brings its entries near 1 and P and Y have norms of a few units.  A
+// matrix whose X starts far below 1 has a power of its own, which the steps use up
+// as they may have grown X (|G| = 1e-12 with eps = 1e-7, 1024 x 1024: without it
+// 5.8e-2 of the result are lost to fp16's smallest numbers).
 // X itself is held as hi + lo, two fp16 halves, and only the terms outside
 // the products see lo.  Directions with small singular values grow by a = 3.4
 // a step through a X, and so would its rounding errors.  Y's diagonal, about
@@ -202,34 +205,41 @@ struct Factor {
   float first, second;   // mantissa 2^e0, 2^e1
   __device__ __forceinline__ float of(float x) const { return x * first * second; }
 };
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-// scale / (|G| + eps), scale a power of two, |G| = root 2^(90 range): in 64 bits up
-// to its mantissa and exponent, as |G| of fp32 entries lies between 2^-149 and 2^144.
-__device__ __forceinline__ Factor normalising_factor(float root, int range, float scale, float eps) {
-  const double norm = static_cast<double>(root) * (range > 0 ? 0x1p90 : range < 0 ? 0x1p-90 : 1.0) + eps;
+// X is lifted by this many powers of two at most (X = 2^-120 is far below any result of use).
+constexpr int kMostLift = 120;
+
+// scale 2^lift / (|G| + eps), scale a power of two, |G| = root 2^(90 range): in 64 bits
+// up to its mantissa and exponent, as |G| of fp32 entries lies between 2^-149 and 2^144.
+// lift: the norm of X = G / (|G| + eps) is at most 2^-lift, and above a quarter of it.
+__device__ __forceinline__ Factor normalising_factor(float root, int range, float scale, float eps, int& lift) {
+  const double g = static_cast<double>(root) * (range > 0 ? 0x1p90 : range < 0 ? 0x1p-90 : 1.0), norm = g + eps;
+  lift = 0;
   if (!(norm > 0.0) || isinf(norm)) return {scale / static_cast<float>(norm), 1.0f};   // Inf, NaN or 0
   const int hi = __double2hiint(norm), e = (hi >> 20) - 1023;
+  if (g > 0.0) lift = min(max(e - ((__double2hiint(g) >> 20) - 1023) - 1, 0), kMostLift);
   const float mantissa = static_cast<float>(__hiloint2double(hi - e * (1 << 20), __double2loint(norm)));
-  const int e0 = -e / 2;
-  return {scale / mantissa * pow2(e0), pow2(-e - e0)};
+  const int e0 = (lift - e) / 2;
+  return {scale / mantissa * pow2(e0), pow2(lift - e - e0)};
 }
 
-// X = G * scale / (|G| + eps) as fp16 halves hi + lo, a 32 x 32 block at a time
+// X = G * scale * 2^lift / (|G| + eps) as fp16 halves hi + lo, a 32 x 32 block at a time
 // with a lane's elements as lo_block has them.  A read of G, a write of X: 16 of
 // 1024 x 2048 fp32 in 39 us, 6.9 TB/s.
 template <class T>
 __global__ void __launch_bounds__(256) ns_normalise_kernel(const T* G, uint32_t rows, uint32_t cols, uint64_t ldg,
                                                            uint64_t stride_g, const float2* partials,
                                                            uint32_t num_partials, float scale, float eps,
-                                                           __half* hi, __half* lo, uint64_t ldx, uint64_t stride_x) {
+                                                           __half* hi, __half* lo, uint64_t ldx, uint64_t stride_x,
+                                                           int32_t* lifts) {
   __shared__ float slots[8];
   grid_dependents_launch();
   grid_dependency_wait();
   const uint32_t lane = lane_idx();
-  int range;
+  int range, lift;
   const float root = sqrtf(partial_sum(partials + blockIdx.y * kMaxPartials, num_partials, slots, range));
-  const Factor f = normalising_factor(root, range, scale, eps);
+  const Factor f = normalising_factor(root, range, scale, eps, lift);
+  if (blockIdx.x == 0 && threadIdx.x == 0) lifts[blockIdx.y] = lift;
   const T* const g = G + blockIdx.y * stride_g;
   const bool vec = (reinterpret_cast<uintptr_t>(g) & (2 * sizeof(T) - 1)) == 0 && ldg % 2 == 0;
   const uint32_t across = (cols + 31) / 32;
@@ -262,7 +272,7 @@ uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 // Where the parts of the workspace start, in bytes.
 struct Layout {
   uint64_t ldx, stride_x, ldp, stride_p;   // elements
-  uint64_t hi[2], lo[2], gram, poly, diag, partials, bytes;
+  uint64_t hi[2], lo[2], gram, poly, diag, lift, partials, bytes;
 };
 
 Layout layout_of(uint64_t batch, uint64_t rows, uint64_t cols) {
@@ -285,6 +295,7 @@ Layout layout_of(uint64_t batch, uint64_t rows, uint64_t cols) {
   w.gram = take(batch * w.stride_p * 2);
   w.poly = take(batch * w.stride_p * 2);
   w.diag = take(batch * m * 4);
+  w.lift = take(batch * 4);
   w.partials = take(batch * kMaxPartials * sizeof(float2));
   w.bytes = at;
   return w;
@@ -325,7 +336,7 @@ int normalise(const NewtonSchulzProblem& p, const Layout& w, float scale, const 
   cudaLaunchKernelEx(&cfg, ns_normalise_kernel<T>, g, p.rows, p.cols, p.ldg, p.stride_g,
                      static_cast<const float2*>(partials), static_cast<uint32_t>(blocks), scale, p.eps,
                      reinterpret_cast<__half*>(ws + w.hi[0]), reinterpret_cast<__half*>(ws + w.lo[0]), w.ldx,
-                     w.stride_x);
+                     w.stride_x, reinterpret_cast<int32_t*>(ws + w.lift));
   return last_launch();
 }
 
@@ -401,6 +412,15 @@ int apply(const CUtensorMap& P, const CUtensorMap& Q, const GroupedArgs& a, cons
                        : launch_grouped<1, OP, MN, false, 64, false>(P, Q, a, tiles(kNarrow), ctx, stream);
 }
 
+// A step's p(s) = a s + b s^3 + c s^5 makes singular values s <= 1 at most this many
+// times larger: the largest |a + b u + c u^2| for u = s^2 <= 1 (1 if it is less).
+double largest_growth(double a, double b, double c) {
+  const auto at = [&](double u) { return std::fabs(a + b * u + c * u * u); };
+  double most = std::fmax(1.0, std::fmax(at(0.0), at(1.0)));
+  if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < 1.0) most = std::fmax(most, at(-b / (2.0 * c)));
+  return most;
+}
+
 int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const LaunchCtx& ctx, cudaStream_t stream) {
   uint8_t* const ws = static_cast<uint8_t*>(p.workspace);
   const bool tall = p.rows > p.cols;
@@ -416,6 +436,7 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
   base.stall_iter = 0xFFFFFFFFu;
   base.diag = reinterpret_cast<float*>(ws + w.diag);
   base.diag_n = m;
+  base.lift = reinterpret_cast<const int32_t*>(ws + w.lift);
 
   // Y as an operand: K-major P or Q; P as both operands of its square.  The boxes
   // are those of every tile size.
@@ -439,8 +460,18 @@ int iterate(const NewtonSchulzProblem& p, const Layout& w, float scale, const La
       return GEMM_ERR_LAUNCH;
   }
 
+  // Where |G| is far below eps (an idle expert's decayed momentum), X starts far below 1,
+  // where fp16 halves hold little: it is then held times 2^lift too.  Singular values up
+  // to 2^-lift can have grown to 2^(spent - lift) by a step, so that many powers remain.
+  const double growth = std::log2(largest_growth(p.a, p.b, p.c));
+  const auto spent = [&](int step) {
+    const double e = std::ceil(growth * step);
+    return e < kMostLift ? static_cast<int32_t>(e) : kMostLift;
+  };
   for (int step = 0; step < p.steps; ++step) {
     const int cur = step & 1;
+    base.spent = spent(step);
+    base.spent_next = spent(step + 1);
     const bool last = step + 1 == p.steps;
     __half* const hi = reinterpret_cast<__half*>(ws + w.hi[cur]);
     const CUtensorMap &xK = byRows[cur], &xKq = byRowsQ[cur], &xMN = byCols[cur];

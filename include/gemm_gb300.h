@@ -376,11 +376,13 @@ int gemm_bf16_grouped_wgrad(const void* dD, const void* A, void* dB, const int32
  * elements (ignored for one matrix), any pitch, element alignment; in_dtype
  * and out_dtype GEMM_DTYPE_BF16 or GEMM_DTYPE_F32.  1 <= steps <= 64; a, b, c
  * finite; eps >= 0 finite.  The products run on the tensor cores with fp16
- * operands and fp32 sums, X between steps in two fp16 halves, the norm from
- * fp32 sums scaled so that no finite G overflows or vanishes: the result is
- * within about 2e-3 of the 64-bit one (2-norm).  Steps
+ * operands and fp32 sums, X between steps in two fp16 halves times a power of
+ * two of each matrix's own, the norm from fp32 sums scaled so that no finite G
+ * overflows or vanishes: the result is within about 2e-3 of the 64-bit one
+ * (2-norm), also where |G| is far below eps (down to a quotient of 2^-120).  Steps
  * whose coefficients drive X far beyond singular values of a few units
- * overflow fp16.  A zero matrix gives zeros with eps > 0; a matrix with an Inf
+ * overflow fp16, and ones that shrink it far below 1e-3 lose its bits.  A zero
+ * matrix gives zeros with eps > 0; a matrix with an Inf
  * or NaN gives NaN, the others of the batch are not affected.
  * workspace: 256-byte aligned device memory of at least
  * gemm_newton_schulz_workspace_bytes(batch, rows, cols) bytes, uninitialised;

@@ -226,3 +226,41 @@ def test_norms_of_mixed_magnitudes():
     close(O, reference(G, eps=0.0), tolerance(5, torch.float32))
     O = g.newton_schulz(G[:5], out_dtype=torch.float32)
     close(O[[0, 1, 3, 4]], reference(G[[0, 1, 3, 4]]), tolerance(5, torch.float32))
+
+
+@pytest.mark.parametrize("rows, cols", [(256, 256), (300, 70), (64, 3000), (384, 1030)])
+@pytest.mark.parametrize("norm", [1e-9, 1e-11, 1e-12, 1e-14, 1e-20, 1e-36])
+@pytest.mark.parametrize("steps", [1, 5, 12])
+def test_norms_below_eps(rows, cols, norm, steps):
+    """X = G / (|G| + eps) far below 1, as an idle expert's decayed momentum gives.
+
+    As long as every step leaves |X| <= 2^-10 the products add less than 2^-17 of X,
+    whose rounding to 16 bits does not show: what is left is X's own.  With entries
+    of 1 / (8 sqrt m) or more times their power of two (m <= 384: 2^-7.3, and up to
+    2 times less while a step's growth is counted in whole powers), halves of quantum
+    2^-24 are off by 2^-25 at most: 2^-16 a step and for the first rounding."""
+    gen = torch.Generator("cuda").manual_seed(rows + steps)
+    G = torch.randn(rows, cols, device="cuda", generator=gen)
+    G *= norm / G.norm()
+    O = g.newton_schulz(G, steps=steps, out_dtype=torch.float32)
+    assert g.gemm_last_status(stream()) == g.GEMM_OK
+    small = norm / 1e-7 * 3.4445 ** steps <= 2.0 ** -10
+    close(O, reference(G, steps), (steps + 1) * 2.0 ** -16 if small else tolerance(steps, torch.float32))
+
+
+@pytest.mark.parametrize("rows, cols", [(200, 520), (520, 200), (1100, 1040)])
+def test_batch_of_norms_around_eps(rows, cols):
+    """Each matrix has its own power of two: nothing of one reaches another; the
+    cubic's steps, a larger eps, a bf16 result."""
+    gen = torch.Generator("cuda").manual_seed(8)
+    G = torch.randn(6, rows, cols, device="cuda", generator=gen)
+    norms = torch.tensor([1.0, 1e-8, 1e-12, 1e-16, 3e4, 0.0], device="cuda")
+    G *= (norms / G.square().sum((1, 2)).sqrt())[:, None, None]
+    for steps, coefficients, eps in ((5, g.NEWTON_SCHULZ_COEFFICIENTS, 1e-7), (14, (1.5, -0.5, 0.0), 1e-7),
+                                     (7, g.NEWTON_SCHULZ_COEFFICIENTS, 50.0)):
+        want = reference(G, steps, coefficients, eps)
+        for dtype in (torch.float32, torch.bfloat16):
+            O = g.newton_schulz(G, steps=steps, coefficients=coefficients, eps=eps, out_dtype=dtype)
+            assert g.gemm_last_status(stream()) == g.GEMM_OK
+            assert (O[5] == 0).all()
+            close(O[:5], want[:5], tolerance(steps, dtype))
