@@ -5,8 +5,9 @@ own kernels.  The entry points keep the C names and arguments (raw device
 pointers as integers, sizes, leading dimensions in elements, a CUDA stream
 handle); ``matmul_bf16`` / ``matmul_mxfp8``, ``matmul_grouped`` with its two
 gradients and ``newton_schulz`` are conveniences that take torch CUDA
-tensors, call the same entry points on the current stream and raise on
-a non-zero status.  There is no CPU or library fallback: when the CUDA
+tensors, call the same entry points on the current stream (or on ``stream``,
+which the caller orders with the tensors' other uses) and raise on a non-zero
+status.  There is no CPU or library fallback: when the CUDA
 library cannot be built or loaded, every call raises.
 """
 from __future__ import annotations
@@ -309,7 +310,7 @@ def matmul_fused(A, B, SFA=None, SFB=None, *, alpha=1.0, beta=0.0, C=None, bias=
         raise ValueError("A and B disagree on K")
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=A.device)
+        out = _new((M, N), out_dtype, A.device, stream)
     _check_2d(out, "out")
     if out.dtype != out_dtype:
         raise TypeError("out must have out_dtype")
@@ -452,6 +453,27 @@ def _stream_handle(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _new(shape, dtype, device, stream, zeroed=False):
+    """A tensor that a call on `stream` writes.  On another stream than torch's
+    current one it comes from that stream's memory: the current stream's could
+    still be in use by what is queued there.  Either may use the result, so its
+    memory is not given away before both are past its release."""
+    import torch
+    make = torch.zeros if zeroed else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    if stream.cuda_stream == current.cuda_stream:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(current)
+    return t
+
+
 def _check_2d(t, name):
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
@@ -472,7 +494,7 @@ def matmul_bf16(A, B, out=None, variant: int = VARIANT_AUTO, stream=None, worksp
     if B.shape[1] != K:
         raise ValueError("A and B disagree on K")
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
+        out = _new((M, N), torch.bfloat16, A.device, stream)
     _check_2d(out, "out")
     if workspace is None:
         rc = gemm_bf16_variant(variant, A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K,
@@ -502,7 +524,7 @@ def matmul_mxfp8(A, SFA, B, SFB, out=None, variant: int = VARIANT_AUTO, stream=N
     if B.shape[1] != K:
         raise ValueError("A and B disagree on K")
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
+        out = _new((M, N), torch.bfloat16, A.device, stream)
     _check_2d(out, "out")
     if workspace is None:
         rc = gemm_mxfp8_variant(variant, A.data_ptr(), B.data_ptr(), SFA.data_ptr(),
@@ -529,8 +551,8 @@ def quantize_mxfp8_tiled(X, stream=None):
         raise TypeError("X must be float32")
     rows, K = X.shape
     n = (rows + 127) // 128 * (((K + 31) // 32 + 3) // 4) * 512
-    Q = torch.empty(rows, K, dtype=torch.uint8, device=X.device)
-    SF = torch.empty(n, dtype=torch.uint8, device=X.device)
+    Q = _new((rows, K), torch.uint8, X.device, stream)
+    SF = _new((n,), torch.uint8, X.device, stream)
     rc = gemm_mxfp8_quantize_tiled(X.data_ptr(), rows, K, X.stride(0), Q.data_ptr(), Q.stride(0),
                                    SF.data_ptr(), _stream_handle(stream))
     if rc != GEMM_OK:
@@ -558,7 +580,7 @@ def matmul_mxfp8_tiled(A, SFA, B, SFB, out=None, variant: int = VARIANT_AUTO, st
         if t.numel() < (R + 127) // 128 * kt * 512:
             raise ValueError(f"{n} is smaller than the tiled layout of {R} rows")
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=A.device)
+        out = _new((M, N), torch.bfloat16, A.device, stream)
     _check_2d(out, "out")
     rc = gemm_mxfp8_tiled(variant, A.data_ptr(), B.data_ptr(), SFA.data_ptr(), SFB.data_ptr(),
                           out.data_ptr(), M, N, K, A.stride(0), B.stride(0), out.stride(0),
@@ -578,8 +600,8 @@ def quantize_mxfp8(X, stream=None):
         raise TypeError("X must be float32")
     rows, K = X.shape
     pitch = max(16, ((K + 31) // 32 + 15) // 16 * 16)
-    Q = torch.empty(rows, K, dtype=torch.uint8, device=X.device)
-    SF = torch.zeros(rows, pitch, dtype=torch.uint8, device=X.device)
+    Q = _new((rows, K), torch.uint8, X.device, stream)
+    SF = _new((rows, pitch), torch.uint8, X.device, stream, zeroed=True)
     rc = gemm_mxfp8_quantize(X.data_ptr(), rows, K, X.stride(0), Q.data_ptr(), Q.stride(0),
                              SF.data_ptr(), SF.stride(0), _stream_handle(stream))
     if rc != GEMM_OK:
@@ -646,14 +668,14 @@ def _refuse_grouped(rc, entry, x, x_name, B, B_name, offsets, groups, out):
     raise GemmError(rc, entry)
 
 
-def _output(out, shape, dtype, device, name):
+def _output(out, shape, dtype, device, stream):
     import torch
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+        return _new(shape, torch.bfloat16 if dtype is None else dtype, device, stream)
     if out.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
+        raise ValueError(f"out must have shape {tuple(shape)}")
     if dtype is not None and out.dtype != dtype:
-        raise TypeError(f"{name} must have out_dtype")
+        raise TypeError("out must have out_dtype")
     return out
 
 
@@ -663,7 +685,7 @@ def _grouped_rows(entry, x, x_name, B, offsets, dgrad, out, out_dtype, stream):
     groups, N, K = B.shape
     if reduced != (N if dgrad else K):
         raise ValueError(f"{x_name} and B disagree on {'N' if dgrad else 'K'}")
-    out = _output(out, (M, K if dgrad else N), out_dtype, x.device, "out")
+    out = _output(out, (M, K if dgrad else N), out_dtype, x.device, stream)
     ldx, x1 = x.stride()
     sb, ldb, b1 = B.stride()
     ldo, o1 = out.stride()
@@ -707,7 +729,7 @@ def matmul_grouped_wgrad(dD, A, offsets, out=None, out_dtype=None, accumulate=Fa
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     groups = max(0, offsets.numel() - 1)
-    out = _output(out, (groups, N, K), out_dtype, A.device, "out")
+    out = _output(out, (groups, N, K), out_dtype, A.device, stream)
     ldd, d1 = dD.stride()
     lda, a1 = A.stride()
     sb, ldb, o1 = out.stride()
@@ -746,7 +768,7 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     batch, rows, cols, ldg, stride_g = _matrices(G, "G")
     if G.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("G must be bfloat16 or float32")
-    out = _output(out, G.shape, out_dtype, G.device, "out")
+    out = _output(out, G.shape, out_dtype, G.device, stream)
     _, _, _, ldo, stride_o = _matrices(out, "out")
     a, b, c = coefficients
     if workspace is None:
