@@ -358,6 +358,32 @@ __device__ __forceinline__ uint64_t lo_block(uint64_t z, uint32_t row, uint32_t 
   return ((z * ((rows + 31) / 32) + row / 32) * ((cols + 31) / 32) + col / 32) * 1024;
 }
 
+// wait_bounded for a thread that does not itself wait for the kernel's predecessor:
+// the limit is for this kernel's loads, so when it runs out before the predecessor is
+// known to have ended (`alone`), the thread waits for that and starts it anew.
+// (Waiting for the predecessor beforehand makes every launch 0.1 to 0.2 us longer.)
+__device__ __forceinline__ bool wait_bounded_alone(uint32_t bar, uint32_t parity, const Watchdog& wd, uint32_t site,
+                                                   bool& alone) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = global_timer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 31u) == 0) {
+      if (*wd.abort_flag) return false;
+      if (global_timer_ns() - t0 > wd.timeout_ns) {
+        if (alone) {
+          *wd.abort_flag = 1u;
+          report_error(wd.status, kDevTimeout, site);
+          return false;
+        }
+        grid_dependency_wait();
+        alone = true;
+        t0 = global_timer_ns();
+      }
+    }
+  }
+}
+
 template <int CG, Op OP, bool P_MN, bool Q_MN, uint32_t NT, bool OUT32, uint32_t SPLIT = 1>
 __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLIT>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
@@ -583,6 +609,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
   } else if (warp == 1) {
     // ==================== MMA issuer: one thread of the leader CTA ==============
     if (leader && lane == 0) {
+      bool alone = !args.pdl;   // known: the predecessor has ended
       uint32_t it = 0, j = 0;
       bool ok = true, issued = false;
       TileItem w;
@@ -602,7 +629,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
           const auto stage = [&](uint32_t kt, uint32_t steps) {
             const uint32_t s = it % C::STAGES;
-            if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
+            if (!wait_bounded_alone(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull, alone)) {
               ok = false;
               return;
             }
