@@ -100,6 +100,9 @@ int launch_grouped(const CUtensorMap& tmP, const CUtensorMap& tmQ, const Grouped
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
+  const uint32_t all = static_cast<uint32_t>(tiles), part = (a.K + C::BK - 1) / C::BK;
+  note_schedule(cfg.gridDim.x / C::kCluster, C::kCluster, SPLIT > 1 ? 0u : all, SPLIT > 1 ? all : 0u,
+                SPLIT > 1 ? (part + SPLIT - 1) / SPLIT : 0u, 0u, 0u);
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmP, tmQ, a); e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();

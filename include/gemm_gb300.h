@@ -422,8 +422,11 @@ int gemm_last_cuda_error(void);
  * included), out[3] tiles split along K by the stream-K schedule, out[4]
  * K-tiles per stream-K unit, out[5] tiles of the last round cut into two
  * column halves (the tail split below), out[6] 1 when right-edge tiles were
- * dealt last (gemm_set_edge_last below).  `out` holds 7 values.  Returns
- * GEMM_OK, or GEMM_ERR_INVALID_ARG for NULL. */
+ * dealt last (gemm_set_edge_last below).  `out` holds 7 values.  A grouped
+ * product's tiles are the most that any offsets can give, as those are read on
+ * the GPU; ones whose reduction a cluster's CTAs share count as split, with the
+ * K-tiles that a CTA takes at most.  A Newton-Schulz call leaves its last
+ * product's schedule.  Returns GEMM_OK, or GEMM_ERR_INVALID_ARG for NULL. */
 int gemm_last_schedule(int64_t* out);
 
 /* Tail split of the data-parallel schedule (b200-gemm-optimization-ladder,

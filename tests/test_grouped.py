@@ -441,3 +441,46 @@ def test_tensor_refusals():
     host = torch.zeros(8, 24, dtype=torch.bfloat16)
     assert g.gemm_bf16_grouped(A.data_ptr(), B.data_ptr(), host.data_ptr(), o.data_ptr(), 2, 8, 24, 16, 16, 16,
                                24 * 16, 24, g.DTYPE_BF16, stream()) == g.GEMM_ERR_INVALID_ARG
+
+
+def ceil_div(a, b):
+    return -(-a // b)
+
+
+def schedule_of(tile_rows, tile_cols, rows, groups, cols):
+    """(CTAs per cluster, most tiles) of a product by rows with such tiles."""
+    blocks = min(rows, rows // tile_rows + min(rows, groups))
+    return 2 if tile_rows == 256 else 1, blocks * ceil_div(cols, tile_cols)
+
+
+def last_schedule():
+    s = g.gemm_last_schedule()
+    return s["ctas_per_cluster"], s["dp_tiles"]
+
+
+def test_last_schedule_is_the_grouped_launch():
+    """Not that of a dense call before it."""
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    g.matmul_bf16(z(1000, 64), z(1000, 64))
+    dense = g.gemm_last_schedule()
+    o = offsets_of([3, 0, 5])
+    g.matmul_grouped(z(8, 64), z(3, 300, 64), o)
+    got = g.gemm_last_schedule()
+    assert got != dense and got == {"clusters": 9, "ctas_per_cluster": 1, "dp_tiles": 9, "sk_tiles": 0, "sk_unit": 0,
+                                    "half_tiles": 0, "edge_last": 0}
+    assert last_schedule() == schedule_of(64, 128, 8, 3, 300)
+    g.matmul_grouped_wgrad(z(8, 304), z(8, 64), o)
+    assert last_schedule() == (1, 3 * 3 * 1)
+    # four CTAs share each of 9 reductions of 40 K-tiles
+    g.matmul_grouped(z(8, 2560), z(3, 300, 2560), o)
+    got = g.gemm_last_schedule()
+    assert (got["clusters"], got["ctas_per_cluster"], got["dp_tiles"], got["sk_tiles"], got["sk_unit"]) == (9, 4, 0, 9, 10)
+    # more tiles than run at once
+    o = offsets_of([6400])
+    g.matmul_grouped_dgrad(z(6400, 64), z(1, 64, 768), o)
+    got = g.gemm_last_schedule()
+    assert got["clusters"] * got["ctas_per_cluster"] <= sms < 2 * got["clusters"] * got["ctas_per_cluster"]
+    g.newton_schulz(torch.ones(300, 500, device="cuda"))
+    assert last_schedule() == (1, 5 * 4)      # the last product's 300 x 500 in tiles of 64 x 128
+    ok()
