@@ -36,9 +36,11 @@ int check_output(const void* p, int64_t cols, int64_t ld, int out_dtype) {
   return aligned(p, out_dtype == GEMM_DTYPE_F32 ? 4 : 2) ? GEMM_OK : GEMM_ERR_ALIGNMENT;
 }
 
-// The groups' matrices [groups, N, K].
+// The groups' matrices [groups, N, K]: stride >= N * ld, a product that 64 bits
+// need not hold.
 int check_stride(int64_t groups, int64_t N, int64_t ld, int64_t stride) {
-  return groups > 1 && (stride < N * ld || stride > kMaxStride) ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+  const bool bad = stride < 0 || stride > kMaxStride || (N > 0 && ld > stride / N);
+  return groups > 1 && bad ? GEMM_ERR_INVALID_ARG : GEMM_OK;
 }
 
 // Forward (dgrad = false): X = A [M, K], out = D [M, N]; else X = dD [M, N], out = dA [M, K].

@@ -82,3 +82,13 @@ def test_newton_schulz_workspace():
     f = g.gemm_newton_schulz_workspace_bytes
     assert f(1, 256, 256) >= 4 * 256 * 256 * 2 + 2 * 256 * 256 * 2
     assert f(-1, 4, 4) == INVALID and f(1, 65537, 4) == INVALID
+
+
+@pytest.mark.parametrize("rows, ld", [((1 << 31) - 1, 1 << 33), (1 << 30, 1 << 33), ((1 << 31) - 1, (1 << 36) - 8),
+                                      (1 << 28, 1 << 36)])
+def test_stride_shorter_than_a_product_past_64_bits(rows, ld):
+    """rows * pitch is compared as it is, not as what is left of it in 64 bits."""
+    wide = (rows + 7) // 8 * 8
+    for entry in (g.gemm_bf16_grouped, g.gemm_bf16_grouped_dgrad):
+        assert rows_call(entry, N=rows, ldx=wide, ldo=wide, ldb=ld, stride=1 << 38) == INVALID
+    assert wgrad_call(N=rows, ldd=wide, ldo=ld, stride=1 << 38) == INVALID
