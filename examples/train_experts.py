@@ -27,6 +27,7 @@ class Experts:
         gen = torch.Generator("cuda").manual_seed(seed)
         rand = lambda *s: torch.randn(*s, device="cuda", generator=gen)
         self.experts, self.top = experts, top
+        self.numbers = torch.arange(experts + 1, device="cuda")
         self.router = (rand(experts, width) / width ** 0.5).bfloat16()
         # fp32 masters, the bf16 copies that the products read, fp32 momenta
         self.masters = [rand(experts, hidden, width) / width ** 0.5, rand(experts, width, hidden) / hidden ** 0.5]
@@ -38,9 +39,9 @@ class Experts:
         """(rows' tokens, rows' weights, offsets): the chosen (token, expert) pairs sorted by expert."""
         weight, expert = torch.softmax(g.matmul_bf16(x, self.router).float(), -1).topk(self.top, -1)
         weight = weight / weight.sum(-1, keepdim=True)
-        order = expert.flatten().argsort(stable=True)
-        counts = torch.bincount(expert.flatten(), minlength=self.experts)
-        offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+        by_expert, order = expert.flatten().sort(stable=True)
+        # (bincount would read the largest expert's number back to the host)
+        offsets = torch.searchsorted(by_expert, self.numbers, out_int32=True)
         return order // self.top, weight.flatten()[order], offsets
 
     def forward(self, x):

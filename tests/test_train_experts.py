@@ -46,3 +46,27 @@ def test_training_reduces_the_loss():
     from train_experts import train
     losses = train(steps=40, tokens=2048)
     assert sum(losses[-5:]) < 0.5 * sum(losses[:5])
+
+
+def test_a_step_does_not_wait_for_the_gpu():
+    """Routing, products, gradients and updates with every read-back an error."""
+    from train_experts import Experts
+    layer = Experts(experts=6, width=64, hidden=128, top=2, seed=5)
+    gen = torch.Generator("cuda").manual_seed(6)
+    x = torch.randn(200, 64, device="cuda", generator=gen).bfloat16()
+
+    def step():
+        y, saved = layer.forward(x)
+        layer.backward(y, saved)
+        layer.update(0.01)
+        return saved[2]
+
+    offsets = step()   # (the library's first-call set-up)
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        again = step()
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    expert = torch.softmax(g.matmul_bf16(x, layer.router).float(), -1).topk(2, -1)[1].flatten()
+    want = [0] + torch.bincount(expert, minlength=6).cumsum(0).tolist()
+    assert offsets.tolist() == want and again.tolist() == want and offsets.dtype == torch.int32
