@@ -264,3 +264,27 @@ def test_batch_of_norms_around_eps(rows, cols):
             assert g.gemm_last_status(stream()) == g.GEMM_OK
             assert (O[5] == 0).all()
             close(O[:5], want[:5], tolerance(steps, dtype))
+
+
+@pytest.mark.parametrize("batch, rows, cols, ctas, nt, lt", [
+    (1, 2500, 2700, 2, 256, 256), (1, 2701, 2497, 2, 256, 256),    # every product on pairs, both orientations
+    (4, 1101, 1490, 2, 256, 256), (4, 1490, 1101, 2, 256, 256),
+    (12, 513, 770, 1, 128, 128), (8, 901, 700, 1, 128, 128),       # the symmetric ones on pairs
+    (2, 1301, 1504, 2, 256, 256), (2, 1504, 1301, 2, 256, 256),    # the symmetric ones in tiles of 128 x 128
+    (30, 900, 300, 1, 128, 128), (40, 200, 300, 1, 128, 128), (30, 300, 900, 1, 64, 128)])
+def test_large_tiles(batch, rows, cols, ctas, nt, lt):
+    """Sizes whose products take pairs and 128 x 128 tiles; the last product says so."""
+    gen = torch.Generator("cuda").manual_seed(rows)
+    G = torch.randn(batch, rows, cols, device="cuda", generator=gen)
+    want = reference(G)
+    for dtype, pad in ((torch.float32, 0), (torch.bfloat16, 1)):
+        flat = torch.full((batch * rows * (cols + pad),), float("nan"), dtype=dtype, device="cuda")
+        O = flat.view(batch, rows, cols + pad)[..., :cols]
+        g.newton_schulz(G, out=O)
+        assert g.gemm_last_status(stream()) == g.GEMM_OK
+        s = g.gemm_last_schedule()
+        assert (s["ctas_per_cluster"], s["dp_tiles"]) == (ctas, batch * -(-rows // nt) * -(-cols // lt))
+        close(O, want, tolerance(5, dtype))
+        assert torch.equal(O, g.newton_schulz(G, out_dtype=dtype))
+        O.fill_(float("nan"))
+        assert flat.isnan().all(), "wrote outside the output"
