@@ -209,16 +209,26 @@ struct Factor {
 // X is lifted by this many powers of two at most (X = 2^-120 is far below any result of use).
 constexpr int kMostLift = 120;
 
-// scale 2^lift / (|G| + eps), scale a power of two, |G| = root 2^(90 range): in 64 bits
-// up to its mantissa and exponent, as |G| of fp32 entries lies between 2^-149 and 2^144.
-// lift: the norm of X = G / (|G| + eps) is at most 2^-lift, and above a quarter of it.
+// The exponent of a positive normal number.
+__device__ __forceinline__ int exponent(float x) { return (__float_as_int(x) >> 23) - 127; }
+
+// scale 2^lift / (|G| + eps), scale a power of two, |G| = root 2^(90 range), which lies
+// between 2^-149 and 2^144: |G| + eps as mantissa 2^e.  (In 64-bit arithmetic this made the
+// kernel 12 % longer.)  lift: the norm of X = G / (|G| + eps) is at most 2^-lift, and
+// above a quarter of it.
 __device__ __forceinline__ Factor normalising_factor(float root, int range, float scale, float eps, int& lift) {
-  const double g = static_cast<double>(root) * (range > 0 ? 0x1p90 : range < 0 ? 0x1p-90 : 1.0), norm = g + eps;
   lift = 0;
-  if (!(norm > 0.0) || isinf(norm)) return {scale / static_cast<float>(norm), 1.0f};   // Inf, NaN or 0
-  const int hi = __double2hiint(norm), e = (hi >> 20) - 1023;
-  if (g > 0.0) lift = min(max(e - ((__double2hiint(g) >> 20) - 1023) - 1, 0), kMostLift);
-  const float mantissa = static_cast<float>(__hiloint2double(hi - e * (1 << 20), __double2loint(norm)));
+  if (root == 0.0f && eps > 0.0f) return {0.0f, 0.0f};   // (0 / eps)
+  int unit = 90 * range;
+  float norm = root + (range > 0 ? eps * 0x1p-90f : range < 0 ? eps * 0x1p90f : eps);   // times 2^unit
+  if (range < 0 && eps > 0x1p30f) {                       // (|G| is below 2^-39)
+    unit = 0;
+    norm = eps;
+  }
+  if (!(norm > 0.0f) || isinf(norm)) return {scale / norm, 1.0f};   // Inf, NaN or 0
+  const int e = exponent(norm) + unit;
+  lift = min(max(e - (exponent(root) + 90 * range) - 1, 0), kMostLift);
+  const float mantissa = __int_as_float((__float_as_int(norm) & 0x7FFFFF) | 0x3F800000);
   const int e0 = (lift - e) / 2;
   return {scale / mantissa * pow2(e0), pow2(lift - e - e0)};
 }
