@@ -394,7 +394,7 @@ def gemm_bf16_grouped_wgrad(dD: int, A: int, dB: int, offsets: int, groups: int,
                                           stride_b, out_dtype, accumulate, stream)
 
 
-# The quintic whose steps bring singular values of [0.003, 1] to about [0.7, 1.2] in five.
+# Muon's published quintic, whose steps bring singular values of [0.003, 1] to about [0.7, 1.2] in five.
 NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
 
@@ -706,7 +706,9 @@ def matmul_grouped(A, B, offsets, out=None, out_dtype=None, stream=None):
     """D[r] = A[r] @ B[e].T for the rows offsets[e] <= r < offsets[e + 1] of
     A [M,K] bf16, B [groups,N,K] bf16, offsets [groups+1] int32, all on the
     GPU; returns D [M,N] of out_dtype (bfloat16 or float32).  Rows that belong
-    to no group are not written."""
+    to no group are not written.  No autograd graph is recorded: the gradients
+    are matmul_grouped_dgrad and matmul_grouped_wgrad, whose dD needs a pitch
+    that is a multiple of 8 like every operand."""
     return _grouped_rows("gemm_bf16_grouped", A, "A", B, offsets, False, out, out_dtype, stream)
 
 

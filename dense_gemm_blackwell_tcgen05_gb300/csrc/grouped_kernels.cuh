@@ -41,7 +41,7 @@
 // What bounds it.  A stage of 64 k brings 32 KB into an SM, 512 clocks at 64 bytes
 // each; a pair's tile of 256 x 256 has MMAs of 512 clocks for it, one CTA's of 128 x
 // 128 of 256.  So large products run on pairs (32 groups of 4096 x 2048, 16384
-// rows: 177 us, 1.55 PFLOP/s at the power limit), few rows a group read the weights
+// rows: 175 us, 1.57 PFLOP/s at the power limit), few rows a group read the weights
 // and little else (64 groups of 2048 x 4096, 256 rows: 152 us, 7.1 TB/s), short
 // reductions write (79 groups of 1536 x 4096 in bf16, 427 rows: 166 us, 6.0 TB/s),
 // and Apply's X adds its traffic to the operands' (16 of 1024 x 2048: 64 us a
@@ -832,6 +832,8 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
           } else if (col < args.L) {
 #pragma unroll
             for (uint32_t t = 0; t < 32; ++t, p += args.ldo)
+              // (ADD: one row at a time, as a store may alias the next load: 16 groups of 4096 x
+              // 2048, 8192 rows, in 1591 us where overwriting takes 139)
               if (c0 + t < w.live) *p = C::ADD ? *p + acc[i][t] : acc[i][t];
           }
         }

@@ -24,8 +24,8 @@
 // 512 x 1024: bf16 operands 1.0e-2 / 0.34, fp16 1.3e-3 / 4.2e-2, X as hi + lo
 // 1.6e-3 / 3.3e-4, and with the diagonal apart 8.6e-4 / 5.8e-4.
 //
-// Measured, five steps: 4096 x 4096 bf16 914 us (1.5 PFLOP/s, the power limit), 16 of
-// 1024 x 2048 fp32 662 us (X's traffic), 2053 x 1040 141 us and 256 x 256 59 us (the
+// Measured, five steps: 4096 x 4096 bf16 925 us (1.5 PFLOP/s, the power limit), 16 of
+// 1024 x 2048 fp32 667 us (X's traffic), 2053 x 1040 142 us and 256 x 256 60 us (the
 // latency of 15 dependent products and two launches before them).
 #include <cmath>
 
