@@ -4,8 +4,8 @@ Argument marshalling only: every step of the GEMM runs in the CUDA library's
 own kernels.  The entry points keep the C names and arguments (raw device
 pointers as integers, sizes, leading dimensions in elements, a CUDA stream
 handle); ``matmul_bf16`` / ``matmul_mxfp8``, ``matmul_grouped`` with its two
-gradients and ``newton_schulz`` are conveniences that take torch CUDA
-tensors, call the same entry points on the current stream (or on ``stream``,
+gradients, ``newton_schulz``, ``matmul_cross_entropy`` and ``matmul_distill``
+with their gradients are conveniences that take torch CUDA tensors, call the same entry points on the current stream (or on ``stream``,
 which the caller orders with the tensors' other uses) and raise on a non-zero
 status.  There is no CPU or library fallback: when the CUDA
 library cannot be built or loaded, every call raises.
@@ -37,6 +37,10 @@ __all__ = [
     "gemm_bf16_grouped_wgrad", "matmul_grouped", "matmul_grouped_dgrad", "matmul_grouped_wgrad",
     "NEWTON_SCHULZ_COEFFICIENTS", "gemm_newton_schulz", "gemm_newton_schulz_workspace_bytes",
     "newton_schulz", "newton_schulz_workspace",
+    "INDEX_I32", "INDEX_I64", "MAX_TOP", "gemm_bf16_cross_entropy", "gemm_bf16_cross_entropy_grad",
+    "gemm_bf16_cross_entropy_workspace_bytes", "gemm_bf16_distill", "gemm_bf16_distill_grad",
+    "gemm_bf16_distill_workspace_bytes", "matmul_cross_entropy", "matmul_cross_entropy_grad",
+    "cross_entropy_workspace", "matmul_distill", "matmul_distill_grad", "distill_workspace",
 ]
 
 GEMM_OK = 0
@@ -66,6 +70,9 @@ EXPORTED_SYMBOLS = (
     "gemm_mxfp8_quantize_tiled", "gemm_set_tail_split", "gemm_tail_split_plan",
     "gemm_set_edge_last", "gemm_bf16_grouped", "gemm_bf16_grouped_dgrad", "gemm_bf16_grouped_wgrad",
     "gemm_newton_schulz", "gemm_newton_schulz_workspace_bytes",
+    "gemm_bf16_cross_entropy", "gemm_bf16_cross_entropy_grad",
+    "gemm_bf16_cross_entropy_workspace_bytes", "gemm_bf16_distill", "gemm_bf16_distill_grad",
+    "gemm_bf16_distill_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -165,6 +172,20 @@ def load() -> ctypes.CDLL:
             L.gemm_newton_schulz.argtypes = [_vp, _vp, *[_i64] * 7, *[ctypes.c_int] * 3,
                                              *[ctypes.c_float] * 4, _vp, _i64, _vp]
             L.gemm_newton_schulz.restype = ctypes.c_int
+            i, f = ctypes.c_int, ctypes.c_float
+            L.gemm_bf16_cross_entropy_workspace_bytes.argtypes = [_i64, _i64, _i64, i]
+            L.gemm_bf16_cross_entropy_workspace_bytes.restype = _i64
+            L.gemm_bf16_cross_entropy.argtypes = [*[_vp] * 5, *[_i64] * 5, i, f, f, f, _vp, _i64, _vp]
+            L.gemm_bf16_cross_entropy_grad.argtypes = [*[_vp] * 7, *[_i64] * 8, i, i, i, f, f, f, i,
+                                                       _vp, _i64, _vp]
+            L.gemm_bf16_distill_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64, i]
+            L.gemm_bf16_distill_workspace_bytes.restype = _i64
+            L.gemm_bf16_distill.argtypes = [*[_vp] * 6, *[_i64] * 8, i, i, f, _vp, _i64, _vp]
+            L.gemm_bf16_distill_grad.argtypes = [*[_vp] * 8, *[_i64] * 11, i, i, i, i, f, i, _vp, _i64,
+                                                 _vp]
+            for name in ("gemm_bf16_cross_entropy", "gemm_bf16_cross_entropy_grad",
+                         "gemm_bf16_distill", "gemm_bf16_distill_grad"):
+                getattr(L, name).restype = i
             L.gemm_last_status.argtypes = [_vp]
             L.gemm_last_status.restype = ctypes.c_int
             L.gemm_last_status_word.argtypes = [_vp]
@@ -409,6 +430,59 @@ def gemm_newton_schulz(G: int, O: int, batch: int, rows: int, cols: int, ldg: in
     return load().gemm_newton_schulz(G, O, batch, rows, cols, ldg, stride_g, ldo, stride_o,
                                      in_dtype, out_dtype, steps, a, b, c, eps, workspace,
                                      workspace_bytes, stream)
+
+
+INDEX_I32, INDEX_I64 = 0, 1
+MAX_TOP = 1024
+
+
+def gemm_bf16_cross_entropy_workspace_bytes(M: int, N: int, K: int, grad: int) -> int:
+    return int(load().gemm_bf16_cross_entropy_workspace_bytes(M, N, K, grad))
+
+
+def gemm_bf16_cross_entropy(A: int, B: int, targets: int, loss: int, lse: int, M: int, N: int, K: int,
+                            lda: int, ldb: int, target_dtype: int, scale: float, smoothing: float,
+                            z_loss: float, workspace: int, workspace_bytes: int,
+                            stream: int = 0) -> int:
+    return load().gemm_bf16_cross_entropy(A, B, targets, loss, lse, M, N, K, lda, ldb, target_dtype,
+                                          scale, smoothing, z_loss, workspace, workspace_bytes, stream)
+
+
+def gemm_bf16_cross_entropy_grad(dloss: int, A: int, B: int, targets: int, lse: int, dA: int, dB: int,
+                                 M: int, N: int, K: int, inc_dloss: int, lda: int, ldb: int,
+                                 ld_da: int, ld_db: int, target_dtype: int, da_dtype: int,
+                                 db_dtype: int, scale: float, smoothing: float, z_loss: float,
+                                 accumulate: int, workspace: int, workspace_bytes: int,
+                                 stream: int = 0) -> int:
+    return load().gemm_bf16_cross_entropy_grad(dloss, A, B, targets, lse, dA, dB, M, N, K, inc_dloss,
+                                               lda, ldb, ld_da, ld_db, target_dtype, da_dtype,
+                                               db_dtype, scale, smoothing, z_loss, accumulate,
+                                               workspace, workspace_bytes, stream)
+
+
+def gemm_bf16_distill_workspace_bytes(M: int, N: int, K: int, top: int, grad: int) -> int:
+    return int(load().gemm_bf16_distill_workspace_bytes(M, N, K, top, grad))
+
+
+def gemm_bf16_distill(A: int, B: int, teacher: int, ids: int, loss: int, lse: int, M: int, N: int,
+                      K: int, top: int, lda: int, ldb: int, ld_teacher: int, ld_ids: int,
+                      teacher_dtype: int, id_dtype: int, temperature: float, workspace: int,
+                      workspace_bytes: int, stream: int = 0) -> int:
+    return load().gemm_bf16_distill(A, B, teacher, ids, loss, lse, M, N, K, top, lda, ldb, ld_teacher,
+                                    ld_ids, teacher_dtype, id_dtype, temperature, workspace,
+                                    workspace_bytes, stream)
+
+
+def gemm_bf16_distill_grad(dloss: int, A: int, B: int, teacher: int, ids: int, lse: int, dA: int,
+                           dB: int, M: int, N: int, K: int, top: int, inc_dloss: int, lda: int,
+                           ldb: int, ld_teacher: int, ld_ids: int, ld_da: int, ld_db: int,
+                           teacher_dtype: int, id_dtype: int, da_dtype: int, db_dtype: int,
+                           temperature: float, accumulate: int, workspace: int,
+                           workspace_bytes: int, stream: int = 0) -> int:
+    return load().gemm_bf16_distill_grad(dloss, A, B, teacher, ids, lse, dA, dB, M, N, K, top,
+                                         inc_dloss, lda, ldb, ld_teacher, ld_ids, ld_da, ld_db,
+                                         teacher_dtype, id_dtype, da_dtype, db_dtype, temperature,
+                                         accumulate, workspace, workspace_bytes, stream)
 
 
 def gemm_last_status(stream: int = 0) -> int:
@@ -783,3 +857,201 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_newton_schulz")
     return out
+
+
+# -------------------------------------------------- losses over a vocabulary
+
+def _index_code(dtype):
+    import torch
+    if dtype is torch.int64:
+        return INDEX_I64
+    if dtype is torch.int32:
+        return INDEX_I32
+    raise TypeError("targets and ids must be int32 or int64")
+
+
+def _vocabulary(A, B):
+    """(M, N, K, lda, ldb) of the rows and the vocabulary's matrix."""
+    import torch
+    _check_2d(A, "A")
+    _check_2d(B, "B")
+    if A.dtype is not torch.bfloat16 or B.dtype is not torch.bfloat16:
+        raise TypeError("A and B must be bfloat16")
+    M, K = A.shape
+    N, KB = B.shape
+    if KB != K:
+        raise ValueError("A and B disagree on K")
+    return M, N, K, A.stride(0), B.stride(0)
+
+
+def _row_values(t, name, M, dtype=None, strided=False):
+    """Checks a value per row: 1-D of M, contiguous unless `strided`."""
+    if t.dim() != 1 or t.shape[0] != M:
+        raise ValueError(f"{name} must be a 1-D tensor with a value for each of the {M} rows")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    if not strided and M > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _entries(teacher, ids, M):
+    """(top, pitches, type codes) of a teacher's lists."""
+    _check_2d(teacher, "teacher")
+    _check_2d(ids, "ids")
+    if teacher.shape != ids.shape or teacher.shape[0] != M:
+        raise ValueError(f"teacher and ids must both have shape ({M}, top)")
+    return teacher.shape[1], teacher.stride(0), ids.stride(0), _out_code(teacher.dtype), _index_code(ids.dtype)
+
+
+def _loss_workspace(entry, sizes, grad, device):
+    import torch
+    n = getattr(load(), entry)(*sizes, 1 if grad else 0)
+    if n < 0:
+        raise GemmError(n, entry)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def cross_entropy_workspace(M: int, N: int, K: int, grad: bool = False, device=None):
+    """A workspace for matmul_cross_entropy (grad: for its gradient) on M rows
+    of width K and a vocabulary of N (one per stream: calls sharing a workspace
+    must not overlap on the GPU)."""
+    return _loss_workspace("gemm_bf16_cross_entropy_workspace_bytes", (M, N, K), grad, device)
+
+
+def distill_workspace(M: int, N: int, K: int, top: int, grad: bool = False, device=None):
+    """The same for matmul_distill with lists of `top` entries."""
+    return _loss_workspace("gemm_bf16_distill_workspace_bytes", (M, N, K, top), grad, device)
+
+
+def _workspace_for(workspace, make, sizes, grad, device, stream):
+    import torch
+    if workspace is None:
+        if stream is not None and stream != torch.cuda.current_stream():
+            raise ValueError("a call on another stream needs its own workspace")
+        return make(*sizes, grad, device)
+    return workspace
+
+
+def _loss_outputs(M, out, device, stream):
+    import torch
+    if out is None:
+        return tuple(_new((M,), torch.float32, device, stream) for _ in range(2))
+    loss, lse = out
+    for t, name in ((loss, "out[0]"), (lse, "out[1]")):
+        _row_values(t, name, M, torch.float32)
+    return loss, lse
+
+
+def _gradient_outputs(A, B, dA, dB, need_dA, need_dB, out_dtype, accumulate, stream):
+    """(dA, dB), None where not wanted, and what the entry points take of them."""
+    if accumulate and dB is None:
+        raise ValueError("accumulate needs dB")
+    dA = _output(dA, A.shape, None if dA is not None else out_dtype, A.device, stream) if need_dA or dA is not None else None
+    dB = _output(dB, B.shape, None if dB is not None else out_dtype, B.device, stream) if need_dB or dB is not None else None
+    of = []
+    for t, name in ((dA, "dA"), (dB, "dB")):
+        if t is None:
+            of.append((0, 0, DTYPE_BF16))
+            continue
+        _check_2d(t, name)
+        of.append((t.data_ptr(), t.stride(0), _out_code(t.dtype)))
+    return dA, dB, of
+
+
+def matmul_cross_entropy(A, B, targets, scale: float = 1.0, label_smoothing: float = 0.0, z_loss: float = 0.0,
+                         out=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits z = scale * A @ B.T, which are never
+    stored: A [M,K] and B [N,K] bf16, targets [M] int32 or int64; returns (loss
+    [M], lse [M]), both float32 (into out=(loss, lse) if given), with
+        loss = lse - (1 - label_smoothing) z[target] - label_smoothing mean(z) + z_loss lse**2.
+    Rows with a negative target are left out: their loss and lse are 0.  A
+    target of N or more makes its row's loss NaN.  No autograd graph is
+    recorded: the gradients are matmul_cross_entropy_grad.  Without `workspace`
+    (from cross_entropy_workspace) one is allocated for the call on torch's
+    current stream."""
+    M, N, K, lda, ldb = _vocabulary(A, B)
+    _row_values(targets, "targets", M)
+    code = _index_code(targets.dtype)
+    loss, lse = _loss_outputs(M, out, A.device, stream)
+    ws = _workspace_for(workspace, cross_entropy_workspace, (M, N, K), False, A.device, stream)
+    rc = (_lib or load()).gemm_bf16_cross_entropy(
+        A.data_ptr(), B.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, lda, ldb, code, scale,
+        label_smoothing, z_loss, ws.data_ptr(), ws.nbytes, _raw_stream(stream, A.get_device()))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_cross_entropy")
+    return loss, lse
+
+
+def matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale: float = 1.0, label_smoothing: float = 0.0,
+                              z_loss: float = 0.0, dA=None, dB=None, need_dA: bool = True, need_dB: bool = True,
+                              out_dtype=None, accumulate: bool = False, workspace=None, stream=None):
+    """The gradients of matmul_cross_entropy to A and B, from the losses' own,
+    dloss [M] float32 (any stride, an expanded one too), and the lse that it
+    returned; returns (dA [M,K], dB [N,K]), into dA and dB if given (bfloat16 or
+    float32 each), else of out_dtype; None for one that is neither given nor
+    needed.  With accumulate, adds to dB.  Rows left out get zeros in dA and add
+    nothing to dB, whatever A holds there."""
+    import torch
+    M, N, K, lda, ldb = _vocabulary(A, B)
+    _row_values(targets, "targets", M)
+    _row_values(dloss, "dloss", M, torch.float32, strided=True)
+    _row_values(lse, "lse", M, torch.float32)
+    code = _index_code(targets.dtype)
+    dA, dB, ((pa, ld_da, ca), (pb, ld_db, cb)) = _gradient_outputs(A, B, dA, dB, need_dA, need_dB, out_dtype, accumulate,
+                                                                   stream)
+    ws = _workspace_for(workspace, cross_entropy_workspace, (M, N, K), True, A.device, stream)
+    rc = (_lib or load()).gemm_bf16_cross_entropy_grad(
+        dloss.data_ptr(), A.data_ptr(), B.data_ptr(), targets.data_ptr(), lse.data_ptr(), pa, pb, M, N, K, dloss.stride(0),
+        lda, ldb, ld_da, ld_db, code, ca, cb, scale, label_smoothing, z_loss, 1 if accumulate else 0, ws.data_ptr(),
+        ws.nbytes, _raw_stream(stream, A.get_device()))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_cross_entropy_grad")
+    return dA, dB
+
+
+def matmul_distill(A, B, teacher, ids, temperature: float = 1.0, out=None, workspace=None, stream=None):
+    """Distillation from a teacher's top logits: teacher [M,top] (bfloat16 or
+    float32) are its logits of the tokens ids [M,top] (int32 or int64, any
+    order), p = softmax(teacher / temperature) over a row's entries; the
+    student's logits z = A @ B.T / temperature, A [M,K] and B [N,K] bf16, are
+    never stored; returns (loss [M], lse [M]), both float32 (into out=(loss,
+    lse) if given), with loss = sum_j p_j (log p_j - z[ids_j] + lse).  Entries
+    with a negative id or a logit of -inf are not there; rows without any are
+    left out: their loss and lse are 0.  An id of N or more makes its row's loss
+    NaN.  No autograd graph is recorded: the gradients are matmul_distill_grad.
+    Without `workspace` (from distill_workspace) one is allocated for the call
+    on torch's current stream."""
+    M, N, K, lda, ldb = _vocabulary(A, B)
+    top, ldt, ldi, ct, ci = _entries(teacher, ids, M)
+    loss, lse = _loss_outputs(M, out, A.device, stream)
+    ws = _workspace_for(workspace, distill_workspace, (M, N, K, top), False, A.device, stream)
+    rc = (_lib or load()).gemm_bf16_distill(
+        A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, top, lda,
+        ldb, ldt, ldi, ct, ci, temperature, ws.data_ptr(), ws.nbytes, _raw_stream(stream, A.get_device()))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_distill")
+    return loss, lse
+
+
+def matmul_distill_grad(dloss, A, B, teacher, ids, lse, temperature: float = 1.0, dA=None, dB=None, need_dA: bool = True,
+                        need_dB: bool = True, out_dtype=None, accumulate: bool = False, workspace=None, stream=None):
+    """The gradients of matmul_distill to A and B (not to the teacher), from the
+    losses' own, dloss [M] float32, and the lse that it returned; arguments and
+    results as in matmul_cross_entropy_grad."""
+    import torch
+    M, N, K, lda, ldb = _vocabulary(A, B)
+    top, ldt, ldi, ct, ci = _entries(teacher, ids, M)
+    _row_values(dloss, "dloss", M, torch.float32, strided=True)
+    _row_values(lse, "lse", M, torch.float32)
+    dA, dB, ((pa, ld_da, ca), (pb, ld_db, cb)) = _gradient_outputs(A, B, dA, dB, need_dA, need_dB, out_dtype, accumulate,
+                                                                   stream)
+    ws = _workspace_for(workspace, distill_workspace, (M, N, K, top), True, A.device, stream)
+    rc = (_lib or load()).gemm_bf16_distill_grad(
+        dloss.data_ptr(), A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), lse.data_ptr(), pa, pb, M, N, K,
+        top, dloss.stride(0), lda, ldb, ldt, ldi, ld_da, ld_db, ct, ci, ca, cb, temperature, 1 if accumulate else 0,
+        ws.data_ptr(), ws.nbytes, _raw_stream(stream, A.get_device()))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_bf16_distill_grad")
+    return dA, dB

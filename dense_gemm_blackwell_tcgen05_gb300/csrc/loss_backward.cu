@@ -1,0 +1,11 @@
+// The losses' backward products over the logits (loss_kernels.cuh).
+#include "launch_loss.cuh"
+
+namespace gb300 {
+
+int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, cudaStream_t stream) {
+  return a.ids != nullptr ? loss_pick<true, true>(o, a, ctx, nullptr, stream)
+                          : loss_pick<true, false>(o, a, ctx, nullptr, stream);
+}
+
+}  // namespace gb300

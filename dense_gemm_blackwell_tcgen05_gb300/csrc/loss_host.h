@@ -1,0 +1,88 @@
+// Host-side interface of the losses over a vocabulary (not part of the public ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_host.h"
+
+namespace gb300 {
+
+// Rows A [M, K] and the vocabulary's matrix B [N, K], bf16, and each row's entries: its
+// target (top = 0) or a teacher's list of `top`.
+struct LossProblem {
+  uint32_t M, N, K, top;
+  const void* A;
+  const void* B;
+  uint64_t lda, ldb;
+  float scale;                 // of the logits: 1 / temperature for a list
+  // a target per row
+  const void* targets;         // [M]
+  bool target64;
+  float smoothing, z_coef;
+  // a teacher's list per row
+  const void* teacher;         // [M, top] fp32 or bf16
+  bool teacher_f32;
+  const void* ids;             // [M, top]
+  bool ids64;
+  uint64_t ld_teacher, ld_ids;
+  // forward
+  float* loss;                 // [M]
+  float* lse_out;              // [M]
+  // backward
+  const float* dloss;          // [M] at inc_dloss elements
+  uint64_t inc_dloss;
+  const float* lse;            // [M]
+  void* dA;                    // [M, K] (nullptr: not wanted)
+  void* dB;                    // [N, K] (nullptr: not wanted)
+  uint64_t ld_da, ld_db;
+  bool da_f32, db_f32, accumulate;
+  void* workspace;
+  uint32_t stall_iter;
+};
+
+uint64_t loss_forward_bytes(uint64_t M, uint64_t N, uint64_t K, uint64_t top);
+uint64_t loss_backward_bytes(uint64_t M, uint64_t N, uint64_t K, uint64_t top);
+int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t stream);
+int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t stream);
+
+// The products (loss_kernels.cuh): rows from A or, where fewer than M count, from
+// `compact`; B's rows from `B` on.
+struct LossArgs;
+struct LossOperands {
+  const void* A;
+  uint64_t lda;
+  const void* compact;
+  uint64_t ld_compact;
+  const void* B;
+  uint64_t ldb;
+};
+// Which tiles: rounds of them over the SMs, each as long as its loads or MMAs.
+struct LossTiles {
+  uint32_t cg, nt;             // CTAs that share a tile of 128 rows each, its columns
+  // Partial results a forward product leaves for each row: one for each tile of columns,
+  // or, over one block of rows, for each cluster.
+  uint64_t slots(uint64_t M, uint64_t N) const;
+};
+// A GB300's SMs, not the current device's: a workspace is sized without a device.
+constexpr uint64_t kLossSms = 152;
+inline uint64_t LossTiles::slots(uint64_t M, uint64_t N) const {
+  const uint64_t columns = (N + nt - 1) / nt;
+  return M <= 128 * cg && columns > kLossSms / cg ? kLossSms / cg : columns;
+}
+inline LossTiles loss_tiles(uint64_t M, uint64_t N, uint64_t K) {
+  const auto time = [&](uint64_t lt, uint64_t nt, uint64_t clusters, double stage) {
+    const uint64_t tiles = ((M + lt - 1) / lt) * ((N + nt - 1) / nt);
+    return static_cast<double>((tiles + clusters - 1) / clusters * ((K + 63) / 64)) * stage;
+  };
+  const double narrow = time(128, 64, kLossSms, 0.24), wide = time(128, 128, kLossSms, 0.27),
+               pair = time(256, 256, kLossSms / 2, 0.30) + 2.0;
+  if (M > 128 && pair < wide && pair < narrow) return {2, 256};
+  return {1, wide < narrow ? 128u : 64u};
+}
+int launch_loss_logits_forward(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_t* slots,
+                               cudaStream_t stream);
+int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, cudaStream_t stream);
+
+}  // namespace gb300

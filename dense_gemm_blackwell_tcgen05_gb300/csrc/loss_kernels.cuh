@@ -1,0 +1,469 @@
+// Losses over a vocabulary: the logits z = scale A B^T (A [M, K] rows, B [N, K]
+// the vocabulary's matrix, bf16) as tiles in TMEM that are never stored.
+//
+//     out of a tile, forward:   per row its largest logit m, the sum of exp(z - m),
+//                               the logits at the row's entries (its target, or a
+//                               teacher's list), and for label smoothing sum z
+//     out of a tile, backward:  the logits' gradient, rounded to bf16, into a
+//                               buffer that holds one piece of the vocabulary:
+//                               g = gq exp(z - lse) - gs - (gt or gt p at the entries)
+//
+// Rows sit in the TMEM lanes (the MMA's M) and the vocabulary in its columns (N), so
+// that a thread holds 32 consecutive logits of one row: maxima and sums need no other
+// thread, an entry's logit is in one thread's registers, and a gradient's row is
+// stored by its thread in whole sectors.
+//
+// Persistent, warp-specialised like the grouped products: a TMA producer, an MMA
+// issuer with two accumulators, eight epilogue warps, two per lane quarter, each with
+// half of the tile's columns.  Rows left out of the loss are left out of the product:
+// the rows that count lie compact, and their number is read on the GPU.
+//
+// Precision.  The tensor core's additions truncate (1.1e-9 of the result a term), so
+// the forward pass, whose losses are fp32, adds up segments of 512 terms in registers.
+// exp is 2^x of the multiprocessor's special function unit (2 units in the last place)
+// on arguments in fp32.
+#pragma once
+
+#include <cstdint>
+
+#include "gemm_kernels.cuh"
+#include "grouped_kernels.cuh"
+#include "ptx_grouped.cuh"
+
+namespace gb300 {
+
+struct LossArgs {
+  uint32_t M, N, K;            // rows in all, vocabulary (of this piece, backward), width
+  const uint32_t* count;       // rows that count (nullptr: all of them, in place)
+  const uint32_t* index;       // [count] where each of them lies among all rows (nullptr: in place)
+  float c;                     // scale log2(e): exp(z) = 2^(c a.b)
+  float scale;
+  uint32_t first;              // number of this piece's first token
+  // entries: a target per row, or a sorted list
+  const void* target;          // [M] int32 or int64, by all rows
+  uint32_t target64;
+  const int32_t* ids;          // [M][top] rising, by all rows
+  const float* prob;           // [M][top] their probabilities (backward)
+  const uint32_t* len;         // [M] how many
+  uint32_t top;
+  // forward
+  float2* part;                // [slots][2][ld_part]: largest c a.b, sum of 2^(c a.b - largest)
+  float* part_sum;             // [slots][2][ld_part] sum of a.b (nullptr: not wanted)
+  uint64_t ld_part;
+  uint32_t runs;               // one block of rows: a slot for each cluster, else for each tile of columns
+  float* entry_z;              // [M] or [M][top], by all rows: the entries' logits
+  // backward
+  const float4* row;           // [count] (lse log2(e), gq, gs, gt)
+  uint16_t* out;               // [count][ld_out] the gradient's piece
+  uint64_t ld_out;
+  unsigned long long* status;
+  unsigned long long timeout_ns;
+  uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
+};
+
+// LIST: a list of entries per row, else one target.
+template <int CG, uint32_t NT, bool BACK, bool LIST>
+struct LossCfg {
+  static_assert(CG == 1 || CG == 2, "cta_group is 1 or 2");
+  static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
+  static constexpr uint32_t LT = 128 * CG;               // rows per tile
+  static constexpr uint32_t Q_ROWS = NT / CG;            // vocabulary rows staged by one CTA
+  static_assert(NT % 64 == 0 && NT <= 256, "two halves of whole 32-column chunks");
+  static constexpr uint32_t P_BOX = 32;                  // rows per load of A: few rows load what they need
+  static constexpr uint32_t Q_BOX = Q_ROWS;
+  static constexpr uint32_t P_BYTES = 128 * 128;
+  static constexpr uint32_t Q_BYTES = Q_ROWS * 128;
+  static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
+  static constexpr uint32_t kEpiWarps = 8;
+  static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps);
+  static constexpr uint32_t SEG_TILES = BACK ? 0xFFFFFFFFu : 8u;
+  static constexpr uint32_t NCH = NT / 64;               // 32-column chunks per epilogue warp
+  static constexpr uint32_t BAR_BYTES = 512;
+  static constexpr uint32_t SMEM_LIMIT = 232448;
+  static constexpr uint32_t ALIGN_SLACK = 1024;
+  static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES) / STAGE_BYTES;
+  static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
+  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + BAR_BYTES;
+  static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t ACC_COLS = 256;              // second accumulator's first column
+};
+
+// Row blocks swept together along the vocabulary.
+constexpr uint32_t kLossRaster = 16;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Element t (< 32) of a register array.
+__device__ __forceinline__ float select32(const float (&v)[32], uint32_t t) {
+  float x = v[0];
+#pragma unroll
+  for (uint32_t i = 1; i < 32; ++i) x = t == i ? v[i] : x;
+  return x;
+}
+
+// A row's target as an offset from `first`; 0xFFFFFFFF where it lies before it or has none.
+__device__ __forceinline__ uint32_t target_offset(const LossArgs& a, uint32_t row) {
+  const int64_t t = a.target64 ? static_cast<const int64_t*>(a.target)[row]
+                               : static_cast<int64_t>(static_cast<const int32_t*>(a.target)[row]);
+  const int64_t d = t - a.first;
+  return d >= 0 && d < 0x7FFFFFFF ? static_cast<uint32_t>(d) : 0xFFFFFFFFu;
+}
+
+template <int CG, uint32_t NT, bool BACK, bool LIST>
+__global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
+    loss_kernel(const __grid_constant__ CUtensorMap tmAll, const __grid_constant__ CUtensorMap tmCompact,
+                const __grid_constant__ CUtensorMap tmQ, const LossArgs args) {
+  using C = LossCfg<CG, NT, BACK, LIST>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bar0 = base + C::STAGES * C::STAGE_BYTES;
+  const auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
+  const auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (C::STAGES + s); };
+  constexpr uint32_t kAccBar0 = 2 * C::STAGES;
+  const auto accf_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + b); };
+  const auto acce_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8 * (kAccBar0 + 4);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (kAccBar0 + 5));
+  volatile uint32_t* const abort_flag = tmem_slot + 1;
+
+  const uint32_t warp = warp_idx_sync();
+  const uint32_t lane = lane_idx();
+  const uint32_t rank = (CG == 2) ? cluster_cta_rank() : 0u;
+  const bool leader = rank == 0;
+  const uint32_t cluster_id = blockIdx.x / CG;
+  const uint32_t G = gridDim.x / CG;
+  const Watchdog wd{args.status, args.timeout_ns, abort_flag};
+
+  // ---- set-up ------------------------------------------------------------------
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmAll);
+      tma_prefetch_desc(&tmCompact);
+      tma_prefetch_desc(&tmQ);
+      *abort_flag = 0u;
+    }
+    for (uint32_t i = lane; i < kAccBar0 + 5; i += 32)
+      mbar_init(bar0 + 8 * i, (i == kAccBar0 + 2 || i == kAccBar0 + 3) ? C::kEpiWarps * CG : 1u);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_addr(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish<CG>();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  const uint32_t count = args.count != nullptr ? min(*args.count, args.M) : args.M;
+  const uint32_t rbs = (count + C::LT - 1) / C::LT, vts = (args.N + NT - 1) / NT;
+  const uint32_t tiles = rbs * vts;
+  const uint32_t kt_n = (args.K + C::BK - 1) / C::BK;
+
+  if (warp == 0) {
+    // ==================== TMA producer: one thread ==============================
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_last();
+      const CUtensorMap* const tmP = args.index != nullptr && count < args.M ? &tmCompact : &tmAll;
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
+        uint32_t rb, vt;
+        tile_coords(t, rbs, vts, kLossRaster, rb, vt);
+        const uint32_t p0 = rb * C::LT + rank * 128;
+        const uint32_t live = count > p0 ? min(128u, count - p0) : 0u;
+        // (a pair's second CTA without rows still loads a box: its stage is waited for)
+        const uint32_t p_boxes = live == 0 ? 1u : (live + C::P_BOX - 1) / C::P_BOX;
+        const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * NT + rank * C::Q_ROWS);
+        uint32_t tx = C::Q_BYTES + p_boxes * C::P_BOX * 128;
+        if constexpr (CG == 2) {
+          const uint32_t p1 = rb * C::LT + 128;
+          const uint32_t live1 = count > p1 ? min(128u, count - p1) : 0u;
+          const uint32_t boxes0 = min(128u, count - rb * C::LT);
+          tx = 2 * C::Q_BYTES + ((boxes0 + C::P_BOX - 1) / C::P_BOX +
+                                 (live1 == 0 ? 1u : (live1 + C::P_BOX - 1) / C::P_BOX)) * C::P_BOX * 128;
+        }
+        for (uint32_t kt = 0; kt < kt_n; ++kt, ++it) {
+          const uint32_t s = it % C::STAGES;
+          if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
+          if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = base + s * C::STAGE_BYTES;
+          const int32_t k0 = static_cast<int32_t>(kt * C::BK);
+          uint32_t bar = full_bar(s);
+          if constexpr (CG == 2) bar = mapa_shared(full_bar(s), 0);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), tx);
+          const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t y) {
+            if (CG == 2) tma_load_3d_pair(dst, m, bar, k0, y, 0, pol);
+            else tma_load_3d(dst, m, bar, k0, y, 0, pol);
+          };
+          for (uint32_t r = 0; r < p_boxes; ++r)
+            load(sb + r * C::P_BOX * 128, tmP, px + static_cast<int32_t>(r * C::P_BOX));
+          load(sb + C::P_BYTES, &tmQ, qy);
+        }
+      }
+      // Exit path after a give-up: let this CTA's issued loads land first.
+      if (*abort_flag && leader) {
+        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
+        for (uint32_t i = first; i < it; ++i) {
+          if (i == args.stall_iter) continue;
+          drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ==================== MMA issuer: one thread of the leader CTA ==============
+    if (leader && lane == 0) {
+      const uint32_t idesc = idesc_f16(C::LT, NT, 1u, false, false);
+      uint32_t it = 0, j = 0;
+      bool ok = true, issued = false;
+      for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
+        for (uint32_t k_begin = 0; ok && k_begin < kt_n; ++j) {
+          const uint32_t k_end = kt_n - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : kt_n;
+          const uint32_t b = j & 1u;
+          // accumulator b must have been drained by every epilogue warp
+          if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
+          const auto stage = [&](uint32_t kt) {
+            const uint32_t s = it % C::STAGES;
+            if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
+              ok = false;
+              return;
+            }
+            tc_fence_after_sync();
+            const uint64_t pd = smem_desc_sw128(base + s * C::STAGE_BYTES);
+            const uint64_t qd = smem_desc_sw128(base + s * C::STAGE_BYTES + C::P_BYTES);
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)   // 16 k per MMA: 32 bytes along a row
+              mma_bf16<CG>(d_tmem, pd + 2 * k, qd + 2 * k, idesc, (kt != k_begin || k != 0u));
+            commit_to<CG>(empty_bar(s));       // frees the stage once these MMAs finish
+            issued = true;
+            ++it;
+          };
+          constexpr uint32_t kUnroll = CG == 2 ? 4 : 1;
+          uint32_t kt = k_begin;
+#pragma unroll kUnroll
+          for (; ok && kt < k_end; ++kt) stage(kt);
+          if (!ok) break;
+          commit_to<CG>(accf_bar(b));
+          k_begin = k_end;
+        }
+      }
+      // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
+      if (issued) {
+        if constexpr (CG == 1)
+          tc_commit(drain_bar);
+        else
+          tc_commit_pair_multicast(drain_bar, 0x1);
+        drain_wait(drain_bar, 0, wd, kSiteMmaDrain);
+      }
+    }
+  } else {
+    // ==================== epilogue: eight warps, two per TMEM lane quarter =======
+    const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
+    const uint32_t eg = (warp - 2u) / 4u;      // this warp's half of the tile's columns
+    uint32_t j = 0;
+    bool ok = true;
+    // forward, `runs`: largest and sums over this cluster's tiles so far
+    float run_m = -INFINITY, run_s = 0.0f, run_z = 0.0f;
+    for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
+      uint32_t rb, vt;
+      tile_coords(t, rbs, vts, kLossRaster, rb, vt);
+      const uint32_t row = rb * C::LT + rank * 128 + q * 32 + lane;
+      const bool live = row < count;
+      const bool any = row - lane < count;               // some lane of the warp has a row
+      const uint32_t n0 = vt * NT + eg * (NT / 2);       // this warp's first column
+      const uint32_t cols = args.N > n0 ? min(NT / 2, args.N - n0) : 0u;
+      const uint32_t at = live ? (args.index != nullptr ? args.index[row] : row) : 0u;
+      // the first entry at or behind n0: its offset from n0, 0xFFFFFFFF where there is none
+      uint32_t next = 0xFFFFFFFFu, cur = 0, len = 0;
+      float p_next = 1.0f;
+      const int32_t* ids = nullptr;
+      const float* prob = nullptr;
+      const uint32_t from = args.first + n0;
+      const auto take = [&]() {
+        next = 0xFFFFFFFFu;
+        if (cur < len) {
+          next = static_cast<uint32_t>(ids[cur]) - from;
+          if constexpr (BACK) p_next = prob[cur];
+        }
+      };
+      if constexpr (LIST) {
+        if (live) {
+          const uint64_t o = static_cast<uint64_t>(at) * args.top;
+          ids = args.ids + o;
+          prob = args.prob + o;
+          len = args.len[at];
+          uint32_t hi = len;
+          while (cur < hi) {
+            const uint32_t mid = (cur + hi) / 2;
+            if (static_cast<uint32_t>(ids[mid]) < from) cur = mid + 1; else hi = mid;
+          }
+          take();
+        }
+      } else if (live) {
+        const uint32_t d = target_offset(args, at);
+        next = d != 0xFFFFFFFFu && d >= n0 ? d - n0 : 0xFFFFFFFFu;
+      }
+      // The hand-back of an accumulator whose reads are complete: it publishes nothing.
+      const auto release = [&](uint32_t b) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) mbar_arrive(acce_bar(b));
+          else mbar_arrive_cluster_relaxed(mapa_shared(acce_bar(b), 0));
+        }
+      };
+      const auto t_addr = [&](uint32_t ch) {
+        return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + eg * (NT / 2) + ch * 32;
+      };
+      const auto acc_wait = [&]() {
+        ok = warp_wait(accf_bar(j & 1u), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane);
+        tc_fence_after_sync();
+        return ok;
+      };
+      if constexpr (!BACK) {
+        float acc[C::NCH][32];
+        for (uint32_t k = 0; k < kt_n; k += C::SEG_TILES, ++j) {
+          if (!acc_wait()) break;
+          if (any) {
+#pragma unroll
+            for (uint32_t i = 0; i < C::NCH; ++i) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32_sync(t_addr(i), v);
+#pragma unroll
+              for (uint32_t e = 0; e < 32; ++e) acc[i][e] = k == 0 ? __uint_as_float(v[e]) : acc[i][e] + __uint_as_float(v[e]);
+            }
+          }
+          release(j & 1u);
+        }
+        if (!ok) break;
+        if (any) {
+          // the entries' logits
+#pragma unroll
+          for (uint32_t i = 0; i < C::NCH; ++i) {
+            while (__any_sync(0xffffffffu, next - 32 * i < 32u)) {
+              const bool here = next - 32 * i < 32u;
+              const float z = args.scale * select32(acc[i], (next - 32 * i) & 31u);
+              if (here && next < cols) args.entry_z[LIST ? static_cast<uint64_t>(at) * args.top + cur : at] = z;
+              if (here) {
+                ++cur;
+                if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
+              }
+            }
+          }
+          float sum_z = 0.0f;
+          if (cols < NT / 2) {   // columns past the vocabulary's end
+#pragma unroll
+            for (uint32_t i = 0; i < C::NCH; ++i)
+#pragma unroll
+              for (uint32_t e = 0; e < 32; ++e) {
+                const bool in = 32 * i + e < cols;
+                sum_z += in ? acc[i][e] : 0.0f;
+                if (!in) acc[i][e] = -INFINITY;
+              }
+          } else if (args.part_sum != nullptr) {
+#pragma unroll
+            for (uint32_t i = 0; i < C::NCH; ++i) {
+              float part = 0.0f;
+#pragma unroll
+              for (uint32_t e = 0; e < 32; ++e) part += acc[i][e];
+              sum_z += part;
+            }
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (uint32_t i = 0; i < C::NCH; ++i)
+#pragma unroll
+            for (uint32_t e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], acc[i][e]);
+          float m = args.c * fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (args.runs) m = fmaxf(m, run_m);
+          const float shift = m == -INFINITY ? 0.0f : m;   // (nothing but masked columns: sums of 0)
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (uint32_t i = 0; i < C::NCH; ++i)
+#pragma unroll
+            for (uint32_t e = 0; e < 32; ++e) s[e & 3] += exp2_approx(fmaf(args.c, acc[i][e], -shift));
+          float sum = (s[0] + s[1]) + (s[2] + s[3]);
+          if (args.runs) {
+            sum += run_s * exp2_approx(run_m - shift);
+            run_m = m;
+            run_s = sum;
+            run_z += sum_z;
+            sum_z = run_z;
+          }
+          if (live && (!args.runs || t + G >= tiles)) {
+            const uint64_t o = ((args.runs ? cluster_id : vt) * 2ull + eg) * args.ld_part + row;
+            args.part[o] = make_float2(m, sum);
+            if (args.part_sum != nullptr) args.part_sum[o] = sum_z;
+          }
+        }
+      } else {
+        const float4 r = live ? args.row[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        uint16_t* const o = args.out + static_cast<uint64_t>(row) * args.ld_out + n0;
+        if (!acc_wait()) break;
+        const uint32_t b = j & 1u;
+        if (any) {
+#pragma unroll 1
+          for (uint32_t i = 0; i < C::NCH; ++i) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32_sync(t_addr(i), v);
+            if (i + 1 == C::NCH) release(b);
+            float g[32];
+#pragma unroll
+            for (uint32_t e = 0; e < 32; ++e)
+              g[e] = fmaf(r.y, exp2_approx(fmaf(args.c, __uint_as_float(v[e]), -r.x)), -r.z);
+            while (__any_sync(0xffffffffu, next - 32 * i < 32u)) {
+              const uint32_t w = next - 32 * i;
+              const float x = r.w * p_next;
+#pragma unroll
+              for (uint32_t e = 0; e < 32; ++e) g[e] = w == e ? g[e] - x : g[e];
+              if (w < 32u) {
+                ++cur;
+                if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
+              }
+            }
+            if (live) {
+#pragma unroll
+              for (uint32_t h = 0; h < 2; ++h) {
+                uint32_t x[8];
+#pragma unroll
+                for (uint32_t e = 0; e < 8; ++e) x[e] = pack_bf16x2(g[16 * h + 2 * e], g[16 * h + 2 * e + 1]);
+                st_global_v8(o + 32 * i + 16 * h, x);
+              }
+            }
+          }
+        } else {
+          release(b);
+        }
+        ++j;
+      }
+    }
+  }
+
+  // ---- teardown: every role is done with TMEM and with the peer's barriers ----
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace gb300

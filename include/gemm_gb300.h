@@ -3,9 +3,10 @@
  *
  *     D[M,N] = A[M,K] * B[N,K]^T      fp32 accumulation, bf16 output
  *
- * and of the products of a mixture of experts' training and serving: grouped
+ * of the products of a mixture of experts' training and serving: grouped
  * (ragged) products with their gradients, and the Newton-Schulz products of
- * the Muon optimiser.
+ * the Muon optimiser; and of the losses over a vocabulary: cross entropy and
+ * distillation, whose logits A * B^T are never stored, with their gradients.
  *
  * The operation is the dense GEMM of b200-gemm-optimization-ladder ("E --
  * Executable steps", step 1: fix the math definition, layout and dtype; "A1 --
@@ -398,6 +399,89 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
                        int64_t ldg, int64_t stride_g, int64_t ldo, int64_t stride_o, int in_dtype,
                        int out_dtype, int steps, float a, float b, float c, float eps,
                        void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Losses over a vocabulary.  Rows A [M, K] (hidden states) and the vocabulary's
+ * matrix B [N, K], both bf16 as in gemm_bf16, have the logits
+ *     z = scale * A * B^T     [M, N], fp32 sums, never stored.
+ *
+ * gemm_bf16_cross_entropy, with a target per row (label smoothing s =
+ * `smoothing` in [0, 1], a penalty c = `z_loss`, finite, on the log-partition):
+ *     lse[r]  = log sum_v exp z[r, v]
+ *     loss[r] = lse - (1 - s) z[r, target] - s / N sum_v z[r, v] + c lse^2
+ * gemm_bf16_distill, with a teacher's `top` largest logits per row, teacher
+ * [M, top], at the tokens ids [M, top] (any order; a token that comes twice
+ * counts twice; 1 <= top <= GEMM_MAX_TOP), scale = 1 / temperature:
+ *     p       = softmax(teacher[r] / temperature) over the row's entries
+ *     lse[r]  = log sum_v exp z[r, v]
+ *     loss[r] = sum_j p_j (log p_j - z[r, ids_j] + lse)
+ * which is the divergence of the student from the teacher's list, not times
+ * temperature^2.  Their gradients, from the losses' own, dloss [M] at inc_dloss
+ * elements (0: one value for all rows), and the lse that the forward call gave:
+ *     dz = dloss * scale * ((1 + 2 c lse) exp(z - lse) - s / N - (1 - s) [v == target])
+ *     dz = dloss / temperature * (exp(z - lse) - sum_j p_j [v == ids_j])
+ *     dA = dz * B       dB = dz^T * A       (dB += with accumulate)
+ *
+ * Rows left out: a negative target, or no entry with an id that is not negative
+ * and a logit that is not -Inf.  Their loss, lse and dA are 0, they add nothing
+ * to dB whatever A, dloss and lse hold there, and where more than 256 rows are
+ * given or a gradient is taken they cost next to nothing.  A target or an id of
+ * N or more makes the row's loss, its dA and dB NaN, like a NaN or an Inf among
+ * its logits, or a NaN or +Inf among the teacher's; the other rows' losses and
+ * dA are not affected.
+ *
+ * targets, ids: int32 or int64 (target_dtype, id_dtype: GEMM_INDEX_I32, _I64);
+ * teacher: bf16 or fp32; loss, lse, dloss: fp32.  scale and temperature are
+ * positive and finite.  dA and dB each bf16 or fp32 (da_dtype, db_dtype), any
+ * pitch and element alignment, either NULL where it is not wanted; accumulate (0
+ * or 1) adds to dB in fp32.  A and B must be 16-byte aligned with pitches that
+ * are multiples of 8; targets, ids, teacher, loss, lse, dloss at their element
+ * alignment, targets, loss and lse contiguous.  Outputs must not overlap inputs.
+ * M == 0 is a no-op (dB is zeroed unless accumulate); N == 0 with rows is
+ * refused; K == 0 gives logits of 0.
+ *
+ * Precision: the forward pass adds up its logits from sums over 512 terms and
+ * joins maxima and sums in fp32.  The gradient goes by pieces of the vocabulary:
+ * a piece's logits are computed again, their dz is rounded to bf16 for the two
+ * products with it (its target's and its list's terms are taken off before
+ * that), and the pieces' dA are added up in fp32.
+ *
+ * workspace: 256-byte aligned device memory of at least the number of bytes that
+ * the _workspace_bytes call gives for these sizes (grad: 0 for the forward call,
+ * 1 for the gradient), uninitialised; calls that share one must not overlap on
+ * the GPU.  Large calls need, forward, 2 MK + MN / 10 bytes, and for the gradient
+ * 6 MK and a piece of dz, 256 MiB or 4096 columns.  Calls are asynchronous on `stream`, allocate
+ * nothing and can be captured; the same call gives the same bits.  Errors as
+ * gemm_bf16.
+ */
+#define GEMM_MAX_TOP 1024
+#define GEMM_INDEX_I32 0
+#define GEMM_INDEX_I64 1
+int64_t gemm_bf16_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K, int grad);
+int gemm_bf16_cross_entropy(const void* A, const void* B, const void* targets, float* loss, float* lse,
+                            int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                            int target_dtype, float scale, float smoothing, float z_loss,
+                            void* workspace, int64_t workspace_bytes, cudaStream_t stream);
+int gemm_bf16_cross_entropy_grad(const float* dloss, const void* A, const void* B,
+                                 const void* targets, const float* lse, void* dA, void* dB,
+                                 int64_t M, int64_t N, int64_t K, int64_t inc_dloss, int64_t lda,
+                                 int64_t ldb, int64_t ld_da, int64_t ld_db, int target_dtype,
+                                 int da_dtype, int db_dtype, float scale, float smoothing,
+                                 float z_loss, int accumulate, void* workspace,
+                                 int64_t workspace_bytes, cudaStream_t stream);
+int64_t gemm_bf16_distill_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t top, int grad);
+int gemm_bf16_distill(const void* A, const void* B, const void* teacher, const void* ids, float* loss,
+                      float* lse, int64_t M, int64_t N, int64_t K, int64_t top, int64_t lda,
+                      int64_t ldb, int64_t ld_teacher, int64_t ld_ids, int teacher_dtype,
+                      int id_dtype, float temperature, void* workspace, int64_t workspace_bytes,
+                      cudaStream_t stream);
+int gemm_bf16_distill_grad(const float* dloss, const void* A, const void* B, const void* teacher,
+                           const void* ids, const float* lse, void* dA, void* dB, int64_t M,
+                           int64_t N, int64_t K, int64_t top, int64_t inc_dloss, int64_t lda,
+                           int64_t ldb, int64_t ld_teacher, int64_t ld_ids, int64_t ld_da,
+                           int64_t ld_db, int teacher_dtype, int id_dtype, int da_dtype,
+                           int db_dtype, float temperature, int accumulate, void* workspace,
+                           int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status
