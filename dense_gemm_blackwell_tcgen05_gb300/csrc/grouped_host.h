@@ -32,7 +32,7 @@ struct GroupedProblem {
   void* out;
   uint64_t lda, ldb, stride_b, ldd;  // pitches of A, B, dD and B's matrix stride, in elements
   uint64_t ldo, stride_o;            // of the output
-  bool out_f32, accumulate;          // accumulate: weight gradient, or row gradient in fp32
+  bool out_f32, accumulate;
   uint32_t stall_iter;
 };
 

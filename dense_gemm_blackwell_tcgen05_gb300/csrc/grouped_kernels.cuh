@@ -24,7 +24,7 @@
 //              or X (a + d) + X B (P K-major), X held as two halves hi + lo
 //              of which hi feeds the tensor cores.  ApplyOut: the last one,
 //              whose X' is rounded once to the result's type.
-//   Op::RowsAdd, Op::SumAdd are Op::Rows and Op::Sum added to what the output holds.
+//   Op::SumAdd is Op::Sum added to what the output holds.
 //   Op::SumLane, Op::SumLaneAdd are these with the operands' places exchanged:
 //              P = dD and Q = A, l the output row and c along its contiguous
 //              dimension, for 16-bit outputs whose rows hold whole pieces of 16
@@ -65,7 +65,7 @@ enum GroupedWaitSite : uint32_t {
   kSiteSplit = 12,          // epilogue waiting for the other CTAs' parts of a reduction
 };
 
-enum class Op { Rows, RowsAdd, Sum, SumAdd, SumLane, SumLaneAdd, Sym, Apply, ApplyOut };
+enum class Op { Rows, Sum, SumAdd, SumLane, SumLaneAdd, Sym, Apply, ApplyOut };
 
 // Groups a launch can hold: the offsets and the tile table sit in shared memory.
 constexpr uint32_t kMaxGroups = 1024;
@@ -136,16 +136,13 @@ struct GroupedCfg {
   static_assert(Q_ROWS % 16 == 0 && Q_ROWS <= 256 && NT <= 256, "tile width");
   // rows per load of a K-major Q: ragged tiles load what they need, the others 64
   // rows at a time (Newton-Schulz products 1 % shorter than with 32)
-  static constexpr bool ROWS = OP == Op::Rows || OP == Op::RowsAdd;
-  static constexpr uint32_t Q_BOX = ROWS ? 32 : 64;
+  static constexpr uint32_t Q_BOX = OP == Op::Rows ? 32 : 64;
   static constexpr uint32_t P_BYTES = 128 * 128;
   static constexpr uint32_t Q_BYTES = Q_ROWS * 128;
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
-  // out += instead of out =
-  static constexpr bool ADD = OP == Op::RowsAdd || OP == Op::SumAdd || OP == Op::SumLaneAdd;
-  static_assert(OP != Op::RowsAdd || OUT32, "rows are added up in fp32");
+  static constexpr bool ADD = OP == Op::SumAdd || OP == Op::SumLaneAdd;   // out += instead of out =
   static constexpr bool LANE = OP == Op::SumLane || OP == Op::SumLaneAdd; // output rows in the lanes
-  static constexpr bool SUM = OP == Op::Sum || OP == Op::SumAdd || LANE;
+  static constexpr bool SUM = OP == Op::Sum || LANE || ADD;
   static_assert(!LANE || !OUT32, "fp32 rows are stored as whole lines either way");
   static constexpr bool APPLY = OP == Op::Apply || OP == Op::ApplyOut;
   static constexpr bool TAIL = SUM;                      // a warp clears ragged reduction ends
@@ -159,8 +156,8 @@ struct GroupedCfg {
   // nearest.  bf16 and fp16 outputs round far above that and take one segment.
   static constexpr uint32_t SEG_TILES = OUT32 ? 8u : 0xFFFFFFFFu;
   static constexpr uint32_t NCH = (NT + 63) / 64;        // 32-column chunks per epilogue warp
-  static constexpr bool GROUPED = ROWS || SUM;
-  static_assert(SPLIT == 1 || (CG == 1 && (ROWS || OP == Op::Sym) && NT == 64), "split reductions");
+  static constexpr bool GROUPED = OP == Op::Rows || SUM;
+  static_assert(SPLIT == 1 || (CG == 1 && (OP == Op::Rows || OP == Op::Sym) && NT == 64), "split reductions");
   static constexpr uint32_t kCluster = CG * SPLIT;       // CTAs a cluster
   // the other CTAs' sums, fp32, in the first one: for each of them a tile of
   // 128 lanes by NT columns, 16 bytes a lane after another
@@ -225,7 +222,7 @@ __device__ __forceinline__ bool tile_item(const GroupedArgs& a, const uint32_t* 
   w.mirror = 0u;
   w.row0 = 0;
   w.k_len = a.K;
-  if constexpr (C::ROWS) {
+  if constexpr (OP == Op::Rows) {
     // Group by group, dealt round-robin: a group's matrix is read by all
     // clusters at about the same time.  (Groups by falling tile width, equal
     // tiles within a group and alternating directions measured the same on
@@ -446,7 +443,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
   if constexpr (C::GROUPED) {
     // offsets clamped into [0, rows] and made to rise: whatever they hold, no
     // access leaves the operands and the groups do not overlap
-    const int32_t rows = static_cast<int32_t>(C::ROWS ? args.C : args.K);
+    const int32_t rows = static_cast<int32_t>(OP == Op::Rows ? args.C : args.K);
     if (warp == 2) {
       int32_t top = 0;
       for (uint32_t e0 = 0; e0 <= args.groups; e0 += 32) {
@@ -463,7 +460,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
       }
       __syncwarp();
     }
-    if constexpr (C::ROWS) {
+    if constexpr (OP == Op::Rows) {
       // first tile of each group: an exclusive sum
       if (warp == 2) {
         const uint32_t lt = (args.L + C::LT - 1) / C::LT;
@@ -590,7 +587,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
             for (uint32_t x = 0; x < C::Q_ROWS; x += 64)
               load(sb + C::P_BYTES + x * 128, &tmQ, qy + static_cast<int32_t>(x), kr, qz);
           } else {
-            const int32_t y = static_cast<int32_t>(C::ROWS ? w.row0 : 0u) + qy;
+            const int32_t y = static_cast<int32_t>(OP == Op::Rows ? w.row0 : 0u) + qy;
             for (uint32_t r = 0; r < q_boxes; ++r)
               load(sb + C::P_BYTES + r * C::Q_BOX * 128, &tmQ, k0, y + static_cast<int32_t>(r * C::Q_BOX), qz);
           }
@@ -727,7 +724,7 @@ __global__ void __launch_bounds__(GroupedCfg<CG, OP, P_MN, Q_MN, NT, OUT32, SPLI
       const uint32_t col = lbase + lane;
       const uint32_t nch = (w.live + 31) / 32;
       // output row of tile column c: matrix z, row c0 + c (Rows: memory row row0 + c0 + c)
-      const uint64_t out0 = C::ROWS
+      const uint64_t out0 = OP == Op::Rows
                                 ? static_cast<uint64_t>(w.row0 + w.c0) * args.ldo
                                 : w.z * args.stride_o + static_cast<uint64_t>(w.c0) * args.ldo;
       // The hand-back of an accumulator whose reads are complete

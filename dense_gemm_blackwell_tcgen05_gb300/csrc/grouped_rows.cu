@@ -14,10 +14,10 @@ uint64_t most_tiles(const GroupedProblem& p, uint64_t nt, uint64_t lt, uint32_t 
 }
 
 // X [M, K'] times each group's matrix; L output columns, K' reduced.
-template <int CG, uint32_t NT, bool P_MN, bool OUT32, uint32_t SPLIT = 1, Op OP = Op::Rows>
+template <int CG, uint32_t NT, bool P_MN, bool OUT32, uint32_t SPLIT = 1>
 int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
               const LaunchCtx& ctx, cudaStream_t stream) {
-  using C = GroupedCfg<CG, OP, P_MN, false, NT, OUT32, SPLIT>;
+  using C = GroupedCfg<CG, Op::Rows, P_MN, false, NT, OUT32, SPLIT>;
   CUtensorMap tmP, tmQ;
   if (!operand_map(&tmP, p.B, p.K, p.N, p.groups, p.ldb, p.stride_b, p_box_rows<C, P_MN>()) ||
       !operand_map(&tmQ, X, K, p.M, 1, ldx, 0, q_box_rows<C, false>()))
@@ -35,7 +35,7 @@ int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
   a.timeout_ns = ctx.timeout_ns;
   a.stall_iter = p.stall_iter;
   const uint64_t tiles = most_tiles(p, NT, C::LT, L);
-  return launch_grouped<CG, OP, P_MN, false, NT, OUT32, SPLIT>(tmP, tmQ, a, tiles, ctx, stream);
+  return launch_grouped<CG, Op::Rows, P_MN, false, NT, OUT32, SPLIT>(tmP, tmQ, a, tiles, ctx, stream);
 }
 
 // Which tiles.  A launch takes its rounds of tiles (those of all groups over
@@ -51,7 +51,7 @@ int rows_impl(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
 // 16.0, 1024: 30.1 / 22.4 / 17.9; 32 groups of 4096 x 2048, 4 rows: 80 / 82 / 89,
 // 32: 90 / 88 / 93, 256: 215 / 141 / 114; 61 of 399 x 1736, 52 rows: 22.4 / 24.5
 // / 24.7.
-template <bool P_MN, bool OUT32, Op OP = Op::Rows>
+template <bool P_MN, bool OUT32>
 int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, uint32_t K,
               const LaunchCtx& ctx, cudaStream_t stream) {
   const uint64_t touched = p.M < p.groups ? p.M : p.groups;   // groups that can have rows
@@ -64,12 +64,12 @@ int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
     const uint64_t narrow = most_tiles(p, 64, 128, L);
     uint64_t room = 0;
     if (narrow <= static_cast<uint64_t>(ctx.num_sms / 4)) {
-      if (const int rc = grouped_room<1, OP, P_MN, false, 64, OUT32, 4>(ctx, &room); rc != GEMM_OK) return rc;
-      if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 4, OP>(p, X, ldx, L, K, ctx, stream);
+      if (const int rc = grouped_room<1, Op::Rows, P_MN, false, 64, OUT32, 4>(ctx, &room); rc != GEMM_OK) return rc;
+      if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 4>(p, X, ldx, L, K, ctx, stream);
     }
     if (narrow <= static_cast<uint64_t>(ctx.num_sms / 2) && K >= 50 * 64) {
-      if (const int rc = grouped_room<1, OP, P_MN, false, 64, OUT32, 2>(ctx, &room); rc != GEMM_OK) return rc;
-      if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 2, OP>(p, X, ldx, L, K, ctx, stream);
+      if (const int rc = grouped_room<1, Op::Rows, P_MN, false, 64, OUT32, 2>(ctx, &room); rc != GEMM_OK) return rc;
+      if (narrow <= room) return rows_impl<1, 64, P_MN, OUT32, 2>(p, X, ldx, L, K, ctx, stream);
     }
   }
   const auto time = [&](uint64_t nt, uint64_t lt, uint64_t clusters, double stage) {
@@ -81,9 +81,9 @@ int rows_pick(const GroupedProblem& p, const void* X, uint64_t ldx, uint32_t L, 
   const uint64_t sms = static_cast<uint64_t>(ctx.num_sms);
   const double narrow = time(64, 128, sms, 0.24), wide = time(128, 128, sms, 0.27),
                pair = time(256, 256, sms / 2, 0.30) + 2.0;
-  if (pair < wide && pair < narrow) return rows_impl<2, 256, P_MN, OUT32, 1, OP>(p, X, ldx, L, K, ctx, stream);
-  return wide < narrow ? rows_impl<1, 128, P_MN, OUT32, 1, OP>(p, X, ldx, L, K, ctx, stream)
-                       : rows_impl<1, 64, P_MN, OUT32, 1, OP>(p, X, ldx, L, K, ctx, stream);
+  if (pair < wide && pair < narrow) return rows_impl<2, 256, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
+  return wide < narrow ? rows_impl<1, 128, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream)
+                       : rows_impl<1, 64, P_MN, OUT32>(p, X, ldx, L, K, ctx, stream);
 }
 
 }  // namespace
@@ -94,7 +94,6 @@ int launch_grouped_forward(const GroupedProblem& p, const LaunchCtx& ctx, cudaSt
 }
 
 int launch_grouped_dgrad(const GroupedProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
-  if (p.accumulate) return rows_pick<true, true, Op::RowsAdd>(p, p.dD, p.ldd, p.K, p.N, ctx, stream);
   return p.out_f32 ? rows_pick<true, true>(p, p.dD, p.ldd, p.K, p.N, ctx, stream)
                    : rows_pick<true, false>(p, p.dD, p.ldd, p.K, p.N, ctx, stream);
 }
