@@ -10,12 +10,30 @@
 
 namespace gb300 {
 
+// A launch's cluster and, for one that follows another kernel of its call, the
+// programmatic dependency on it.
+inline void loss_attributes(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], int cg, bool chained) {
+  unsigned n = 0;
+  if (cg > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cg);
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (chained) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+}
+
 // Clusters of a kernel that run at once on the current device (found once, with
 // the kernel's shared memory opted in).
-template <int CG, uint32_t NT, bool BACK, bool LIST>
+template <class C, auto kern, int CG>
 int loss_room(const LaunchCtx& ctx, uint64_t* room) {
-  using C = LossCfg<CG, NT, BACK, LIST>;
-  const auto kern = loss_kernel<CG, NT, BACK, LIST>;
   static std::mutex mu;
   static int resident[128] = {0};   // per device (0: not set up yet)
   if (ctx.device < 0 || ctx.device >= 128) return GEMM_ERR_UNSUPPORTED_DEVICE;
@@ -58,7 +76,7 @@ int launch_loss(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_
   using C = LossCfg<CG, NT, BACK, LIST>;
   const auto kern = loss_kernel<CG, NT, BACK, LIST>;
   uint64_t room = 0;
-  if (const int rc = loss_room<CG, NT, BACK, LIST>(ctx, &room); rc != GEMM_OK) return rc;
+  if (const int rc = loss_room<C, loss_kernel<CG, NT, BACK, LIST>, CG>(ctx, &room); rc != GEMM_OK) return rc;
   CUtensorMap all, compact, q;
   if (!operand_map(&all, o.A, a.K, a.M, 1, o.lda, 0, C::P_BOX) || !operand_map(&q, o.B, a.K, a.N, 1, o.ldb, 0, C::Q_BOX))
     return GEMM_ERR_LAUNCH;
@@ -80,15 +98,8 @@ int launch_loss(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (CG > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-  }
-  cfg.attrs = attr;
+  cudaLaunchAttribute attr[2];
+  loss_attributes(cfg, attr, CG, o.chained);
   a.status = ctx.status;
   a.timeout_ns = ctx.timeout_ns;
   note_schedule(cfg.gridDim.x / CG, CG, static_cast<uint32_t>(tiles), 0u, 0u, 0u, 0u);

@@ -12,10 +12,13 @@
 //   backward   list, rows, gather as above, with each row's factors; then for each
 //              piece of the vocabulary
 //              product  g = dloss dloss/dz of the piece, bf16 (loss_kernel)
-//              dA      += g B[piece]         a grouped product with one group of
-//              dB[piece] (+)= g^T A          `count` rows, in fp32 sums
-//              spread   dA's rows to where they belong, zeros to the others
+//              dA      += g B[piece]         in fp32, the reduction in parts
+//              dB[piece] (+)= g^T A
+//              spread   dA's parts joined, its rows to where they belong, zeros to the
+//                       others
 //
+// Every kernel but a call's first is launched while the one before it runs, and waits for
+// it before it touches memory.
 // Only a piece's g is held: kPieceBytes, or a piece of kLeastPiece columns.
 #include <cuda_bf16.h>
 
@@ -36,7 +39,8 @@ uint64_t up(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
 
 struct Layout {
   uint64_t offs, index, pos, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
-  uint64_t ld_compact, ld_part, ld_sums, width, bytes;   // width: of a piece
+  uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
+  LossRowsPlan plan;
 };
 
 Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
@@ -65,7 +69,9 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     w.width = up((N + pieces - 1) / (pieces > 0 ? pieces : 1), 256);
     w.piece = take(2 * M * w.width);
     w.ld_sums = up(K, 32);
-    w.sums = take(4 * M * w.ld_sums);
+    w.stride_sums = M * w.ld_sums;
+    w.plan = loss_rows_plan(M, w.width < N ? w.width : N, K);
+    w.sums = take(4 * w.stride_sums * w.plan.split);
   } else {
     if (M > kInPlace) w.compact = take(2 * M * w.ld_compact);
     w.entry_z = take(4 * M * (top > 0 ? top : 1));
@@ -107,6 +113,8 @@ __device__ __forceinline__ float block_all(float v, bool largest, float* slots) 
 __global__ void __launch_bounds__(256) loss_list_kernel(const void* teacher, bool f32, uint64_t ld_teacher, const void* ids,
                                                         bool ids64, uint64_t ld_ids, uint32_t top, uint32_t N, float scale,
                                                         int32_t* out_ids, float* out_prob, uint32_t* len, float* entropy) {
+  grid_dependents_launch();
+  grid_dependency_wait();
   __shared__ int32_t s_id[GEMM_MAX_TOP];
   __shared__ float slots[8];
   const uint64_t r = blockIdx.x;
@@ -155,30 +163,55 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const void* teacher, boo
 }
 
 // One block: index[i] = the i-th row that counts, pos[r] its place (-1: left out), offs =
-// {0, their number}; a forward pass's results for the rows left out.
+// {0, their number}; a forward pass's results for the rows left out.  8192 rows at a time,
+// their flags on the way together.
 __global__ void __launch_bounds__(1024) loss_rows_kernel(uint32_t M, const void* targets, bool target64, const uint32_t* len,
                                                          int32_t* offs, uint32_t* index, int32_t* pos, float* loss, float* lse) {
-  __shared__ uint32_t warps[32];
+  __shared__ uint32_t votes[256], sums[8];
+  grid_dependents_launch();
+  grid_dependency_wait();
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
   uint32_t before = 0;
-  for (uint32_t r0 = 0; r0 < M; r0 += 1024) {
-    const uint32_t r = r0 + threadIdx.x;
-    const bool in = r < M && (len != nullptr ? len[r] > 0 : index_at(targets, target64, r) >= 0);
-    const uint32_t votes = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) warps[warp] = __popc(votes);
+  for (uint32_t r0 = 0; r0 < M; r0 += 8192) {   // (M < 2^31)
+    bool in[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t r = r0 + i * 1024 + threadIdx.x;
+      in[i] = r < M && (len != nullptr ? len[r] > 0 : index_at(targets, target64, r) >= 0);
+    }
+    uint32_t vote[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      vote[i] = __ballot_sync(0xffffffffu, in[i]);
+      if (lane == 0) votes[i * 32 + warp] = __popc(vote[i]);
+    }
     __syncthreads();
-    uint32_t lower = 0, all = 0;
-    for (uint32_t i = 0; i < 32; ++i) {
-      lower += i < warp ? warps[i] : 0u;
-      all += warps[i];
+    // votes[w]: rows that count in the warps before w of this turn
+    if (warp < 8) {
+      const uint32_t n = votes[threadIdx.x];
+      uint32_t incl = n;
+#pragma unroll
+      for (uint32_t d = 1; d < 32; d *= 2) {
+        const uint32_t lower = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += lower;
+      }
+      votes[threadIdx.x] = incl - n;
+      if (lane == 31) sums[warp] = incl;
     }
-    const uint32_t at = before + lower + __popc(votes & ((1u << lane) - 1u));
-    if (in) index[at] = r;
-    if (r < M) {
-      pos[r] = in ? static_cast<int32_t>(at) : -1;
-      if (!in && loss != nullptr) loss[r] = lse[r] = 0.0f;
+    __syncthreads();
+    uint32_t base = before;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      const uint32_t r = r0 + i * 1024 + threadIdx.x;
+      const uint32_t at = base + votes[i * 32 + warp] + __popc(vote[i] & ((1u << lane) - 1u));
+      if (in[i]) index[at] = r;
+      if (r < M) {
+        pos[r] = in[i] ? static_cast<int32_t>(at) : -1;
+        if (!in[i] && loss != nullptr) loss[r] = lse[r] = 0.0f;
+      }
+      base += sums[i];
     }
-    before += all;
+    before = base;
     __syncthreads();
   }
   if (threadIdx.x == 0) {
@@ -201,14 +234,20 @@ struct RowFactors {
   float4* row;
 };
 
-// A warp per row that counts: its row of A (where some row is left out, or `always`), and
-// its factors.
+// A warp per row that counts: its row of A (where some row is left out, or `back`) and,
+// for a backward pass, its factors, and zeros up to a multiple of 64 rows.
 __global__ void __launch_bounds__(256) loss_gather_kernel(const uint16_t* A, uint64_t lda, uint32_t M, uint32_t K,
                                                           const uint32_t* count, const uint32_t* index, uint16_t* out,
-                                                          uint64_t ldo, bool always, const RowFactors f) {
+                                                          uint64_t ldo, bool back, const RowFactors f) {
+  grid_dependents_launch();
+  grid_dependency_wait();
   const uint32_t lane = lane_idx(), n = *count;
-  const bool copy = always || n < M;
-  for (uint32_t i = blockIdx.x * 8 + threadIdx.x / 32; i < n; i += gridDim.x * 8) {
+  const bool copy = back || n < M;
+  for (uint32_t i = blockIdx.x * 8 + threadIdx.x / 32; i < (back ? min((n + 63) / 64 * 64, M) : n); i += gridDim.x * 8) {
+    if (i >= n) {
+      for (uint32_t c = lane; c < ldo / 8; c += 32) reinterpret_cast<uint4*>(out + i * ldo)[c] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
     const uint32_t r = index[i];
     if (copy) {
       const uint16_t* const from = A + r * lda;
@@ -218,7 +257,7 @@ __global__ void __launch_bounds__(256) loss_gather_kernel(const uint16_t* A, uin
         reinterpret_cast<uint4*>(to)[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
       if (8 * whole + lane < K) to[8 * whole + lane] = from[8 * whole + lane];
     }
-    if (f.row != nullptr && lane == 0) {
+    if (back && lane == 0) {
       const float g = f.dloss[r * f.inc_dloss] * f.scale, l = f.lse[r];
       float gq = g * (1.0f + 2.0f * f.z_coef * l);
       const bool wrong = f.entropy != nullptr ? isnan(f.entropy[r]) : index_at(f.targets, f.target64, r) >= f.N;
@@ -246,6 +285,7 @@ struct FinishArgs {
 // A lane per row, the block's 32 warps share its partial results, joined in a fixed order.
 __global__ void __launch_bounds__(1024) loss_finish_kernel(const FinishArgs a) {
   __shared__ float s_m[32][33], s_s[32][33], s_z[32][33];
+  grid_dependency_wait();
   const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
   const uint32_t n = a.count != nullptr ? *a.count : a.M;
   const uint32_t i = blockIdx.x * 32 + lane;
@@ -254,13 +294,27 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const FinishArgs a) {
   const uint32_t r = in ? (a.index != nullptr ? a.index[i] : i) : 0u;
   float m = -INFINITY, s = 0.0f, sum = 0.0f;
   const uint32_t parts = 2 * a.slots;
-#pragma unroll 4
-  for (uint32_t p = warp; p < parts; p += 32) {
-    if (!in) continue;
-    const float2 x = a.part[p * a.ld_part + i];
-    if (a.part_sum != nullptr) sum += a.part_sum[p * a.ld_part + i];
-    const float top = fmaxf(m, x.x), shift = top == -INFINITY ? 0.0f : top;
-    s = s * exp2_approx(m - shift) + x.y * exp2_approx(x.x - shift);
+  // (a lane without a row takes the last one's, eight loads on their way at a time)
+  const uint32_t at = in ? i : n - 1;
+  for (uint32_t p0 = warp; p0 < parts; p0 += 256) {
+    float2 x[8];
+    float z[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t p = p0 + 32 * k;
+      x[k] = p < parts ? a.part[p * a.ld_part + at] : make_float2(-INFINITY, 0.0f);
+      z[k] = p < parts && a.part_sum != nullptr ? a.part_sum[p * a.ld_part + at] : 0.0f;
+    }
+    float top = m;
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
+    const float shift = top == -INFINITY ? 0.0f : top;
+    s *= exp2_approx(m - shift);
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      s += x[k].y * exp2_approx(x[k].x - shift);
+      sum += z[k];
+    }
     m = top;
   }
   s_m[warp][lane] = m;
@@ -310,18 +364,31 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const FinishArgs a) {
   }
 }
 
-// dA[r] = sums[pos[r]], rounded once, or zeros.
+// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros.
 template <class T>
-__global__ void __launch_bounds__(256) loss_spread_kernel(const float* sums, uint64_t ld_sums, const int32_t* pos, uint32_t M,
-                                                          uint32_t K, T* dA, uint64_t ldo) {
+__global__ void __launch_bounds__(256) loss_spread_kernel(const float* sums, uint64_t ld_sums, uint64_t stride_sums,
+                                                          uint32_t split, const int32_t* pos, uint32_t M, uint32_t K, T* dA,
+                                                          uint64_t ldo) {
+  grid_dependency_wait();
   const uint32_t lane = lane_idx();
   const bool vec = ((reinterpret_cast<uintptr_t>(dA) | (ldo * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
-  for (uint32_t r = blockIdx.x * 8 + threadIdx.x / 32; r < M; r += gridDim.x * 8) {
+  // a warp takes 128 columns of a row at a time: rows alone could be too few
+  const uint32_t pieces = (K + 127) / 128;
+  const uint64_t units = static_cast<uint64_t>(M) * pieces;
+  for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
+    const uint32_t r = static_cast<uint32_t>(u / pieces), c = static_cast<uint32_t>(u % pieces) * 128 + 4 * lane;
     const int32_t i = pos[r];
-    const float* const from = sums + (i < 0 ? 0u : static_cast<uint32_t>(i)) * ld_sums;
     T* const to = dA + r * ldo;
-    for (uint32_t c = 4 * lane; c < K; c += 128) {
-      const float4 x = i < 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4*>(from + c);
+    if (c < K) {
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i >= 0) {
+        const float* from = sums + static_cast<uint32_t>(i) * ld_sums + c;
+#pragma unroll 8
+        for (uint32_t p = 0; p < split; ++p, from += stride_sums) {
+          const float4 y = *reinterpret_cast<const float4*>(from);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+      }
       if constexpr (sizeof(T) == 2) {
         const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
         if (vec && c + 4 <= K) {
@@ -342,9 +409,20 @@ __global__ void __launch_bounds__(256) loss_spread_kernel(const float* sums, uin
   }
 }
 
-int launched() {
-  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) {
+template <class... P, class... A>
+int launch(void (*kern)(P...), unsigned grid, unsigned block, bool chained, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...); e != cudaSuccess) {
     note_cuda_error(e);
+    cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }
   return GEMM_OK;
@@ -357,11 +435,9 @@ unsigned row_blocks(uint64_t rows, uint64_t per, int num_sms) {
 
 int launch_list(const LossProblem& p, const Layout& w, uint8_t* ws, cudaStream_t stream) {
   const uint32_t threads = p.top >= 256 ? 256u : (p.top + 31) / 32 * 32;
-  loss_list_kernel<<<p.M, threads, 0, stream>>>(p.teacher, p.teacher_f32, p.ld_teacher, p.ids, p.ids64, p.ld_ids, p.top, p.N,
-                                                p.scale, reinterpret_cast<int32_t*>(ws + w.ids),
-                                                reinterpret_cast<float*>(ws + w.prob), reinterpret_cast<uint32_t*>(ws + w.len),
-                                                reinterpret_cast<float*>(ws + w.entropy));
-  return launched();
+  return launch(loss_list_kernel, p.M, threads, false, stream, p.teacher, p.teacher_f32, p.ld_teacher, p.ids, p.ids64, p.ld_ids,
+                p.top, p.N, p.scale, reinterpret_cast<int32_t*>(ws + w.ids), reinterpret_cast<float*>(ws + w.prob),
+                reinterpret_cast<uint32_t*>(ws + w.len), reinterpret_cast<float*>(ws + w.entropy));
 }
 
 LossArgs logits_args(const LossProblem& p, const Layout& w, uint8_t* ws) {
@@ -394,20 +470,22 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   int rc;
   if (p.top > 0 && (rc = launch_list(p, w, ws, stream)) != GEMM_OK) return rc;
   LossArgs a = logits_args(p, w, ws);
-  LossOperands o = {p.A, p.lda, nullptr, 0, p.B, p.ldb};
+  LossOperands o = {p.A, p.lda, nullptr, 0, p.B, p.ldb, p.top > 0};
   if (p.M > kInPlace) {
     int32_t* const offs = reinterpret_cast<int32_t*>(ws + w.offs);
     uint32_t* const index = reinterpret_cast<uint32_t*>(ws + w.index);
-    loss_rows_kernel<<<1, 1024, 0, stream>>>(p.M, p.targets, p.target64, a.len, offs, index,
-                                             reinterpret_cast<int32_t*>(ws + w.pos), p.loss, p.lse_out);
+    if ((rc = launch(loss_rows_kernel, 1, 1024, p.top > 0, stream, p.M, p.targets, p.target64, a.len, offs, index,
+                     reinterpret_cast<int32_t*>(ws + w.pos), p.loss, p.lse_out)) != GEMM_OK)
+      return rc;
     a.count = reinterpret_cast<const uint32_t*>(offs + 1);
     a.index = index;
     o.compact = ws + w.compact;
     o.ld_compact = w.ld_compact;
-    loss_gather_kernel<<<row_blocks(p.M, 8, ctx.num_sms), 256, 0, stream>>>(
-        static_cast<const uint16_t*>(p.A), p.lda, p.M, p.K, a.count, a.index, reinterpret_cast<uint16_t*>(ws + w.compact),
-        w.ld_compact, false, RowFactors{});
-    if ((rc = launched()) != GEMM_OK) return rc;
+    o.chained = true;
+    if ((rc = launch(loss_gather_kernel, row_blocks(p.M, 8, ctx.num_sms), 256, true, stream, static_cast<const uint16_t*>(p.A),
+                     p.lda, p.M, p.K, a.count, a.index, reinterpret_cast<uint16_t*>(ws + w.compact), w.ld_compact, false,
+                     RowFactors{})) != GEMM_OK)
+      return rc;
   }
   a.part = reinterpret_cast<float2*>(ws + w.part);
   a.part_sum = p.smoothing > 0.0f ? reinterpret_cast<float*>(ws + w.part_sum) : nullptr;
@@ -436,8 +514,7 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   f.entropy = reinterpret_cast<const float*>(ws + w.entropy);
   f.loss = p.loss;
   f.lse = p.lse_out;
-  loss_finish_kernel<<<(p.M + 31) / 32, 1024, 0, stream>>>(f);
-  return launched();
+  return launch(loss_finish_kernel, (p.M + 31) / 32, 1024, p.K > 0 || o.chained, stream, f);
 }
 
 int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
@@ -451,7 +528,9 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   int32_t* const pos = reinterpret_cast<int32_t*>(ws + w.pos);
   uint16_t* const compact = reinterpret_cast<uint16_t*>(ws + w.compact);
   float* const sums = reinterpret_cast<float*>(ws + w.sums);
-  loss_rows_kernel<<<1, 1024, 0, stream>>>(p.M, p.targets, p.target64, a.len, offs, index, pos, nullptr, nullptr);
+  if ((rc = launch(loss_rows_kernel, 1, 1024, p.top > 0, stream, p.M, p.targets, p.target64, a.len, offs, index, pos, nullptr,
+                   nullptr)) != GEMM_OK)
+    return rc;
   a.count = reinterpret_cast<const uint32_t*>(offs + 1);
   a.index = index;
   a.row = reinterpret_cast<const float4*>(ws + w.row);
@@ -467,10 +546,10 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   f.z_coef = p.z_coef;
   f.N = p.N;
   f.row = reinterpret_cast<float4*>(ws + w.row);
-  loss_gather_kernel<<<row_blocks(p.M, 8, ctx.num_sms), 256, 0, stream>>>(static_cast<const uint16_t*>(p.A), p.lda, p.M, p.K,
-                                                                          a.count, a.index, compact, w.ld_compact, true, f);
-  if ((rc = launched()) != GEMM_OK) return rc;
-  const LossOperands all = {compact, w.ld_compact, compact, w.ld_compact, p.B, p.ldb};
+  if ((rc = launch(loss_gather_kernel, row_blocks(p.M, 8, ctx.num_sms), 256, true, stream, static_cast<const uint16_t*>(p.A),
+                   p.lda, p.M, p.K, a.count, a.index, compact, w.ld_compact, true, f)) != GEMM_OK)
+    return rc;
+  const LossOperands all = {compact, w.ld_compact, compact, w.ld_compact, p.B, p.ldb, true};
   a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
   a.ld_out = w.width;
   for (uint64_t v0 = 0; v0 < p.N; v0 += w.width) {
@@ -481,41 +560,59 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
     a.first = static_cast<uint32_t>(v0);
     if ((rc = launch_loss_logits_backward(o, a, ctx, stream)) != GEMM_OK) return rc;
     a.stall_iter = 0xFFFFFFFFu;
-    GroupedProblem g = {};
+    LossProduct g = {};
     g.M = p.M;
-    g.N = n;
+    g.n = n;
     g.K = p.K;
-    g.groups = 1;
-    g.offsets = offs;
-    g.dD = a.out;
-    g.ldd = w.width;
-    g.stall_iter = 0xFFFFFFFFu;
+    g.count = a.count;
+    g.g = a.out;
+    g.ldg = w.width;
     if (p.dA != nullptr) {
-      g.B = o.B;
-      g.ldb = p.ldb;
+      g.X = o.B;
+      g.ldx = p.ldb;
       g.out = sums;
       g.ldo = w.ld_sums;
+      g.stride_o = w.stride_sums;
       g.out_f32 = true;
-      g.accumulate = v0 > 0;
-      if ((rc = launch_grouped_dgrad(g, ctx, stream)) != GEMM_OK) return rc;
+      g.add = v0 > 0;
+      if ((rc = launch_loss_rows(g, w.plan, ctx, stream)) != GEMM_OK) return rc;
     }
     if (p.dB != nullptr) {
-      g.A = compact;
-      g.lda = w.ld_compact;
+      g.X = compact;
+      g.ldx = w.ld_compact;
       g.out = static_cast<uint8_t*>(p.dB) + v0 * p.ld_db * (p.db_f32 ? 4 : 2);
       g.ldo = p.ld_db;
       g.out_f32 = p.db_f32;
-      g.accumulate = p.accumulate;
-      if ((rc = launch_grouped_wgrad(g, ctx, stream)) != GEMM_OK) return rc;
+      g.add = p.accumulate;
+      if (loss_matrix_ok(g.out, g.ldo, g.out_f32)) {
+        if ((rc = launch_loss_matrix(g, ctx, stream)) != GEMM_OK) return rc;
+      } else {
+        // rows that start inside sectors: the grouped product, whose warps store along rows
+        GroupedProblem d = {};
+        d.M = p.M;
+        d.N = n;
+        d.K = p.K;
+        d.groups = 1;
+        d.offsets = offs;
+        d.dD = a.out;
+        d.ldd = w.width;
+        d.A = compact;
+        d.lda = w.ld_compact;
+        d.out = g.out;
+        d.ldo = p.ld_db;
+        d.out_f32 = p.db_f32;
+        d.accumulate = p.accumulate;
+        d.stall_iter = 0xFFFFFFFFu;
+        if ((rc = launch_grouped_wgrad(d, ctx, stream)) != GEMM_OK) return rc;
+      }
     }
   }
   if (p.dA == nullptr) return GEMM_OK;
-  const unsigned blocks = row_blocks(p.M, 8, ctx.num_sms);
-  if (p.da_f32)
-    loss_spread_kernel<<<blocks, 256, 0, stream>>>(sums, w.ld_sums, pos, p.M, p.K, static_cast<float*>(p.dA), p.ld_da);
-  else
-    loss_spread_kernel<<<blocks, 256, 0, stream>>>(sums, w.ld_sums, pos, p.M, p.K, static_cast<uint16_t*>(p.dA), p.ld_da);
-  return launched();
+  const unsigned blocks = row_blocks(static_cast<uint64_t>(p.M) * ((p.K + 127) / 128), 8, ctx.num_sms);
+  return p.da_f32 ? launch(loss_spread_kernel<float>, blocks, 256, true, stream, sums, w.ld_sums, w.stride_sums, w.plan.split,
+                           pos, p.M, p.K, static_cast<float*>(p.dA), p.ld_da)
+                  : launch(loss_spread_kernel<uint16_t>, blocks, 256, true, stream, sums, w.ld_sums, w.stride_sums,
+                           w.plan.split, pos, p.M, p.K, static_cast<uint16_t*>(p.dA), p.ld_da);
 }
 
 }  // namespace gb300

@@ -57,6 +57,7 @@ struct LossOperands {
   uint64_t ld_compact;
   const void* B;
   uint64_t ldb;
+  bool chained;                // the launch follows another kernel of its call
 };
 // Which tiles: rounds of them over the SMs, each as long as its loads or MMAs.
 struct LossTiles {
@@ -84,5 +85,27 @@ inline LossTiles loss_tiles(uint64_t M, uint64_t N, uint64_t K) {
 int launch_loss_logits_forward(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_t* slots,
                                cudaStream_t stream);
 int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, cudaStream_t stream);
+
+// The products with a piece of the logits' gradient (loss_products.cuh).
+struct LossProduct {
+  uint32_t M, n, K;            // rows at most, the piece's columns, width
+  const uint32_t* count;
+  const void* g;               // [M, n]
+  const void* X;               // rows: B's rows of the piece; matrix: the compact rows of A
+  uint64_t ldg, ldx;
+  void* out;                   // rows: [split][M][K] fp32; matrix: [n, K]
+  uint64_t ldo, stride_o;
+  bool out_f32, add;
+};
+// How the product to the rows is dealt out: CTAs that share a tile, columns of a tile,
+// parts of the reduction.
+struct LossRowsPlan {
+  uint32_t cg, nt, split;
+};
+LossRowsPlan loss_rows_plan(uint64_t M, uint64_t n, uint64_t K);
+int launch_loss_rows(const LossProduct& p, const LossRowsPlan& plan, const LaunchCtx& ctx, cudaStream_t stream);
+// Whether the product to the matrix can be stored at `out`: rows that start on 32 bytes.
+bool loss_matrix_ok(const void* out, uint64_t ldo, bool out_f32);
+int launch_loss_matrix(const LossProduct& p, const LaunchCtx& ctx, cudaStream_t stream);
 
 }  // namespace gb300

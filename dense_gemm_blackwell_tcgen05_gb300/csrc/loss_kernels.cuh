@@ -54,7 +54,7 @@ struct LossArgs {
   float* entry_z;              // [M] or [M][top], by all rows: the entries' logits
   // backward
   const float4* row;           // [count] (lse log2(e), gq, gs, gt)
-  uint16_t* out;               // [count][ld_out] the gradient's piece
+  uint16_t* out;               // [count][ld_out] the gradient's piece; zeros up to a multiple of 64 rows
   uint64_t ld_out;
   unsigned long long* status;
   unsigned long long timeout_ns;
@@ -157,12 +157,15 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
     tmem_alloc<CG>(smem_addr(tmem_slot), C::TMEM_COLS);
     tmem_relinquish<CG>();
   }
+  grid_dependents_launch();
   tc_fence_before_sync();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
+  // (every thread: the rows, their number and their entries are earlier kernels')
+  grid_dependency_wait();
   const uint32_t count = args.count != nullptr ? min(*args.count, args.M) : args.M;
   const uint32_t rbs = (count + C::LT - 1) / C::LT, vts = (args.N + NT - 1) / NT;
   const uint32_t tiles = rbs * vts;
@@ -415,9 +418,12 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
       } else {
         const float4 r = live ? args.row[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         uint16_t* const o = args.out + static_cast<uint64_t>(row) * args.ld_out + n0;
+        // the product that sums over rows takes 64 at a time
+        const uint32_t padded = min((count + 63) / 64 * 64, args.M);
+        const bool stored = row < padded;
         if (!acc_wait()) break;
         const uint32_t b = j & 1u;
-        if (any) {
+        if (row - lane < padded) {
 #pragma unroll 1
           for (uint32_t i = 0; i < C::NCH; ++i) {
             uint32_t v[32];
@@ -437,12 +443,13 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
                 if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
               }
             }
-            if (live) {
+            if (stored) {
 #pragma unroll
               for (uint32_t h = 0; h < 2; ++h) {
                 uint32_t x[8];
+                // (a padding row's accumulator is whatever its operand's rows held)
 #pragma unroll
-                for (uint32_t e = 0; e < 8; ++e) x[e] = pack_bf16x2(g[16 * h + 2 * e], g[16 * h + 2 * e + 1]);
+                for (uint32_t e = 0; e < 8; ++e) x[e] = live ? pack_bf16x2(g[16 * h + 2 * e], g[16 * h + 2 * e + 1]) : 0u;
                 st_global_v8(o + 32 * i + 16 * h, x);
               }
             }

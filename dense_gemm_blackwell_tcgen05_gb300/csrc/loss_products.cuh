@@ -1,0 +1,333 @@
+// The two products with a piece of the logits' gradient g [rows, n] (bf16, compact rows,
+// zeros in the rows between `count` and the next multiple of 64):
+//
+//     Rows    sums[s][r, k] (+)= sum over the s-th part of the piece's v of g[r, v] B[v, k]
+//     Matrix  dB[v, k]      (+)= sum_r g[r, v] A[r, k]
+//
+// Output rows sit in the TMEM lanes (the MMA's M), the width in its columns (N): a width
+// that fills no tile costs what it holds, in steps of 32 (16 on one CTA), and a thread
+// stores its row's elements in whole sectors.  Rows has few tiles and a long reduction,
+// so it is dealt to the clusters in `split` parts, whose sums lie apart and are joined in
+// order: the same bits every time.  Matrix has many tiles.
+//
+// Persistent, warp-specialised like the other products: a TMA producer, an MMA issuer with
+// two accumulators, eight epilogue warps (two per lane quarter, alternating 32-column
+// chunks).
+#pragma once
+
+#include "gemm_kernels.cuh"
+#include "grouped_kernels.cuh"
+#include "ptx_grouped.cuh"
+
+namespace gb300 {
+
+enum class LossOp { Rows, Matrix };
+
+struct LossProductArgs {
+  uint32_t M, n, K;            // rows at most, columns of the piece, width
+  const uint32_t* count;       // rows that count
+  uint32_t nt;                 // columns of a tile, a multiple of 32
+  uint32_t split;              // Rows: parts of the reduction
+  uint32_t add;                // out += instead of out =
+  void* out;
+  uint64_t ldo, stride_o;      // pitch; Rows: between the parts' sums
+  unsigned long long* status;
+  unsigned long long timeout_ns;
+};
+
+template <int CG, LossOp OP>
+struct LossProductCfg {
+  static constexpr bool ROWS = OP == LossOp::Rows;
+  static constexpr uint32_t BK = 64;
+  static constexpr uint32_t LT = 128 * CG;               // output rows per tile
+  static constexpr uint32_t NT = 128 * CG;               // columns per tile at most
+  static constexpr uint32_t P_BYTES = 128 * 128, Q_BYTES = 128 * 128;   // a CTA's 128 rows, 128 columns
+  static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
+  static constexpr uint32_t kEpiWarps = 8;
+  static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps);
+  static constexpr uint32_t BAR_BYTES = 512;
+  static constexpr uint32_t SMEM_LIMIT = 232448;
+  static constexpr uint32_t ALIGN_SLACK = 1024;
+  static constexpr uint32_t STAGES = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES) / STAGE_BYTES;
+  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + BAR_BYTES;
+  static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t ACC_COLS = 256;
+};
+
+// The wi-th item of cluster c among G: rows l0.., columns c0.., stages k0 .. k1 - 1, part s.
+template <class C>
+__device__ __forceinline__ bool loss_item(const LossProductArgs& a, uint32_t count, uint32_t c, uint32_t G, uint32_t wi,
+                                          uint32_t& l0, uint32_t& c0, uint32_t& k0, uint32_t& k1, uint32_t& s) {
+  const uint32_t rows = C::ROWS ? count : a.n;
+  const uint32_t kt_n = ((C::ROWS ? a.n : count) + C::BK - 1) / C::BK;
+  const uint32_t rb_n = (rows + C::LT - 1) / C::LT, cb_n = (a.K + a.nt - 1) / a.nt, per = rb_n * cb_n;
+  const uint32_t t = c + wi * G;
+  const uint32_t split = C::ROWS ? a.split : 1u;
+  if (t >= per * split) return false;
+  s = t / per;
+  uint32_t rb, cb;
+  tile_coords(t - s * per, rb_n, cb_n, 8u, rb, cb);
+  l0 = rb * C::LT;
+  c0 = cb * a.nt;
+  k0 = static_cast<uint32_t>(static_cast<uint64_t>(kt_n) * s / split);
+  k1 = static_cast<uint32_t>(static_cast<uint64_t>(kt_n) * (s + 1) / split);
+  return true;
+}
+
+// 32 fp32 values, or their bf16 roundings, at p: `cols` of them (at most 32); p on 32 bytes.
+template <class T, bool ADD>
+__device__ __forceinline__ void store_row_chunk(T* p, const uint32_t (&v)[32], uint32_t cols) {
+  constexpr uint32_t kPer = 32 / sizeof(T);              // elements of a sector
+  if constexpr (ADD) {
+    float had[32];
+    if (cols >= 32) {
+#pragma unroll
+      for (uint32_t i = 0; i < 32 / kPer; ++i) {
+        const uint4* const q = reinterpret_cast<const uint4*>(p + i * kPer);
+        const uint4 x = q[0], y = q[1];
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (uint32_t e = 0; e < kPer; ++e)
+          had[i * kPer + e] = sizeof(T) == 4 ? __uint_as_float(w[e % 8]) : bf16_bits_to_f32((w[e / 2 % 8] >> (16 * (e % 2))) & 0xFFFFu);
+      }
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < 32; ++e) {
+        if constexpr (sizeof(T) == 4) had[e] = e < cols ? __uint_as_float(p[e]) : 0.0f;
+        else had[e] = e < cols ? bf16_bits_to_f32(p[e]) : 0.0f;
+      }
+    }
+    uint32_t x[32];
+#pragma unroll
+    for (uint32_t e = 0; e < 32; ++e) x[e] = __float_as_uint(had[e] + __uint_as_float(v[e]));
+    store_row_chunk<T, false>(p, x, cols);
+  } else {
+#pragma unroll
+    for (uint32_t i = 0; i < 32 / kPer; ++i) {
+      uint32_t x[8];
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 4) x[e] = v[i * 8 + e];
+        else x[e] = pack_bf16x2(__uint_as_float(v[i * 16 + 2 * e]), __uint_as_float(v[i * 16 + 2 * e + 1]));
+      }
+      if ((i + 1) * kPer <= cols) {
+        st_global_v8(p + i * kPer, x);
+      } else {
+#pragma unroll
+        for (uint32_t e = 0; e < kPer; ++e)
+          if (i * kPer + e < cols) {
+            if constexpr (sizeof(T) == 4) p[i * kPer + e] = x[e];
+            else p[i * kPer + e] = static_cast<T>(x[e / 2] >> (16 * (e % 2)));
+          }
+      }
+    }
+  }
+}
+
+// T: uint32_t (fp32) or uint16_t (bf16).
+template <int CG, LossOp OP, class T>
+__global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
+    loss_product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                        const LossProductArgs args) {
+  using C = LossProductCfg<CG, OP>;
+  constexpr bool P_MN = !C::ROWS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bar0 = base + C::STAGES * C::STAGE_BYTES;
+  const auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
+  const auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (C::STAGES + s); };
+  constexpr uint32_t kAccBar0 = 2 * C::STAGES;
+  const auto accf_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + b); };
+  const auto acce_bar = [&](uint32_t b) { return bar0 + 8 * (kAccBar0 + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8 * (kAccBar0 + 4);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + (bar0 - base) + 8 * (kAccBar0 + 5));
+  volatile uint32_t* const abort_flag = tmem_slot + 1;
+
+  const uint32_t warp = warp_idx_sync();
+  const uint32_t lane = lane_idx();
+  const uint32_t rank = (CG == 2) ? cluster_cta_rank() : 0u;
+  const bool leader = rank == 0;
+  const uint32_t cluster_id = blockIdx.x / CG;
+  const uint32_t G = gridDim.x / CG;
+  const Watchdog wd{args.status, args.timeout_ns, abort_flag};
+
+  // ---- set-up ------------------------------------------------------------------
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmP);
+      tma_prefetch_desc(&tmQ);
+      *abort_flag = 0u;
+    }
+    for (uint32_t i = lane; i < kAccBar0 + 5; i += 32)
+      mbar_init(bar0 + 8 * i, (i == kAccBar0 + 2 || i == kAccBar0 + 3) ? C::kEpiWarps * CG : 1u);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_addr(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish<CG>();
+  }
+  grid_dependents_launch();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  // (every thread: the number of rows is an earlier kernel's)
+  grid_dependency_wait();
+  const uint32_t count = min(*args.count, args.M);
+  uint32_t l0, c0, k0, k1, part;
+
+  if (warp == 0) {
+    // ==================== TMA producer: one thread ==============================
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_last();
+      uint32_t it = 0;
+      bool ok = true;
+      for (uint32_t wi = 0; ok && loss_item<C>(args, count, cluster_id, G, wi, l0, c0, k0, k1, part); ++wi) {
+        const uint32_t live = min(args.nt, args.K - c0);
+        const uint32_t h = mma_n<CG>(live) / CG;         // columns this CTA contributes to the MMA
+        const uint32_t q_boxes = (h + 63) / 64;
+        const uint32_t tx = C::P_BYTES + q_boxes * 8192;
+        const int32_t px = static_cast<int32_t>(l0 + rank * 128), qx = static_cast<int32_t>(c0 + rank * h);
+        for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
+          const uint32_t s = it % C::STAGES;
+          if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = base + s * C::STAGE_BYTES;
+          const int32_t k = static_cast<int32_t>(kt * C::BK);
+          uint32_t bar = full_bar(s);
+          if constexpr (CG == 2) bar = mapa_shared(full_bar(s), 0);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), CG * tx);
+          const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y) {
+            if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, 0, pol);
+            else tma_load_3d(dst, m, bar, x, y, 0, pol);
+          };
+          if constexpr (P_MN) {
+            load(sb, &tmP, px, k);
+            load(sb + 8192, &tmP, px + 64, k);
+          } else {
+            load(sb, &tmP, k, px);
+          }
+          for (uint32_t b = 0; b < q_boxes; ++b)
+            load(sb + C::P_BYTES + b * 8192, &tmQ, qx + static_cast<int32_t>(64 * b), k);
+        }
+      }
+      // Exit path after a give-up: let this CTA's issued loads land first.
+      if (*abort_flag && leader) {
+        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
+        for (uint32_t i = first; i < it; ++i)
+          drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
+      }
+    }
+  } else if (warp == 1) {
+    // ==================== MMA issuer: one thread of the leader CTA ==============
+    if (leader && lane == 0) {
+      uint32_t it = 0, j = 0;
+      bool ok = true, issued = false;
+      for (uint32_t wi = 0; ok && loss_item<C>(args, count, cluster_id, G, wi, l0, c0, k0, k1, part); ++wi) {
+        if (k0 == k1) continue;
+        const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - c0)), 1u, P_MN, true);
+        const uint32_t b = j & 1u;
+        // accumulator b must have been drained by every epilogue warp
+        if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) break;
+        ++j;
+        tc_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
+        constexpr uint32_t kUnroll = CG == 2 ? 4 : 1;
+#pragma unroll kUnroll
+        for (uint32_t kt = k0; kt < k1; ++kt) {
+          const uint32_t s = it % C::STAGES;
+          if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sb = base + s * C::STAGE_BYTES;
+          const uint64_t pd = P_MN ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
+          const uint64_t qd = smem_desc_mn_sw128(sb + C::P_BYTES);
+          // 16 k per MMA: 32 bytes along a K-major row, 16 rows of an MN-major tile
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            mma_bf16<CG>(d_tmem, pd + (P_MN ? 128 : 2) * k, qd + 128 * k, idesc, (kt != k0 || k != 0u));
+          commit_to<CG>(empty_bar(s));   // frees the stage once these MMAs finish
+          issued = true;
+          ++it;
+        }
+        if (!ok) break;
+        commit_to<CG>(accf_bar(b));
+      }
+      // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
+      if (issued) {
+        if constexpr (CG == 1)
+          tc_commit(drain_bar);
+        else
+          tc_commit_pair_multicast(drain_bar, 0x1);
+        drain_wait(drain_bar, 0, wd, kSiteMmaDrain);
+      }
+    }
+  } else {
+    // ==================== epilogue: eight warps, two per TMEM lane quarter =======
+    const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
+    const uint32_t eg = (warp - 2u) / 4u;      // chunks eg, eg + 2, ...
+    const uint32_t rows = C::ROWS ? count : args.n;
+    uint32_t j = 0;
+    for (uint32_t wi = 0; loss_item<C>(args, count, cluster_id, G, wi, l0, c0, k0, k1, part); ++wi) {
+      const uint32_t live = min(args.nt, args.K - c0), nch = (live + 31) / 32;
+      const uint32_t row = l0 + rank * 128 + q * 32 + lane;
+      T* const o = static_cast<T*>(args.out) + part * args.stride_o + row * args.ldo + c0;
+      const bool empty = k0 == k1;             // nothing is added up: zeros
+      if (empty && args.add) continue;
+      const uint32_t b = j & 1u;
+      if (!empty) {
+        if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) break;
+        tc_fence_after_sync();
+        ++j;
+      }
+      bool held = !empty;
+      // The hand-back of an accumulator whose reads are complete: it publishes nothing.
+      const auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 1) mbar_arrive(acce_bar(b));
+          else mbar_arrive_cluster_relaxed(mapa_shared(acce_bar(b), 0));
+        }
+        held = false;
+      };
+#pragma unroll 1
+      for (uint32_t ch = eg; ch < nch; ch += 2) {
+        uint32_t v[32];
+        if (!empty) {
+          tmem_ld_32x32b_x32_sync(tmem_base + ((q * 32u) << 16) + b * C::ACC_COLS + ch * 32, v);
+          if (ch + 2 >= nch) release();   // all of it is in registers
+        } else {
+#pragma unroll
+          for (uint32_t e = 0; e < 32; ++e) v[e] = 0u;
+        }
+        if (row < rows) {
+          const uint32_t cols = min(32u, live - ch * 32);
+          if (args.add) store_row_chunk<T, true>(o + ch * 32, v, cols);
+          else store_row_chunk<T, false>(o + ch * 32, v, cols);
+        }
+      }
+      if (held) release();   // (a warp without a chunk)
+    }
+  }
+
+  // ---- teardown: every role is done with TMEM and with the peer's barriers ----
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc<CG>(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace gb300

@@ -100,8 +100,9 @@ def test_cross_entropy(M, N, K, exact):
 
 
 @pytest.mark.parametrize("exact", [True, False])
+@pytest.mark.parametrize("odd", [True, False])
 @pytest.mark.parametrize("M, N, K", SHAPES)
-def test_cross_entropy_gradient(M, N, K, exact):
+def test_cross_entropy_gradient(M, N, K, odd, exact):
     r, A, B = problem(M, N, K, exact, seed=1)
     scale = scale_of(K, exact)
     dloss = torch.randn(M, generator=r, device="cuda")
@@ -111,7 +112,9 @@ def test_cross_entropy_gradient(M, N, K, exact):
         live = targets >= 0
         t = ref.target_matrix(targets, N, smoothing)
         lse = ref.forward(A, B, t, torch.zeros(M, device="cuda", dtype=torch.float64), live, scale)[1].float()
-        (_, dA), (_, dB) = bufs = marked(M, K, da, 3, 1), marked(N, K, db, 5, 1)
+        # rows that start on an element, and on 32 bytes
+        (_, dA), (_, dB) = bufs = (marked(M, K, da, 3, 1), marked(N, K, db, 5, 1)) if odd else \
+            (marked(M, K, da, -K % 16), marked(N, K, db, -K % 16 + 16))
         got = g.matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale=scale, label_smoothing=smoothing, z_loss=z_loss,
                                           dA=dA, dB=dB)
         ok()
@@ -216,11 +219,12 @@ def test_a_sure_row_keeps_its_small_gradient():
     assert (want[:, 5].abs() > 100 * 2.0 ** -19).sum() >= 3
 
 
+@pytest.mark.parametrize("K", [72, 80, 528])
 @pytest.mark.parametrize("top", [0, 9])
-@pytest.mark.parametrize("M", [200, 700])
-def test_pieces_of_the_vocabulary(M, top):
+@pytest.mark.parametrize("M", [100, 200, 700])
+def test_pieces_of_the_vocabulary(M, top, K):
     """A vocabulary of several pieces, entries on both sides of each border."""
-    N, K = 10007, 72
+    N = 10007
     r, A, B = problem(M, N, K, True, seed=4)
     scale = scale_of(K, True)
     dloss = torch.randn(M, generator=r, device="cuda")
@@ -336,7 +340,7 @@ def test_far_logits():
 
 
 @pytest.mark.parametrize("db", [BF16, F32])
-@pytest.mark.parametrize("M, N, K", [(60, 200, 64), (500, 1000, 200), (300, 9001, 96)])
+@pytest.mark.parametrize("M, N, K", [(60, 200, 64), (500, 1000, 200), (300, 9001, 96), (300, 9001, 100), (130, 1000, 1040)])
 def test_accumulate(M, N, K, db):
     r, A, B = problem(M, N, K, True, seed=7)
     scale = scale_of(K, True)
