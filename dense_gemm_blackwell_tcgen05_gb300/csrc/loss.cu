@@ -4,33 +4,35 @@
 //
 //   forward    list     a teacher's entries of a row, sorted by token, with their
 //                       probabilities (distillation only)
-//              rows     which rows count, compact (more than kInPlace rows only)
-//              gather   their rows of A, where some are left out
+//              rows     which rows count, and a compact copy of them where some are left
+//                       out (more than kInPlace rows only)
 //              product  per tile the largest logit, the sum of exponentials and the
 //                       entries' logits (loss_kernel)
 //              finish   the tiles' results joined, losses and lse
-//   backward   list, rows, gather as above, with each row's factors; then for each
-//              piece of the vocabulary
-//              product  g = dloss dloss/dz of the piece, bf16 (loss_kernel)
-//              dA      += g B[piece]         in fp32, the reduction in parts
-//              dB[piece] (+)= g^T A
+//   backward   list, rows as above, with each row's factors; then for each piece of the
+//              vocabulary
+//              product  g = dloss dloss/dz of the piece, bf16 (loss_kernel; up to kInPlace
+//                       rows it also copies the rows that count, without the others)
+//              products dA += g B[piece] in fp32, the reduction in parts, and
+//                       dB[piece] (+)= g^T A (loss_product_kernel)
 //              spread   dA's parts joined, its rows to where they belong, zeros to the
 //                       others
 //
 // Every kernel but a call's first is launched while the one before it runs, and waits for
-// it before it touches memory.
-// Only a piece's g is held: kPieceBytes, or a piece of kLeastPiece columns.
+// it before it touches memory.  Only a piece's g is held: kPieceBytes, or a piece of
+// kLeastPiece columns.
 #include <cuda_bf16.h>
 
 #include "gemm_gb300.h"
 #include "grouped_host.h"
 #include "loss_host.h"
 #include "loss_kernels.cuh"
+#include "loss_products.cuh"
 
 namespace gb300 {
 namespace {
 
-constexpr uint32_t kInPlace = 256;             // up to so many rows, a forward pass takes them as they lie
+constexpr uint32_t kInPlace = 256;             // up to so many rows are taken as they lie
 constexpr uint64_t kPieceBytes = 256ull << 20;
 constexpr uint64_t kLeastPiece = 4096;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -38,9 +40,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 uint64_t up(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
 
 struct Layout {
-  uint64_t offs, index, pos, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
+  uint64_t count, index, pos, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
   uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
-  LossRowsPlan plan;
+  uint32_t parts;                                        // of dA's sums at most
 };
 
 Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
@@ -50,7 +52,7 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     w.bytes += up(bytes, 256);
     return at;
   };
-  w.offs = take(16);
+  w.count = take(8);
   w.index = take(4 * M);
   w.pos = take(4 * M);
   if (top > 0) {
@@ -70,8 +72,8 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     w.piece = take(2 * M * w.width);
     w.ld_sums = up(K, 32);
     w.stride_sums = M * w.ld_sums;
-    w.plan = loss_rows_plan(M, w.width < N ? w.width : N, K);
-    w.sums = take(4 * w.stride_sums * w.plan.split);
+    w.parts = loss_most_parts(M, w.width < N ? w.width : N, K);
+    w.sums = take(4 * w.stride_sums * w.parts);
   } else {
     if (M > kInPlace) w.compact = take(2 * M * w.ld_compact);
     w.entry_z = take(4 * M * (top > 0 ? top : 1));
@@ -81,10 +83,6 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     w.part_sum = take(8 * slots * w.ld_part);
   }
   return w;
-}
-
-__device__ __forceinline__ int64_t index_at(const void* p, bool wide, uint64_t i) {
-  return wide ? static_cast<const int64_t*>(p)[i] : static_cast<int64_t>(static_cast<const int32_t*>(p)[i]);
 }
 
 __device__ __forceinline__ float warp_all(float v, bool largest) {
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const void* teacher, boo
   bool wrong = false;
   uint32_t mine = 0;
   for (uint32_t i = threadIdx.x; i < top; i += blockDim.x) {
-    const int64_t id = index_at(ids, ids64, r * ld_ids + i);
+    const int64_t id = loss_index_at(ids, ids64, r * ld_ids + i);
     const float t = logit(i);
     const bool there = id >= 0 && t != -INFINITY;
     wrong |= there && id >= N;
@@ -162,114 +160,106 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const void* teacher, boo
   }
 }
 
-// One block: index[i] = the i-th row that counts, pos[r] its place (-1: left out), offs =
-// {0, their number}; a forward pass's results for the rows left out.  8192 rows at a time,
-// their flags on the way together.
-__global__ void __launch_bounds__(1024) loss_rows_kernel(uint32_t M, const void* targets, bool target64, const uint32_t* len,
-                                                         int32_t* offs, uint32_t* index, int32_t* pos, float* loss, float* lse) {
-  __shared__ uint32_t votes[256], sums[8];
-  grid_dependents_launch();
-  grid_dependency_wait();
-  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
-  uint32_t before = 0;
-  for (uint32_t r0 = 0; r0 < M; r0 += 8192) {   // (M < 2^31)
-    bool in[8];
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
-      const uint32_t r = r0 + i * 1024 + threadIdx.x;
-      in[i] = r < M && (len != nullptr ? len[r] > 0 : index_at(targets, target64, r) >= 0);
-    }
-    uint32_t vote[8];
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
-      vote[i] = __ballot_sync(0xffffffffu, in[i]);
-      if (lane == 0) votes[i * 32 + warp] = __popc(vote[i]);
-    }
-    __syncthreads();
-    // votes[w]: rows that count in the warps before w of this turn
-    if (warp < 8) {
-      const uint32_t n = votes[threadIdx.x];
-      uint32_t incl = n;
-#pragma unroll
-      for (uint32_t d = 1; d < 32; d *= 2) {
-        const uint32_t lower = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += lower;
-      }
-      votes[threadIdx.x] = incl - n;
-      if (lane == 31) sums[warp] = incl;
-    }
-    __syncthreads();
-    uint32_t base = before;
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
-      const uint32_t r = r0 + i * 1024 + threadIdx.x;
-      const uint32_t at = base + votes[i * 32 + warp] + __popc(vote[i] & ((1u << lane) - 1u));
-      if (in[i]) index[at] = r;
-      if (r < M) {
-        pos[r] = in[i] ? static_cast<int32_t>(at) : -1;
-        if (!in[i] && loss != nullptr) loss[r] = lse[r] = 0.0f;
-      }
-      base += sums[i];
-    }
-    before = base;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    offs[0] = 0;
-    offs[1] = static_cast<int32_t>(before);
-  }
-}
-
-// What a row's gradient is made of: g = gq exp(z - lse) - gs - gt (at the target; times p
-// at a list's entries).
-struct RowFactors {
-  const float* dloss;
-  uint64_t inc_dloss;
-  const float* lse;
+// Which rows count: index[i] = the i-th of them, pos[r] its place (-1: left out), count =
+// {0, their number}.  A forward pass's results for the rows left out; the compact copy of
+// the others where there are such, or for a backward pass, which also gets their factors
+// and zeros up to a multiple of 64 rows.
+struct RowsArgs {
+  uint32_t M, K, per;          // per: rows a block
   const void* targets;
-  bool target64;
-  const float* entropy;        // a list's: NaN where it is wrong
-  float scale, smoothing, z_coef;
-  uint32_t N;
+  bool target64, back;
+  const uint32_t* len;         // (nullptr: targets)
+  int32_t* count;
+  uint32_t* index;
+  int32_t* pos;
+  float *loss, *lse;
+  const uint16_t* A;
+  uint64_t lda;
+  uint16_t* compact;
+  uint64_t ld_compact;
+  LossFactors factors;
   float4* row;
 };
 
-// A warp per row that counts: its row of A (where some row is left out, or `back`) and,
-// for a backward pass, its factors, and zeros up to a multiple of 64 rows.
-__global__ void __launch_bounds__(256) loss_gather_kernel(const uint16_t* A, uint64_t lda, uint32_t M, uint32_t K,
-                                                          const uint32_t* count, const uint32_t* index, uint16_t* out,
-                                                          uint64_t ldo, bool back, const RowFactors f) {
+// Blocks of 256 threads, each for `per` rows of its own; to know their places, each counts
+// all rows: at most 1024 blocks read M targets each, from L2.
+__global__ void __launch_bounds__(256) loss_rows_kernel(const RowsArgs a) {
+  __shared__ uint32_t sums[2][8], votes[8];
   grid_dependents_launch();
   grid_dependency_wait();
-  const uint32_t lane = lane_idx(), n = *count;
-  const bool copy = back || n < M;
-  for (uint32_t i = blockIdx.x * 8 + threadIdx.x / 32; i < (back ? min((n + 63) / 64 * 64, M) : n); i += gridDim.x * 8) {
-    if (i >= n) {
-      for (uint32_t c = lane; c < ldo / 8; c += 32) reinterpret_cast<uint4*>(out + i * ldo)[c] = make_uint4(0, 0, 0, 0);
-      continue;
+  const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
+  const auto counts = [&](uint32_t r) {
+    return a.len != nullptr ? a.len[r] > 0 : loss_index_at(a.targets, a.target64, r) >= 0;
+  };
+  const uint32_t first = blockIdx.x * a.per, last = min(first + a.per, a.M);
+  uint32_t before = 0, all = 0;
+  for (uint32_t r0 = 0; r0 < a.M; r0 += 2048) {   // (M < 2^31)
+    bool in[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) in[i] = r0 + i * 256 + threadIdx.x < a.M && counts(r0 + i * 256 + threadIdx.x);
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      all += in[i] ? 1u : 0u;
+      before += in[i] && r0 + i * 256 + threadIdx.x < first ? 1u : 0u;
     }
-    const uint32_t r = index[i];
-    if (copy) {
-      const uint16_t* const from = A + r * lda;
-      uint16_t* const to = out + i * ldo;
-      const uint32_t whole = K / 8;
-      for (uint32_t c = lane; c < whole; c += 32)
-        reinterpret_cast<uint4*>(to)[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
-      if (8 * whole + lane < K) to[8 * whole + lane] = from[8 * whole + lane];
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) sums[0][warp] = before, sums[1][warp] = all;
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < 8; ++i) before += sums[0][i], all += sums[1][i];
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.count[0] = 0, a.count[1] = static_cast<int32_t>(all);
+  const bool copy = a.back || all < a.M;
+  for (uint32_t r0 = first; r0 < last; r0 += 256) {
+    const uint32_t r = r0 + threadIdx.x;
+    const bool in = r < last && counts(r);
+    const uint32_t vote = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) votes[warp] = __popc(vote);
+    __syncthreads();
+    uint32_t lower = 0, turn = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+      lower += i < warp ? votes[i] : 0u;
+      turn += votes[i];
     }
-    if (back && lane == 0) {
-      const float g = f.dloss[r * f.inc_dloss] * f.scale, l = f.lse[r];
-      float gq = g * (1.0f + 2.0f * f.z_coef * l);
-      const bool wrong = f.entropy != nullptr ? isnan(f.entropy[r]) : index_at(f.targets, f.target64, r) >= f.N;
-      if (wrong) gq = NAN;
-      f.row[i] = make_float4(l * kLog2e, gq, g * f.smoothing / static_cast<float>(f.N), g * (1.0f - f.smoothing));
+    const uint32_t at = before + lower + __popc(vote & ((1u << lane) - 1u));
+    if (r < last) {
+      a.pos[r] = in ? static_cast<int32_t>(at) : -1;
+      if (in) {
+        a.index[at] = r;
+        if (a.back) a.row[at] = loss_row_factors(a.factors, a.targets, a.target64, r);
+      } else if (!a.back) {
+        a.loss[r] = a.lse[r] = 0.0f;
+      }
     }
+    before += turn;
+    __syncthreads();
+  }
+  if (!copy) return;
+  // (a block's own writes of pos, which the last turn's barrier ordered before)
+  const uint32_t whole = a.K / 8;
+  for (uint32_t r = first + warp; r < last; r += 8) {
+    const int32_t i = a.pos[r];
+    if (i < 0) continue;
+    const uint16_t* const from = a.A + r * a.lda;
+    uint16_t* const to = a.compact + static_cast<uint32_t>(i) * a.ld_compact;
+#pragma unroll 4
+    for (uint32_t c = lane; c < whole; c += 32)
+      reinterpret_cast<uint4*>(to)[c] = __ldg(reinterpret_cast<const uint4*>(from) + c);
+    if (8 * whole + lane < a.K) to[8 * whole + lane] = from[8 * whole + lane];
+  }
+  if (a.back && blockIdx.x == gridDim.x - 1) {
+    for (uint32_t i = all + warp; i < min((all + 63) / 64 * 64, a.M); i += 8)
+      for (uint32_t c = lane; c < a.ld_compact / 8; c += 32)
+        reinterpret_cast<uint4*>(a.compact + i * a.ld_compact)[c] = make_uint4(0, 0, 0, 0);
   }
 }
 
 struct FinishArgs {
   uint32_t M, N, slots, top;
-  const uint32_t* count;       // (nullptr: all rows, in place)
+  const uint32_t* count;       // (nullptr: in place)
   const uint32_t* index;
   const float2* part;
   const float* part_sum;
@@ -282,128 +272,184 @@ struct FinishArgs {
   float *loss, *lse;
 };
 
-// A lane per row, the block's 32 warps share its partial results, joined in a fixed order.
-__global__ void __launch_bounds__(1024) loss_finish_kernel(const FinishArgs a) {
-  __shared__ float s_m[32][33], s_s[32][33], s_z[32][33];
-  grid_dependency_wait();
-  const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
-  const uint32_t n = a.count != nullptr ? *a.count : a.M;
-  const uint32_t i = blockIdx.x * 32 + lane;
-  if (blockIdx.x * 32 >= n) return;
-  const bool in = i < n;
-  const uint32_t r = in ? (a.index != nullptr ? a.index[i] : i) : 0u;
-  float m = -INFINITY, s = 0.0f, sum = 0.0f;
-  const uint32_t parts = 2 * a.slots;
-  // (a lane without a row takes the last one's, eight loads on their way at a time)
-  const uint32_t at = in ? i : n - 1;
-  for (uint32_t p0 = warp; p0 < parts; p0 += 256) {
-    float2 x[8];
-    float z[8];
+// A row's partial results: 2^top times `sum`, and the sum of its products with B.
+struct RowPart {
+  float top, sum, products;
+};
+// Joins N of them.
+template <uint32_t N>
+__device__ __forceinline__ void join(RowPart& r, const float2 (&x)[N], const float (&z)[N]) {
+  float top = r.top;
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-      const uint32_t p = p0 + 32 * k;
-      x[k] = p < parts ? a.part[p * a.ld_part + at] : make_float2(-INFINITY, 0.0f);
-      z[k] = p < parts && a.part_sum != nullptr ? a.part_sum[p * a.ld_part + at] : 0.0f;
-    }
-    float top = m;
+  for (uint32_t k = 0; k < N; ++k) top = fmaxf(top, x[k].x);
+  const float shift = top == -INFINITY ? 0.0f : top;   // (nothing yet: sums of 0)
+  r.sum *= exp2_approx(r.top - shift);
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) top = fmaxf(top, x[k].x);
-    const float shift = top == -INFINITY ? 0.0f : top;
-    s *= exp2_approx(m - shift);
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k) {
-      s += x[k].y * exp2_approx(x[k].x - shift);
-      sum += z[k];
-    }
-    m = top;
+  for (uint32_t k = 0; k < N; ++k) {
+    r.sum += x[k].y * exp2_approx(x[k].x - shift);
+    r.products += z[k];
   }
-  s_m[warp][lane] = m;
-  s_s[warp][lane] = s;
-  s_z[warp][lane] = sum;
-  __syncthreads();
-  float top = -INFINITY;
-  for (uint32_t w = 0; w < 32; ++w) top = fmaxf(top, s_m[w][lane]);
-  const float shift = top == -INFINITY ? 0.0f : top;
-  s = sum = 0.0f;
-  for (uint32_t w = 0; w < 32; ++w) {
-    s += s_s[w][lane] * exp2_approx(s_m[w][lane] - shift);
-    sum += s_z[w][lane];
-  }
-  if (a.slots == 0) {   // no width: all logits are 0
-    top = 0.0f;
-    s = static_cast<float>(a.N);
-  }
-  const float lse = kLn2 * (top + log2f(s));
+  r.top = top;
+}
+// Joins the warp's, in an order that does not depend on timing; every lane gets the result.
+__device__ __forceinline__ void join_warp(RowPart& r) {
+  const float top = warp_all(r.top, true), shift = top == -INFINITY ? 0.0f : top;
+  r.sum = warp_all(r.sum * exp2_approx(r.top - shift), false);
+  r.products = warp_all(r.products, false);
+  r.top = top;
+}
+
+// Row r's loss and lse, by one warp.
+__device__ __forceinline__ void finish_row(const FinishArgs& a, uint32_t r, RowPart p) {
+  const uint32_t lane = lane_idx();
+  if (a.slots == 0) p = RowPart{0.0f, static_cast<float>(a.N), 0.0f};   // no width: all logits are 0
+  const float lse = kLn2 * (p.top + log2f(p.sum));
   float loss;
   bool counts;
   if (a.top > 0) {
-    // sum p log p + sum p (lse - z), the entries dealt to the warps
-    const uint32_t len = in ? a.len[r] : 0u;
+    // sum p log p + sum p (lse - z)
+    const uint32_t len = a.len[r];
     const uint64_t at = static_cast<uint64_t>(r) * a.top;
     float x = 0.0f;
-    for (uint32_t e = warp; e < len; e += 32) x += a.prob[at + e] * (lse - (a.slots == 0 ? 0.0f : a.entry_z[at + e]));
-    __syncthreads();
-    s_z[warp][lane] = x;
-    __syncthreads();
-    loss = in ? a.entropy[r] : 0.0f;
-    x = 0.0f;
-    for (uint32_t w = 0; w < 32; ++w) x += s_z[w][lane];
-    loss += x;
+    for (uint32_t e = lane; e < len; e += 32) x += a.prob[at + e] * (lse - (a.slots == 0 ? 0.0f : a.entry_z[at + e]));
+    loss = a.entropy[r] + warp_all(x, false);
     counts = len > 0;
   } else {
-    const int64_t t = in ? index_at(a.targets, a.target64, r) : -1;
+    const int64_t t = loss_index_at(a.targets, a.target64, r);
     counts = t >= 0;
     const float z = a.slots != 0 && counts && t < a.N ? a.entry_z[r] : 0.0f;
     loss = (1.0f - a.smoothing) * (lse - z) + a.z_coef * lse * lse;
-    if (a.smoothing > 0.0f) loss += a.smoothing * (lse - a.scale * sum / static_cast<float>(a.N));
+    if (a.smoothing > 0.0f) loss += a.smoothing * (lse - a.scale * p.products / static_cast<float>(a.N));
     if (t >= a.N) loss = NAN;
   }
-  if (warp == 0 && in) {
+  if (lane == 0) {
     a.loss[r] = counts ? loss : 0.0f;
     a.lse[r] = counts ? lse : 0.0f;
   }
 }
 
-// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros.
-template <class T>
-__global__ void __launch_bounds__(256) loss_spread_kernel(const float* sums, uint64_t ld_sums, uint64_t stride_sums,
-                                                          uint32_t split, const int32_t* pos, uint32_t M, uint32_t K, T* dA,
-                                                          uint64_t ldo) {
+// In place: a warp per row, its partial results dealt to the lanes.
+__global__ void __launch_bounds__(128) loss_finish_few_kernel(const FinishArgs a) {
   grid_dependency_wait();
-  const uint32_t lane = lane_idx();
-  const bool vec = ((reinterpret_cast<uintptr_t>(dA) | (ldo * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
-  // a warp takes 128 columns of a row at a time: rows alone could be too few
+  const uint32_t lane = lane_idx(), r = blockIdx.x * 4 + threadIdx.x / 32, parts = 2 * a.slots;
+  if (r >= a.M) return;
+  RowPart p = {-INFINITY, 0.0f, 0.0f};
+  for (uint32_t p0 = lane; p0 < parts; p0 += 320) {
+    float2 x[10];
+    float z[10];
+#pragma unroll
+    for (uint32_t k = 0; k < 10; ++k) {
+      const uint32_t i = p0 + 32 * k;
+      x[k] = i < parts ? a.part[i * a.ld_part + r] : make_float2(-INFINITY, 0.0f);
+      z[k] = i < parts && a.part_sum != nullptr ? a.part_sum[i * a.ld_part + r] : 0.0f;
+    }
+    join(p, x, z);
+  }
+  join_warp(p);
+  finish_row(a, r, p);
+}
+
+// Rows that count, compact: 32 to a block, a lane per row while the 32 warps read its partial
+// results (whole lines), a warp per row from there on.
+__global__ void __launch_bounds__(1024) loss_finish_kernel(const FinishArgs a) {
+  __shared__ float s_m[32][33], s_s[32][33], s_z[32][33];
+  grid_dependency_wait();
+  const uint32_t lane = lane_idx(), warp = threadIdx.x / 32, n = *a.count, parts = 2 * a.slots;
+  if (blockIdx.x * 32 >= n) return;
+  const uint32_t at = min(blockIdx.x * 32 + lane, n - 1);
+  RowPart p = {-INFINITY, 0.0f, 0.0f};
+  for (uint32_t p0 = warp; p0 < parts; p0 += 256) {
+    float2 x[8];
+    float z[8];
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t i = p0 + 32 * k;
+      x[k] = i < parts ? a.part[i * a.ld_part + at] : make_float2(-INFINITY, 0.0f);
+      z[k] = i < parts && a.part_sum != nullptr ? a.part_sum[i * a.ld_part + at] : 0.0f;
+    }
+    join(p, x, z);
+  }
+  s_m[warp][lane] = p.top;
+  s_s[warp][lane] = p.sum;
+  s_z[warp][lane] = p.products;
+  __syncthreads();
+  const uint32_t i = blockIdx.x * 32 + warp;
+  if (i >= n) return;
+  p = RowPart{s_m[lane][warp], s_s[lane][warp], s_z[lane][warp]};
+  join_warp(p);
+  finish_row(a, a.index[i], p);
+}
+
+struct SpreadArgs {
+  LossProductArgs products;    // by which the number of parts is found
+  uint32_t clusters;
+  const int32_t* pos;          // (nullptr: in place, by targets or len)
+  const void* targets;
+  bool target64;
+  const uint32_t* len;
+  void* dA;
+  uint64_t ldo;
+};
+
+// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros.  A block per 128 columns
+// of a row where there are many parts, which its warps share; a warp where there are few.
+template <int CG, class T>
+__global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
+  __shared__ float4 joined[8][32];
+  grid_dependency_wait();
+  const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
+  const uint32_t M = a.products.M, K = a.products.K;
+  const uint32_t parts = loss_deal<CG>(a.products, a.clusters).parts;
+  const uint32_t share = parts > 4 ? 8u : 1u;            // warps a piece
+  const bool vec = ((reinterpret_cast<uintptr_t>(a.dA) | (a.ldo * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
   const uint32_t pieces = (K + 127) / 128;
-  const uint64_t units = static_cast<uint64_t>(M) * pieces;
-  for (uint64_t u = blockIdx.x * 8ull + threadIdx.x / 32; u < units; u += gridDim.x * 8ull) {
+  const uint64_t units = static_cast<uint64_t>(M) * pieces, step = static_cast<uint64_t>(gridDim.x) * (8 / share);
+  // (a block's warps take the same turns)
+  for (uint64_t u0 = blockIdx.x * static_cast<uint64_t>(8 / share); u0 < units; u0 += step) {
+    const uint64_t u = u0 + (share == 1 ? warp : 0u);
     const uint32_t r = static_cast<uint32_t>(u / pieces), c = static_cast<uint32_t>(u % pieces) * 128 + 4 * lane;
-    const int32_t i = pos[r];
-    T* const to = dA + r * ldo;
-    if (c < K) {
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (i >= 0) {
-        const float* from = sums + static_cast<uint32_t>(i) * ld_sums + c;
-#pragma unroll 8
-        for (uint32_t p = 0; p < split; ++p, from += stride_sums) {
-          const float4 y = *reinterpret_cast<const float4*>(from);
+    const bool in = u < units;
+    int32_t i = -1;
+    if (in && a.pos != nullptr) i = a.pos[r];
+    else if (in && (a.len != nullptr ? a.len[r] > 0 : loss_index_at(a.targets, a.target64, r) >= 0)) i = static_cast<int32_t>(r);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i >= 0 && c < K) {
+      const float* const from = a.products.sums + static_cast<uint32_t>(i) * a.products.ld_sums + c;
+#pragma unroll 4
+      for (uint32_t p = share == 1 ? 0u : warp; p < parts; p += share) {
+        const float4 y = *reinterpret_cast<const float4*>(from + p * a.products.stride_sums);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+    }
+    if (share > 1) {
+      joined[warp][lane] = x;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (uint32_t w = 1; w < 8; ++w) {
+          const float4 y = joined[w][lane];
           x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
       }
-      if constexpr (sizeof(T) == 2) {
-        const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-        if (vec && c + 4 <= K) {
-          *reinterpret_cast<uint2*>(to + c) = h;
-        } else {
-          const uint32_t v[2] = {h.x, h.y};
-          for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[c + e] = static_cast<T>(v[e / 2] >> (16 * (e % 2)));
-        }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    if (!in || c >= K) continue;
+    T* const to = static_cast<T*>(a.dA) + r * a.ldo;
+    if constexpr (sizeof(T) == 2) {
+      const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+      if (vec && c + 4 <= K) {
+        *reinterpret_cast<uint2*>(to + c) = h;
       } else {
-        if (vec && c + 4 <= K) {
-          *reinterpret_cast<float4*>(to + c) = x;
-        } else {
-          const float v[4] = {x.x, x.y, x.z, x.w};
-          for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[c + e] = v[e];
-        }
+        const uint32_t v[2] = {h.x, h.y};
+        for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[c + e] = static_cast<T>(v[e / 2] >> (16 * (e % 2)));
+      }
+    } else {
+      if (vec && c + 4 <= K) {
+        *reinterpret_cast<float4*>(to + c) = x;
+      } else {
+        const float v[4] = {x.x, x.y, x.z, x.w};
+        for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[c + e] = v[e];
       }
     }
   }
@@ -426,11 +472,6 @@ int launch(void (*kern)(P...), unsigned grid, unsigned block, bool chained, cuda
     return GEMM_ERR_LAUNCH;
   }
   return GEMM_OK;
-}
-
-unsigned row_blocks(uint64_t rows, uint64_t per, int num_sms) {
-  const uint64_t n = (rows + per - 1) / per, most = 16ull * static_cast<uint64_t>(num_sms);
-  return static_cast<unsigned>(n < most ? n : most);
 }
 
 int launch_list(const LossProblem& p, const Layout& w, uint8_t* ws, cudaStream_t stream) {
@@ -459,6 +500,45 @@ LossArgs logits_args(const LossProblem& p, const Layout& w, uint8_t* ws) {
   return a;
 }
 
+LossFactors factors_of(const LossProblem& p, const Layout& w, uint8_t* ws) {
+  LossFactors f = {};
+  f.dloss = p.dloss;
+  f.inc_dloss = p.inc_dloss;
+  f.lse = p.lse;
+  f.entropy = p.top > 0 ? reinterpret_cast<const float*>(ws + w.entropy) : nullptr;
+  f.scale = p.scale;
+  f.smoothing = p.smoothing;
+  f.z_coef = p.z_coef;
+  f.N = p.N;
+  return f;
+}
+
+// More than kInPlace rows: those that count, compact.
+int launch_rows(const LossProblem& p, const Layout& w, uint8_t* ws, LossArgs& a, bool back, cudaStream_t stream) {
+  RowsArgs r = {};
+  r.M = p.M;
+  r.K = p.K;
+  r.per = p.M <= 16 * 1024 ? 16u : (p.M + 1023) / 1024;
+  r.targets = p.targets;
+  r.target64 = p.target64;
+  r.back = back;
+  r.len = a.len;
+  r.count = reinterpret_cast<int32_t*>(ws + w.count);
+  r.index = reinterpret_cast<uint32_t*>(ws + w.index);
+  r.pos = reinterpret_cast<int32_t*>(ws + w.pos);
+  r.loss = p.loss;
+  r.lse = p.lse_out;
+  r.A = static_cast<const uint16_t*>(p.A);
+  r.lda = p.lda;
+  r.compact = reinterpret_cast<uint16_t*>(ws + w.compact);
+  r.ld_compact = w.ld_compact;
+  r.factors = factors_of(p, w, ws);
+  r.row = reinterpret_cast<float4*>(ws + w.row);
+  a.count = reinterpret_cast<const uint32_t*>(r.count + 1);
+  a.index = r.index;
+  return launch(loss_rows_kernel, (p.M + r.per - 1) / r.per, 256, p.top > 0, stream, r);
+}
+
 }  // namespace
 
 uint64_t loss_forward_bytes(uint64_t M, uint64_t N, uint64_t K, uint64_t top) { return layout_of(M, N, K, top, false).bytes; }
@@ -472,20 +552,10 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   LossArgs a = logits_args(p, w, ws);
   LossOperands o = {p.A, p.lda, nullptr, 0, p.B, p.ldb, p.top > 0};
   if (p.M > kInPlace) {
-    int32_t* const offs = reinterpret_cast<int32_t*>(ws + w.offs);
-    uint32_t* const index = reinterpret_cast<uint32_t*>(ws + w.index);
-    if ((rc = launch(loss_rows_kernel, 1, 1024, p.top > 0, stream, p.M, p.targets, p.target64, a.len, offs, index,
-                     reinterpret_cast<int32_t*>(ws + w.pos), p.loss, p.lse_out)) != GEMM_OK)
-      return rc;
-    a.count = reinterpret_cast<const uint32_t*>(offs + 1);
-    a.index = index;
+    if ((rc = launch_rows(p, w, ws, a, false, stream)) != GEMM_OK) return rc;
     o.compact = ws + w.compact;
     o.ld_compact = w.ld_compact;
     o.chained = true;
-    if ((rc = launch(loss_gather_kernel, row_blocks(p.M, 8, ctx.num_sms), 256, true, stream, static_cast<const uint16_t*>(p.A),
-                     p.lda, p.M, p.K, a.count, a.index, reinterpret_cast<uint16_t*>(ws + w.compact), w.ld_compact, false,
-                     RowFactors{})) != GEMM_OK)
-      return rc;
   }
   a.part = reinterpret_cast<float2*>(ws + w.part);
   a.part_sum = p.smoothing > 0.0f ? reinterpret_cast<float*>(ws + w.part_sum) : nullptr;
@@ -514,7 +584,9 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   f.entropy = reinterpret_cast<const float*>(ws + w.entropy);
   f.loss = p.loss;
   f.lse = p.lse_out;
-  return launch(loss_finish_kernel, (p.M + 31) / 32, 1024, p.K > 0 || o.chained, stream, f);
+  const bool chained = p.K > 0 || o.chained;
+  return f.count == nullptr ? launch(loss_finish_few_kernel, (p.M + 3) / 4, 128, chained, stream, f)
+                            : launch(loss_finish_kernel, (p.M + 31) / 32, 1024, chained, stream, f);
 }
 
 int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t stream) {
@@ -523,96 +595,104 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   int rc;
   if (p.top > 0 && (rc = launch_list(p, w, ws, stream)) != GEMM_OK) return rc;
   LossArgs a = logits_args(p, w, ws);
-  int32_t* const offs = reinterpret_cast<int32_t*>(ws + w.offs);
-  uint32_t* const index = reinterpret_cast<uint32_t*>(ws + w.index);
-  int32_t* const pos = reinterpret_cast<int32_t*>(ws + w.pos);
   uint16_t* const compact = reinterpret_cast<uint16_t*>(ws + w.compact);
-  float* const sums = reinterpret_cast<float*>(ws + w.sums);
-  if ((rc = launch(loss_rows_kernel, 1, 1024, p.top > 0, stream, p.M, p.targets, p.target64, a.len, offs, index, pos, nullptr,
-                   nullptr)) != GEMM_OK)
-    return rc;
-  a.count = reinterpret_cast<const uint32_t*>(offs + 1);
-  a.index = index;
-  a.row = reinterpret_cast<const float4*>(ws + w.row);
-  RowFactors f = {};
-  f.dloss = p.dloss;
-  f.inc_dloss = p.inc_dloss;
-  f.lse = p.lse;
-  f.targets = p.targets;
-  f.target64 = p.target64;
-  f.entropy = p.top > 0 ? reinterpret_cast<const float*>(ws + w.entropy) : nullptr;
-  f.scale = p.scale;
-  f.smoothing = p.smoothing;
-  f.z_coef = p.z_coef;
-  f.N = p.N;
-  f.row = reinterpret_cast<float4*>(ws + w.row);
-  if ((rc = launch(loss_gather_kernel, row_blocks(p.M, 8, ctx.num_sms), 256, true, stream, static_cast<const uint16_t*>(p.A),
-                   p.lda, p.M, p.K, a.count, a.index, compact, w.ld_compact, true, f)) != GEMM_OK)
-    return rc;
-  const LossOperands all = {compact, w.ld_compact, compact, w.ld_compact, p.B, p.ldb, true};
+  LossOperands o = {compact, w.ld_compact, compact, w.ld_compact, p.B, p.ldb, true};
+  const bool in_place = p.M <= kInPlace;
+  if (in_place) {
+    o.A = p.A;
+    o.lda = p.lda;
+    o.compact = nullptr;
+    o.chained = p.top > 0;
+    a.factors = factors_of(p, w, ws);
+    a.A = static_cast<const uint16_t*>(p.A);
+    a.lda = p.lda;
+    a.clean = compact;
+    a.ld_clean = w.ld_compact;
+    a.offsets = reinterpret_cast<int32_t*>(ws + w.count);
+  } else {
+    if ((rc = launch_rows(p, w, ws, a, true, stream)) != GEMM_OK) return rc;
+    a.row = reinterpret_cast<const float4*>(ws + w.row);
+  }
   a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
   a.ld_out = w.width;
+
+  LossProduct g = {};
+  g.M = p.M;
+  g.K = p.K;
+  g.width = static_cast<uint32_t>(w.width < p.N ? w.width : p.N);
+  g.count = a.count;
+  g.g = a.out;
+  g.ldg = w.width;
+  g.ldb = p.ldb;
+  g.A = compact;
+  g.lda = w.ld_compact;
+  g.sums = p.dA != nullptr ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
+  g.ld_sums = w.ld_sums;
+  g.stride_sums = w.stride_sums;
+  g.most = w.parts;
+  // rows that start inside sectors: the grouped product, whose warps store along rows
+  const bool whole = p.dB != nullptr && loss_matrix_ok(p.dB, p.ld_db, p.db_f32);
+  g.dB = whole ? p.dB : nullptr;
+  g.ld_db = p.ld_db;
+  g.db_f32 = p.db_f32;
+  g.add_db = p.accumulate;
+  LossProductPlan plan = {};
+  if ((g.sums != nullptr || whole) && (rc = loss_product_plan(g, ctx, &plan)) != GEMM_OK) return rc;
   for (uint64_t v0 = 0; v0 < p.N; v0 += w.width) {
     const uint32_t n = static_cast<uint32_t>(p.N - v0 < w.width ? p.N - v0 : w.width);
-    LossOperands o = all;
     o.B = static_cast<const uint16_t*>(p.B) + v0 * p.ldb;
     a.N = n;
     a.first = static_cast<uint32_t>(v0);
     if ((rc = launch_loss_logits_backward(o, a, ctx, stream)) != GEMM_OK) return rc;
     a.stall_iter = 0xFFFFFFFFu;
-    LossProduct g = {};
-    g.M = p.M;
+    a.clean = nullptr;
+    o.chained = true;
     g.n = n;
-    g.K = p.K;
-    g.count = a.count;
-    g.g = a.out;
-    g.ldg = w.width;
-    if (p.dA != nullptr) {
-      g.X = o.B;
-      g.ldx = p.ldb;
-      g.out = sums;
-      g.ldo = w.ld_sums;
-      g.stride_o = w.stride_sums;
-      g.out_f32 = true;
-      g.add = v0 > 0;
-      if ((rc = launch_loss_rows(g, w.plan, ctx, stream)) != GEMM_OK) return rc;
+    g.B = o.B;
+    void* const dB = p.dB != nullptr ? static_cast<uint8_t*>(p.dB) + v0 * p.ld_db * (p.db_f32 ? 4 : 2) : nullptr;
+    if (g.sums != nullptr || whole) {
+      g.dB = whole ? dB : nullptr;
+      if ((rc = launch_loss_products(g, plan, ctx, stream)) != GEMM_OK) return rc;
+      g.add_sums = true;
     }
-    if (p.dB != nullptr) {
-      g.X = compact;
-      g.ldx = w.ld_compact;
-      g.out = static_cast<uint8_t*>(p.dB) + v0 * p.ld_db * (p.db_f32 ? 4 : 2);
-      g.ldo = p.ld_db;
-      g.out_f32 = p.db_f32;
-      g.add = p.accumulate;
-      if (loss_matrix_ok(g.out, g.ldo, g.out_f32)) {
-        if ((rc = launch_loss_matrix(g, ctx, stream)) != GEMM_OK) return rc;
-      } else {
-        // rows that start inside sectors: the grouped product, whose warps store along rows
-        GroupedProblem d = {};
-        d.M = p.M;
-        d.N = n;
-        d.K = p.K;
-        d.groups = 1;
-        d.offsets = offs;
-        d.dD = a.out;
-        d.ldd = w.width;
-        d.A = compact;
-        d.lda = w.ld_compact;
-        d.out = g.out;
-        d.ldo = p.ld_db;
-        d.out_f32 = p.db_f32;
-        d.accumulate = p.accumulate;
-        d.stall_iter = 0xFFFFFFFFu;
-        if ((rc = launch_grouped_wgrad(d, ctx, stream)) != GEMM_OK) return rc;
-      }
+    if (dB != nullptr && !whole) {
+      GroupedProblem d = {};
+      d.M = p.M;
+      d.N = n;
+      d.K = p.K;
+      d.groups = 1;
+      d.offsets = reinterpret_cast<const int32_t*>(ws + w.count);
+      d.dD = a.out;
+      d.ldd = w.width;
+      d.A = compact;
+      d.lda = w.ld_compact;
+      d.out = dB;
+      d.ldo = p.ld_db;
+      d.out_f32 = p.db_f32;
+      d.accumulate = p.accumulate;
+      d.stall_iter = 0xFFFFFFFFu;
+      if ((rc = launch_grouped_wgrad(d, ctx, stream)) != GEMM_OK) return rc;
     }
   }
   if (p.dA == nullptr) return GEMM_OK;
-  const unsigned blocks = row_blocks(static_cast<uint64_t>(p.M) * ((p.K + 127) / 128), 8, ctx.num_sms);
-  return p.da_f32 ? launch(loss_spread_kernel<float>, blocks, 256, true, stream, sums, w.ld_sums, w.stride_sums, w.plan.split,
-                           pos, p.M, p.K, static_cast<float*>(p.dA), p.ld_da)
-                  : launch(loss_spread_kernel<uint16_t>, blocks, 256, true, stream, sums, w.ld_sums, w.stride_sums,
-                           w.plan.split, pos, p.M, p.K, static_cast<uint16_t*>(p.dA), p.ld_da);
+  g.n = g.width;
+  SpreadArgs d = {};
+  d.products = loss_product_args(g, plan, ctx);
+  d.products.dB = whole ? p.dB : nullptr;   // (whether there is one, not where)
+  d.clusters = plan.clusters;
+  d.pos = in_place ? nullptr : reinterpret_cast<const int32_t*>(ws + w.pos);
+  d.targets = p.targets;
+  d.target64 = p.target64;
+  d.len = a.len;
+  d.dA = p.dA;
+  d.ldo = p.ld_da;
+  const uint64_t units = static_cast<uint64_t>(p.M) * ((p.K + 127) / 128), most = 16ull * static_cast<uint64_t>(ctx.num_sms);
+  const unsigned blocks = static_cast<unsigned>(units < most ? units : most);
+  if (plan.cg == 2)
+    return p.da_f32 ? launch(loss_spread_kernel<2, float>, blocks, 256, true, stream, d)
+                    : launch(loss_spread_kernel<2, uint16_t>, blocks, 256, true, stream, d);
+  return p.da_f32 ? launch(loss_spread_kernel<1, float>, blocks, 256, true, stream, d)
+                  : launch(loss_spread_kernel<1, uint16_t>, blocks, 256, true, stream, d);
 }
 
 }  // namespace gb300

@@ -88,24 +88,29 @@ int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const 
 
 // The products with a piece of the logits' gradient (loss_products.cuh).
 struct LossProduct {
-  uint32_t M, n, K;            // rows at most, the piece's columns, width
+  uint32_t M, n, K, width;     // rows at most, the piece's columns, the width, the first piece's columns
   const uint32_t* count;
-  const void* g;               // [M, n]
-  const void* X;               // rows: B's rows of the piece; matrix: the compact rows of A
-  uint64_t ldg, ldx;
-  void* out;                   // rows: [split][M][K] fp32; matrix: [n, K]
-  uint64_t ldo, stride_o;
-  bool out_f32, add;
+  const void *g, *B, *A;       // [M, n], B's rows of the piece, the rows that count
+  uint64_t ldg, ldb, lda;
+  float* sums;                 // (nullptr: not wanted) [most][M][K]
+  uint64_t ld_sums, stride_sums;
+  uint32_t most;
+  bool add_sums;
+  void* dB;                    // (nullptr: not wanted) [n, K]
+  uint64_t ld_db;
+  bool db_f32, add_db;
 };
-// How the product to the rows is dealt out: CTAs that share a tile, columns of a tile,
-// parts of the reduction.
-struct LossRowsPlan {
-  uint32_t cg, nt, split;
-};
-LossRowsPlan loss_rows_plan(uint64_t M, uint64_t n, uint64_t K);
-int launch_loss_rows(const LossProduct& p, const LossRowsPlan& plan, const LaunchCtx& ctx, cudaStream_t stream);
+// Parts that the sums' reduction over a piece may be dealt in, at most.
+uint32_t loss_most_parts(uint64_t M, uint64_t width, uint64_t K);
 // Whether the product to the matrix can be stored at `out`: rows that start on 32 bytes.
 bool loss_matrix_ok(const void* out, uint64_t ldo, bool out_f32);
-int launch_loss_matrix(const LossProduct& p, const LaunchCtx& ctx, cudaStream_t stream);
+// What loss_spread_kernel has to know of these launches: CTAs that share a tile, clusters.
+struct LossProductPlan {
+  uint32_t cg, nt, clusters;
+};
+int loss_product_plan(const LossProduct& p, const LaunchCtx& ctx, LossProductPlan* plan);
+struct LossProductArgs;
+LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& ctx);
+int launch_loss_products(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& ctx, cudaStream_t stream);
 
 }  // namespace gb300

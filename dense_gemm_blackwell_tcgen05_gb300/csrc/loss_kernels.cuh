@@ -32,6 +32,17 @@
 
 namespace gb300 {
 
+// What a row's gradient is made of: g = gq exp(z - lse) - gs - gt (at the target; times p
+// at a list's entries).
+struct LossFactors {
+  const float* dloss;
+  uint64_t inc_dloss;
+  const float* lse;
+  const float* entropy;        // a list's: NaN where it is wrong (nullptr: targets)
+  float scale, smoothing, z_coef;
+  uint32_t N;                  // the whole vocabulary
+};
+
 struct LossArgs {
   uint32_t M, N, K;            // rows in all, vocabulary (of this piece, backward), width
   const uint32_t* count;       // rows that count (nullptr: all of them, in place)
@@ -53,7 +64,13 @@ struct LossArgs {
   uint32_t runs;               // one block of rows: a slot for each cluster, else for each tile of columns
   float* entry_z;              // [M] or [M][top], by all rows: the entries' logits
   // backward
-  const float4* row;           // [count] (lse log2(e), gq, gs, gt)
+  const float4* row;           // [count] (lse log2(e), gq, gs, gt) (nullptr: in place, from `factors`)
+  LossFactors factors;
+  const uint16_t* A;           // in place: rows copied to `clean` (nullptr: not by this launch),
+  uint64_t lda;                //   zeros for those left out
+  uint16_t* clean;
+  uint64_t ld_clean;
+  int32_t* offsets;            //   and {0, M}, as one group's offsets
   uint16_t* out;               // [count][ld_out] the gradient's piece; zeros up to a multiple of 64 rows
   uint64_t ld_out;
   unsigned long long* status;
@@ -106,11 +123,21 @@ __device__ __forceinline__ float select32(const float (&v)[32], uint32_t t) {
   return x;
 }
 
+__device__ __forceinline__ int64_t loss_index_at(const void* p, bool wide, uint64_t i) {
+  return wide ? static_cast<const int64_t*>(p)[i] : static_cast<int64_t>(static_cast<const int32_t*>(p)[i]);
+}
+
+// (lse log2(e), gq, gs, gt) of row r; NaN for a target or an entry past the vocabulary.
+__device__ __forceinline__ float4 loss_row_factors(const LossFactors& f, const void* targets, bool target64, uint32_t r) {
+  const float g = f.dloss[r * f.inc_dloss] * f.scale, l = f.lse[r];
+  const bool wrong = f.entropy != nullptr ? isnan(f.entropy[r]) : loss_index_at(targets, target64, r) >= f.N;
+  return make_float4(l * 1.4426950408889634f, wrong ? NAN : g * (1.0f + 2.0f * f.z_coef * l),
+                     g * f.smoothing / static_cast<float>(f.N), g * (1.0f - f.smoothing));
+}
+
 // A row's target as an offset from `first`; 0xFFFFFFFF where it lies before it or has none.
 __device__ __forceinline__ uint32_t target_offset(const LossArgs& a, uint32_t row) {
-  const int64_t t = a.target64 ? static_cast<const int64_t*>(a.target)[row]
-                               : static_cast<int64_t>(static_cast<const int32_t*>(a.target)[row]);
-  const int64_t d = t - a.first;
+  const int64_t d = loss_index_at(a.target, a.target64, row) - a.first;
   return d >= 0 && d < 0x7FFFFFFF ? static_cast<uint32_t>(d) : 0xFFFFFFFFu;
 }
 
@@ -281,13 +308,32 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
     const uint32_t eg = (warp - 2u) / 4u;      // this warp's half of the tile's columns
     uint32_t j = 0;
     bool ok = true;
+    const auto counts = [&](uint32_t r) {      // in place: whether row r does
+      return LIST ? args.len[r] > 0 : loss_index_at(args.target, args.target64, r) >= 0;
+    };
+    if (BACK && args.clean != nullptr) {
+      // rows in pieces of 8 elements, the last of them element by element
+      const uint32_t per = (args.K + 7) / 8, n = args.M * per;   // (few rows)
+      if (blockIdx.x == 0 && threadIdx.x == 64) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(args.M);
+      for (uint32_t i = blockIdx.x * 256 + threadIdx.x - 64; i < n; i += gridDim.x * 256) {
+        const uint32_t r = i / per, e = i % per * 8;
+        const uint16_t* const from = args.A + r * args.lda + e;
+        uint16_t* const to = args.clean + r * args.ld_clean + e;
+        const bool in = counts(r);
+        if (e + 8 <= args.K) {
+          *reinterpret_cast<uint4*>(to) = in ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
+        } else {
+          for (uint32_t k = 0; e + k < args.K; ++k) to[k] = in ? from[k] : uint16_t(0);
+        }
+      }
+    }
     // forward, `runs`: largest and sums over this cluster's tiles so far
     float run_m = -INFINITY, run_s = 0.0f, run_z = 0.0f;
     for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
       uint32_t rb, vt;
       tile_coords(t, rbs, vts, kLossRaster, rb, vt);
       const uint32_t row = rb * C::LT + rank * 128 + q * 32 + lane;
-      const bool live = row < count;
+      const bool live = row < count && (!BACK || args.row != nullptr || counts(row));
       const bool any = row - lane < count;               // some lane of the warp has a row
       const uint32_t n0 = vt * NT + eg * (NT / 2);       // this warp's first column
       const uint32_t cols = args.N > n0 ? min(NT / 2, args.N - n0) : 0u;
@@ -416,7 +462,8 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
           }
         }
       } else {
-        const float4 r = live ? args.row[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (live) r = args.row != nullptr ? args.row[row] : loss_row_factors(args.factors, args.target, args.target64, row);
         uint16_t* const o = args.out + static_cast<uint64_t>(row) * args.ld_out + n0;
         // the product that sums over rows takes 64 at a time
         const uint32_t padded = min((count + 63) / 64 * 64, args.M);

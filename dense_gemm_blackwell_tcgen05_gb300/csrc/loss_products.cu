@@ -1,5 +1,5 @@
-// The losses' products with a piece of the logits' gradient (loss_products.cuh): tiles,
-// parts of the reduction, launches.
+// The losses' products with a piece of the logits' gradient (loss_products.cuh): tiles and
+// launches.
 #include "launch_loss.cuh"
 #include "loss_products.cuh"
 
@@ -11,39 +11,36 @@ uint32_t tile_columns(uint64_t K, uint64_t most) {
   return static_cast<uint32_t>(ceil_div_u64(ceil_div_u64(K, ceil_div_u64(K, most)), 32) * 32);
 }
 
-template <int CG, LossOp OP, class T>
-int launch(const LossProduct& p, uint32_t nt, uint32_t split, const LaunchCtx& ctx, cudaStream_t stream) {
-  using C = LossProductCfg<CG, OP>;
+template <int CG>
+int room_of(bool f32, const LaunchCtx& ctx, uint64_t* room) {
+  using C = LossProductCfg<CG>;
+  return f32 ? loss_room<C, loss_product_kernel<CG, uint32_t>, CG>(ctx, room)
+             : loss_room<C, loss_product_kernel<CG, uint16_t>, CG>(ctx, room);
+}
+
+template <int CG, class T>
+int launch(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& ctx, cudaStream_t stream) {
+  using C = LossProductCfg<CG>;
   uint64_t room = 0;
-  if (const int rc = loss_room<C, loss_product_kernel<CG, OP, T>, CG>(ctx, &room); rc != GEMM_OK) return rc;
-  CUtensorMap g, x;
-  if (!operand_map(&g, p.g, p.n, p.M, 1, p.ldg, 0, C::ROWS ? 128 : 64) ||
-      !operand_map(&x, p.X, p.K, C::ROWS ? p.n : p.M, 1, p.ldx, 0, 64))
+  if (const int rc = room_of<CG>(p.db_f32, ctx, &room); rc != GEMM_OK) return rc;
+  CUtensorMap gr, gc, b, a;
+  if (!operand_map(&gr, p.g, p.n, p.M, 1, p.ldg, 0, 128) || !operand_map(&gc, p.g, p.n, p.M, 1, p.ldg, 0, 64) ||
+      !operand_map(&b, p.B, p.K, p.n, 1, p.ldb, 0, 64) || !operand_map(&a, p.A, p.K, p.M, 1, p.lda, 0, 64))
     return GEMM_ERR_LAUNCH;
-  const uint64_t tiles = ceil_div_u64(C::ROWS ? p.M : p.n, C::LT) * ceil_div_u64(p.K, nt) * split;
+  const uint64_t columns = ceil_div_u64(p.K, plan.nt);
+  const uint64_t tiles = (p.sums != nullptr ? ceil_div_u64(p.M, C::LT) * p.most : 0) * columns +
+                         (p.dB != nullptr ? ceil_div_u64(p.n, C::LT) : 0) * columns;
   if (tiles > 0x7FFFFFFFull) return GEMM_ERR_INVALID_ARG;
-  LossProductArgs a = {};
-  a.M = p.M;
-  a.n = p.n;
-  a.K = p.K;
-  a.count = p.count;
-  a.nt = nt;
-  a.split = split;
-  a.add = p.add ? 1u : 0u;
-  a.out = p.out;
-  a.ldo = p.ldo;
-  a.stride_o = p.stride_o;
-  a.status = ctx.status;
-  a.timeout_ns = ctx.timeout_ns;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((tiles < room ? tiles : room) * CG));
+  cfg.gridDim = dim3(plan.clusters * CG);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   loss_attributes(cfg, attr, CG, true);
-  note_schedule(cfg.gridDim.x / CG, CG, static_cast<uint32_t>(tiles), 0u, 0u, 0u, 0u);
-  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_product_kernel<CG, OP, T>, g, x, a); e != cudaSuccess) {
+  note_schedule(plan.clusters, CG, static_cast<uint32_t>(tiles), 0u, 0u, 0u, 0u);
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_product_kernel<CG, T>, gr, gc, b, a, loss_product_args(p, plan, ctx));
+      e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
@@ -53,54 +50,65 @@ int launch(const LossProduct& p, uint32_t nt, uint32_t split, const LaunchCtx& c
 
 }  // namespace
 
-// Rounds of items, each as long as its stages and a store, and the parts' sums, which are
-// written and read again: at most kMostSums of them beyond the first part.
-LossRowsPlan loss_rows_plan(uint64_t M, uint64_t n, uint64_t K) {
-  constexpr uint64_t kMostSums = 256ull << 20;
-  const uint64_t kt = ceil_div_u64(n, 64);
-  LossRowsPlan best = {2, 256, 1};
-  double least = 1e300;
-  for (uint32_t cg = M <= 128 ? 1 : 2; cg >= 1; --cg) {
-    const uint32_t nt = tile_columns(K, 128 * cg);
-    const uint64_t tiles = ceil_div_u64(M, 128 * cg) * ceil_div_u64(K, nt);
-    for (uint64_t split = 1; split <= 152 && split <= ceil_div_u64(kt, 4); ++split) {
-      if (split > 1 && split * M * K * 4 > kMostSums) break;
-      const uint64_t rounds = ceil_div_u64(tiles * split, kLossSms / cg);
-      const double t = static_cast<double>(rounds) * (static_cast<double>(ceil_div_u64(kt, split)) * (cg == 2 ? 0.30 : 0.27) + 1.5) +
-                       (cg == 2 ? 2.0 : 0.0) + static_cast<double>(split * M * K) * 8.0 / 5e6;
-      if (t < least) {
-        least = t;
-        best = {cg, nt, static_cast<uint32_t>(split)};
-      }
-    }
-  }
-  return best;
-}
-
-int launch_loss_rows(const LossProduct& p, const LossRowsPlan& plan, const LaunchCtx& ctx, cudaStream_t stream) {
-  return plan.cg == 2 ? launch<2, LossOp::Rows, uint32_t>(p, plan.nt, plan.split, ctx, stream)
-                      : launch<1, LossOp::Rows, uint32_t>(p, plan.nt, plan.split, ctx, stream);
+uint32_t loss_most_parts(uint64_t M, uint64_t width, uint64_t K) {
+  constexpr uint64_t kMostSums = 128ull << 20;
+  const uint64_t by_size = kMostSums / (4 * M * (K > 0 ? K : 1)), by_length = ceil_div_u64(width, 4 * 64);
+  const uint64_t n = by_size < by_length ? by_size : by_length;
+  return static_cast<uint32_t>(n < 1 ? 1 : n > 32 ? 32 : n);
 }
 
 bool loss_matrix_ok(const void* out, uint64_t ldo, bool out_f32) {
   return ((reinterpret_cast<uintptr_t>(out) | ldo * (out_f32 ? 4 : 2)) & 31u) == 0;
 }
 
-int launch_loss_matrix(const LossProduct& p, const LaunchCtx& ctx, cudaStream_t stream) {
-  // rounds of tiles, each as long as its loads or its store
-  const uint64_t kt = ceil_div_u64(p.M, 64);
+int loss_product_plan(const LossProduct& p, const LaunchCtx& ctx, LossProductPlan* plan) {
+  // rounds of items, each as long as its stages, or a tile's store
   const auto time = [&](uint64_t cg, double stage, double store) {
-    const uint64_t tiles = ceil_div_u64(p.n, 128 * cg) * ceil_div_u64(p.K, 128 * cg);
-    const double load = static_cast<double>(kt) * stage;
-    return static_cast<double>(ceil_div_u64(tiles, kLossSms / cg)) * (load > store ? load : store);
+    const uint64_t cb = ceil_div_u64(p.K, 128 * cg);
+    double t = 0.0;
+    if (p.sums != nullptr)
+      t += static_cast<double>(ceil_div_u64(p.M, 128 * cg) * cb * ceil_div_u64(p.width, 64)) * stage;
+    if (p.dB != nullptr) {
+      const double load = static_cast<double>(ceil_div_u64(p.M, 64)) * stage;
+      t += static_cast<double>(ceil_div_u64(p.width, 128 * cg) * cb) * (load > store ? load : store);
+    }
+    return t * static_cast<double>(cg) / static_cast<double>(kLossSms);
   };
-  const bool pair = time(2, 0.30, p.out_f32 ? 2.8 : 1.6) + 2.5 < time(1, 0.27, p.out_f32 ? 1.4 : 1.2);
-  const uint32_t nt = tile_columns(p.K, pair ? 256 : 128);
-  if (p.out_f32)
-    return pair ? launch<2, LossOp::Matrix, uint32_t>(p, nt, 1, ctx, stream)
-                : launch<1, LossOp::Matrix, uint32_t>(p, nt, 1, ctx, stream);
-  return pair ? launch<2, LossOp::Matrix, uint16_t>(p, nt, 1, ctx, stream)
-              : launch<1, LossOp::Matrix, uint16_t>(p, nt, 1, ctx, stream);
+  const bool pair = p.M > 128 && time(2, 0.30, p.db_f32 ? 2.8 : 1.6) + 2.5 < time(1, 0.27, p.db_f32 ? 1.4 : 1.2);
+  plan->cg = pair ? 2 : 1;
+  plan->nt = tile_columns(p.K, 128 * plan->cg);
+  uint64_t room = 0;
+  const int rc = pair ? room_of<2>(p.db_f32, ctx, &room) : room_of<1>(p.db_f32, ctx, &room);
+  plan->clusters = static_cast<uint32_t>(room);
+  return rc;
+}
+
+LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& ctx) {
+  LossProductArgs a = {};
+  a.M = p.M;
+  a.n = p.n;
+  a.K = p.K;
+  a.count = p.count;
+  a.nt = plan.nt;
+  a.width = p.width;
+  a.most = p.most;
+  a.sums = p.sums;
+  a.ld_sums = p.ld_sums;
+  a.stride_sums = p.stride_sums;
+  a.add_sums = p.add_sums ? 1u : 0u;
+  a.dB = p.dB;
+  a.ld_db = p.ld_db;
+  a.add_db = p.add_db ? 1u : 0u;
+  a.db_cost = p.db_f32 ? 10u : 6u;
+  a.status = ctx.status;
+  a.timeout_ns = ctx.timeout_ns;
+  return a;
+}
+
+int launch_loss_products(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& ctx, cudaStream_t stream) {
+  if (plan.cg == 2)
+    return p.db_f32 ? launch<2, uint32_t>(p, plan, ctx, stream) : launch<2, uint16_t>(p, plan, ctx, stream);
+  return p.db_f32 ? launch<1, uint32_t>(p, plan, ctx, stream) : launch<1, uint16_t>(p, plan, ctx, stream);
 }
 
 }  // namespace gb300

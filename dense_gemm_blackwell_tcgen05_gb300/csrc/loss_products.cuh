@@ -7,8 +7,9 @@
 // Output rows sit in the TMEM lanes (the MMA's M), the width in its columns (N): a width
 // that fills no tile costs what it holds, in steps of 32 (16 on one CTA), and a thread
 // stores its row's elements in whole sectors.  Rows has few tiles and a long reduction,
-// so it is dealt to the clusters in `split` parts, whose sums lie apart and are joined in
-// order: the same bits every time.  Matrix has many tiles.
+// so it is dealt to the clusters in parts, whose sums lie apart and are joined in order:
+// the same bits every time.  Matrix has many tiles.  One launch takes the items of both
+// in turn, so that one last round is ragged instead of two.
 //
 // Persistent, warp-specialised like the other products: a TMA producer, an MMA issuer with
 // two accumulators, eight epilogue warps (two per lane quarter, alternating 32-column
@@ -21,23 +22,24 @@
 
 namespace gb300 {
 
-enum class LossOp { Rows, Matrix };
-
 struct LossProductArgs {
   uint32_t M, n, K;            // rows at most, columns of the piece, width
-  const uint32_t* count;       // rows that count
+  const uint32_t* count;       // rows that count (nullptr: all of them)
   uint32_t nt;                 // columns of a tile, a multiple of 32
-  uint32_t split;              // Rows: parts of the reduction
-  uint32_t add;                // out += instead of out =
-  void* out;
-  uint64_t ldo, stride_o;      // pitch; Rows: between the parts' sums
+  uint32_t width;              // of the first piece, by which the parts are chosen
+  uint32_t most;               // parts at most
+  float* sums;                 // Rows: [parts][M][ld_sums] (nullptr: not wanted)
+  uint64_t ld_sums, stride_sums;
+  uint32_t add_sums;           // not the first piece
+  void* dB;                    // Matrix: the piece's rows (nullptr: not wanted)
+  uint64_t ld_db;
+  uint32_t add_db, db_cost;    // dB += instead of dB =; a tile's store in stages
   unsigned long long* status;
   unsigned long long timeout_ns;
 };
 
-template <int CG, LossOp OP>
+template <int CG>
 struct LossProductCfg {
-  static constexpr bool ROWS = OP == LossOp::Rows;
   static constexpr uint32_t BK = 64;
   static constexpr uint32_t LT = 128 * CG;               // output rows per tile
   static constexpr uint32_t NT = 128 * CG;               // columns per tile at most
@@ -55,24 +57,74 @@ struct LossProductCfg {
   static constexpr uint32_t ACC_COLS = 256;
 };
 
-// The wi-th item of cluster c among G: rows l0.., columns c0.., stages k0 .. k1 - 1, part s.
-template <class C>
-__device__ __forceinline__ bool loss_item(const LossProductArgs& a, uint32_t count, uint32_t c, uint32_t G, uint32_t wi,
-                                          uint32_t& l0, uint32_t& c0, uint32_t& k0, uint32_t& k1, uint32_t& s) {
-  const uint32_t rows = C::ROWS ? count : a.n;
-  const uint32_t kt_n = ((C::ROWS ? a.n : count) + C::BK - 1) / C::BK;
-  const uint32_t rb_n = (rows + C::LT - 1) / C::LT, cb_n = (a.K + a.nt - 1) / a.nt, per = rb_n * cb_n;
-  const uint32_t t = c + wi * G;
-  const uint32_t split = C::ROWS ? a.split : 1u;
-  if (t >= per * split) return false;
-  s = t / per;
+// The parts that Rows' reduction over the piece is dealt in, of `kt` stages a tile: the
+// number whose last cluster ends first, over `tiles` tiles of Rows and `others` items of
+// Matrix, `cost` stages each, dealt in turn to G clusters; each part costs its sums' way to
+// memory and back (`extra` stages over all clusters).  The 32 lanes try a number each; every
+// warp of every block, of the kernel that joins the sums too, finds the same.
+__device__ __forceinline__ uint32_t loss_parts(uint32_t tiles, uint32_t others, uint32_t kt, uint32_t cost, uint32_t extra,
+                                               uint32_t G, uint32_t most) {
+  const uint32_t s = lane_idx() + 1;
+  uint32_t time = 0xFFFFFFFFu;
+  // (what is beyond these needs no parts, and would leave 32 bits)
+  const bool few = tiles <= 0x4000u && others <= 0x100000u && kt <= 0x4000u && cost <= 0x4000u && extra <= 0x10000u;
+  if (s <= most && few) {
+    constexpr uint32_t kEnds = 5;                        // an item's first loads and last store, in stages
+    const uint32_t items = tiles * s, x = items / G, r = items - x * G;
+    const uint32_t y = others / G, p = others - y * G;
+    const uint32_t each = (kt + s - 1) / s + kEnds;
+    const uint32_t a = r == 0 ? 0u : (x + 1) * each + (y + (p > G - r ? 1u : 0u)) * cost;
+    const uint32_t b = x * each + (y + (p > 0 ? 1u : 0u)) * cost;
+    time = max(a, b) + s * extra;
+  } else if (s == 1) {
+    time = 0xFFFFFFFEu;
+  }
+  const uint32_t best = __reduce_min_sync(0xffffffffu, time);
+  return static_cast<uint32_t>(__ffs(__ballot_sync(0xffffffffu, time == best)));
+}
+
+// What all roles, and the kernel that joins the sums, know of a launch's items.
+struct LossDeal {
+  uint32_t count, rb_x, rb_y, cb, parts, items_x, items;
+};
+template <int CG>
+__device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t G) {
+  constexpr uint32_t LT = 128 * CG;
+  LossDeal d;
+  d.count = a.count != nullptr ? min(*a.count, a.M) : a.M;
+  d.cb = (a.K + a.nt - 1) / a.nt;
+  d.rb_x = a.sums != nullptr ? (d.count + LT - 1) / LT : 0u;
+  d.rb_y = a.dB != nullptr ? (a.n + LT - 1) / LT : 0u;
+  const uint32_t full_y = a.dB != nullptr ? (a.width + LT - 1) / LT : 0u;
+  const uint32_t kt_y = (d.count + 63) / 64;
+  // 4 bytes written and read of each sum at 5 TB/s; 0.3 us a stage
+  const uint32_t extra = static_cast<uint32_t>(static_cast<uint64_t>(d.count) * a.K * 8 / 1500000);
+  d.parts = loss_parts(d.rb_x * d.cb, full_y * d.cb, (a.width + 63) / 64, max(kt_y + 3, a.db_cost), extra, G, a.most);
+  d.items_x = d.rb_x * d.cb * d.parts;
+  d.items = d.items_x + d.rb_y * d.cb;
+  return d;
+}
+
+// The t-th item: rows l0.., columns c0.., stages k0 .. k1 - 1; part s of Rows, or Matrix.
+struct LossItem {
+  uint32_t l0, c0, k0, k1, s;
+  bool matrix;
+};
+template <int CG>
+__device__ __forceinline__ LossItem loss_item(const LossProductArgs& a, const LossDeal& d, uint32_t t) {
+  LossItem w;
+  w.matrix = t >= d.items_x;
+  const uint32_t rb_n = w.matrix ? d.rb_y : d.rb_x, per = rb_n * d.cb;
+  if (w.matrix) t -= d.items_x;
+  w.s = t / per;                                         // (Matrix: 0)
   uint32_t rb, cb;
-  tile_coords(t - s * per, rb_n, cb_n, 8u, rb, cb);
-  l0 = rb * C::LT;
-  c0 = cb * a.nt;
-  k0 = static_cast<uint32_t>(static_cast<uint64_t>(kt_n) * s / split);
-  k1 = static_cast<uint32_t>(static_cast<uint64_t>(kt_n) * (s + 1) / split);
-  return true;
+  tile_coords(t - w.s * per, rb_n, d.cb, 8u, rb, cb);
+  w.l0 = rb * 128 * CG;
+  w.c0 = cb * a.nt;
+  const uint32_t kt = ((w.matrix ? d.count : a.n) + 63) / 64, parts = w.matrix ? 1u : d.parts;
+  w.k0 = static_cast<uint32_t>(static_cast<uint64_t>(kt) * w.s / parts);
+  w.k1 = static_cast<uint32_t>(static_cast<uint64_t>(kt) * (w.s + 1) / parts);
+  return w;
 }
 
 // 32 fp32 values, or their bf16 roundings, at p: `cols` of them (at most 32); p on 32 bytes.
@@ -125,13 +177,14 @@ __device__ __forceinline__ void store_row_chunk(T* p, const uint32_t (&v)[32], u
   }
 }
 
-// T: uint32_t (fp32) or uint16_t (bf16).
-template <int CG, LossOp OP, class T>
-__global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
-    loss_product_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+// T: dB's elements, uint32_t (fp32) or uint16_t (bf16).  Maps: g by its rows (boxes of 128)
+// and by its columns, B's piece and the rows of A (boxes of 64 x 64).
+template <int CG, class T>
+__global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
+    loss_product_kernel(const __grid_constant__ CUtensorMap tmGr, const __grid_constant__ CUtensorMap tmGc,
+                        const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
                         const LossProductArgs args) {
-  using C = LossProductCfg<CG, OP>;
-  constexpr bool P_MN = !C::ROWS;
+  using C = LossProductCfg<CG>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -157,8 +210,10 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
   // ---- set-up ------------------------------------------------------------------
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&tmP);
-      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmGr);
+      tma_prefetch_desc(&tmGc);
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmA);
       *abort_flag = 0u;
     }
     for (uint32_t i = lane; i < kAccBar0 + 5; i += 32)
@@ -177,8 +232,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // (every thread: the number of rows is an earlier kernel's)
   grid_dependency_wait();
-  const uint32_t count = min(*args.count, args.M);
-  uint32_t l0, c0, k0, k1, part;
+  const LossDeal deal = loss_deal<CG>(args, G);
 
   if (warp == 0) {
     // ==================== TMA producer: one thread ==============================
@@ -186,13 +240,15 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
       const uint64_t pol = l2_policy_evict_last();
       uint32_t it = 0;
       bool ok = true;
-      for (uint32_t wi = 0; ok && loss_item<C>(args, count, cluster_id, G, wi, l0, c0, k0, k1, part); ++wi) {
-        const uint32_t live = min(args.nt, args.K - c0);
+      for (uint32_t t = cluster_id; ok && t < deal.items; t += G) {
+        const LossItem w = loss_item<CG>(args, deal, t);
+        const uint32_t live = min(args.nt, args.K - w.c0);
         const uint32_t h = mma_n<CG>(live) / CG;         // columns this CTA contributes to the MMA
         const uint32_t q_boxes = (h + 63) / 64;
         const uint32_t tx = C::P_BYTES + q_boxes * 8192;
-        const int32_t px = static_cast<int32_t>(l0 + rank * 128), qx = static_cast<int32_t>(c0 + rank * h);
-        for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
+        const int32_t px = static_cast<int32_t>(w.l0 + rank * 128), qx = static_cast<int32_t>(w.c0 + rank * h);
+        const CUtensorMap* const tmQ = w.matrix ? &tmA : &tmB;
+        for (uint32_t kt = w.k0; kt < w.k1; ++kt, ++it) {
           const uint32_t s = it % C::STAGES;
           if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
             ok = false;
@@ -207,14 +263,14 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
             if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, 0, pol);
             else tma_load_3d(dst, m, bar, x, y, 0, pol);
           };
-          if constexpr (P_MN) {
-            load(sb, &tmP, px, k);
-            load(sb + 8192, &tmP, px + 64, k);
+          if (w.matrix) {
+            load(sb, &tmGc, px, k);
+            load(sb + 8192, &tmGc, px + 64, k);
           } else {
-            load(sb, &tmP, k, px);
+            load(sb, &tmGr, k, px);
           }
           for (uint32_t b = 0; b < q_boxes; ++b)
-            load(sb + C::P_BYTES + b * 8192, &tmQ, qx + static_cast<int32_t>(64 * b), k);
+            load(sb + C::P_BYTES + b * 8192, tmQ, qx + static_cast<int32_t>(64 * b), k);
         }
       }
       // Exit path after a give-up: let this CTA's issued loads land first.
@@ -229,9 +285,11 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
     if (leader && lane == 0) {
       uint32_t it = 0, j = 0;
       bool ok = true, issued = false;
-      for (uint32_t wi = 0; ok && loss_item<C>(args, count, cluster_id, G, wi, l0, c0, k0, k1, part); ++wi) {
-        if (k0 == k1) continue;
-        const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - c0)), 1u, P_MN, true);
+      for (uint32_t t = cluster_id; ok && t < deal.items; t += G) {
+        const LossItem w = loss_item<CG>(args, deal, t);
+        if (w.k0 == w.k1) continue;
+        const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - w.c0)), 1u, w.matrix, true);
+        const uint64_t p_step = w.matrix ? 128 : 2;   // 16 k: 16 rows of an MN-major tile, 32 bytes along a K-major row
         const uint32_t b = j & 1u;
         // accumulator b must have been drained by every epilogue warp
         if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) break;
@@ -240,7 +298,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
         const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
         constexpr uint32_t kUnroll = CG == 2 ? 4 : 1;
 #pragma unroll kUnroll
-        for (uint32_t kt = k0; kt < k1; ++kt) {
+        for (uint32_t kt = w.k0; kt < w.k1; ++kt) {
           const uint32_t s = it % C::STAGES;
           if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
             ok = false;
@@ -248,12 +306,11 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
           }
           tc_fence_after_sync();
           const uint32_t sb = base + s * C::STAGE_BYTES;
-          const uint64_t pd = P_MN ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
+          const uint64_t pd = w.matrix ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
           const uint64_t qd = smem_desc_mn_sw128(sb + C::P_BYTES);
-          // 16 k per MMA: 32 bytes along a K-major row, 16 rows of an MN-major tile
 #pragma unroll
           for (uint32_t k = 0; k < 4; ++k)
-            mma_bf16<CG>(d_tmem, pd + (P_MN ? 128 : 2) * k, qd + 128 * k, idesc, (kt != k0 || k != 0u));
+            mma_bf16<CG>(d_tmem, pd + p_step * k, qd + 128 * k, idesc, (kt != w.k0 || k != 0u));
           commit_to<CG>(empty_bar(s));   // frees the stage once these MMAs finish
           issued = true;
           ++it;
@@ -274,14 +331,14 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
     // ==================== epilogue: eight warps, two per TMEM lane quarter =======
     const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
     const uint32_t eg = (warp - 2u) / 4u;      // chunks eg, eg + 2, ...
-    const uint32_t rows = C::ROWS ? count : args.n;
     uint32_t j = 0;
-    for (uint32_t wi = 0; loss_item<C>(args, count, cluster_id, G, wi, l0, c0, k0, k1, part); ++wi) {
-      const uint32_t live = min(args.nt, args.K - c0), nch = (live + 31) / 32;
-      const uint32_t row = l0 + rank * 128 + q * 32 + lane;
-      T* const o = static_cast<T*>(args.out) + part * args.stride_o + row * args.ldo + c0;
-      const bool empty = k0 == k1;             // nothing is added up: zeros
-      if (empty && args.add) continue;
+    for (uint32_t t = cluster_id; t < deal.items; t += G) {
+      const LossItem w = loss_item<CG>(args, deal, t);
+      const uint32_t live = min(args.nt, args.K - w.c0), nch = (live + 31) / 32;
+      const uint32_t row = w.l0 + rank * 128 + q * 32 + lane;
+      const bool stored = row < (w.matrix ? args.n : deal.count);
+      const bool empty = w.k0 == w.k1;         // nothing is added up: zeros
+      if (empty && (w.matrix ? args.add_db : args.add_sums)) continue;
       const uint32_t b = j & 1u;
       if (!empty) {
         if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) break;
@@ -309,10 +366,16 @@ __global__ void __launch_bounds__(LossProductCfg<CG, OP>::kThreads, 1)
 #pragma unroll
           for (uint32_t e = 0; e < 32; ++e) v[e] = 0u;
         }
-        if (row < rows) {
-          const uint32_t cols = min(32u, live - ch * 32);
-          if (args.add) store_row_chunk<T, true>(o + ch * 32, v, cols);
-          else store_row_chunk<T, false>(o + ch * 32, v, cols);
+        if (!stored) continue;
+        const uint32_t cols = min(32u, live - ch * 32);
+        if (w.matrix) {
+          T* const o = static_cast<T*>(args.dB) + row * args.ld_db + w.c0 + ch * 32;
+          if (args.add_db) store_row_chunk<T, true>(o, v, cols);
+          else store_row_chunk<T, false>(o, v, cols);
+        } else {
+          uint32_t* const o = reinterpret_cast<uint32_t*>(args.sums) + w.s * args.stride_sums + row * args.ld_sums + w.c0 + ch * 32;
+          if (args.add_sums) store_row_chunk<uint32_t, true>(o, v, cols);
+          else store_row_chunk<uint32_t, false>(o, v, cols);
         }
       }
       if (held) release();   // (a warp without a chunk)
