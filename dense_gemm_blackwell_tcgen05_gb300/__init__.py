@@ -13,6 +13,7 @@ library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 from . import _build
@@ -860,6 +861,10 @@ def newton_schulz(G, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, ep
 
 
 # -------------------------------------------------- losses over a vocabulary
+#
+# A few rows' losses take the GPU little longer than a launch, so these calls
+# too check in one expression on the way, and work out what was wrong only once
+# something is.
 
 def _index_code(dtype):
     import torch
@@ -868,20 +873,6 @@ def _index_code(dtype):
     if dtype is torch.int32:
         return INDEX_I32
     raise TypeError("targets and ids must be int32 or int64")
-
-
-def _vocabulary(A, B):
-    """(M, N, K, lda, ldb) of the rows and the vocabulary's matrix."""
-    import torch
-    _check_2d(A, "A")
-    _check_2d(B, "B")
-    if A.dtype is not torch.bfloat16 or B.dtype is not torch.bfloat16:
-        raise TypeError("A and B must be bfloat16")
-    M, K = A.shape
-    N, KB = B.shape
-    if KB != K:
-        raise ValueError("A and B disagree on K")
-    return M, N, K, A.stride(0), B.stride(0)
 
 
 def _row_values(t, name, M, dtype=None, strided=False):
@@ -896,68 +887,72 @@ def _row_values(t, name, M, dtype=None, strided=False):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _entries(teacher, ids, M):
-    """(top, pitches, type codes) of a teacher's lists."""
-    _check_2d(teacher, "teacher")
-    _check_2d(ids, "ids")
-    if teacher.shape != ids.shape or teacher.shape[0] != M:
-        raise ValueError(f"teacher and ids must both have shape ({M}, top)")
-    return teacher.shape[1], teacher.stride(0), ids.stride(0), _out_code(teacher.dtype), _index_code(ids.dtype)
-
-
-def _loss_workspace(entry, sizes, grad, device):
+def _refuse_loss(rc, entry, A, B, of_rows, lists, outputs):
+    """Raises for what is wrong with a loss's tensors, else `rc`: of_rows are
+    (tensor, name, dtype, strided) with a value per row."""
     import torch
-    n = getattr(load(), entry)(*sizes, 1 if grad else 0)
+    _check_2d(A, "A")
+    _check_2d(B, "B")
+    if A.dtype != torch.bfloat16 or B.dtype != torch.bfloat16:
+        raise TypeError("A and B must be bfloat16")
+    M, K = A.shape
+    if B.shape[1] != K:
+        raise ValueError("A and B disagree on K")
+    for t, name in lists:
+        _check_2d(t, name)
+        if t.shape != lists[0][0].shape or t.shape[0] != M:
+            raise ValueError(f"teacher and ids must both have shape ({M}, top)")
+    for t, name, dtype, strided in of_rows:
+        _row_values(t, name, M, dtype, strided)
+    for t, name in outputs:
+        if t is not None:
+            _check_2d(t, name)
+    raise GemmError(rc, entry)
+
+
+@functools.lru_cache(maxsize=1024)
+def _loss_bytes(entry, *sizes):
+    n = getattr(load(), entry)(*sizes)
     if n < 0:
         raise GemmError(n, entry)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return n
+
+
+_CE_BYTES, _KD_BYTES = "gemm_bf16_cross_entropy_workspace_bytes", "gemm_bf16_distill_workspace_bytes"
 
 
 def cross_entropy_workspace(M: int, N: int, K: int, grad: bool = False, device=None):
     """A workspace for matmul_cross_entropy (grad: for its gradient) on M rows
     of width K and a vocabulary of N (one per stream: calls sharing a workspace
     must not overlap on the GPU)."""
-    return _loss_workspace("gemm_bf16_cross_entropy_workspace_bytes", (M, N, K), grad, device)
+    import torch
+    return torch.empty(_loss_bytes(_CE_BYTES, M, N, K, int(grad)), dtype=torch.uint8, device=device or "cuda")
 
 
 def distill_workspace(M: int, N: int, K: int, top: int, grad: bool = False, device=None):
     """The same for matmul_distill with lists of `top` entries."""
-    return _loss_workspace("gemm_bf16_distill_workspace_bytes", (M, N, K, top), grad, device)
-
-
-def _workspace_for(workspace, make, sizes, grad, device, stream):
     import torch
-    if workspace is None:
-        if stream is not None and stream != torch.cuda.current_stream():
-            raise ValueError("a call on another stream needs its own workspace")
-        return make(*sizes, grad, device)
-    return workspace
+    return torch.empty(_loss_bytes(_KD_BYTES, M, N, K, top, int(grad)), dtype=torch.uint8, device=device or "cuda")
 
 
-def _loss_outputs(M, out, device, stream):
+def _own_workspace(device, stream, entry, *sizes):
+    """A call's workspace where the caller gave none."""
     import torch
-    if out is None:
-        return tuple(_new((M,), torch.float32, device, stream) for _ in range(2))
-    loss, lse = out
-    for t, name in ((loss, "out[0]"), (lse, "out[1]")):
-        _row_values(t, name, M, torch.float32)
-    return loss, lse
+    if stream is not None and stream != torch.cuda.current_stream():
+        raise ValueError("a call on another stream needs its own workspace")
+    return torch.empty(_loss_bytes(entry, *sizes), dtype=torch.uint8, device=device)
 
 
-def _gradient_outputs(A, B, dA, dB, need_dA, need_dB, out_dtype, accumulate, stream):
-    """(dA, dB), None where not wanted, and what the entry points take of them."""
-    if accumulate and dB is None:
-        raise ValueError("accumulate needs dB")
-    dA = _output(dA, A.shape, None if dA is not None else out_dtype, A.device, stream) if need_dA or dA is not None else None
-    dB = _output(dB, B.shape, None if dB is not None else out_dtype, B.device, stream) if need_dB or dB is not None else None
-    of = []
-    for t, name in ((dA, "dA"), (dB, "dB")):
-        if t is None:
-            of.append((0, 0, DTYPE_BF16))
-            continue
-        _check_2d(t, name)
-        of.append((t.data_ptr(), t.stride(0), _out_code(t.dtype)))
-    return dA, dB, of
+def _gradient(t, like, needed, out_dtype, stream):
+    """(a gradient's tensor or None, pointer, pitch, its columns' stride, type code)."""
+    if t is None:
+        if not needed:
+            return None, 0, 0, 1, DTYPE_BF16
+        t = _output(None, like.shape, out_dtype, like.device, stream)
+    elif t.shape != like.shape:
+        raise ValueError(f"a gradient given must have shape {tuple(like.shape)}")
+    ld, unit = t.stride() if t.dim() == 2 else (0, 0)
+    return t, t.data_ptr(), ld, unit, _out_code(t.dtype)
 
 
 def matmul_cross_entropy(A, B, targets, scale: float = 1.0, label_smoothing: float = 0.0, z_loss: float = 0.0,
@@ -971,16 +966,25 @@ def matmul_cross_entropy(A, B, targets, scale: float = 1.0, label_smoothing: flo
     recorded: the gradients are matmul_cross_entropy_grad.  Without `workspace`
     (from cross_entropy_workspace) one is allocated for the call on torch's
     current stream."""
-    M, N, K, lda, ldb = _vocabulary(A, B)
-    _row_values(targets, "targets", M)
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    rc, loss, lse = GEMM_ERR_INVALID_ARG, None, None
     code = _index_code(targets.dtype)
-    loss, lse = _loss_outputs(M, out, A.device, stream)
-    ws = _workspace_for(workspace, cross_entropy_workspace, (M, N, K), False, A.device, stream)
-    rc = (_lib or load()).gemm_bf16_cross_entropy(
-        A.data_ptr(), B.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, lda, ldb, code, scale,
-        label_smoothing, z_loss, ws.data_ptr(), ws.nbytes, _raw_stream(stream, A.get_device()))
+    if A.dim() == B.dim() == 2:
+        (M, K), (N, KB) = A.shape, B.shape
+        (lda, a1), (ldb, b1) = A.stride(), B.stride()
+        loss, lse = (_new((M,), f32, A.device, stream), _new((M,), f32, A.device, stream)) if out is None else out
+        if (K == KB and a1 == b1 == 1 and A.dtype is bf16 and B.dtype is bf16 and A.is_cuda
+                and targets.shape == loss.shape == lse.shape == (M,) and loss.dtype is f32 and lse.dtype is f32
+                and targets.is_contiguous() and loss.is_contiguous() and lse.is_contiguous()):
+            if workspace is None:
+                workspace = _own_workspace(A.device, stream, _CE_BYTES, M, N, K, 0)
+            rc = (_lib or load()).gemm_bf16_cross_entropy(
+                A.data_ptr(), B.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, lda, ldb, code,
+                scale, label_smoothing, z_loss, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, A.get_device()))
     if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_cross_entropy")
+        outputs = () if loss is None else ((loss, "out[0]", f32, False), (lse, "out[1]", f32, False))
+        _refuse_loss(rc, "gemm_bf16_cross_entropy", A, B, ((targets, "targets", None, False), *outputs), (), ())
     return loss, lse
 
 
@@ -994,20 +998,29 @@ def matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale: float = 1.0, lab
     needed.  With accumulate, adds to dB.  Rows left out get zeros in dA and add
     nothing to dB, whatever A holds there."""
     import torch
-    M, N, K, lda, ldb = _vocabulary(A, B)
-    _row_values(targets, "targets", M)
-    _row_values(dloss, "dloss", M, torch.float32, strided=True)
-    _row_values(lse, "lse", M, torch.float32)
+    bf16, f32 = torch.bfloat16, torch.float32
+    if accumulate and dB is None:
+        raise ValueError("accumulate needs dB")
+    rc = GEMM_ERR_INVALID_ARG
     code = _index_code(targets.dtype)
-    dA, dB, ((pa, ld_da, ca), (pb, ld_db, cb)) = _gradient_outputs(A, B, dA, dB, need_dA, need_dB, out_dtype, accumulate,
-                                                                   stream)
-    ws = _workspace_for(workspace, cross_entropy_workspace, (M, N, K), True, A.device, stream)
-    rc = (_lib or load()).gemm_bf16_cross_entropy_grad(
-        dloss.data_ptr(), A.data_ptr(), B.data_ptr(), targets.data_ptr(), lse.data_ptr(), pa, pb, M, N, K, dloss.stride(0),
-        lda, ldb, ld_da, ld_db, code, ca, cb, scale, label_smoothing, z_loss, 1 if accumulate else 0, ws.data_ptr(),
-        ws.nbytes, _raw_stream(stream, A.get_device()))
+    if A.dim() == B.dim() == 2:
+        (M, K), (N, KB) = A.shape, B.shape
+        (lda, a1), (ldb, b1) = A.stride(), B.stride()
+        dA, pa, ld_da, da1, ca = _gradient(dA, A, need_dA, out_dtype, stream)
+        dB, pb, ld_db, db1, cb = _gradient(dB, B, need_dB, out_dtype, stream)
+        if (K == KB and a1 == b1 == da1 == db1 == 1 and A.dtype is bf16 and B.dtype is bf16 and A.is_cuda
+                and targets.shape == dloss.shape == lse.shape == (M,) and dloss.dtype is f32 and lse.dtype is f32
+                and targets.is_contiguous() and lse.is_contiguous()):
+            if workspace is None:
+                workspace = _own_workspace(A.device, stream, _CE_BYTES, M, N, K, 1)
+            rc = (_lib or load()).gemm_bf16_cross_entropy_grad(
+                dloss.data_ptr(), A.data_ptr(), B.data_ptr(), targets.data_ptr(), lse.data_ptr(), pa, pb, M, N, K,
+                dloss.stride(0), lda, ldb, ld_da, ld_db, code, ca, cb, scale, label_smoothing, z_loss,
+                1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, A.get_device()))
     if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_cross_entropy_grad")
+        _refuse_loss(rc, "gemm_bf16_cross_entropy_grad", A, B,
+                     ((targets, "targets", None, False), (dloss, "dloss", f32, True), (lse, "lse", f32, False)), (),
+                     ((dA, "dA"), (dB, "dB")))
     return dA, dB
 
 
@@ -1023,15 +1036,27 @@ def matmul_distill(A, B, teacher, ids, temperature: float = 1.0, out=None, works
     NaN.  No autograd graph is recorded: the gradients are matmul_distill_grad.
     Without `workspace` (from distill_workspace) one is allocated for the call
     on torch's current stream."""
-    M, N, K, lda, ldb = _vocabulary(A, B)
-    top, ldt, ldi, ct, ci = _entries(teacher, ids, M)
-    loss, lse = _loss_outputs(M, out, A.device, stream)
-    ws = _workspace_for(workspace, distill_workspace, (M, N, K, top), False, A.device, stream)
-    rc = (_lib or load()).gemm_bf16_distill(
-        A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, top, lda,
-        ldb, ldt, ldi, ct, ci, temperature, ws.data_ptr(), ws.nbytes, _raw_stream(stream, A.get_device()))
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    rc, loss, lse = GEMM_ERR_INVALID_ARG, None, None
+    ct, ci = _out_code(teacher.dtype), _index_code(ids.dtype)
+    if A.dim() == B.dim() == teacher.dim() == ids.dim() == 2:
+        (M, K), (N, KB) = A.shape, B.shape
+        (lda, a1), (ldb, b1), (ldt, t1), (ldi, i1) = A.stride(), B.stride(), teacher.stride(), ids.stride()
+        top = ids.shape[1]
+        loss, lse = (_new((M,), f32, A.device, stream), _new((M,), f32, A.device, stream)) if out is None else out
+        if (K == KB and a1 == b1 == t1 == i1 == 1 and A.dtype is bf16 and B.dtype is bf16 and A.is_cuda
+                and teacher.shape == ids.shape == (M, top) and loss.shape == lse.shape == (M,) and loss.dtype is f32
+                and lse.dtype is f32 and loss.is_contiguous() and lse.is_contiguous() and 1 <= top <= MAX_TOP):
+            if workspace is None:
+                workspace = _own_workspace(A.device, stream, _KD_BYTES, M, N, K, top, 0)
+            rc = (_lib or load()).gemm_bf16_distill(
+                A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, top,
+                lda, ldb, ldt, ldi, ct, ci, temperature, workspace.data_ptr(), workspace.nbytes,
+                _raw_stream(stream, A.get_device()))
     if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_distill")
+        outputs = () if loss is None else ((loss, "out[0]", f32, False), (lse, "out[1]", f32, False))
+        _refuse_loss(rc, "gemm_bf16_distill", A, B, outputs, ((teacher, "teacher"), (ids, "ids")), ())
     return loss, lse
 
 
@@ -1041,17 +1066,27 @@ def matmul_distill_grad(dloss, A, B, teacher, ids, lse, temperature: float = 1.0
     losses' own, dloss [M] float32, and the lse that it returned; arguments and
     results as in matmul_cross_entropy_grad."""
     import torch
-    M, N, K, lda, ldb = _vocabulary(A, B)
-    top, ldt, ldi, ct, ci = _entries(teacher, ids, M)
-    _row_values(dloss, "dloss", M, torch.float32, strided=True)
-    _row_values(lse, "lse", M, torch.float32)
-    dA, dB, ((pa, ld_da, ca), (pb, ld_db, cb)) = _gradient_outputs(A, B, dA, dB, need_dA, need_dB, out_dtype, accumulate,
-                                                                   stream)
-    ws = _workspace_for(workspace, distill_workspace, (M, N, K, top), True, A.device, stream)
-    rc = (_lib or load()).gemm_bf16_distill_grad(
-        dloss.data_ptr(), A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), lse.data_ptr(), pa, pb, M, N, K,
-        top, dloss.stride(0), lda, ldb, ldt, ldi, ld_da, ld_db, ct, ci, ca, cb, temperature, 1 if accumulate else 0,
-        ws.data_ptr(), ws.nbytes, _raw_stream(stream, A.get_device()))
+    bf16, f32 = torch.bfloat16, torch.float32
+    if accumulate and dB is None:
+        raise ValueError("accumulate needs dB")
+    rc = GEMM_ERR_INVALID_ARG
+    ct, ci = _out_code(teacher.dtype), _index_code(ids.dtype)
+    if A.dim() == B.dim() == teacher.dim() == ids.dim() == 2:
+        (M, K), (N, KB) = A.shape, B.shape
+        (lda, a1), (ldb, b1), (ldt, t1), (ldi, i1) = A.stride(), B.stride(), teacher.stride(), ids.stride()
+        top = ids.shape[1]
+        dA, pa, ld_da, da1, ca = _gradient(dA, A, need_dA, out_dtype, stream)
+        dB, pb, ld_db, db1, cb = _gradient(dB, B, need_dB, out_dtype, stream)
+        if (K == KB and a1 == b1 == t1 == i1 == da1 == db1 == 1 and A.dtype is bf16 and B.dtype is bf16 and A.is_cuda
+                and teacher.shape == ids.shape == (M, top) and dloss.shape == lse.shape == (M,) and dloss.dtype is f32
+                and lse.dtype is f32 and lse.is_contiguous() and 1 <= top <= MAX_TOP):
+            if workspace is None:
+                workspace = _own_workspace(A.device, stream, _KD_BYTES, M, N, K, top, 1)
+            rc = (_lib or load()).gemm_bf16_distill_grad(
+                dloss.data_ptr(), A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), lse.data_ptr(), pa, pb, M, N,
+                K, top, dloss.stride(0), lda, ldb, ldt, ldi, ld_da, ld_db, ct, ci, ca, cb, temperature,
+                1 if accumulate else 0, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, A.get_device()))
     if rc != GEMM_OK:
-        raise GemmError(rc, "gemm_bf16_distill_grad")
+        _refuse_loss(rc, "gemm_bf16_distill_grad", A, B, ((dloss, "dloss", f32, True), (lse, "lse", f32, False)),
+                     ((teacher, "teacher"), (ids, "ids")), ((dA, "dA"), (dB, "dB")))
     return dA, dB

@@ -501,3 +501,44 @@ def test_a_step_as_it_is_used():
     ref.check(dB, b.grad, tb + off.T @ h.abs().detach(), "dB")
     want, S = dH.double().T @ X.double(), dH.double().abs().T @ X.double().abs()
     ref.check(dW1, want, (32 + 2) * 2.0 ** -19 * S + 2.0 ** -24 * want.abs(), "dW1")
+
+
+def test_refusals():
+    M, N, K, top = 40, 300, 64, 6
+    r, A, B = problem(M, N, K, True, seed=12)
+    t, f = some_targets(r, M, N, torch.int64, 0.0), torch.ones(M, device="cuda")
+    teacher, ids = some_entries(r, M, N, top, torch.int32, F32, 0.0)
+    bad = [
+        (ValueError, "disagree", dict(B=B[:, :56])), (TypeError, "bfloat16", dict(A=A.half())), (TypeError, "bfloat16", dict(B=B.float())),
+        (ValueError, "CUDA", dict(B=B.cpu())), (ValueError, "2-D", dict(A=A.T)), (g.GemmError, "alignment", dict(A=A[:, 1:], B=B[:, 1:])),
+    ]
+    for error, match, change in bad:
+        x = {"A": A, "B": B, **change}
+        for call in (lambda: g.matmul_cross_entropy(x["A"], x["B"], t), lambda: g.matmul_cross_entropy_grad(f, x["A"], x["B"], t, f),
+                     lambda: g.matmul_distill(x["A"], x["B"], teacher, ids),
+                     lambda: g.matmul_distill_grad(f, x["A"], x["B"], teacher, ids, f)):
+            with pytest.raises(error, match=match):
+                call()
+    two = torch.zeros(2 * M, dtype=torch.int64, device="cuda")[::2]
+    for error, match, call in (
+            (ValueError, "targets", lambda: g.matmul_cross_entropy(A, B, t[1:])),
+            (ValueError, "contiguous", lambda: g.matmul_cross_entropy(A, B, two)),
+            (ValueError, "CUDA", lambda: g.matmul_cross_entropy(A, B, t.cpu())),
+            (ValueError, "out", lambda: g.matmul_cross_entropy(A, B, t, out=(f[1:], f))),
+            (TypeError, "out", lambda: g.matmul_cross_entropy(A, B, t, out=(f, f.double()))),
+            (TypeError, "dloss", lambda: g.matmul_cross_entropy_grad(f.half(), A, B, t, f)),
+            (ValueError, "lse", lambda: g.matmul_cross_entropy_grad(f, A, B, t, f[:5])),
+            (TypeError, "bfloat16 or float32", lambda: g.matmul_cross_entropy_grad(f, A, B, t, f, out_dtype=torch.float16)),
+            (ValueError, "dA", lambda: g.matmul_cross_entropy_grad(f, A, B, t, f, dA=torch.empty(K, M, dtype=BF16, device="cuda").T)),
+            (ValueError, "shape", lambda: g.matmul_distill(A, B, teacher, ids[:, 1:])),
+            (ValueError, "shape", lambda: g.matmul_distill(A, B, teacher[1:], ids[1:])),
+            (ValueError, "2-D", lambda: g.matmul_distill(A, B, teacher[:, 0], ids)),
+            (TypeError, "bfloat16 or float32", lambda: g.matmul_distill(A, B, teacher.half(), ids)),
+            (g.GemmError, "invalid", lambda: g.matmul_distill(A, B, teacher[:, :0], ids[:, :0])),
+            (g.GemmError, "invalid", lambda: g.matmul_distill(A, B, teacher, ids, temperature=0.0)),
+            (g.GemmError, "invalid", lambda: g.matmul_cross_entropy(A, B, t, scale=-1.0)),
+            (g.GemmError, "invalid", lambda: g.matmul_cross_entropy(A, B, t, label_smoothing=1.5)),
+            (g.GemmError, "invalid", lambda: g.matmul_cross_entropy(A, B[:0], t))):
+        with pytest.raises(error, match=match):
+            call()
+    ok()

@@ -109,12 +109,31 @@ def cpu(M=8, N=24, K=16):
 
 def test_python_refusals():
     A, B = cpu()
+    t, f = torch.zeros(8, dtype=torch.int64), torch.zeros(8)
+    teacher, ids = torch.zeros(8, 4), torch.zeros(8, 4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
-        g.matmul_cross_entropy(A, B, torch.zeros(8, dtype=torch.int64))
-    with pytest.raises(ValueError, match="2-D"):
-        g.matmul_cross_entropy(A[0], B, torch.zeros(8, dtype=torch.int64))
-    with pytest.raises(ValueError, match="2-D"):
-        g.matmul_distill(A.T, B, None, None)
+        g.matmul_cross_entropy(A, B, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        g.matmul_cross_entropy_grad(f, A, B, t, f)
+    with pytest.raises(ValueError, match="CUDA"):
+        g.matmul_distill(A, B, teacher, ids)
+    with pytest.raises(ValueError, match="CUDA"):
+        g.matmul_distill_grad(f, A, B, teacher, ids, f)
+    for bad in (A[0], A.T, A[None]):
+        with pytest.raises(ValueError, match="2-D"):
+            g.matmul_cross_entropy(bad, B, t)
+        with pytest.raises(ValueError, match="2-D"):
+            g.matmul_distill(bad, B, teacher, ids)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        g.matmul_cross_entropy(A, B, f)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        g.matmul_distill(A, B, teacher, teacher)
+    with pytest.raises(ValueError, match="accumulate"):
+        g.matmul_cross_entropy_grad(f, A, B, t, f, accumulate=True)
+    with pytest.raises(ValueError, match="accumulate"):
+        g.matmul_distill_grad(f, A, B, teacher, ids, f, accumulate=True)
+    with pytest.raises(ValueError, match="shape"):
+        g.matmul_cross_entropy_grad(f, A, B, t, f, dB=A)
     assert g.MAX_TOP == 1024
 
 
