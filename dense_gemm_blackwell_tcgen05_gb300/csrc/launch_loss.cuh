@@ -72,24 +72,26 @@ int loss_room(const LaunchCtx& ctx, uint64_t* room) {
 // Launches on min(tiles, room) clusters.  A launch over one block of rows writes a slot
 // of partial results for each cluster, any other one for each tile of columns.
 template <int CG, uint32_t NT, bool BACK, bool LIST>
-int launch_loss(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_t* slots, cudaStream_t stream) {
+int launch_loss(const LossOperands& o, LossArgs a, const LossTiles& tile, const LaunchCtx& ctx, uint32_t* slots,
+                cudaStream_t stream) {
   using C = LossCfg<CG, NT, BACK, LIST>;
   const auto kern = loss_kernel<CG, NT, BACK, LIST>;
   uint64_t room = 0;
   if (const int rc = loss_room<C, loss_kernel<CG, NT, BACK, LIST>, CG>(ctx, &room); rc != GEMM_OK) return rc;
   CUtensorMap all, compact, q;
-  if (!operand_map(&all, o.A, a.K, a.M, 1, o.lda, 0, C::P_BOX) || !operand_map(&q, o.B, a.K, a.N, 1, o.ldb, 0, C::Q_BOX))
+  if (!operand_map(&all, o.A, a.K, a.M, 1, o.lda, 0, C::P_BOX) || !operand_map(&q, o.B, a.K, a.N, 1, o.ldb, 0, tile.nt / CG))
     return GEMM_ERR_LAUNCH;
   compact = all;
   if (o.compact != nullptr && !operand_map(&compact, o.compact, a.K, a.M, 1, o.ld_compact, 0, C::P_BOX))
     return GEMM_ERR_LAUNCH;
-  const uint64_t blocks = ceil_div_u64(a.M, C::LT), columns = ceil_div_u64(a.N, NT);
+  a.nt = tile.nt;
+  const uint64_t blocks = ceil_div_u64(a.M, C::LT), columns = ceil_div_u64(a.N, a.nt);
   if (blocks > 0x7FFFFFFFull / columns) return GEMM_ERR_INVALID_ARG;
   const uint64_t tiles = blocks * columns;
   uint64_t clusters = tiles < room ? tiles : room;
   if (!BACK) {
     a.runs = blocks == 1 ? 1u : 0u;
-    const uint64_t most = LossTiles{CG, NT}.slots(a.M, a.N);
+    const uint64_t most = tile.slots(a.M, a.N);
     if (a.runs && clusters > most) clusters = most;
     *slots = static_cast<uint32_t>(a.runs ? clusters : columns);
   }
@@ -114,9 +116,8 @@ int launch_loss(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_
 template <bool BACK, bool LIST>
 int loss_pick(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, uint32_t* slots, cudaStream_t stream) {
   const LossTiles t = loss_tiles(a.M, a.N, a.K);
-  if (t.cg == 2) return launch_loss<2, 256, BACK, LIST>(o, a, ctx, slots, stream);
-  return t.nt == 128 ? launch_loss<1, 128, BACK, LIST>(o, a, ctx, slots, stream)
-                     : launch_loss<1, 64, BACK, LIST>(o, a, ctx, slots, stream);
+  return t.cg == 2 ? launch_loss<2, 256, BACK, LIST>(o, a, t, ctx, slots, stream)
+                   : launch_loss<1, 128, BACK, LIST>(o, a, t, ctx, slots, stream);
 }
 
 }  // namespace gb300

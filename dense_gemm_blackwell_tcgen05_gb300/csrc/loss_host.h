@@ -59,28 +59,40 @@ struct LossOperands {
   uint64_t ldb;
   bool chained;                // the launch follows another kernel of its call
 };
-// Which tiles: rounds of them over the SMs, each as long as its loads or MMAs.
+// A GB300's SMs, not the current device's: a workspace is sized without a device.
+constexpr uint64_t kLossSms = 152;
+// Which tiles of the logits.
 struct LossTiles {
   uint32_t cg, nt;             // CTAs that share a tile of 128 rows each, its columns
   // Partial results a forward product leaves for each row: one for each tile of columns,
   // or, over one block of rows, for each cluster.
-  uint64_t slots(uint64_t M, uint64_t N) const;
+  uint64_t slots(uint64_t M, uint64_t N) const {
+    const uint64_t columns = (N + nt - 1) / nt;
+    return M <= 128 * cg && columns > kLossSms / cg ? kLossSms / cg : columns;
+  }
 };
-// A GB300's SMs, not the current device's: a workspace is sized without a device.
-constexpr uint64_t kLossSms = 152;
-inline uint64_t LossTiles::slots(uint64_t M, uint64_t N) const {
-  const uint64_t columns = (N + nt - 1) / nt;
-  return M <= 128 * cg && columns > kLossSms / cg ? kLossSms / cg : columns;
-}
+// Rounds of tiles over the SMs, each as long as its stages' loads, at 64 bytes a clock into
+// an SM, or their MMAs, and about 1000 clocks of a tile's first loads and last results; and
+// the launch of pairs.  The width is what fills the last round: 129 rows against 32768 tokens are
+// 128 tiles of 256 columns, two rounds of 76 pairs, but 147 of 224.
 inline LossTiles loss_tiles(uint64_t M, uint64_t N, uint64_t K) {
-  const auto time = [&](uint64_t lt, uint64_t nt, uint64_t clusters, double stage) {
-    const uint64_t tiles = ((M + lt - 1) / lt) * ((N + nt - 1) / nt);
-    return static_cast<double>((tiles + clusters - 1) / clusters * ((K + 63) / 64)) * stage;
-  };
-  const double narrow = time(128, 64, kLossSms, 0.24), wide = time(128, 128, kLossSms, 0.27),
-               pair = time(256, 256, kLossSms / 2, 0.30) + 2.0;
-  if (M > 128 && pair < wide && pair < narrow) return {2, 256};
-  return {1, wide < narrow ? 128u : 64u};
+  LossTiles best = {1, 128};
+  uint64_t least = ~0ull;
+  for (uint32_t cg = 1; cg <= 2; ++cg) {
+    if (cg == 2 && M <= 128) break;
+    const uint64_t rows = M < 128 ? (M + 31) / 32 * 32 : 128;
+    for (uint32_t nt = 128 * cg; nt >= 32; nt -= 32) {
+      const uint64_t tiles = (M + 128 * cg - 1) / (128 * cg) * ((N + nt - 1) / nt), clusters = kLossSms / cg;
+      const uint64_t load = 2 * rows + 2 * nt / cg, mma = 2 * nt;
+      const uint64_t t = (tiles + clusters - 1) / clusters * ((K + 63) / 64 * (load > mma ? load : mma) + 1000) +
+                         (cg == 2 ? 3800 : 0);
+      if (t < least) {
+        least = t;
+        best = {cg, nt};
+      }
+    }
+  }
+  return best;
 }
 int launch_loss_logits_forward(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_t* slots,
                                cudaStream_t stream);

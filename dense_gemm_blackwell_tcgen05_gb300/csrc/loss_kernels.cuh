@@ -45,6 +45,7 @@ struct LossFactors {
 
 struct LossArgs {
   uint32_t M, N, K;            // rows in all, vocabulary (of this piece, backward), width
+  uint32_t nt;                 // columns of a tile, a multiple of 32
   const uint32_t* count;       // rows that count (nullptr: all of them, in place)
   const uint32_t* index;       // [count] where each of them lies among all rows (nullptr: in place)
   float c;                     // scale log2(e): exp(z) = 2^(c a.b)
@@ -78,23 +79,21 @@ struct LossArgs {
   uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
 };
 
-// LIST: a list of entries per row, else one target.
+// NT: columns of a tile at most.  LIST: a list of entries per row, else one target.
 template <int CG, uint32_t NT, bool BACK, bool LIST>
 struct LossCfg {
   static_assert(CG == 1 || CG == 2, "cta_group is 1 or 2");
   static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
   static constexpr uint32_t LT = 128 * CG;               // rows per tile
-  static constexpr uint32_t Q_ROWS = NT / CG;            // vocabulary rows staged by one CTA
   static_assert(NT % 64 == 0 && NT <= 256, "two halves of whole 32-column chunks");
   static constexpr uint32_t P_BOX = 32;                  // rows per load of A: few rows load what they need
-  static constexpr uint32_t Q_BOX = Q_ROWS;
   static constexpr uint32_t P_BYTES = 128 * 128;
-  static constexpr uint32_t Q_BYTES = Q_ROWS * 128;
+  static constexpr uint32_t Q_BYTES = NT / CG * 128;     // vocabulary rows staged by one CTA
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
   static constexpr uint32_t kEpiWarps = 8;
   static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps);
   static constexpr uint32_t SEG_TILES = BACK ? 0xFFFFFFFFu : 8u;
-  static constexpr uint32_t NCH = NT / 64;               // 32-column chunks per epilogue warp
+  static constexpr uint32_t NCH = NT / 64;               // 32-column chunks per epilogue warp at most
   static constexpr uint32_t BAR_BYTES = 512;
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;
@@ -194,7 +193,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
   // (every thread: the rows, their number and their entries are earlier kernels')
   grid_dependency_wait();
   const uint32_t count = args.count != nullptr ? min(*args.count, args.M) : args.M;
-  const uint32_t rbs = (count + C::LT - 1) / C::LT, vts = (args.N + NT - 1) / NT;
+  const uint32_t rbs = (count + C::LT - 1) / C::LT, vts = (args.N + args.nt - 1) / args.nt;
   const uint32_t tiles = rbs * vts;
   const uint32_t kt_n = (args.K + C::BK - 1) / C::BK;
 
@@ -202,6 +201,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
     // ==================== TMA producer: one thread ==============================
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_last();
+      const uint32_t q_rows = args.nt / CG, q_bytes = q_rows * 128;
       const CUtensorMap* const tmP = args.index != nullptr && count < args.M ? &tmCompact : &tmAll;
       uint32_t it = 0;
       bool ok = true;
@@ -212,13 +212,13 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         const uint32_t live = count > p0 ? min(128u, count - p0) : 0u;
         // (a pair's second CTA without rows still loads a box: its stage is waited for)
         const uint32_t p_boxes = live == 0 ? 1u : (live + C::P_BOX - 1) / C::P_BOX;
-        const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * NT + rank * C::Q_ROWS);
-        uint32_t tx = C::Q_BYTES + p_boxes * C::P_BOX * 128;
+        const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * args.nt + rank * q_rows);
+        uint32_t tx = q_bytes + p_boxes * C::P_BOX * 128;
         if constexpr (CG == 2) {
           const uint32_t p1 = rb * C::LT + 128;
           const uint32_t live1 = count > p1 ? min(128u, count - p1) : 0u;
           const uint32_t boxes0 = min(128u, count - rb * C::LT);
-          tx = 2 * C::Q_BYTES + ((boxes0 + C::P_BOX - 1) / C::P_BOX +
+          tx = 2 * q_bytes + ((boxes0 + C::P_BOX - 1) / C::P_BOX +
                                  (live1 == 0 ? 1u : (live1 + C::P_BOX - 1) / C::P_BOX)) * C::P_BOX * 128;
         }
         for (uint32_t kt = 0; kt < kt_n; ++kt, ++it) {
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
   } else if (warp == 1) {
     // ==================== MMA issuer: one thread of the leader CTA ==============
     if (leader && lane == 0) {
-      const uint32_t idesc = idesc_f16(C::LT, NT, 1u, false, false);
+      const uint32_t idesc = idesc_f16(C::LT, args.nt, 1u, false, false);
       uint32_t it = 0, j = 0;
       bool ok = true, issued = false;
       for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
   } else {
     // ==================== epilogue: eight warps, two per TMEM lane quarter =======
     const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
-    const uint32_t eg = (warp - 2u) / 4u;      // this warp's half of the tile's columns
+    const uint32_t eg = (warp - 2u) / 4u;      // this warp's half of the tile's chunks of 32 columns
+    const uint32_t ch0 = eg == 0 ? 0u : (args.nt / 32 + 1) / 2, chunks = eg == 0 ? (args.nt / 32 + 1) / 2 : args.nt / 32 - ch0;
     uint32_t j = 0;
     bool ok = true;
     const auto counts = [&](uint32_t r) {      // in place: whether row r does
@@ -335,8 +336,8 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
       const uint32_t row = rb * C::LT + rank * 128 + q * 32 + lane;
       const bool live = row < count && (!BACK || args.row != nullptr || counts(row));
       const bool any = row - lane < count;               // some lane of the warp has a row
-      const uint32_t n0 = vt * NT + eg * (NT / 2);       // this warp's first column
-      const uint32_t cols = args.N > n0 ? min(NT / 2, args.N - n0) : 0u;
+      const uint32_t n0 = vt * args.nt + ch0 * 32;       // this warp's first column
+      const uint32_t cols = args.N > n0 ? min(chunks * 32, args.N - n0) : 0u;
       const uint32_t at = live ? (args.index != nullptr ? args.index[row] : row) : 0u;
       // the first entry at or behind n0: its offset from n0, 0xFFFFFFFF where there is none
       uint32_t next = 0xFFFFFFFFu, cur = 0, len = 0;
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         }
       };
       const auto t_addr = [&](uint32_t ch) {
-        return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + eg * (NT / 2) + ch * 32;
+        return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + (ch0 + ch) * 32;
       };
       const auto acc_wait = [&]() {
         ok = warp_wait(accf_bar(j & 1u), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane);
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
           if (any) {
 #pragma unroll
             for (uint32_t i = 0; i < C::NCH; ++i) {
+              if (i >= chunks) break;
               uint32_t v[32];
               tmem_ld_32x32b_x32_sync(t_addr(i), v);
 #pragma unroll
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
           // the entries' logits
 #pragma unroll
           for (uint32_t i = 0; i < C::NCH; ++i) {
+            if (i >= chunks) break;
             while (__any_sync(0xffffffffu, next - 32 * i < 32u)) {
               const bool here = next - 32 * i < 32u;
               const float z = args.scale * select32(acc[i], (next - 32 * i) & 31u);
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
             }
           }
           float sum_z = 0.0f;
-          if (cols < NT / 2) {   // columns past the vocabulary's end
+          if (cols < 32 * C::NCH) {   // columns past the tile's or the vocabulary's end
 #pragma unroll
             for (uint32_t i = 0; i < C::NCH; ++i)
 #pragma unroll
@@ -470,12 +473,12 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         const bool stored = row < padded;
         if (!acc_wait()) break;
         const uint32_t b = j & 1u;
-        if (row - lane < padded) {
+        if (row - lane < padded && chunks > 0) {
 #pragma unroll 1
-          for (uint32_t i = 0; i < C::NCH; ++i) {
+          for (uint32_t i = 0; i < chunks; ++i) {
             uint32_t v[32];
             tmem_ld_32x32b_x32_sync(t_addr(i), v);
-            if (i + 1 == C::NCH) release(b);
+            if (i + 1 == chunks) release(b);
             float g[32];
 #pragma unroll
             for (uint32_t e = 0; e < 32; ++e)
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
                 if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
               }
             }
-            if (stored) {
+            if (stored && 32 * i < cols) {   // (the pitch has room for whole chunks)
 #pragma unroll
               for (uint32_t h = 0; h < 2; ++h) {
                 uint32_t x[8];

@@ -57,36 +57,47 @@ struct LossProductCfg {
   static constexpr uint32_t ACC_COLS = 256;
 };
 
-// The parts that Rows' reduction over the piece is dealt in, of `kt` stages a tile: the
-// number whose last cluster ends first, over `tiles` tiles of Rows and `others` items of
-// Matrix, `cost` stages each, dealt in turn to G clusters; each part costs its sums' way to
-// memory and back (`extra` stages over all clusters).  The 32 lanes try a number each; every
-// warp of every block, of the kernel that joins the sums too, finds the same.
-__device__ __forceinline__ uint32_t loss_parts(uint32_t tiles, uint32_t others, uint32_t kt, uint32_t cost, uint32_t extra,
-                                               uint32_t G, uint32_t most) {
+// How the items are dealt.  Rows' reduction over the piece goes in `parts`, and its items
+// in turn to the G clusters, so that the first `r` have one more than the others' x; Matrix's
+// follow, n1 at most to each of those and n0 to each of the others, who end no later for it.
+struct LossDeal {
+  uint32_t count, rb_x, rb_y, cb;      // rows that count; tiles down, of either, and across
+  uint32_t parts, x, r, n1, n0;
+};
+
+// The deal that ends first, of `kt` stages a tile over `tiles` tiles of Rows and `others`
+// items of Matrix, `cost` stages each; each part costs its sums' way to memory and back
+// (`extra` stages over all clusters).  The 32 lanes try a number of parts each; every warp
+// of every block, of the kernel that joins the sums too, finds the same.
+__device__ __forceinline__ void loss_parts(LossDeal& d, uint32_t tiles, uint32_t others, uint32_t kt, uint32_t cost,
+                                           uint32_t extra, uint32_t G, uint32_t most) {
+  constexpr uint32_t kEnds = 5;                          // an item's first loads and last store, in stages
   const uint32_t s = lane_idx() + 1;
-  uint32_t time = 0xFFFFFFFFu;
   // (what is beyond these needs no parts, and would leave 32 bits)
   const bool few = tiles <= 0x4000u && others <= 0x100000u && kt <= 0x4000u && cost <= 0x4000u && extra <= 0x10000u;
+  const uint32_t items = tiles * (few ? s : 1u), x = items / G, r = items - x * G;
+  uint32_t n1 = others / G, n0 = n1, time = s == 1 ? 0xFFFFFFFEu : 0xFFFFFFFFu;
   if (s <= most && few) {
-    constexpr uint32_t kEnds = 5;                        // an item's first loads and last store, in stages
-    const uint32_t items = tiles * s, x = items / G, r = items - x * G;
-    const uint32_t y = others / G, p = others - y * G;
-    const uint32_t each = (kt + s - 1) / s + kEnds;
-    const uint32_t a = r == 0 ? 0u : (x + 1) * each + (y + (p > G - r ? 1u : 0u)) * cost;
-    const uint32_t b = x * each + (y + (p > 0 ? 1u : 0u)) * cost;
-    time = max(a, b) + s * extra;
-  } else if (s == 1) {
-    time = 0xFFFFFFFEu;
+    const uint32_t each = (kt + s - 1) / s + kEnds, l0 = x * each, l1 = r > 0 ? l0 + each : l0;
+    uint32_t t = max((r * l1 + (G - r) * l0 + others * cost + G - 1) / G, l1);
+    for (uint32_t i = 0; i < 4; ++i) {
+      n1 = (t - l1) / cost;
+      n0 = (t - l0) / cost;
+      if (r * n1 + (G - r) * n0 >= others) break;
+      t = min(l0 + (n0 + 1) * cost, l1 + (n1 + 1) * cost);
+    }
+    time = t + s * extra;
   }
+  if (r * n1 < others) n0 = max(n0, (others - r * n1 + G - r - 1) / (G - r));
   const uint32_t best = __reduce_min_sync(0xffffffffu, time);
-  return static_cast<uint32_t>(__ffs(__ballot_sync(0xffffffffu, time == best)));
+  const int lane = __ffs(__ballot_sync(0xffffffffu, time == best)) - 1;
+  d.parts = static_cast<uint32_t>(lane) + 1;
+  d.x = __shfl_sync(0xffffffffu, x, lane);
+  d.r = __shfl_sync(0xffffffffu, r, lane);
+  d.n1 = __shfl_sync(0xffffffffu, n1, lane);
+  d.n0 = __shfl_sync(0xffffffffu, n0, lane);
 }
 
-// What all roles, and the kernel that joins the sums, know of a launch's items.
-struct LossDeal {
-  uint32_t count, rb_x, rb_y, cb, parts, items_x, items;
-};
 template <int CG>
 __device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t G) {
   constexpr uint32_t LT = 128 * CG;
@@ -95,27 +106,33 @@ __device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t
   d.cb = (a.K + a.nt - 1) / a.nt;
   d.rb_x = a.sums != nullptr ? (d.count + LT - 1) / LT : 0u;
   d.rb_y = a.dB != nullptr ? (a.n + LT - 1) / LT : 0u;
-  const uint32_t full_y = a.dB != nullptr ? (a.width + LT - 1) / LT : 0u;
-  const uint32_t kt_y = (d.count + 63) / 64;
+  // (by the first piece: later ones, which may be narrower, add to the same parts)
+  const uint32_t others = a.dB != nullptr ? (a.width + LT - 1) / LT * d.cb : 0u;
   // 4 bytes written and read of each sum at 5 TB/s; 0.3 us a stage
   const uint32_t extra = static_cast<uint32_t>(static_cast<uint64_t>(d.count) * a.K * 8 / 1500000);
-  d.parts = loss_parts(d.rb_x * d.cb, full_y * d.cb, (a.width + 63) / 64, max(kt_y + 3, a.db_cost), extra, G, a.most);
-  d.items_x = d.rb_x * d.cb * d.parts;
-  d.items = d.items_x + d.rb_y * d.cb;
+  loss_parts(d, d.rb_x * d.cb, others, (a.width + 63) / 64, max((d.count + 63) / 64 + 3, a.db_cost), extra, G, a.most);
   return d;
 }
 
-// The t-th item: rows l0.., columns c0.., stages k0 .. k1 - 1; part s of Rows, or Matrix.
+// Cluster c's i-th item: rows l0.., columns c0.., stages k0 .. k1 - 1; part s of Rows, or
+// Matrix.  False past the last.
 struct LossItem {
   uint32_t l0, c0, k0, k1, s;
   bool matrix;
 };
 template <int CG>
-__device__ __forceinline__ LossItem loss_item(const LossProductArgs& a, const LossDeal& d, uint32_t t) {
-  LossItem w;
-  w.matrix = t >= d.items_x;
+__device__ __forceinline__ bool loss_item(const LossProductArgs& a, const LossDeal& d, uint32_t c, uint32_t G, uint32_t i,
+                                          LossItem& w) {
+  const uint32_t mine = d.x + (c < d.r ? 1u : 0u);
+  w.matrix = i >= mine;
   const uint32_t rb_n = w.matrix ? d.rb_y : d.rb_x, per = rb_n * d.cb;
-  if (w.matrix) t -= d.items_x;
+  uint32_t t = c + i * G;
+  if (w.matrix) {
+    i -= mine;
+    if (i >= (c < d.r ? d.n1 : d.n0)) return false;
+    t = i < d.n1 ? c + i * G : d.n1 * G + (i - d.n1) * (G - d.r) + (c - d.r);
+    if (t >= per) return false;
+  }
   w.s = t / per;                                         // (Matrix: 0)
   uint32_t rb, cb;
   tile_coords(t - w.s * per, rb_n, d.cb, 8u, rb, cb);
@@ -124,7 +141,7 @@ __device__ __forceinline__ LossItem loss_item(const LossProductArgs& a, const Lo
   const uint32_t kt = ((w.matrix ? d.count : a.n) + 63) / 64, parts = w.matrix ? 1u : d.parts;
   w.k0 = static_cast<uint32_t>(static_cast<uint64_t>(kt) * w.s / parts);
   w.k1 = static_cast<uint32_t>(static_cast<uint64_t>(kt) * (w.s + 1) / parts);
-  return w;
+  return true;
 }
 
 // 32 fp32 values, or their bf16 roundings, at p: `cols` of them (at most 32); p on 32 bytes.
@@ -240,8 +257,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       const uint64_t pol = l2_policy_evict_last();
       uint32_t it = 0;
       bool ok = true;
-      for (uint32_t t = cluster_id; ok && t < deal.items; t += G) {
-        const LossItem w = loss_item<CG>(args, deal, t);
+      LossItem w;
+      for (uint32_t i = 0; ok && loss_item<CG>(args, deal, cluster_id, G, i, w); ++i) {
         const uint32_t live = min(args.nt, args.K - w.c0);
         const uint32_t h = mma_n<CG>(live) / CG;         // columns this CTA contributes to the MMA
         const uint32_t q_boxes = (h + 63) / 64;
@@ -276,8 +293,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       // Exit path after a give-up: let this CTA's issued loads land first.
       if (*abort_flag && leader) {
         const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
-        for (uint32_t i = first; i < it; ++i)
-          drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
+        for (uint32_t k = first; k < it; ++k)
+          drain_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1u, wd, kSiteProducerDrain);
       }
     }
   } else if (warp == 1) {
@@ -285,8 +302,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     if (leader && lane == 0) {
       uint32_t it = 0, j = 0;
       bool ok = true, issued = false;
-      for (uint32_t t = cluster_id; ok && t < deal.items; t += G) {
-        const LossItem w = loss_item<CG>(args, deal, t);
+      LossItem w;
+      for (uint32_t i = 0; ok && loss_item<CG>(args, deal, cluster_id, G, i, w); ++i) {
         if (w.k0 == w.k1) continue;
         const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - w.c0)), 1u, w.matrix, true);
         const uint64_t p_step = w.matrix ? 128 : 2;   // 16 k: 16 rows of an MN-major tile, 32 bytes along a K-major row
@@ -332,8 +349,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
     const uint32_t eg = (warp - 2u) / 4u;      // chunks eg, eg + 2, ...
     uint32_t j = 0;
-    for (uint32_t t = cluster_id; t < deal.items; t += G) {
-      const LossItem w = loss_item<CG>(args, deal, t);
+    LossItem w;
+    for (uint32_t i = 0; loss_item<CG>(args, deal, cluster_id, G, i, w); ++i) {
       const uint32_t live = min(args.nt, args.K - w.c0), nch = (live + 31) / 32;
       const uint32_t row = w.l0 + rank * 128 + q * 32 + lane;
       const bool stored = row < (w.matrix ? args.n : deal.count);
