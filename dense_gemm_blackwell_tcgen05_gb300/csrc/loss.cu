@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(1024) loss_finish_kernel(const FinishArgs a) {
 struct SpreadArgs {
   LossProductArgs products;    // by which the number of parts is found
   uint32_t clusters;
+  const float* sums;
+  uint64_t ld_sums, stride_sums;
   const int32_t* pos;          // (nullptr: in place, by targets or len)
   const void* targets;
   bool target64;
@@ -414,10 +416,10 @@ __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
     else if (in && (a.len != nullptr ? a.len[r] > 0 : loss_index_at(a.targets, a.target64, r) >= 0)) i = static_cast<int32_t>(r);
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i >= 0 && c < K) {
-      const float* const from = a.products.sums + static_cast<uint32_t>(i) * a.products.ld_sums + c;
+      const float* const from = a.sums + static_cast<uint32_t>(i) * a.ld_sums + c;
 #pragma unroll 4
       for (uint32_t p = share == 1 ? 0u : warp; p < parts; p += share) {
-        const float4 y = *reinterpret_cast<const float4*>(from + p * a.products.stride_sums);
+        const float4 y = *reinterpret_cast<const float4*>(from + p * a.stride_sums);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
     }
@@ -630,8 +632,8 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   g.ld_sums = w.ld_sums;
   g.stride_sums = w.stride_sums;
   g.most = w.parts;
-  // rows that start inside sectors: the grouped product, whose warps store along rows
-  const bool whole = p.dB != nullptr && loss_matrix_ok(p.dB, p.ld_db, p.db_f32);
+  // rows that TMA cannot store, and bf16 to be added to: the grouped product
+  const bool whole = p.dB != nullptr && loss_matrix_ok(p.dB, p.ld_db, p.K, p.db_f32, p.accumulate);
   g.dB = whole ? p.dB : nullptr;
   g.ld_db = p.ld_db;
   g.db_f32 = p.db_f32;
@@ -678,7 +680,9 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   g.n = g.width;
   SpreadArgs d = {};
   d.products = loss_product_args(g, plan, ctx);
-  d.products.dB = whole ? p.dB : nullptr;   // (whether there is one, not where)
+  d.sums = g.sums;
+  d.ld_sums = w.ld_sums;
+  d.stride_sums = w.stride_sums;
   d.clusters = plan.clusters;
   d.pos = in_place ? nullptr : reinterpret_cast<const int32_t*>(ws + w.pos);
   d.targets = p.targets;

@@ -114,8 +114,9 @@ struct LossProduct {
 };
 // Parts that the sums' reduction over a piece may be dealt in, at most.
 uint32_t loss_most_parts(uint64_t M, uint64_t width, uint64_t K);
-// Whether the product to the matrix can be stored at `out`: rows that start on 32 bytes.
-bool loss_matrix_ok(const void* out, uint64_t ldo, bool out_f32);
+// Whether the product to the matrix can be stored at `out`: TMA takes rows that start and
+// end on 16 bytes.
+bool loss_matrix_ok(const void* out, uint64_t ldo, uint64_t K, bool out_f32, bool add);
 // What loss_spread_kernel has to know of these launches: CTAs that share a tile, clusters.
 struct LossProductPlan {
   uint32_t cg, nt, clusters;

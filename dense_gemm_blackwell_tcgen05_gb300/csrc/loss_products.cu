@@ -6,9 +6,21 @@
 namespace gb300 {
 namespace {
 
-// Columns of a tile: the width in equal tiles of at most `most`, in steps of 32.
+// Columns of a tile: the width in equal tiles of at most `most`, in steps of 64, the columns
+// of a box of bf16.
 uint32_t tile_columns(uint64_t K, uint64_t most) {
-  return static_cast<uint32_t>(ceil_div_u64(ceil_div_u64(K, ceil_div_u64(K, most)), 32) * 32);
+  return static_cast<uint32_t>(ceil_div_u64(ceil_div_u64(K, ceil_div_u64(K, most)), 64) * 64);
+}
+
+// Tensor map of outputs [batch][rows][K] stored in boxes of 32 rows of 128 bytes.
+bool output_map(CUtensorMap* map, void* base, bool f32, uint64_t K, uint64_t rows, uint64_t batch, uint64_t ld,
+                uint64_t stride) {
+  const uint64_t size = f32 ? 4 : 2;
+  const uint64_t dims[3] = {K, rows, batch};
+  const uint64_t strides[2] = {ld * size, (batch > 1 ? stride : ld) * size};
+  const uint32_t box[3] = {static_cast<uint32_t>(128 / size), 32, 1};
+  return encode_map_3d(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int CG>
@@ -23,10 +35,14 @@ int launch(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& c
   using C = LossProductCfg<CG>;
   uint64_t room = 0;
   if (const int rc = room_of<CG>(p.db_f32, ctx, &room); rc != GEMM_OK) return rc;
-  CUtensorMap gr, gc, b, a;
+  CUtensorMap gr, gc, b, a, sums = {}, out = {};
   if (!operand_map(&gr, p.g, p.n, p.M, 1, p.ldg, 0, 128) || !operand_map(&gc, p.g, p.n, p.M, 1, p.ldg, 0, 64) ||
       !operand_map(&b, p.B, p.K, p.n, 1, p.ldb, 0, 64) || !operand_map(&a, p.A, p.K, p.M, 1, p.lda, 0, 64))
     return GEMM_ERR_LAUNCH;
+  if (p.sums != nullptr && !output_map(&sums, p.sums, true, p.K, p.M, p.most, p.ld_sums, p.stride_sums)) return GEMM_ERR_LAUNCH;
+  if (p.dB != nullptr && !output_map(&out, p.dB, p.db_f32, p.K, p.n, 1, p.ld_db, 0)) return GEMM_ERR_LAUNCH;
+  if (p.sums == nullptr) sums = out;   // (prefetched, not used)
+  if (p.dB == nullptr) out = sums;
   const uint64_t columns = ceil_div_u64(p.K, plan.nt);
   const uint64_t tiles = (p.sums != nullptr ? ceil_div_u64(p.M, C::LT) * p.most : 0) * columns +
                          (p.dB != nullptr ? ceil_div_u64(p.n, C::LT) : 0) * columns;
@@ -39,7 +55,8 @@ int launch(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& c
   cudaLaunchAttribute attr[2];
   loss_attributes(cfg, attr, CG, true);
   note_schedule(plan.clusters, CG, static_cast<uint32_t>(tiles), 0u, 0u, 0u, 0u);
-  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_product_kernel<CG, T>, gr, gc, b, a, loss_product_args(p, plan, ctx));
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_product_kernel<CG, T>, gr, gc, b, a, sums, out,
+                                               loss_product_args(p, plan, ctx));
       e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
@@ -57,8 +74,11 @@ uint32_t loss_most_parts(uint64_t M, uint64_t width, uint64_t K) {
   return static_cast<uint32_t>(n < 1 ? 1 : n > 32 ? 32 : n);
 }
 
-bool loss_matrix_ok(const void* out, uint64_t ldo, bool out_f32) {
-  return ((reinterpret_cast<uintptr_t>(out) | ldo * (out_f32 ? 4 : 2)) & 31u) == 0;
+bool loss_matrix_ok(const void* out, uint64_t ldo, uint64_t K, bool out_f32, bool add) {
+  // TMA leaves out what lies past a row's end by pieces of 16 bytes, and adds in the output's
+  // type: bf16 would be rounded before it is added
+  return ((reinterpret_cast<uintptr_t>(out) | ldo * (out_f32 ? 4 : 2) | K * (out_f32 ? 4 : 2)) & 15u) == 0 &&
+         (out_f32 || !add);
 }
 
 int loss_product_plan(const LossProduct& p, const LaunchCtx& ctx, LossProductPlan* plan) {
@@ -92,12 +112,9 @@ LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& p
   a.nt = plan.nt;
   a.width = p.width;
   a.most = p.most;
-  a.sums = p.sums;
-  a.ld_sums = p.ld_sums;
-  a.stride_sums = p.stride_sums;
+  a.rows = p.sums != nullptr ? 1u : 0u;
+  a.matrix = p.dB != nullptr ? 1u : 0u;
   a.add_sums = p.add_sums ? 1u : 0u;
-  a.dB = p.dB;
-  a.ld_db = p.ld_db;
   a.add_db = p.add_db ? 1u : 0u;
   a.db_cost = p.db_f32 ? 10u : 6u;
   a.status = ctx.status;

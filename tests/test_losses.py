@@ -78,7 +78,7 @@ def only_inside(buf, view):
 
 # M, N, K: every tile choice, tile edges on each side, K tails, one row, one token
 SHAPES = [(1, 1, 8), (1, 300, 64), (3, 65, 24), (31, 64, 200), (128, 129, 72), (129, 130, 520), (127, 1000, 1032),
-          (256, 513, 64), (257, 1000, 96), (300, 2049, 1100), (513, 777, 40), (700, 5003, 264)]
+          (256, 513, 64), (257, 1000, 96), (300, 2049, 1100), (300, 2049, 1104), (513, 777, 40), (700, 5003, 264)]
 
 
 @pytest.mark.parametrize("exact", [True, False])
