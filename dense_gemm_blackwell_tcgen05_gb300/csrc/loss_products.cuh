@@ -53,8 +53,9 @@ struct LossProductCfg {
   static constexpr uint32_t ALIGN_SLACK = 1024;
   static constexpr uint32_t BOX_BYTES = 32 * 128;        // a warp's rows on their way out
   static constexpr uint32_t OUT_BYTES = kEpiWarps * BOX_BYTES;
-  static constexpr uint32_t STAGES = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - OUT_BYTES) / STAGE_BYTES;
-  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + OUT_BYTES + BAR_BYTES;
+  static constexpr uint32_t STAGES = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - OUT_BYTES - 64 * 24) / STAGE_BYTES;
+  static constexpr uint32_t ITEM_BYTES = 64 * 24;        // a cluster's first items
+  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + OUT_BYTES + BAR_BYTES + ITEM_BYTES;
   static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = 256;
@@ -121,13 +122,16 @@ __device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t
 // Matrix.  False past the last.
 struct LossItem {
   uint32_t l0, c0, k0, k1, s;
-  bool matrix;
+  uint16_t matrix, valid;
 };
+// (a cluster's first kLossAhead are worked out ahead by as many threads: the divisions
+// would otherwise stand between two tiles)
+constexpr uint32_t kLossAhead = 64;
 template <int CG>
 __device__ __forceinline__ bool loss_item(const LossProductArgs& a, const LossDeal& d, uint32_t c, uint32_t G, uint32_t i,
                                           LossItem& w) {
   const uint32_t mine = d.x + (c < d.r ? 1u : 0u);
-  w.matrix = i >= mine;
+  w.matrix = i >= mine ? 1 : 0;
   const uint32_t rb_n = w.matrix ? d.rb_y : d.rb_x, per = rb_n * d.cb;
   uint32_t t = c + i * G;
   if (w.matrix) {
@@ -208,6 +212,19 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
   // (every thread: the number of rows is an earlier kernel's)
   grid_dependency_wait();
   const LossDeal deal = loss_deal<CG>(args, G);
+  static_assert(sizeof(LossItem) == 24 && C::ITEM_BYTES == kLossAhead * sizeof(LossItem), "the items' table");
+  LossItem* const ahead = reinterpret_cast<LossItem*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
+  if (threadIdx.x < kLossAhead) {
+    LossItem w;
+    w.valid = loss_item<CG>(args, deal, cluster_id, G, threadIdx.x, w) ? 1 : 0;
+    ahead[threadIdx.x] = w;
+  }
+  __syncthreads();
+  const auto item = [&](uint32_t i, LossItem& w) {
+    if (i >= kLossAhead) return loss_item<CG>(args, deal, cluster_id, G, i, w);
+    w = ahead[i];
+    return w.valid != 0;
+  };
 
   if (warp == 0) {
     // ==================== TMA producer: one thread ==============================
@@ -216,7 +233,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       uint32_t it = 0;
       bool ok = true;
       LossItem w;
-      for (uint32_t i = 0; ok && loss_item<CG>(args, deal, cluster_id, G, i, w); ++i) {
+      for (uint32_t i = 0; ok && item(i, w); ++i) {
         const uint32_t live = min(args.nt, args.K - w.c0);
         const uint32_t h = mma_n<CG>(live) / CG;         // columns this CTA contributes to the MMA
         const uint32_t q_boxes = (h + 63) / 64;
@@ -261,7 +278,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       uint32_t it = 0, j = 0;
       bool ok = true, issued = false;
       LossItem w;
-      for (uint32_t i = 0; ok && loss_item<CG>(args, deal, cluster_id, G, i, w); ++i) {
+      for (uint32_t i = 0; ok && item(i, w); ++i) {
         if (w.k0 == w.k1) continue;
         const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - w.c0)), 1u, w.matrix, true);
         const uint64_t p_step = w.matrix ? 128 : 2;   // 16 k: 16 rows of an MN-major tile, 32 bytes along a K-major row
@@ -309,21 +326,41 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     const uint32_t box = out0 + (warp - 2u) * C::BOX_BYTES;
     uint32_t j = 0;
     LossItem w;
-    for (uint32_t i = 0; loss_item<CG>(args, deal, cluster_id, G, i, w); ++i) {
+    for (uint32_t i = 0; item(i, w); ++i) {
       // columns of a box: 128 bytes a row
       const uint32_t wide = w.matrix ? 128u / static_cast<uint32_t>(sizeof(T)) : 32u;
       const uint32_t nch = (min(args.nt, args.K - w.c0) + wide - 1) / wide;
       const int32_t row = static_cast<int32_t>(w.l0 + rank * 128 + q * 32);
-      const bool empty = w.k0 == w.k1;         // nothing is added up: zeros
       const bool add = w.matrix ? args.add_db != 0u : args.add_sums != 0u;
-      if (empty && add) continue;
-      const uint32_t b = j & 1u;
-      if (!empty) {
-        if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) break;
-        tc_fence_after_sync();
-        ++j;
+      // a box on its way: rows past the output's are nobody's
+      const auto send = [&](uint32_t ch) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row < static_cast<int32_t>(w.matrix ? args.n : deal.count)) {
+          const CUtensorMap* const out = w.matrix ? &tmOut : &tmSums;
+          const int32_t x = static_cast<int32_t>(w.c0 + ch * wide), z = static_cast<int32_t>(w.s);
+          if (add) tma_add_3d(out, box, x, row, z);
+          else tma_store_3d(out, box, x, row, z);
+          bulk_commit_group();
+        }
+      };
+      const auto box_free = [&]() {
+        if (lane == 0) bulk_wait_group_read<0>();   // its last store has read it
+        __syncwarp();
+      };
+      if (w.k0 == w.k1) {   // nothing is added up: zeros
+        if (add) continue;
+        const uint32_t v[32] = {};
+        box_free();
+        stage_row(box, lane, 0, v);
+        for (uint32_t ch = eg; ch < nch; ch += 2) send(ch);
+        continue;
       }
-      bool held = !empty;
+      const uint32_t b = j & 1u;
+      if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) break;
+      tc_fence_after_sync();
+      ++j;
+      bool held = true;
       // The hand-back of an accumulator whose reads are complete: it publishes nothing.
       const auto release = [&]() {
         tc_fence_before_sync();
@@ -337,37 +374,26 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       const uint32_t acc = tmem_base + ((q * 32u) << 16) + b * C::ACC_COLS;
 #pragma unroll 1
       for (uint32_t ch = eg; ch < nch; ch += 2) {
-        const bool last = ch + 2 >= nch;
-        if (lane == 0) bulk_wait_group_read<0>();   // the box's last store has read it
-        __syncwarp();
-        uint32_t v[32];
+        const bool last = ch + 2 >= nch;   // all of it is in registers: hand it back
         if (!w.matrix || sizeof(T) == 4) {
-          if (!empty) tmem_ld_32x32b_x32_sync(acc + ch * 32, v);
-          if (last && held) release();              // all of it is in registers
-#pragma unroll
-          for (uint32_t e = 0; e < 32; ++e) v[e] = empty ? 0u : v[e];
+          uint32_t v[32];
+          tmem_ld_32x32b_x32_sync(acc + ch * 32, v);
+          if (last) release();
+          box_free();
           stage_row(box, lane, 0, v);
         } else {
+          uint32_t v0[32], v1[32], x[32];
+          tmem_ld2_32x32b_x32_sync(acc + ch * 64, acc + ch * 64 + 32, v0, v1);
+          if (last) release();
 #pragma unroll
-          for (uint32_t h = 0; h < 2; ++h) {
-            if (!empty) tmem_ld_32x32b_x32_sync(acc + ch * 64 + h * 32, v);
-            if (h == 1 && last && held) release();
-            uint32_t x[16];
-#pragma unroll
-            for (uint32_t e = 0; e < 16; ++e)
-              x[e] = empty ? 0u : pack_bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-            stage_row(box, lane, 4 * h, x);
+          for (uint32_t e = 0; e < 16; ++e) {
+            x[e] = pack_bf16x2(__uint_as_float(v0[2 * e]), __uint_as_float(v0[2 * e + 1]));
+            x[16 + e] = pack_bf16x2(__uint_as_float(v1[2 * e]), __uint_as_float(v1[2 * e + 1]));
           }
+          box_free();
+          stage_row(box, lane, 0, x);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && row < static_cast<int32_t>(w.matrix ? args.n : deal.count)) {
-          const CUtensorMap* const out = w.matrix ? &tmOut : &tmSums;
-          const int32_t x = static_cast<int32_t>(w.c0 + ch * wide), z = static_cast<int32_t>(w.s);
-          if (add) tma_add_3d(out, box, x, row, z);
-          else tma_store_3d(out, box, x, row, z);
-          bulk_commit_group();
-        }
+        send(ch);
       }
       if (held) release();   // (a warp without a chunk)
     }
