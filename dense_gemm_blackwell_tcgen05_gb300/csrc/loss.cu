@@ -93,70 +93,94 @@ __device__ __forceinline__ float warp_all(float v, bool largest) {
   }
   return v;
 }
-// The same over a block; `slots` holds a value per warp.
-__device__ __forceinline__ float block_all(float v, bool largest, float* slots) {
+// The same over T threads, a warp or a block of 256; `slots` holds a value per warp.
+template <uint32_t T>
+__device__ __forceinline__ float all_of(float v, bool largest, float* slots) {
   v = warp_all(v, largest);
-  __syncthreads();
-  if ((threadIdx.x & 31u) == 0) slots[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = slots[0];
-  for (uint32_t i = 1; i < blockDim.x / 32; ++i) v = largest ? fmaxf(v, slots[i]) : v + slots[i];
+  if constexpr (T > 32) {
+    __syncthreads();
+    if ((threadIdx.x & 31u) == 0) slots[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = slots[0];
+    for (uint32_t i = 1; i < T / 32; ++i) v = largest ? fmaxf(v, slots[i]) : v + slots[i];
+  }
   return v;
 }
 
-// A block per row: p = softmax(teacher scale) over the entries that are there (id >= 0,
+// T threads per row: p = softmax(teacher scale) over the entries that are there (id >= 0,
 // logit not -Inf), sorted by id, and sum p log p, which is NaN where an id lies past the
 // vocabulary or a logit is NaN or +Inf.  The place of an entry is the number of entries
-// before it: top^2 / threads comparisons from shared memory.
-__global__ void __launch_bounds__(256) loss_list_kernel(const void* teacher, bool f32, uint64_t ld_teacher, const void* ids,
-                                                        bool ids64, uint64_t ld_ids, uint32_t top, uint32_t N, float scale,
-                                                        int32_t* out_ids, float* out_prob, uint32_t* len, float* entropy) {
+// before it: top^2 / T comparisons from shared memory.  A warp has room for 128 entries.
+constexpr uint32_t kWarpTop = 128;
+struct ListArgs {
+  const void* teacher;
+  const void* ids;
+  uint64_t ld_teacher, ld_ids;
+  bool f32, ids64;
+  uint32_t M, top, N;
+  float scale;
+  int32_t* out_ids;
+  float* out_prob;
+  uint32_t* len;
+  float* entropy;
+};
+template <uint32_t T>
+__global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
+  constexpr uint32_t kRows = 256 / T, kRoom = T == 32 ? kWarpTop : GEMM_MAX_TOP;
+  __shared__ int32_t ids_of[kRows][kRoom];
+  __shared__ float logits_of[kRows][kRoom];
+  __shared__ float slots[8];
   grid_dependents_launch();
   grid_dependency_wait();
-  __shared__ int32_t s_id[GEMM_MAX_TOP];
-  __shared__ float slots[8];
-  const uint64_t r = blockIdx.x;
-  const auto logit = [&](uint32_t i) {
-    const uint64_t at = r * ld_teacher + i;
-    return scale * (f32 ? static_cast<const float*>(teacher)[at]
-                        : bf16_bits_to_f32(static_cast<const uint16_t*>(teacher)[at]));
-  };
+  const uint32_t me = threadIdx.x % T, top = a.top;
+  const uint64_t r = blockIdx.x * static_cast<uint64_t>(kRows) + threadIdx.x / T;
+  if (r >= a.M) return;   // (a whole warp; a block has one row)
+  int32_t* const s_id = ids_of[threadIdx.x / T];
+  float* const s_t = logits_of[threadIdx.x / T];
   float most = -INFINITY;
   bool wrong = false;
   uint32_t mine = 0;
-  for (uint32_t i = threadIdx.x; i < top; i += blockDim.x) {
-    const int64_t id = loss_index_at(ids, ids64, r * ld_ids + i);
-    const float t = logit(i);
+  for (uint32_t i = me; i < top; i += T) {
+    const int64_t id = loss_index_at(a.ids, a.ids64, r * a.ld_ids + i);
+    const uint64_t at = r * a.ld_teacher + i;
+    const float t = a.scale * (a.f32 ? static_cast<const float*>(a.teacher)[at]
+                                     : bf16_bits_to_f32(static_cast<const uint16_t*>(a.teacher)[at]));
     const bool there = id >= 0 && t != -INFINITY;
-    wrong |= there && id >= N;
+    wrong |= there && id >= a.N;
     s_id[i] = there ? static_cast<int32_t>(min(id, static_cast<int64_t>(0x7FFFFFFF))) : -1;
+    s_t[i] = t;
     if (there) {
       most = fmaxf(most, t);
       ++mine;
     }
   }
-  most = block_all(most, true, slots);
+  most = all_of<T>(most, true, slots);
   float sum = 0.0f;
-  for (uint32_t i = threadIdx.x; i < top; i += blockDim.x)
-    if (s_id[i] >= 0) sum += expf(logit(i) - most);
-  sum = block_all(sum, false, slots);
+  for (uint32_t i = me; i < top; i += T) {
+    if (s_id[i] < 0) continue;
+    const float e = expf(s_t[i] - most);
+    sum += e;
+  }
+  sum = all_of<T>(sum, false, slots);
   const float log_sum = logf(sum);
   float h = wrong ? NAN : 0.0f;
-  for (uint32_t i = threadIdx.x; i < top; i += blockDim.x) {
+  __syncwarp();   // (T > 32: all_of's barriers)
+  for (uint32_t i = me; i < top; i += T) {
     const int32_t id = s_id[i];
     if (id < 0) continue;
     uint32_t place = 0;
+#pragma unroll 8
     for (uint32_t k = 0; k < top; ++k) place += s_id[k] >= 0 && (s_id[k] < id || (s_id[k] == id && k < i)) ? 1u : 0u;
-    const float d = logit(i) - most, p = expf(d) / sum;
-    out_ids[r * top + place] = id;
-    out_prob[r * top + place] = p;
+    const float d = s_t[i] - most, p = expf(d) / sum;
+    a.out_ids[r * top + place] = id;
+    a.out_prob[r * top + place] = p;
     h += p == 0.0f ? 0.0f : p * (d - log_sum);
   }
-  h = block_all(h, false, slots);
-  const uint32_t n = static_cast<uint32_t>(block_all(static_cast<float>(mine), false, slots));
-  if (threadIdx.x == 0) {
-    len[r] = n;
-    entropy[r] = h;
+  h = all_of<T>(h, false, slots);
+  const uint32_t n = static_cast<uint32_t>(all_of<T>(static_cast<float>(mine), false, slots));
+  if (me == 0) {
+    a.len[r] = n;
+    a.entropy[r] = h;
   }
 }
 
@@ -477,10 +501,23 @@ int launch(void (*kern)(P...), unsigned grid, unsigned block, bool chained, cuda
 }
 
 int launch_list(const LossProblem& p, const Layout& w, uint8_t* ws, cudaStream_t stream) {
-  const uint32_t threads = p.top >= 256 ? 256u : (p.top + 31) / 32 * 32;
-  return launch(loss_list_kernel, p.M, threads, false, stream, p.teacher, p.teacher_f32, p.ld_teacher, p.ids, p.ids64, p.ld_ids,
-                p.top, p.N, p.scale, reinterpret_cast<int32_t*>(ws + w.ids), reinterpret_cast<float*>(ws + w.prob),
-                reinterpret_cast<uint32_t*>(ws + w.len), reinterpret_cast<float*>(ws + w.entropy));
+  ListArgs a = {};
+  a.teacher = p.teacher;
+  a.ids = p.ids;
+  a.ld_teacher = p.ld_teacher;
+  a.ld_ids = p.ld_ids;
+  a.f32 = p.teacher_f32;
+  a.ids64 = p.ids64;
+  a.M = p.M;
+  a.top = p.top;
+  a.N = p.N;
+  a.scale = p.scale;
+  a.out_ids = reinterpret_cast<int32_t*>(ws + w.ids);
+  a.out_prob = reinterpret_cast<float*>(ws + w.prob);
+  a.len = reinterpret_cast<uint32_t*>(ws + w.len);
+  a.entropy = reinterpret_cast<float*>(ws + w.entropy);
+  return p.top <= kWarpTop ? launch(loss_list_kernel<32>, (p.M + 7) / 8, 256, false, stream, a)
+                           : launch(loss_list_kernel<256>, p.M, 256, false, stream, a);
 }
 
 LossArgs logits_args(const LossProblem& p, const Layout& w, uint8_t* ws) {
