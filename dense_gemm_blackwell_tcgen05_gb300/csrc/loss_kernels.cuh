@@ -86,7 +86,8 @@ struct LossCfg {
   static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
   static constexpr uint32_t LT = 128 * CG;               // rows per tile
   static_assert(NT % 64 == 0 && NT <= 256, "two halves of whole 32-column chunks");
-  static constexpr uint32_t P_BOX = 32;                  // rows per load of A: few rows load what they need
+  // rows per load of A: few rows load what they need, pairs keep their one thread's loads few
+  static constexpr uint32_t P_BOX = CG == 2 ? 128 : 32;
   static constexpr uint32_t P_BYTES = 128 * 128;
   static constexpr uint32_t Q_BYTES = NT / CG * 128;     // vocabulary rows staged by one CTA
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
