@@ -935,12 +935,11 @@ def distill_workspace(M: int, N: int, K: int, top: int, grad: bool = False, devi
     return torch.empty(_loss_bytes(_KD_BYTES, M, N, K, top, int(grad)), dtype=torch.uint8, device=device or "cuda")
 
 
-def _own_workspace(device, stream, entry, *sizes):
-    """A call's workspace where the caller gave none."""
+def _foreign(stream):
+    """Refuses to allocate a workspace for a call on another stream than torch's current one."""
     import torch
     if stream is not None and stream != torch.cuda.current_stream():
         raise ValueError("a call on another stream needs its own workspace")
-    return torch.empty(_loss_bytes(entry, *sizes), dtype=torch.uint8, device=device)
 
 
 def _gradient(t, like, needed, out_dtype, stream):
@@ -969,16 +968,24 @@ def matmul_cross_entropy(A, B, targets, scale: float = 1.0, label_smoothing: flo
     import torch
     bf16, f32 = torch.bfloat16, torch.float32
     rc, loss, lse = GEMM_ERR_INVALID_ARG, None, None
-    code = _index_code(targets.dtype)
+    code = INDEX_I64 if targets.dtype is torch.int64 else _index_code(targets.dtype)
     if A.dim() == B.dim() == 2:
         (M, K), (N, KB) = A.shape, B.shape
         (lda, a1), (ldb, b1) = A.stride(), B.stride()
-        loss, lse = (_new((M,), f32, A.device, stream), _new((M,), f32, A.device, stream)) if out is None else out
+        device = A.device
+        if out is not None:
+            loss, lse = out
+        elif stream is None:
+            loss, lse = torch.empty(M, dtype=f32, device=device), torch.empty(M, dtype=f32, device=device)
+        else:
+            loss, lse = _new((M,), f32, device, stream), _new((M,), f32, device, stream)
         if (K == KB and a1 == b1 == 1 and A.dtype is bf16 and B.dtype is bf16 and A.is_cuda
                 and targets.shape == loss.shape == lse.shape == (M,) and loss.dtype is f32 and lse.dtype is f32
                 and targets.is_contiguous() and loss.is_contiguous() and lse.is_contiguous()):
             if workspace is None:
-                workspace = _own_workspace(A.device, stream, _CE_BYTES, M, N, K, 0)
+                if stream is not None:
+                    _foreign(stream)
+                workspace = torch.empty(_loss_bytes(_CE_BYTES, M, N, K, 0), dtype=torch.uint8, device=device)
             rc = (_lib or load()).gemm_bf16_cross_entropy(
                 A.data_ptr(), B.data_ptr(), targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, lda, ldb, code,
                 scale, label_smoothing, z_loss, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, A.get_device()))
@@ -1002,7 +1009,7 @@ def matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale: float = 1.0, lab
     if accumulate and dB is None:
         raise ValueError("accumulate needs dB")
     rc = GEMM_ERR_INVALID_ARG
-    code = _index_code(targets.dtype)
+    code = INDEX_I64 if targets.dtype is torch.int64 else _index_code(targets.dtype)
     if A.dim() == B.dim() == 2:
         (M, K), (N, KB) = A.shape, B.shape
         (lda, a1), (ldb, b1) = A.stride(), B.stride()
@@ -1012,7 +1019,9 @@ def matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale: float = 1.0, lab
                 and targets.shape == dloss.shape == lse.shape == (M,) and dloss.dtype is f32 and lse.dtype is f32
                 and targets.is_contiguous() and lse.is_contiguous()):
             if workspace is None:
-                workspace = _own_workspace(A.device, stream, _CE_BYTES, M, N, K, 1)
+                if stream is not None:
+                    _foreign(stream)
+                workspace = torch.empty(_loss_bytes(_CE_BYTES, M, N, K, 1), dtype=torch.uint8, device=A.device)
             rc = (_lib or load()).gemm_bf16_cross_entropy_grad(
                 dloss.data_ptr(), A.data_ptr(), B.data_ptr(), targets.data_ptr(), lse.data_ptr(), pa, pb, M, N, K,
                 dloss.stride(0), lda, ldb, ld_da, ld_db, code, ca, cb, scale, label_smoothing, z_loss,
@@ -1044,12 +1053,20 @@ def matmul_distill(A, B, teacher, ids, temperature: float = 1.0, out=None, works
         (M, K), (N, KB) = A.shape, B.shape
         (lda, a1), (ldb, b1), (ldt, t1), (ldi, i1) = A.stride(), B.stride(), teacher.stride(), ids.stride()
         top = ids.shape[1]
-        loss, lse = (_new((M,), f32, A.device, stream), _new((M,), f32, A.device, stream)) if out is None else out
+        device = A.device
+        if out is not None:
+            loss, lse = out
+        elif stream is None:
+            loss, lse = torch.empty(M, dtype=f32, device=device), torch.empty(M, dtype=f32, device=device)
+        else:
+            loss, lse = _new((M,), f32, device, stream), _new((M,), f32, device, stream)
         if (K == KB and a1 == b1 == t1 == i1 == 1 and A.dtype is bf16 and B.dtype is bf16 and A.is_cuda
                 and teacher.shape == ids.shape == (M, top) and loss.shape == lse.shape == (M,) and loss.dtype is f32
                 and lse.dtype is f32 and loss.is_contiguous() and lse.is_contiguous() and 1 <= top <= MAX_TOP):
             if workspace is None:
-                workspace = _own_workspace(A.device, stream, _KD_BYTES, M, N, K, top, 0)
+                if stream is not None:
+                    _foreign(stream)
+                workspace = torch.empty(_loss_bytes(_KD_BYTES, M, N, K, top, 0), dtype=torch.uint8, device=device)
             rc = (_lib or load()).gemm_bf16_distill(
                 A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), loss.data_ptr(), lse.data_ptr(), M, N, K, top,
                 lda, ldb, ldt, ldi, ct, ci, temperature, workspace.data_ptr(), workspace.nbytes,
@@ -1081,7 +1098,9 @@ def matmul_distill_grad(dloss, A, B, teacher, ids, lse, temperature: float = 1.0
                 and teacher.shape == ids.shape == (M, top) and dloss.shape == lse.shape == (M,) and dloss.dtype is f32
                 and lse.dtype is f32 and lse.is_contiguous() and 1 <= top <= MAX_TOP):
             if workspace is None:
-                workspace = _own_workspace(A.device, stream, _KD_BYTES, M, N, K, top, 1)
+                if stream is not None:
+                    _foreign(stream)
+                workspace = torch.empty(_loss_bytes(_KD_BYTES, M, N, K, top, 1), dtype=torch.uint8, device=A.device)
             rc = (_lib or load()).gemm_bf16_distill_grad(
                 dloss.data_ptr(), A.data_ptr(), B.data_ptr(), teacher.data_ptr(), ids.data_ptr(), lse.data_ptr(), pa, pb, M, N,
                 K, top, dloss.stride(0), lda, ldb, ldt, ldi, ld_da, ld_db, ct, ci, ca, cb, temperature,
