@@ -127,7 +127,7 @@ struct ListArgs {
 template <uint32_t T>
 __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
   constexpr uint32_t kRows = 256 / T, kRoom = T == 32 ? kWarpTop : GEMM_MAX_TOP;
-  __shared__ int32_t ids_of[kRows][kRoom];
+  __shared__ alignas(16) int32_t ids_of[kRows][kRoom];
   __shared__ float logits_of[kRows][kRoom];
   __shared__ float slots[8];
   grid_dependents_launch();
@@ -157,23 +157,34 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
   most = all_of<T>(most, true, slots);
   float sum = 0.0f;
   for (uint32_t i = me; i < top; i += T) {
-    if (s_id[i] < 0) continue;
-    const float e = expf(s_t[i] - most);
-    sum += e;
+    if (s_id[i] >= 0) sum += expf(s_t[i] - most);
   }
   sum = all_of<T>(sum, false, slots);
   const float log_sum = logf(sum);
   float h = wrong ? NAN : 0.0f;
   __syncwarp();   // (T > 32: all_of's barriers)
-  for (uint32_t i = me; i < top; i += T) {
-    const int32_t id = s_id[i];
-    if (id < 0) continue;
-    uint32_t place = 0;
-#pragma unroll 8
-    for (uint32_t k = 0; k < top; ++k) place += s_id[k] >= 0 && (s_id[k] < id || (s_id[k] == id && k < i)) ? 1u : 0u;
+  // the places of this thread's entries, four others at a time (absent ones come after all)
+  constexpr uint32_t kMine = kRoom / T;
+  uint32_t place[kMine] = {}, id_of[kMine];
+#pragma unroll
+  for (uint32_t j = 0; j < kMine; ++j) id_of[j] = me + j * T < top ? static_cast<uint32_t>(s_id[me + j * T]) : 0xFFFFFFFFu;
+  for (uint32_t k = 0; k < top; k += 4) {
+    const int4 x = *reinterpret_cast<const int4*>(s_id + k);
+    const uint32_t other[4] = {static_cast<uint32_t>(x.x), static_cast<uint32_t>(x.y), static_cast<uint32_t>(x.z),
+                               static_cast<uint32_t>(x.w)};
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e)
+#pragma unroll
+      for (uint32_t j = 0; j < kMine; ++j)
+        place[j] += k + e < top && (other[e] < id_of[j] || (other[e] == id_of[j] && k + e < me + j * T)) ? 1u : 0u;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < kMine; ++j) {
+    const uint32_t i = me + j * T;
+    if (static_cast<int32_t>(id_of[j]) < 0) continue;
     const float d = s_t[i] - most, p = expf(d) / sum;
-    a.out_ids[r * top + place] = id;
-    a.out_prob[r * top + place] = p;
+    a.out_ids[r * top + place[j]] = static_cast<int32_t>(id_of[j]);
+    a.out_prob[r * top + place[j]] = p;
     h += p == 0.0f ? 0.0f : p * (d - log_sum);
   }
   h = all_of<T>(h, false, slots);

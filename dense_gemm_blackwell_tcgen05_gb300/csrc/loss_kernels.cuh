@@ -29,6 +29,7 @@
 #include "gemm_kernels.cuh"
 #include "grouped_kernels.cuh"
 #include "ptx_grouped.cuh"
+#include "ptx_loss.cuh"
 
 namespace gb300 {
 
@@ -253,49 +254,48 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ==================== MMA issuer: one thread of the leader CTA ==============
-    if (leader && lane == 0) {
+    // ==================== MMA issuer: the leader CTA's, one thread issues ========
+    if (leader) {
       const uint32_t idesc = idesc_f16(C::LT, args.nt, 1u, false, false);
-      uint32_t it = 0, j = 0;
+      const uint64_t pd0 = smem_desc_sw128(base), qd0 = smem_desc_sw128(base + C::P_BYTES);
+      RingStage r;
+      uint32_t j = 0;
       bool ok = true, issued = false;
       for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
         for (uint32_t k_begin = 0; ok && k_begin < kt_n; ++j) {
           const uint32_t k_end = kt_n - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : kt_n;
           const uint32_t b = j & 1u;
           // accumulator b must have been drained by every epilogue warp
-          if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) {
+          if (!uniform_wait(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty, lane)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
-          const auto stage = [&](uint32_t kt) {
-            const uint32_t s = it % C::STAGES;
-            if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
+          for (uint32_t kt = k_begin; kt < k_end; ++kt) {
+            if (!uniform_wait(full_bar(r.s), r.round, wd, kSiteMmaFull, lane)) {
               ok = false;
-              return;
+              break;
             }
             tc_fence_after_sync();
-            const uint64_t pd = smem_desc_sw128(base + s * C::STAGE_BYTES);
-            const uint64_t qd = smem_desc_sw128(base + s * C::STAGE_BYTES + C::P_BYTES);
+            const uint64_t step = static_cast<uint64_t>(r.s * (C::STAGE_BYTES / 16));
+            if (lane == 0) {
 #pragma unroll
-            for (uint32_t k = 0; k < 4; ++k)   // 16 k per MMA: 32 bytes along a row
-              mma_bf16<CG>(d_tmem, pd + 2 * k, qd + 2 * k, idesc, (kt != k_begin || k != 0u));
-            commit_to<CG>(empty_bar(s));       // frees the stage once these MMAs finish
+              for (uint32_t k = 0; k < 4; ++k)   // 16 k per MMA: 32 bytes along a row
+                mma_bf16<CG>(d_tmem, pd0 + step + 2 * k, qd0 + step + 2 * k, idesc, (kt != k_begin || k != 0u));
+              commit_to<CG>(empty_bar(r.s));     // frees the stage once these MMAs finish
+            }
+            __syncwarp();
             issued = true;
-            ++it;
-          };
-          constexpr uint32_t kUnroll = CG == 2 ? 4 : 1;
-          uint32_t kt = k_begin;
-#pragma unroll kUnroll
-          for (; ok && kt < k_end; ++kt) stage(kt);
+            r.next<C::STAGES>();
+          }
           if (!ok) break;
-          commit_to<CG>(accf_bar(b));
+          if (lane == 0) commit_to<CG>(accf_bar(b));
           k_begin = k_end;
         }
       }
       // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
-      if (issued) {
+      if (issued && lane == 0) {
         if constexpr (CG == 1)
           tc_commit(drain_bar);
         else

@@ -273,45 +273,46 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ==================== MMA issuer: one thread of the leader CTA ==============
-    if (leader && lane == 0) {
-      uint32_t it = 0, j = 0;
+    // ==================== MMA issuer: the leader CTA's, one thread issues ========
+    if (leader) {
+      const uint64_t gr0 = smem_desc_sw128(base), gc0 = smem_desc_mn_sw128(base), qd0 = smem_desc_mn_sw128(base + C::P_BYTES);
+      RingStage r;
+      uint32_t j = 0;
       bool ok = true, issued = false;
       LossItem w;
       for (uint32_t i = 0; ok && item(i, w); ++i) {
         if (w.k0 == w.k1) continue;
         const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - w.c0)), 1u, w.matrix, true);
-        const uint64_t p_step = w.matrix ? 128 : 2;   // 16 k: 16 rows of an MN-major tile, 32 bytes along a K-major row
+        // 16 k: 16 rows of an MN-major tile, 32 bytes along a K-major row
+        const uint64_t pd0 = w.matrix ? gc0 : gr0, p_step = w.matrix ? 128 : 2;
         const uint32_t b = j & 1u;
         // accumulator b must have been drained by every epilogue warp
-        if (!wait_bounded(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty)) break;
+        if (!uniform_wait(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty, lane)) break;
         ++j;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
-        constexpr uint32_t kUnroll = CG == 2 ? 4 : 1;
-#pragma unroll kUnroll
         for (uint32_t kt = w.k0; kt < w.k1; ++kt) {
-          const uint32_t s = it % C::STAGES;
-          if (!wait_bounded(full_bar(s), (it / C::STAGES) & 1u, wd, kSiteMmaFull)) {
+          if (!uniform_wait(full_bar(r.s), r.round, wd, kSiteMmaFull, lane)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t sb = base + s * C::STAGE_BYTES;
-          const uint64_t pd = w.matrix ? smem_desc_mn_sw128(sb) : smem_desc_sw128(sb);
-          const uint64_t qd = smem_desc_mn_sw128(sb + C::P_BYTES);
+          const uint64_t step = static_cast<uint64_t>(r.s * (C::STAGE_BYTES / 16));
+          if (lane == 0) {
 #pragma unroll
-          for (uint32_t k = 0; k < 4; ++k)
-            mma_bf16<CG>(d_tmem, pd + p_step * k, qd + 128 * k, idesc, (kt != w.k0 || k != 0u));
-          commit_to<CG>(empty_bar(s));   // frees the stage once these MMAs finish
+            for (uint32_t k = 0; k < 4; ++k)
+              mma_bf16<CG>(d_tmem, pd0 + step + p_step * k, qd0 + step + 128 * k, idesc, (kt != w.k0 || k != 0u));
+            commit_to<CG>(empty_bar(r.s));   // frees the stage once these MMAs finish
+          }
+          __syncwarp();
           issued = true;
-          ++it;
+          r.next<C::STAGES>();
         }
         if (!ok) break;
-        commit_to<CG>(accf_bar(b));
+        if (lane == 0) commit_to<CG>(accf_bar(b));
       }
       // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
-      if (issued) {
+      if (issued && lane == 0) {
         if constexpr (CG == 1)
           tc_commit(drain_bar);
         else
