@@ -87,7 +87,7 @@ struct LossCfg {
   static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
   static constexpr uint32_t LT = 128 * CG;               // rows per tile
   static_assert(NT % 64 == 0 && NT <= 256, "two halves of whole 32-column chunks");
-  // rows per load of A: few rows load what they need, pairs keep their one thread's loads few
+  // rows per load of A: few rows load what they need, pairs all at once
   static constexpr uint32_t P_BOX = CG == 2 ? 128 : 32;
   static constexpr uint32_t P_BYTES = 128 * 128;
   static constexpr uint32_t Q_BYTES = NT / CG * 128;     // vocabulary rows staged by one CTA
@@ -200,57 +200,53 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
   const uint32_t kt_n = (args.K + C::BK - 1) / C::BK;
 
   if (warp == 0) {
-    // ==================== TMA producer: one thread ==============================
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_last();
-      const uint32_t q_rows = args.nt / CG, q_bytes = q_rows * 128;
-      const CUtensorMap* const tmP = args.index != nullptr && count < args.M ? &tmCompact : &tmAll;
-      uint32_t it = 0;
-      bool ok = true;
-      for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
-        uint32_t rb, vt;
-        tile_coords(t, rbs, vts, kLossRaster, rb, vt);
-        const uint32_t p0 = rb * C::LT + rank * 128;
-        const uint32_t live = count > p0 ? min(128u, count - p0) : 0u;
-        // (a pair's second CTA without rows still loads a box: its stage is waited for)
-        const uint32_t p_boxes = live == 0 ? 1u : (live + C::P_BOX - 1) / C::P_BOX;
-        const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * args.nt + rank * q_rows);
-        uint32_t tx = q_bytes + p_boxes * C::P_BOX * 128;
-        if constexpr (CG == 2) {
-          const uint32_t p1 = rb * C::LT + 128;
-          const uint32_t live1 = count > p1 ? min(128u, count - p1) : 0u;
-          const uint32_t boxes0 = min(128u, count - rb * C::LT);
-          tx = 2 * q_bytes + ((boxes0 + C::P_BOX - 1) / C::P_BOX +
-                                 (live1 == 0 ? 1u : (live1 + C::P_BOX - 1) / C::P_BOX)) * C::P_BOX * 128;
+    // ==================== TMA producer: one thread issues =======================
+    const uint64_t pol = l2_policy_evict_last();
+    const uint32_t q_rows = args.nt / CG, q_bytes = q_rows * 128;
+    const CUtensorMap* const tmP = args.index != nullptr && count < args.M ? &tmCompact : &tmAll;
+    RingStage r;
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
+      uint32_t rb, vt;
+      tile_coords(t, rbs, vts, kLossRaster, rb, vt);
+      // boxes of A that a CTA of the tile loads (one without rows loads one: its stage is waited for)
+      const auto boxes = [&](uint32_t p) {
+        const uint32_t live = count > p ? min(128u, count - p) : 1u;
+        return (live + C::P_BOX - 1) / C::P_BOX;
+      };
+      const uint32_t p0 = rb * C::LT + rank * 128, p_boxes = boxes(p0);
+      const uint32_t tx = CG * q_bytes + (CG == 2 ? boxes(rb * C::LT) + boxes(rb * C::LT + 128) : p_boxes) * C::P_BOX * 128;
+      const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * args.nt + rank * q_rows);
+      for (uint32_t kt = 0; kt < kt_n; ++kt, ++it, r.next<C::STAGES>()) {
+        if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
+        if (!uniform_wait(empty_bar(r.s), r.round ^ 1u, wd, kSiteProducerEmpty, lane)) {
+          ok = false;
+          break;
         }
-        for (uint32_t kt = 0; kt < kt_n; ++kt, ++it) {
-          const uint32_t s = it % C::STAGES;
-          if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
-          if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sb = base + s * C::STAGE_BYTES;
+        if (lane == 0) {
+          const uint32_t sb = base + r.s * C::STAGE_BYTES;
           const int32_t k0 = static_cast<int32_t>(kt * C::BK);
-          uint32_t bar = full_bar(s);
-          if constexpr (CG == 2) bar = mapa_shared(full_bar(s), 0);
-          if (leader) mbar_arrive_expect_tx(full_bar(s), tx);
+          uint32_t bar = full_bar(r.s);
+          if constexpr (CG == 2) bar = mapa_shared(full_bar(r.s), 0);
+          if (leader) mbar_arrive_expect_tx(full_bar(r.s), tx);
           const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t y) {
             if (CG == 2) tma_load_3d_pair(dst, m, bar, k0, y, 0, pol);
             else tma_load_3d(dst, m, bar, k0, y, 0, pol);
           };
-          for (uint32_t r = 0; r < p_boxes; ++r)
-            load(sb + r * C::P_BOX * 128, tmP, px + static_cast<int32_t>(r * C::P_BOX));
+          for (uint32_t i = 0; i < (CG == 2 ? 1u : p_boxes); ++i)
+            load(sb + i * C::P_BOX * 128, tmP, px + static_cast<int32_t>(i * C::P_BOX));
           load(sb + C::P_BYTES, &tmQ, qy);
         }
+        __syncwarp();
       }
-      // Exit path after a give-up: let this CTA's issued loads land first.
-      if (*abort_flag && leader) {
-        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
-        for (uint32_t i = first; i < it; ++i) {
-          if (i == args.stall_iter) continue;
-          drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
-        }
+    }
+    // Exit path after a give-up: let this CTA's issued loads land first.
+    if (lane == 0 && leader && *abort_flag) {
+      const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
+      for (uint32_t i = first; i < it; ++i) {
+        if (i == args.stall_iter) continue;
+        drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
       }
     }
   } else if (warp == 1) {

@@ -227,30 +227,29 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
   };
 
   if (warp == 0) {
-    // ==================== TMA producer: one thread ==============================
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_last();
-      uint32_t it = 0;
-      bool ok = true;
-      LossItem w;
-      for (uint32_t i = 0; ok && item(i, w); ++i) {
-        const uint32_t live = min(args.nt, args.K - w.c0);
-        const uint32_t h = mma_n<CG>(live) / CG;         // columns this CTA contributes to the MMA
-        const uint32_t q_boxes = (h + 63) / 64;
-        const uint32_t tx = C::P_BYTES + q_boxes * 8192;
-        const int32_t px = static_cast<int32_t>(w.l0 + rank * 128), qx = static_cast<int32_t>(w.c0 + rank * h);
-        const CUtensorMap* const tmQ = w.matrix ? &tmA : &tmB;
-        for (uint32_t kt = w.k0; kt < w.k1; ++kt, ++it) {
-          const uint32_t s = it % C::STAGES;
-          if (!wait_bounded(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, wd, kSiteProducerEmpty)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sb = base + s * C::STAGE_BYTES;
+    // ==================== TMA producer: one thread issues =======================
+    const uint64_t pol = l2_policy_evict_last();
+    RingStage r;
+    uint32_t it = 0;
+    bool ok = true;
+    LossItem w;
+    for (uint32_t i = 0; ok && item(i, w); ++i) {
+      const uint32_t h = mma_n<CG>(min(args.nt, args.K - w.c0)) / CG;   // columns this CTA contributes to the MMA
+      const uint32_t q_boxes = (h + 63) / 64;
+      const uint32_t tx = CG * (C::P_BYTES + q_boxes * 8192);
+      const int32_t px = static_cast<int32_t>(w.l0 + rank * 128), qx = static_cast<int32_t>(w.c0 + rank * h);
+      const CUtensorMap* const tmQ = w.matrix ? &tmA : &tmB;
+      for (uint32_t kt = w.k0; kt < w.k1; ++kt, ++it, r.next<C::STAGES>()) {
+        if (!uniform_wait(empty_bar(r.s), r.round ^ 1u, wd, kSiteProducerEmpty, lane)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t sb = base + r.s * C::STAGE_BYTES;
           const int32_t k = static_cast<int32_t>(kt * C::BK);
-          uint32_t bar = full_bar(s);
-          if constexpr (CG == 2) bar = mapa_shared(full_bar(s), 0);
-          if (leader) mbar_arrive_expect_tx(full_bar(s), CG * tx);
+          uint32_t bar = full_bar(r.s);
+          if constexpr (CG == 2) bar = mapa_shared(full_bar(r.s), 0);
+          if (leader) mbar_arrive_expect_tx(full_bar(r.s), tx);
           const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t x, int32_t y) {
             if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, 0, pol);
             else tma_load_3d(dst, m, bar, x, y, 0, pol);
@@ -264,13 +263,14 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
           for (uint32_t b = 0; b < q_boxes; ++b)
             load(sb + C::P_BYTES + b * 8192, tmQ, qx + static_cast<int32_t>(64 * b), k);
         }
+        __syncwarp();
       }
-      // Exit path after a give-up: let this CTA's issued loads land first.
-      if (*abort_flag && leader) {
-        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
-        for (uint32_t k = first; k < it; ++k)
-          drain_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1u, wd, kSiteProducerDrain);
-      }
+    }
+    // Exit path after a give-up: let this CTA's issued loads land first.
+    if (lane == 0 && leader && *abort_flag) {
+      const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
+      for (uint32_t k = first; k < it; ++k)
+        drain_wait(full_bar(k % C::STAGES), (k / C::STAGES) & 1u, wd, kSiteProducerDrain);
     }
   } else if (warp == 1) {
     // ==================== MMA issuer: the leader CTA's, one thread issues ========
