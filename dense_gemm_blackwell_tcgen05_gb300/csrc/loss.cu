@@ -196,13 +196,13 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
 }
 
 // Which rows count: index[i] = the i-th of them, pos[r] its place (-1: left out), count =
-// {0, their number}.  A forward pass's results for the rows left out; the compact copy of
-// the others where there are such, or for a backward pass, which also gets their factors
-// and zeros up to a multiple of 64 rows.
+// {0, their number}.  A forward pass's results for the rows left out, a backward pass's
+// factors of the others; where there are some left out, the compact copy of the others, for
+// a backward pass with zeros up to a multiple of 64 rows.
 struct RowsArgs {
   uint32_t M, K, per;          // per: rows a block
   const void* targets;
-  bool target64, back;
+  bool target64, back, always;  // always: the copy is wanted where no row is left out, too
   const uint32_t* len;         // (nullptr: targets)
   int32_t* count;
   uint32_t* index;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const RowsArgs a) {
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i) before += sums[0][i], all += sums[1][i];
   if (blockIdx.x == 0 && threadIdx.x == 0) a.count[0] = 0, a.count[1] = static_cast<int32_t>(all);
-  const bool copy = a.back || all < a.M;
+  const bool copy = a.always || all < a.M;
   for (uint32_t r0 = first; r0 < last; r0 += 256) {
     const uint32_t r = r0 + threadIdx.x;
     const bool in = r < last && counts(r);
@@ -428,7 +428,8 @@ struct SpreadArgs {
   uint64_t ldo;
 };
 
-// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros.  A block per 128 columns
+// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros; nothing where the
+// products have stored it themselves.  A block per 128 columns
 // of a row where there are many parts, which its warps share; a warp where there are few.
 template <int CG, class T>
 __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
@@ -436,7 +437,9 @@ __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
   grid_dependency_wait();
   const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
   const uint32_t M = a.products.M, K = a.products.K;
-  const uint32_t parts = loss_deal<CG>(a.products, a.clusters).parts;
+  const LossDeal deal = loss_deal<CG>(a.products, a.clusters);
+  if (deal.direct) return;
+  const uint32_t parts = deal.parts;
   const uint32_t share = parts > 4 ? 8u : 1u;            // warps a piece
   const bool vec = ((reinterpret_cast<uintptr_t>(a.dA) | (a.ldo * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
   const uint32_t pieces = (K + 127) / 128;
@@ -564,7 +567,8 @@ LossFactors factors_of(const LossProblem& p, const Layout& w, uint8_t* ws) {
 }
 
 // More than kInPlace rows: those that count, compact.
-int launch_rows(const LossProblem& p, const Layout& w, uint8_t* ws, LossArgs& a, bool back, cudaStream_t stream) {
+int launch_rows(const LossProblem& p, const Layout& w, uint8_t* ws, LossArgs& a, bool back, bool always,
+                cudaStream_t stream) {
   RowsArgs r = {};
   r.M = p.M;
   r.K = p.K;
@@ -572,6 +576,7 @@ int launch_rows(const LossProblem& p, const Layout& w, uint8_t* ws, LossArgs& a,
   r.targets = p.targets;
   r.target64 = p.target64;
   r.back = back;
+  r.always = always;
   r.len = a.len;
   r.count = reinterpret_cast<int32_t*>(ws + w.count);
   r.index = reinterpret_cast<uint32_t*>(ws + w.index);
@@ -602,7 +607,7 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   LossArgs a = logits_args(p, w, ws);
   LossOperands o = {p.A, p.lda, nullptr, 0, p.B, p.ldb, p.top > 0};
   if (p.M > kInPlace) {
-    if ((rc = launch_rows(p, w, ws, a, false, stream)) != GEMM_OK) return rc;
+    if ((rc = launch_rows(p, w, ws, a, false, false, stream)) != GEMM_OK) return rc;
     o.compact = ws + w.compact;
     o.ld_compact = w.ld_compact;
     o.chained = true;
@@ -646,11 +651,11 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   if (p.top > 0 && (rc = launch_list(p, w, ws, stream)) != GEMM_OK) return rc;
   LossArgs a = logits_args(p, w, ws);
   uint16_t* const compact = reinterpret_cast<uint16_t*>(ws + w.compact);
-  LossOperands o = {compact, w.ld_compact, compact, w.ld_compact, p.B, p.ldb, true};
+  LossOperands o = {p.A, p.lda, compact, w.ld_compact, p.B, p.ldb, true};
   const bool in_place = p.M <= kInPlace;
+  // rows that TMA cannot store, and bf16 to be added to: the grouped product
+  const bool whole = p.dB != nullptr && loss_matrix_ok(p.dB, p.ld_db, p.K, p.db_f32, p.accumulate);
   if (in_place) {
-    o.A = p.A;
-    o.lda = p.lda;
     o.compact = nullptr;
     o.chained = p.top > 0;
     a.factors = factors_of(p, w, ws);
@@ -660,7 +665,7 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
     a.ld_clean = w.ld_compact;
     a.offsets = reinterpret_cast<int32_t*>(ws + w.count);
   } else {
-    if ((rc = launch_rows(p, w, ws, a, true, stream)) != GEMM_OK) return rc;
+    if ((rc = launch_rows(p, w, ws, a, true, p.dB != nullptr && !whole, stream)) != GEMM_OK) return rc;
     a.row = reinterpret_cast<const float4*>(ws + w.row);
   }
   a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
@@ -674,14 +679,20 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   g.g = a.out;
   g.ldg = w.width;
   g.ldb = p.ldb;
-  g.A = compact;
-  g.lda = w.ld_compact;
+  g.compact = compact;
+  g.ld_compact = w.ld_compact;
+  g.A = in_place ? compact : p.A;
+  g.lda = in_place ? w.ld_compact : p.lda;
   g.sums = p.dA != nullptr ? reinterpret_cast<float*>(ws + w.sums) : nullptr;
   g.ld_sums = w.ld_sums;
   g.stride_sums = w.stride_sums;
   g.most = w.parts;
-  // rows that TMA cannot store, and bf16 to be added to: the grouped product
-  const bool whole = p.dB != nullptr && loss_matrix_ok(p.dB, p.ld_db, p.K, p.db_f32, p.accumulate);
+  // one piece of more rows than are taken in place: dA needs no joining where none is left out
+  if (!in_place && w.width >= p.N && p.dA != nullptr && loss_matrix_ok(p.dA, p.ld_da, p.K, p.da_f32, false)) {
+    g.dA = p.dA;
+    g.ld_da = p.ld_da;
+    g.da_f32 = p.da_f32;
+  }
   g.dB = whole ? p.dB : nullptr;
   g.ld_db = p.ld_db;
   g.db_f32 = p.db_f32;

@@ -102,12 +102,16 @@ int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const 
 struct LossProduct {
   uint32_t M, n, K, width;     // rows at most, the piece's columns, the width, the first piece's columns
   const uint32_t* count;
-  const void *g, *B, *A;       // [M, n], B's rows of the piece, the rows that count
-  uint64_t ldg, ldb, lda;
+  const void *g, *B;           // [M, n], B's rows of the piece
+  const void *A, *compact;     // all rows of A, for where none is left out, and those that count
+  uint64_t ldg, ldb, lda, ld_compact;
   float* sums;                 // (nullptr: not wanted) [most][M][K]
   uint64_t ld_sums, stride_sums;
   uint32_t most;
   bool add_sums;
+  void* dA;                    // (nullptr: not wanted) instead of sums where they need no joining
+  uint64_t ld_da;
+  bool da_f32;
   void* dB;                    // (nullptr: not wanted) [n, K]
   uint64_t ld_db;
   bool db_f32, add_db;

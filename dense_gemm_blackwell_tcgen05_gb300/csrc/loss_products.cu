@@ -35,14 +35,14 @@ int launch(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& c
   using C = LossProductCfg<CG>;
   uint64_t room = 0;
   if (const int rc = room_of<CG>(p.db_f32, ctx, &room); rc != GEMM_OK) return rc;
-  CUtensorMap gr, gc, b, a, sums = {}, out = {};
-  if (!operand_map(&gr, p.g, p.n, p.M, 1, p.ldg, 0, 128) || !operand_map(&gc, p.g, p.n, p.M, 1, p.ldg, 0, 64) ||
-      !operand_map(&b, p.B, p.K, p.n, 1, p.ldb, 0, 64) || !operand_map(&a, p.A, p.K, p.M, 1, p.lda, 0, 64))
+  LossMaps m = {};
+  if (!operand_map(&m.g_rows, p.g, p.n, p.M, 1, p.ldg, 0, 128) || !operand_map(&m.g_columns, p.g, p.n, p.M, 1, p.ldg, 0, 64) ||
+      !operand_map(&m.B, p.B, p.K, p.n, 1, p.ldb, 0, 64) || !operand_map(&m.A, p.A, p.K, p.M, 1, p.lda, 0, 64) ||
+      !operand_map(&m.compact, p.compact, p.K, p.M, 1, p.ld_compact, 0, 64) ||
+      (p.sums != nullptr && !output_map(&m.sums, p.sums, true, p.K, p.M, p.most, p.ld_sums, p.stride_sums)) ||
+      (p.dA != nullptr && !output_map(&m.dA, p.dA, p.da_f32, p.K, p.M, 1, p.ld_da, 0)) ||
+      (p.dB != nullptr && !output_map(&m.dB, p.dB, p.db_f32, p.K, p.n, 1, p.ld_db, 0)))
     return GEMM_ERR_LAUNCH;
-  if (p.sums != nullptr && !output_map(&sums, p.sums, true, p.K, p.M, p.most, p.ld_sums, p.stride_sums)) return GEMM_ERR_LAUNCH;
-  if (p.dB != nullptr && !output_map(&out, p.dB, p.db_f32, p.K, p.n, 1, p.ld_db, 0)) return GEMM_ERR_LAUNCH;
-  if (p.sums == nullptr) sums = out;   // (prefetched, not used)
-  if (p.dB == nullptr) out = sums;
   const uint64_t columns = ceil_div_u64(p.K, plan.nt);
   const uint64_t tiles = (p.sums != nullptr ? ceil_div_u64(p.M, C::LT) * p.most : 0) * columns +
                          (p.dB != nullptr ? ceil_div_u64(p.n, C::LT) : 0) * columns;
@@ -55,8 +55,7 @@ int launch(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& c
   cudaLaunchAttribute attr[2];
   loss_attributes(cfg, attr, CG, true);
   note_schedule(plan.clusters, CG, static_cast<uint32_t>(tiles), 0u, 0u, 0u, 0u);
-  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_product_kernel<CG, T>, gr, gc, b, a, sums, out,
-                                               loss_product_args(p, plan, ctx));
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, loss_product_kernel<CG, T>, m, loss_product_args(p, plan, ctx));
       e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
@@ -113,6 +112,7 @@ LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& p
   a.width = p.width;
   a.most = p.most;
   a.rows = p.sums != nullptr ? 1u : 0u;
+  a.direct = p.dA == nullptr ? 0u : p.da_f32 ? 2u : 1u;
   a.matrix = p.dB != nullptr ? 1u : 0u;
   a.add_sums = p.add_sums ? 1u : 0u;
   a.add_db = p.add_db ? 1u : 0u;

@@ -33,6 +33,7 @@ struct LossProductArgs {
   uint32_t width;              // of the first piece, by which the parts are chosen
   uint32_t most;               // parts at most
   uint32_t rows, matrix;       // which of them are wanted
+  uint32_t direct;             // Rows to dA, bf16 (1) or fp32 (2), where there is nothing to join (0: never)
   uint32_t add_sums, add_db;   // added to what is there
   uint32_t db_cost;            // a tile of dB's store in stages
   unsigned long long* status;
@@ -67,6 +68,7 @@ struct LossProductCfg {
 struct LossDeal {
   uint32_t count, rb_x, rb_y, cb;      // rows that count; tiles down, of either, and across
   uint32_t parts, x, r, n1, n0;
+  bool direct;                         // Rows go to dA: one part, and no row left out
 };
 
 // The deal that ends first, of `kt` stages a tile over `tiles` tiles of Rows and `others`
@@ -115,6 +117,7 @@ __device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t
   // 4 bytes written and read of each sum at 5 TB/s; 0.3 us a stage
   const uint32_t extra = static_cast<uint32_t>(static_cast<uint64_t>(d.count) * a.K * 8 / 1500000);
   loss_parts(d, d.rb_x * d.cb, others, (a.width + 63) / 64, max((d.count + 63) / 64 + 3, a.db_cost), extra, G, a.most);
+  d.direct = a.direct != 0u && d.parts == 1 && d.count == a.M;
   return d;
 }
 
@@ -151,15 +154,17 @@ __device__ __forceinline__ bool loss_item(const LossProductArgs& a, const LossDe
   return true;
 }
 
-// T: dB's elements, uint32_t (fp32) or uint16_t (bf16).  Maps: g by its rows (boxes of 128)
-// and by its columns, B's piece and the rows of A (boxes of 64 x 64); the sums
-// [parts][M][K] and dB's rows of the piece (boxes of 128 bytes x 32).
+// g by its rows (boxes of 128) and by its columns, B's piece and the rows of A, all and those
+// that count (boxes of 64 x 64); the sums [parts][M][K], dA and dB's rows of the piece (boxes
+// of 128 bytes x 32).
+struct LossMaps {
+  CUtensorMap g_rows, g_columns, B, A, compact, sums, dA, dB;
+};
+
+// T: dB's elements, uint32_t (fp32) or uint16_t (bf16).
 template <int CG, class T>
 __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
-    loss_product_kernel(const __grid_constant__ CUtensorMap tmGr, const __grid_constant__ CUtensorMap tmGc,
-                        const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA,
-                        const __grid_constant__ CUtensorMap tmSums, const __grid_constant__ CUtensorMap tmOut,
-                        const LossProductArgs args) {
+    loss_product_kernel(const __grid_constant__ LossMaps maps, const LossProductArgs args) {
   using C = LossProductCfg<CG>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -187,12 +192,10 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
   // ---- set-up ------------------------------------------------------------------
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&tmGr);
-      tma_prefetch_desc(&tmGc);
-      tma_prefetch_desc(&tmB);
-      tma_prefetch_desc(&tmA);
-      tma_prefetch_desc(&tmSums);
-      tma_prefetch_desc(&tmOut);
+      tma_prefetch_desc(&maps.g_rows);
+      tma_prefetch_desc(&maps.g_columns);
+      tma_prefetch_desc(&maps.B);
+      tma_prefetch_desc(&maps.A);
       *abort_flag = 0u;
     }
     for (uint32_t i = lane; i < kAccBar0 + 5; i += 32)
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
       const uint32_t q_boxes = (h + 63) / 64;
       const uint32_t tx = CG * (C::P_BYTES + q_boxes * 8192);
       const int32_t px = static_cast<int32_t>(w.l0 + rank * 128), qx = static_cast<int32_t>(w.c0 + rank * h);
-      const CUtensorMap* const tmQ = w.matrix ? &tmA : &tmB;
+      const CUtensorMap* const tmQ = w.matrix ? (deal.count < args.M ? &maps.compact : &maps.A) : &maps.B;
       for (uint32_t kt = w.k0; kt < w.k1; ++kt, ++it, r.next<C::STAGES>()) {
         if (!uniform_wait(empty_bar(r.s), r.round ^ 1u, wd, kSiteProducerEmpty, lane)) {
           ok = false;
@@ -255,10 +258,10 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
             else tma_load_3d(dst, m, bar, x, y, 0, pol);
           };
           if (w.matrix) {
-            load(sb, &tmGc, px, k);
-            load(sb + 8192, &tmGc, px + 64, k);
+            load(sb, &maps.g_columns, px, k);
+            load(sb + 8192, &maps.g_columns, px + 64, k);
           } else {
-            load(sb, &tmGr, k, px);
+            load(sb, &maps.g_rows, k, px);
           }
           for (uint32_t b = 0; b < q_boxes; ++b)
             load(sb + C::P_BYTES + b * 8192, tmQ, qx + static_cast<int32_t>(64 * b), k);
@@ -329,7 +332,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     LossItem w;
     for (uint32_t i = 0; item(i, w); ++i) {
       // columns of a box: 128 bytes a row
-      const uint32_t wide = w.matrix ? 128u / static_cast<uint32_t>(sizeof(T)) : 32u;
+      const bool bf16 = w.matrix ? sizeof(T) == 2 : deal.direct && args.direct == 1u;
+      const uint32_t wide = bf16 ? 64u : 32u;
       const uint32_t nch = (min(args.nt, args.K - w.c0) + wide - 1) / wide;
       const int32_t row = static_cast<int32_t>(w.l0 + rank * 128 + q * 32);
       const bool add = w.matrix ? args.add_db != 0u : args.add_sums != 0u;
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && row < static_cast<int32_t>(w.matrix ? args.n : deal.count)) {
-          const CUtensorMap* const out = w.matrix ? &tmOut : &tmSums;
+          const CUtensorMap* const out = w.matrix ? &maps.dB : deal.direct ? &maps.dA : &maps.sums;
           const int32_t x = static_cast<int32_t>(w.c0 + ch * wide), z = static_cast<int32_t>(w.s);
           if (add) tma_add_3d(out, box, x, row, z);
           else tma_store_3d(out, box, x, row, z);
@@ -376,7 +380,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
 #pragma unroll 1
       for (uint32_t ch = eg; ch < nch; ch += 2) {
         const bool last = ch + 2 >= nch;   // all of it is in registers: hand it back
-        if (!w.matrix || sizeof(T) == 4) {
+        if (!bf16) {
           uint32_t v[32];
           tmem_ld_32x32b_x32_sync(acc + ch * 32, v);
           if (last) release();
