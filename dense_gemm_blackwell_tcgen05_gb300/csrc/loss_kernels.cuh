@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         return tmem_base + ((q * 32u) << 16) + (j & 1u) * C::ACC_COLS + (ch0 + ch) * 32;
       };
       const auto acc_wait = [&]() {
-        ok = warp_wait(accf_bar(j & 1u), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane);
+        ok = uniform_wait(accf_bar(j & 1u), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane);
         tc_fence_after_sync();
         return ok;
       };

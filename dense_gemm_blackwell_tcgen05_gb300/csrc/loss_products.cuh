@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
         continue;
       }
       const uint32_t b = j & 1u;
-      if (!warp_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) break;
+      if (!uniform_wait(accf_bar(b), (j >> 1) & 1u, wd, kSiteEpiAccFull, lane)) break;
       tc_fence_after_sync();
       ++j;
       bool held = true;
