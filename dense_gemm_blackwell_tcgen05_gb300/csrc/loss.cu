@@ -39,8 +39,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 uint64_t up(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
 
+// Whether a list's entries are found by buckets.  Few rows have a tile or two a cluster, whose
+// search hides behind the first loads, and a short list is searched in three loads.
+bool bucketed(uint64_t M, uint64_t top) { return M > kInPlace && top > 8; }
+
 struct Layout {
-  uint64_t count, index, pos, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
+  uint64_t count, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
   uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
   uint32_t parts;                                        // of dA's sums at most
 };
@@ -59,6 +63,7 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     w.ids = take(4 * M * top);
     w.prob = take(4 * M * top);
     w.len = take(4 * M);
+    if (bucketed(M, top)) w.start = take(2 * (kLossBuckets + 1) * M);
     w.entropy = take(4 * M);
   }
   w.ld_compact = up(K, 64);
@@ -122,6 +127,8 @@ struct ListArgs {
   int32_t* out_ids;
   float* out_prob;
   uint32_t* len;
+  uint16_t* start;             // (nullptr: not wanted)
+  uint32_t bucket;
   float* entropy;
 };
 template <uint32_t T>
@@ -192,6 +199,26 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
   if (me == 0) {
     a.len[r] = n;
     a.entropy[r] = h;
+  }
+  if (a.start == nullptr) return;
+  // how many lie before each bucket, from the sorted ids
+  const auto sync = [] {
+    if constexpr (T > 32) __syncthreads();
+    else __syncwarp();
+  };
+  sync();
+#pragma unroll
+  for (uint32_t j = 0; j < kMine; ++j)
+    if (static_cast<int32_t>(id_of[j]) >= 0) s_id[place[j]] = static_cast<int32_t>(id_of[j]);
+  sync();
+  for (uint32_t b = me; b <= kLossBuckets; b += T) {
+    const uint64_t border = static_cast<uint64_t>(b) * a.bucket;
+    uint32_t lo = 0, hi = n;
+    while (lo < hi && b < kLossBuckets) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (static_cast<uint32_t>(s_id[mid]) < border) lo = mid + 1; else hi = mid;
+    }
+    a.start[b * static_cast<uint64_t>(a.M) + r] = static_cast<uint16_t>(b < kLossBuckets ? lo : n);
   }
 }
 
@@ -530,6 +557,8 @@ int launch_list(const LossProblem& p, const Layout& w, uint8_t* ws, cudaStream_t
   a.out_prob = reinterpret_cast<float*>(ws + w.prob);
   a.len = reinterpret_cast<uint32_t*>(ws + w.len);
   a.entropy = reinterpret_cast<float*>(ws + w.entropy);
+  a.start = bucketed(p.M, p.top) ? reinterpret_cast<uint16_t*>(ws + w.start) : nullptr;
+  a.bucket = (p.N + kLossBuckets - 1) / kLossBuckets;
   return p.top <= kWarpTop ? launch(loss_list_kernel<32>, (p.M + 7) / 8, 256, false, stream, a)
                            : launch(loss_list_kernel<256>, p.M, 256, false, stream, a);
 }
@@ -548,6 +577,8 @@ LossArgs logits_args(const LossProblem& p, const Layout& w, uint8_t* ws) {
     a.ids = reinterpret_cast<const int32_t*>(ws + w.ids);
     a.prob = reinterpret_cast<const float*>(ws + w.prob);
     a.len = reinterpret_cast<const uint32_t*>(ws + w.len);
+    a.start = bucketed(p.M, p.top) ? reinterpret_cast<const uint16_t*>(ws + w.start) : nullptr;
+    a.bucket = (p.N + kLossBuckets - 1) / kLossBuckets;
   }
   a.stall_iter = p.stall_iter;
   return a;

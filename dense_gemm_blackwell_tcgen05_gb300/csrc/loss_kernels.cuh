@@ -44,6 +44,10 @@ struct LossFactors {
   uint32_t N;                  // the whole vocabulary
 };
 
+// A list's entries are found from the number of them before each of so many buckets of
+// tokens: a row's own search would be seven loads, one after another.
+constexpr uint32_t kLossBuckets = 64;
+
 struct LossArgs {
   uint32_t M, N, K;            // rows in all, vocabulary (of this piece, backward), width
   uint32_t nt;                 // columns of a tile, a multiple of 32
@@ -58,6 +62,8 @@ struct LossArgs {
   const int32_t* ids;          // [M][top] rising, by all rows
   const float* prob;           // [M][top] their probabilities (backward)
   const uint32_t* len;         // [M] how many
+  const uint16_t* start;       // [kLossBuckets + 1][M] how many lie before a bucket of tokens (nullptr: not known)
+  uint32_t bucket;             // its tokens
   uint32_t top;
   // forward
   float2* part;                // [slots][2][ld_part]: largest c a.b, sum of 2^(c a.b - largest)
@@ -327,15 +333,21 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
     }
     // forward, `runs`: largest and sums over this cluster's tiles so far
     float run_m = -INFINITY, run_s = 0.0f, run_z = 0.0f;
-    for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
-      uint32_t rb, vt;
+    // a tile's place, and this lane's row among all rows: loaded a tile ahead
+    uint32_t rb = 0, vt = 0, at_ahead = 0;
+    const auto look = [&](uint32_t t) {
+      if (t >= tiles) return;
       tile_coords(t, rbs, vts, kLossRaster, rb, vt);
       const uint32_t row = rb * C::LT + rank * 128 + q * 32 + lane;
+      at_ahead = row < count ? (args.index != nullptr ? args.index[row] : row) : 0u;
+    };
+    look(cluster_id);
+    for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
+      const uint32_t row = rb * C::LT + rank * 128 + q * 32 + lane, at = at_ahead, column = vt;
       const bool live = row < count && (!BACK || args.row != nullptr || counts(row));
       const bool any = row - lane < count;               // some lane of the warp has a row
       const uint32_t n0 = vt * args.nt + ch0 * 32;       // this warp's first column
       const uint32_t cols = args.N > n0 ? min(chunks * 32, args.N - n0) : 0u;
-      const uint32_t at = live ? (args.index != nullptr ? args.index[row] : row) : 0u;
       // the first entry at or behind n0: its offset from n0, 0xFFFFFFFF where there is none
       uint32_t next = 0xFFFFFFFFu, cur = 0, len = 0;
       float p_next = 1.0f;
@@ -356,6 +368,11 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
           prob = args.prob + o;
           len = args.len[at];
           uint32_t hi = len;
+          if (args.start != nullptr) {
+            const uint64_t bucket = min(from / args.bucket, kLossBuckets - 1);
+            cur = args.start[bucket * args.M + at];
+            hi = args.start[(bucket + 1) * args.M + at];
+          }
           while (cur < hi) {
             const uint32_t mid = (cur + hi) / 2;
             if (static_cast<uint32_t>(ids[mid]) < from) cur = mid + 1; else hi = mid;
@@ -366,6 +383,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         const uint32_t d = target_offset(args, at);
         next = d != 0xFFFFFFFFu && d >= n0 ? d - n0 : 0xFFFFFFFFu;
       }
+      look(t + G);
       // The hand-back of an accumulator whose reads are complete: it publishes nothing.
       const auto release = [&](uint32_t b) {
         tc_fence_before_sync();
@@ -456,7 +474,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
             sum_z = run_z;
           }
           if (live && (!args.runs || t + G >= tiles)) {
-            const uint64_t o = ((args.runs ? cluster_id : vt) * 2ull + eg) * args.ld_part + row;
+            const uint64_t o = ((args.runs ? cluster_id : column) * 2ull + eg) * args.ld_part + row;
             args.part[o] = make_float2(m, sum);
             if (args.part_sum != nullptr) args.part_sum[o] = sum_z;
           }
