@@ -425,7 +425,7 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * Rows left out: a negative target, or no entry with an id that is not negative
  * and a logit that is not -Inf.  Their loss, lse and dA are 0, they add nothing
  * to dB whatever A, dloss and lse hold there, and where more than 256 rows are
- * given or a gradient is taken they cost next to nothing.  A target or an id of
+ * given they cost next to nothing.  A target or an id of
  * N or more makes the row's loss, its dA and dB NaN, like a NaN or an Inf among
  * its logits, or a NaN or +Inf among the teacher's; the other rows' losses and
  * dA are not affected.
