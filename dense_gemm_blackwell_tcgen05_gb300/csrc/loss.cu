@@ -43,10 +43,16 @@ uint64_t up(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
 // search hides behind the first loads, and a short list is searched in three loads.
 bool bucketed(uint64_t M, uint64_t top) { return M > kInPlace && top > 8; }
 
+// Up to so many rows, one tile's, g keeps two bf16 halves: the products are bound by what they
+// read and write there, not by the MMAs of twice the rows (64 rows, 131072 tokens of width
+// 4096: 640 us, 623 with one half; 128 rows: 613, 640).  Over thousands it would double them.
+constexpr uint64_t kTwoHalves = 128;
+
 struct Layout {
   uint64_t count, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
   uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
   uint32_t parts;                                        // of dA's sums at most
+  uint64_t lo, rows;                                     // where g's lower halves follow (0: none), rows of g
 };
 
 Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
@@ -68,16 +74,18 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
   }
   w.ld_compact = up(K, 64);
   if (back) {
-    w.compact = take(2 * M * w.ld_compact);
+    w.lo = M <= kTwoHalves ? up(M, 64) : 0;
+    w.rows = w.lo + M;
+    w.compact = take(2 * w.rows * w.ld_compact);
     w.row = take(16 * M);
-    uint64_t width = kPieceBytes / 2 / (M > 0 ? M : 1);
+    uint64_t width = kPieceBytes / 2 / (w.rows > 0 ? w.rows : 1);
     width = width < kLeastPiece ? kLeastPiece : width;
     const uint64_t pieces = (N + width - 1) / width;
     w.width = up((N + pieces - 1) / (pieces > 0 ? pieces : 1), 256);
-    w.piece = take(2 * M * w.width);
+    w.piece = take(2 * w.rows * w.width);
     w.ld_sums = up(K, 32);
-    w.stride_sums = M * w.ld_sums;
-    w.parts = loss_most_parts(M, w.width < N ? w.width : N, K);
+    w.stride_sums = w.rows * w.ld_sums;
+    w.parts = loss_most_parts(w.rows, w.width < N ? w.width : N, K);
     w.sums = take(4 * w.stride_sums * w.parts);
   } else {
     if (M > kInPlace) w.compact = take(2 * M * w.ld_compact);
@@ -447,6 +455,7 @@ struct SpreadArgs {
   uint32_t clusters;
   const float* sums;
   uint64_t ld_sums, stride_sums;
+  uint32_t M, lo;              // rows; where g's lower halves' sums follow (0: none)
   const int32_t* pos;          // (nullptr: in place, by targets or len)
   const void* targets;
   bool target64;
@@ -463,7 +472,7 @@ __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
   __shared__ float4 joined[8][32];
   grid_dependency_wait();
   const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
-  const uint32_t M = a.products.M, K = a.products.K;
+  const uint32_t M = a.M, K = a.products.K;
   const LossDeal deal = loss_deal<CG>(a.products, a.clusters);
   if (deal.direct) return;
   const uint32_t parts = deal.parts;
@@ -486,6 +495,10 @@ __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
       for (uint32_t p = share == 1 ? 0u : warp; p < parts; p += share) {
         const float4 y = *reinterpret_cast<const float4*>(from + p * a.stride_sums);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        if (a.lo != 0) {
+          const float4 z = *reinterpret_cast<const float4*>(from + p * a.stride_sums + a.lo * a.ld_sums);
+          x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
+        }
       }
     }
     if (share > 1) {
@@ -701,9 +714,10 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   }
   a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
   a.ld_out = w.width;
+  a.lo_row = static_cast<uint32_t>(w.lo);
 
   LossProduct g = {};
-  g.M = p.M;
+  g.M = static_cast<uint32_t>(w.rows);
   g.K = p.K;
   g.width = static_cast<uint32_t>(w.width < p.N ? w.width : p.N);
   g.count = a.count;
@@ -749,7 +763,7 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
     }
     if (dB != nullptr && !whole) {
       GroupedProblem d = {};
-      d.M = p.M;
+      d.M = g.M;
       d.N = n;
       d.K = p.K;
       d.groups = 1;
@@ -774,6 +788,8 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   d.ld_sums = w.ld_sums;
   d.stride_sums = w.stride_sums;
   d.clusters = plan.clusters;
+  d.M = p.M;
+  d.lo = a.lo_row;
   d.pos = in_place ? nullptr : reinterpret_cast<const int32_t*>(ws + w.pos);
   d.targets = p.targets;
   d.target64 = p.target64;

@@ -21,7 +21,10 @@
 // Precision.  The tensor core's additions truncate (1.1e-9 of the result a term), so
 // the forward pass, whose losses are fp32, adds up segments of 512 terms in registers.
 // exp is 2^x of the multiprocessor's special function unit (2 units in the last place)
-// on arguments in fp32.
+// on arguments in fp32.  The gradient g is rounded to bf16 for the products with it, at
+// 2^-9 of itself: over many rows as much as rounding the products' bf16 results adds (2.4e-3
+// of dA and dB where fp32 logits, rounded once at the end, give 1.7e-3).  Of few rows a
+// row's error shows, and what g's rounding left follows as rows of its own (1.7e-3).
 #pragma once
 
 #include <cstdint>
@@ -80,6 +83,7 @@ struct LossArgs {
   uint64_t ld_clean;
   int32_t* offsets;            //   and {0, M}, as one group's offsets
   uint16_t* out;               // [count][ld_out] the gradient's piece; zeros up to a multiple of 64 rows
+  uint32_t lo_row;             // where what that rounding left follows, row by row (0: it is dropped)
   uint64_t ld_out;
   unsigned long long* status;
   unsigned long long timeout_ns;
@@ -317,13 +321,15 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
     };
     if (BACK && args.clean != nullptr) {
       // rows in pieces of 8 elements, the last of them element by element
-      const uint32_t per = (args.K + 7) / 8, n = args.M * per;   // (few rows)
-      if (blockIdx.x == 0 && threadIdx.x == 64) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(args.M);
+      const uint32_t rows = args.lo_row + args.M;
+      const uint32_t per = (args.K + 7) / 8, n = rows * per;     // (few rows)
+      if (blockIdx.x == 0 && threadIdx.x == 64) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(rows);
       for (uint32_t i = blockIdx.x * 256 + threadIdx.x - 64; i < n; i += gridDim.x * 256) {
-        const uint32_t r = i / per, e = i % per * 8;
+        const uint32_t to_row = i / per, e = i % per * 8;
+        const uint32_t r = args.lo_row != 0 && to_row >= args.lo_row ? to_row - args.lo_row : to_row;
         const uint16_t* const from = args.A + r * args.lda + e;
-        uint16_t* const to = args.clean + r * args.ld_clean + e;
-        const bool in = counts(r);
+        uint16_t* const to = args.clean + to_row * args.ld_clean + e;
+        const bool in = r < args.M && counts(r);
         if (e + 8 <= args.K) {
           *reinterpret_cast<uint4*>(to) = in ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
         } else {
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         if (live) r = args.row != nullptr ? args.row[row] : loss_row_factors(args.factors, args.target, args.target64, row);
         uint16_t* const o = args.out + static_cast<uint64_t>(row) * args.ld_out + n0;
         // the product that sums over rows takes 64 at a time
-        const uint32_t padded = min((count + 63) / 64 * 64, args.M);
+        const uint32_t padded = args.lo_row != 0 ? args.lo_row : min((count + 63) / 64 * 64, args.M);
         const bool stored = row < padded;
         if (!acc_wait()) break;
         const uint32_t b = j & 1u;
@@ -509,6 +515,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
               }
             }
             if (stored && 32 * i < cols) {   // (the pitch has room for whole chunks)
+              uint16_t* const lo = o + static_cast<uint64_t>(args.lo_row) * args.ld_out;
 #pragma unroll
               for (uint32_t h = 0; h < 2; ++h) {
                 uint32_t x[8];
@@ -516,6 +523,14 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
 #pragma unroll
                 for (uint32_t e = 0; e < 8; ++e) x[e] = live ? pack_bf16x2(g[16 * h + 2 * e], g[16 * h + 2 * e + 1]) : 0u;
                 st_global_v8(o + 32 * i + 16 * h, x);
+                if (args.lo_row != 0 && row < args.M) {
+#pragma unroll
+                  for (uint32_t e = 0; e < 8; ++e)
+                    x[e] = live ? pack_bf16x2(g[16 * h + 2 * e] - bf16_bits_to_f32(x[e] & 0xFFFFu),
+                                              g[16 * h + 2 * e + 1] - bf16_bits_to_f32(x[e] >> 16))
+                                : 0u;
+                  st_global_v8(lo + 32 * i + 16 * h, x);
+                }
               }
             }
           }

@@ -444,7 +444,8 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * joins maxima and sums in fp32.  The gradient goes by pieces of the vocabulary:
  * a piece's logits are computed again, their dz is rounded to bf16 for the two
  * products with it (its target's and its list's terms are taken off before
- * that), and the pieces' dA are added up in fp32.
+ * that; for up to 128 rows dz keeps what is left in a second bf16 term), and
+ * the pieces' dA are added up in fp32.
  *
  * workspace: 256-byte aligned device memory of at least the number of bytes that
  * the _workspace_bytes call gives for these sizes (grad: 0 for the forward call,

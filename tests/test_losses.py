@@ -201,6 +201,32 @@ def test_every_element_of_the_logits_gradient(N):
     ref.check(dA, dz, 2.0 ** -8 * dz.abs() + size * 2.0 ** -15, "dz of a list")
 
 
+@pytest.mark.parametrize("M", [1, 63, 64, 65, 127, 128])
+def test_few_rows_gradients_keep_two_halves(M):
+    """Up to 128 rows dz is a sum of two bf16 terms, each rounded by 2^-8 of itself: 2^-16 in all.
+    B and A select single elements of it, in sums that are exact but for their last rounding."""
+    N, K = 257, 264
+    r = gen(M)
+    B = torch.zeros(N, K, dtype=BF16, device="cuda")
+    B[:, :N] = torch.eye(N, dtype=BF16, device="cuda")
+    A = torch.zeros(M, K, dtype=BF16, device="cuda")
+    A[:, :N] = torch.randint(-6, 7, (M, N), generator=r, device="cuda").to(BF16)
+    targets = some_targets(r, M, N, torch.int64, 0.2)
+    live = targets >= 0
+    dloss = torch.randn(M, generator=r, device="cuda")
+    t = ref.target_matrix(targets, N, 0.1)
+    lse = ref.forward(A, B, t, torch.zeros(M, device="cuda", dtype=torch.float64), live, 1.0)[1].float()
+    dA, dB = g.matmul_cross_entropy_grad(dloss, A, B, targets, lse, label_smoothing=0.1, out_dtype=F32)
+    dz, size = ref.dlogits(A, B, t, live, dloss, lse, 1.0)
+    off = 2.0 ** -16 * dz.abs() + size * 2.0 ** -16
+    ref.check(dA[:, :N], dz, off, "dz")
+    assert not dA[:, N:].any()
+    a = A.double()
+    # (a step of the tensor core cuts 17 addends off below 2^-23 of the largest: 2^-18.9 of all)
+    want, steps = dz.T @ a, (2 * M + 142) // 16
+    ref.check(dB, want, off.T @ a.abs() + steps * 2.0 ** -18.9 * (dz.abs().T @ a.abs()), "dB")
+
+
 def test_a_sure_row_keeps_its_small_gradient():
     """exp(z - lse) near 1 at the target: the difference is taken before anything is rounded to bf16."""
     N = 64

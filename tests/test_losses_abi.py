@@ -93,7 +93,7 @@ def test_workspace_bytes():
     assert g.gemm_bf16_distill_workspace_bytes(8, 8, 8, 0, 0) == INVALID
     assert g.gemm_bf16_distill_workspace_bytes(8, 8, 8, g.MAX_TOP + 1, 0) == INVALID
     assert g.gemm_bf16_cross_entropy_workspace_bytes(0, 8, 8, 1) == 0
-    for M, N, K in ((1, 1, 1), (300, 5000, 96), (8192, 131072, 4096), (100000, 50021, 1040)):
+    for M, N, K in ((1, 1, 1), (1, 1 << 28, 8), (128, 1 << 24, 96), (300, 5000, 96), (8192, 131072, 4096), (100000, 50021, 1040)):
         forward, back = (g.gemm_bf16_cross_entropy_workspace_bytes(M, N, K, x) for x in (0, 1))
         # nothing like the logits: what the header says, and room for vectors
         assert forward <= 2 * M * (K + 64) + M * N // 16 * 1.6 + 64 * M * 4 + 65536
