@@ -202,8 +202,11 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
-  // (every thread: the rows, their number and their entries are earlier kernels')
-  grid_dependency_wait();
+  // the rows, their number and their entries are earlier kernels'.  In place, ahead of the
+  // first piece, there are only entries, which the epilogue takes: the operands are on their
+  // way while a few rows' lists are sorted (by a kernel that writes no operand and began after
+  // all work before the call).  Before later pieces the wait would count as the watchdog's.
+  if (warp > 1 || args.count != nullptr || args.first != 0) grid_dependency_wait();
   const uint32_t count = args.count != nullptr ? min(*args.count, args.M) : args.M;
   const uint32_t rbs = (count + C::LT - 1) / C::LT, vts = (args.N + args.nt - 1) / args.nt;
   const uint32_t tiles = rbs * vts;
@@ -285,10 +288,12 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
             }
             tc_fence_after_sync();
             const uint64_t step = static_cast<uint64_t>(r.s * (C::STAGE_BYTES / 16));
+            const uint32_t left = args.K - kt * C::BK;   // (no MMAs over nothing but the zeros past the width)
             if (lane == 0) {
 #pragma unroll
               for (uint32_t k = 0; k < 4; ++k)   // 16 k per MMA: 32 bytes along a row
-                mma_bf16<CG>(d_tmem, pd0 + step + 2 * k, qd0 + step + 2 * k, idesc, (kt != k_begin || k != 0u));
+                if (16 * k < left)
+                  mma_bf16<CG>(d_tmem, pd0 + step + 2 * k, qd0 + step + 2 * k, idesc, (kt != k_begin || k != 0u));
               commit_to<CG>(empty_bar(r.s));     // frees the stage once these MMAs finish
             }
             __syncwarp();

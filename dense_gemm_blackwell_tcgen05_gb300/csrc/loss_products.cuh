@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
         const uint32_t idesc = idesc_f16(C::LT, mma_n<CG>(min(args.nt, args.K - w.c0)), 1u, w.matrix, true);
         // 16 k: 16 rows of an MN-major tile, 32 bytes along a K-major row
         const uint64_t pd0 = w.matrix ? gc0 : gr0, p_step = w.matrix ? 128 : 2;
+        const uint32_t length = w.matrix ? deal.count : args.n;   // (no MMAs over nothing but zeros past it)
         const uint32_t b = j & 1u;
         // accumulator b must have been drained by every epilogue warp
         if (!uniform_wait(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty, lane)) break;
@@ -304,7 +305,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
           if (lane == 0) {
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
-              mma_bf16<CG>(d_tmem, pd0 + step + p_step * k, qd0 + step + 128 * k, idesc, (kt != w.k0 || k != 0u));
+              if (kt * C::BK + 16 * k < length)
+                mma_bf16<CG>(d_tmem, pd0 + step + p_step * k, qd0 + step + 128 * k, idesc, (kt != w.k0 || k != 0u));
             commit_to<CG>(empty_bar(r.s));   // frees the stage once these MMAs finish
           }
           __syncwarp();
