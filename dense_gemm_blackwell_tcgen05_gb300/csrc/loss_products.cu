@@ -93,7 +93,7 @@ int loss_product_plan(const LossProduct& p, const LaunchCtx& ctx, LossProductPla
     }
     return t * static_cast<double>(cg) / static_cast<double>(kLossSms);
   };
-  const bool pair = p.M > 128 && time(2, 0.30, p.db_f32 ? 2.8 : 1.6) + 2.5 < time(1, 0.27, p.db_f32 ? 1.4 : 1.2);
+  const bool pair = p.M > 64 && time(2, 0.30, p.db_f32 ? 2.8 : 1.6) + 2.5 < time(1, 0.27, p.db_f32 ? 1.4 : 1.2);
   plan->cg = pair ? 2 : 1;
   plan->nt = tile_columns(p.K, 128 * plan->cg);
   uint64_t room = 0;
