@@ -13,6 +13,8 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxPitch = int64_t(1) << 36;
 
+// (exponents are taken in base 2)
+bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale * 1.4426950408889634f); }
 bool dim_ok(int64_t x) { return x >= 0 && x <= kMaxDim; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -133,7 +135,7 @@ bool sizes_ok(const Sizes& z) { return dim_ok(z.M) && dim_ok(z.N) && dim_ok(z.K)
 
 int cross_entropy_problem(LossProblem& p, const Sizes& z, const void* targets, int target_dtype, float scale, float smoothing,
                           float z_loss) {
-  if (!sizes_ok(z) || !index_code_ok(target_dtype) || !std::isfinite(scale) || !(scale > 0.0f) || !(smoothing >= 0.0f) ||
+  if (!sizes_ok(z) || !index_code_ok(target_dtype) || !scale_ok(scale) || !(smoothing >= 0.0f) ||
       !(smoothing <= 1.0f) || !std::isfinite(z_loss))
     return GEMM_ERR_INVALID_ARG;
   p = {};
@@ -147,9 +149,8 @@ int cross_entropy_problem(LossProblem& p, const Sizes& z, const void* targets, i
 
 int distill_problem(LossProblem& p, const Sizes& z, const void* teacher, int teacher_dtype, const void* ids, int id_dtype,
                     int64_t ld_teacher, int64_t ld_ids, float temperature) {
-  // (1 / temperature is what the products use)
   if (!sizes_ok(z) || z.top < 1 || z.top > GEMM_MAX_TOP || !float_code_ok(teacher_dtype) || !index_code_ok(id_dtype) ||
-      !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+      !(temperature > 0.0f) || !std::isfinite(temperature) || !scale_ok(1.0f / temperature))
     return GEMM_ERR_INVALID_ARG;
   p = {};
   p.teacher = teacher;

@@ -327,10 +327,12 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
     if (BACK && args.clean != nullptr) {
       // rows in pieces of 8 elements, the last of them element by element
       const uint32_t rows = args.lo_row + args.M;
-      const uint32_t per = (args.K + 7) / 8, n = rows * per;     // (few rows)
+      const uint32_t per = (args.K + 7) / 8;
+      const uint64_t n = static_cast<uint64_t>(rows) * per;      // (few rows, of any width)
       if (blockIdx.x == 0 && threadIdx.x == 64) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(rows);
-      for (uint32_t i = blockIdx.x * 256 + threadIdx.x - 64; i < n; i += gridDim.x * 256) {
-        const uint32_t to_row = i / per, e = i % per * 8;
+      for (uint64_t i = blockIdx.x * 256u + threadIdx.x - 64u; i < n; i += gridDim.x * 256u) {
+        const uint32_t to_row = static_cast<uint32_t>(n >> 32 ? i / per : static_cast<uint32_t>(i) / per);
+        const uint32_t e = static_cast<uint32_t>(i - static_cast<uint64_t>(to_row) * per) * 8;
         const uint32_t r = args.lo_row != 0 && to_row >= args.lo_row ? to_row - args.lo_row : to_row;
         const uint16_t* const from = args.A + r * args.lda + e;
         uint16_t* const to = args.clean + to_row * args.ld_clean + e;

@@ -426,13 +426,12 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * and a logit that is not -Inf.  Their loss, lse and dA are 0, they add nothing
  * to dB whatever A, dloss and lse hold there, and where more than 256 rows are
  * given they cost next to nothing.  A target or an id of
- * N or more makes the row's loss, its dA and dB NaN, like a NaN or an Inf among
- * its logits, or a NaN or +Inf among the teacher's; the other rows' losses and
- * dA are not affected.
+ * N or more makes the row's loss, its dA and dB NaN, like a NaN or +Inf among
+ * its logits or the teacher's; the other rows' losses and dA are not affected.
  *
  * targets, ids: int32 or int64 (target_dtype, id_dtype: GEMM_INDEX_I32, _I64);
  * teacher: bf16 or fp32; loss, lse, dloss: fp32.  scale and temperature are
- * positive and finite.  dA and dB each bf16 or fp32 (da_dtype, db_dtype), any
+ * positive and finite, 1.45 * scale and 1.45 / temperature too.  dA and dB each bf16 or fp32 (da_dtype, db_dtype), any
  * pitch and element alignment, either NULL where it is not wanted; accumulate (0
  * or 1) adds to dB in fp32.  A and B must be 16-byte aligned with pitches that
  * are multiples of 8; targets, ids, teacher, loss, lse, dloss at their element
@@ -451,7 +450,7 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * the _workspace_bytes call gives for these sizes (grad: 0 for the forward call,
  * 1 for the gradient), uninitialised; calls that share one must not overlap on
  * the GPU.  Large calls need, forward, 2 MK + MN / 10 bytes, and for the gradient
- * 6 MK and a piece of dz, 256 MiB or 4096 columns.  Calls are asynchronous on `stream`, allocate
+ * 6 MK (at least 6 * 64 K) and a piece of dz, 256 MiB or 4096 columns.  Calls are asynchronous on `stream`, allocate
  * nothing and can be captured; the same call gives the same bits.  Errors as
  * gemm_bf16.
  */

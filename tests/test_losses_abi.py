@@ -59,7 +59,7 @@ BACKWARD = [
 ]
 TARGET = [
     (dict(targets=0), INVALID), (dict(targets=FAKE + 2), ALIGN), (dict(code=2), INVALID),
-    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=NAN), INVALID), (dict(scale=INF), INVALID), (dict(scale=3e38), INVALID),
     (dict(smoothing=-0.1), INVALID), (dict(smoothing=1.5), INVALID), (dict(smoothing=NAN), INVALID),
     (dict(z=INF), INVALID), (dict(z=NAN), INVALID),
 ]
@@ -67,7 +67,7 @@ LIST = [
     (dict(top=0), INVALID), (dict(top=g.MAX_TOP + 1, ldt=2000, ldi=2000), INVALID), (dict(teacher=0), INVALID),
     (dict(ids=0), INVALID), (dict(teacher=FAKE + 1), ALIGN), (dict(ids=FAKE + 2), ALIGN), (dict(ldt=3), INVALID),
     (dict(ldi=3), INVALID), (dict(ct=2), INVALID), (dict(ci=-1), INVALID), (dict(t=0.0), INVALID), (dict(t=-1.0), INVALID),
-    (dict(t=NAN), INVALID), (dict(t=INF), INVALID), (dict(t=1e-45), INVALID),
+    (dict(t=NAN), INVALID), (dict(t=INF), INVALID), (dict(t=1e-45), INVALID), (dict(t=3e-39), INVALID),
 ]
 
 
