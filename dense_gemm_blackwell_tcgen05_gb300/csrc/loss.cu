@@ -33,7 +33,8 @@ namespace gb300 {
 namespace {
 
 constexpr uint32_t kInPlace = 256;             // up to so many rows are taken as they lie
-constexpr uint64_t kPieceBytes = 256ull << 20;
+// (4099 rows, 50021 tokens of width 1040: 572 us in one piece of 410 MB, 587 in two)
+constexpr uint64_t kPieceBytes = 512ull << 20;
 constexpr uint64_t kLeastPiece = 4096;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 

@@ -450,7 +450,7 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * the _workspace_bytes call gives for these sizes (grad: 0 for the forward call,
  * 1 for the gradient), uninitialised; calls that share one must not overlap on
  * the GPU.  Large calls need, forward, 2 MK + MN / 10 bytes, and for the gradient
- * 6 MK (at least 6 * 64 K) and a piece of dz, 256 MiB or 4096 columns.  Calls are asynchronous on `stream`, allocate
+ * 6 MK (at least 6 * 64 K) and a piece of dz, 512 MiB or 4096 columns.  Calls are asynchronous on `stream`, allocate
  * nothing and can be captured; the same call gives the same bits.  Errors as
  * gemm_bf16.
  */

@@ -97,7 +97,7 @@ def test_workspace_bytes():
         forward, back = (g.gemm_bf16_cross_entropy_workspace_bytes(M, N, K, x) for x in (0, 1))
         # nothing like the logits: what the header says, and room for vectors
         assert forward <= 2 * M * (K + 64) + M * N // 16 * 1.6 + 64 * M * 4 + 65536
-        assert back <= 6 * M * (K + 64) + max(1 << 28, 2 * M * 4096) * 1.1 + 64 * M + 65536
+        assert back <= 6 * M * (K + 64) + max(1 << 29, 2 * M * 4096) * 1.1 + 64 * M + 65536
         assert g.gemm_bf16_distill_workspace_bytes(M, N, K, 8, 0) > forward
 
 

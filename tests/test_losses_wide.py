@@ -109,6 +109,35 @@ def test_a_million_tokens(M):
     ref.check(dB, rb, tb, "dB")
 
 
+# M, N, K: pieces of 4096 tokens at least, and of 512 MiB of g at most
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("M, N, K, wide", [(34000, 9000, 72, 4608), (34000, 9000, 74, 4608), (300, 1800000, 24, 600064),
+                                           (128, 2200000, 16, 733440), (5, 9000000, 8, 3000064)])
+def test_pieces(M, N, K, wide, listed):
+    """Gradients by several pieces of the vocabulary, entries on both sides of a border."""
+    A, B, targets, dloss, scale = problem(M, N, (K + 7) // 8 * 8)
+    A, B = A[:, :K], B[:, :K]
+    border = min(M, 60)
+    targets[:border] = torch.arange(wide - border // 2, wide - border // 2 + border, device="cuda")
+    if listed:
+        ids = torch.stack([targets, targets.flip(0), targets], 1).int()
+        ids[:, 2] = torch.where(ids[:, 2] < 0, -1, (ids[:, 2] + 1) % N)
+        teacher = torch.linspace(-1.0, 1.0, 3 * M, device="cuda").view(M, 3)
+        t, entropy, live = ref.teacher_matrix(teacher, ids, N, 1.0 / scale)
+        loss, lse = g.matmul_distill(A, B, teacher, ids, temperature=1.0 / scale)
+        dA, dB = g.matmul_distill_grad(dloss, A, B, teacher, ids, lse, temperature=1.0 / scale, out_dtype=F32)
+    else:
+        t, live = ref.target_matrix(targets, N, 0.0), targets >= 0
+        loss, lse = g.matmul_cross_entropy(A, B, targets, scale=scale)
+        dA, dB = g.matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale=scale, out_dtype=F32)
+    assert status() == g.GEMM_OK
+    (ra, ta), (rb, tb) = ref.gradients(A, B, t, live, dloss, lse, scale, dA=F32, dB=F32, exact=True)
+    # a list's p is off by 2^-20 (1 + |teacher / T|) of itself, and these are below 1
+    more = 2.0 ** -19 * torch.where(live, dloss.double().abs() * scale, 0.0)[:, None] * t if listed else torch.zeros_like(t[:, :1])
+    ref.check(dA, ra, ta + (more @ B.double().abs() if listed else 0.0), "dA")
+    ref.check(dB, rb, tb + (more.T @ A.double().abs() if listed else 0.0), "dB")
+
+
 def test_a_long_width():
     M, N, K = 40, 300, 1 << 17
     A, B, targets, dloss, scale = problem(M, N, K)
