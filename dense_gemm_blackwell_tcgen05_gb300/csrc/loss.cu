@@ -471,11 +471,12 @@ struct SpreadArgs {
 template <int CG, class T>
 __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
   __shared__ float4 joined[8][32];
-  grid_dependency_wait();
+  if (a.pos != nullptr) grid_dependency_wait();          // (in place the deal needs no earlier kernel's count)
   const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
   const uint32_t M = a.M, K = a.products.K;
   const LossDeal deal = loss_deal<CG>(a.products, a.clusters);
   if (deal.direct) return;
+  if (a.pos == nullptr) grid_dependency_wait();
   const uint32_t parts = deal.parts;
   const uint32_t share = parts > 4 ? 8u : 1u;            // warps a piece
   const bool vec = ((reinterpret_cast<uintptr_t>(a.dA) | (a.ldo * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;

@@ -216,8 +216,9 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
-  // (every thread: the number of rows is an earlier kernel's)
-  grid_dependency_wait();
+  // (every thread: g is an earlier kernel's; the number of rows only where some may be left out,
+  // else the items are dealt ahead)
+  if (args.count != nullptr) grid_dependency_wait();
   const LossDeal deal = loss_deal<CG>(args, G);
   static_assert(sizeof(LossItem) == 24 && C::ITEM_BYTES == kLossAhead * sizeof(LossItem), "the items' table");
   LossItem* const ahead = reinterpret_cast<LossItem*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     ahead[threadIdx.x] = w;
   }
   __syncthreads();
+  if (args.count == nullptr) grid_dependency_wait();
   const auto item = [&](uint32_t i, LossItem& w) {
     if (i >= kLossAhead) return loss_item<CG>(args, deal, cluster_id, G, i, w);
     w = ahead[i];
