@@ -50,7 +50,7 @@ bool bucketed(uint64_t M, uint64_t top) { return M > kInPlace && top > 8; }
 constexpr uint64_t kTwoHalves = 128;
 
 struct Layout {
-  uint64_t count, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
+  uint64_t count, deal, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
   uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
   uint32_t parts;                                        // of dA's sums at most
   uint64_t lo, rows;                                     // where g's lower halves follow (0: none), rows of g
@@ -64,6 +64,7 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     return at;
   };
   w.count = take(8);
+  w.deal = back ? take(sizeof(LossDeal)) : 0;
   w.index = take(4 * M);
   w.pos = take(4 * M);
   if (top > 0) {
@@ -250,6 +251,9 @@ struct RowsArgs {
   uint64_t ld_compact;
   LossFactors factors;
   float4* row;
+  LossDeal* deal;              // the products' items (nullptr: not wanted)
+  LossProductArgs products;
+  uint32_t lt, clusters;
 };
 
 // Blocks of 256 threads, each for `per` rows of its own; to know their places, each counts
@@ -307,6 +311,10 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(const RowsArgs a) {
     }
     before += turn;
     __syncthreads();
+  }
+  if (a.deal != nullptr && blockIdx.x == 0 && warp == 7) {
+    const LossDeal d = loss_deal(a.products, all, a.lt, a.clusters);
+    if (lane == 0) *a.deal = d;
   }
   if (!copy) return;
   // (a block's own writes of pos, which the last turn's barrier ordered before)
@@ -474,7 +482,7 @@ __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
   if (a.pos != nullptr) grid_dependency_wait();          // (in place the deal needs no earlier kernel's count)
   const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
   const uint32_t M = a.M, K = a.products.K;
-  const LossDeal deal = loss_deal<CG>(a.products, a.clusters);
+  const LossDeal deal = loss_deal_of<CG>(a.products, a.clusters);
   if (deal.direct) return;
   if (a.pos == nullptr) grid_dependency_wait();
   const uint32_t parts = deal.parts;
@@ -613,9 +621,8 @@ LossFactors factors_of(const LossProblem& p, const Layout& w, uint8_t* ws) {
 }
 
 // More than kInPlace rows: those that count, compact.
-int launch_rows(const LossProblem& p, const Layout& w, uint8_t* ws, LossArgs& a, bool back, bool always,
+int launch_rows(const LossProblem& p, const Layout& w, uint8_t* ws, LossArgs& a, RowsArgs r, bool back, bool always,
                 cudaStream_t stream) {
-  RowsArgs r = {};
   r.M = p.M;
   r.K = p.K;
   r.per = p.M <= 16 * 1024 ? 16u : (p.M + 1023) / 1024;
@@ -653,7 +660,7 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   LossArgs a = logits_args(p, w, ws);
   LossOperands o = {p.A, p.lda, nullptr, 0, p.B, p.ldb, p.top > 0};
   if (p.M > kInPlace) {
-    if ((rc = launch_rows(p, w, ws, a, false, false, stream)) != GEMM_OK) return rc;
+    if ((rc = launch_rows(p, w, ws, a, RowsArgs{}, false, false, stream)) != GEMM_OK) return rc;
     o.compact = ws + w.compact;
     o.ld_compact = w.ld_compact;
     o.chained = true;
@@ -701,29 +708,12 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   const bool in_place = p.M <= kInPlace;
   // rows that TMA cannot store, and bf16 to be added to: the grouped product
   const bool whole = p.dB != nullptr && loss_matrix_ok(p.dB, p.ld_db, p.K, p.db_f32, p.accumulate);
-  if (in_place) {
-    o.compact = nullptr;
-    o.chained = p.top > 0;
-    a.factors = factors_of(p, w, ws);
-    a.A = static_cast<const uint16_t*>(p.A);
-    a.lda = p.lda;
-    a.clean = compact;
-    a.ld_clean = w.ld_compact;
-    a.offsets = reinterpret_cast<int32_t*>(ws + w.count);
-  } else {
-    if ((rc = launch_rows(p, w, ws, a, true, p.dB != nullptr && !whole, stream)) != GEMM_OK) return rc;
-    a.row = reinterpret_cast<const float4*>(ws + w.row);
-  }
-  a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
-  a.ld_out = w.width;
-  a.lo_row = static_cast<uint32_t>(w.lo);
-
   LossProduct g = {};
   g.M = static_cast<uint32_t>(w.rows);
   g.K = p.K;
   g.width = static_cast<uint32_t>(w.width < p.N ? w.width : p.N);
-  g.count = a.count;
-  g.g = a.out;
+  g.deal = in_place ? nullptr : reinterpret_cast<const LossDeal*>(ws + w.deal);
+  g.g = ws + w.piece;
   g.ldg = w.width;
   g.ldb = p.ldb;
   g.compact = compact;
@@ -746,6 +736,30 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   g.add_db = p.accumulate;
   LossProductPlan plan = {};
   if ((g.sums != nullptr || whole) && (rc = loss_product_plan(g, ctx, &plan)) != GEMM_OK) return rc;
+  if (in_place) {
+    o.compact = nullptr;
+    o.chained = p.top > 0;
+    a.factors = factors_of(p, w, ws);
+    a.A = static_cast<const uint16_t*>(p.A);
+    a.lda = p.lda;
+    a.clean = compact;
+    a.ld_clean = w.ld_compact;
+    a.offsets = reinterpret_cast<int32_t*>(ws + w.count);
+  } else {
+    RowsArgs r = {};
+    if (g.sums != nullptr || whole) {
+      r.deal = reinterpret_cast<LossDeal*>(ws + w.deal);
+      r.products = loss_product_args(g, plan, ctx);
+      r.lt = 128 * plan.cg;
+      r.clusters = plan.clusters;
+    }
+    if ((rc = launch_rows(p, w, ws, a, r, true, p.dB != nullptr && !whole, stream)) != GEMM_OK) return rc;
+    a.row = reinterpret_cast<const float4*>(ws + w.row);
+  }
+  a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
+  a.ld_out = w.width;
+  a.lo_row = static_cast<uint32_t>(w.lo);
+
   for (uint64_t v0 = 0; v0 < p.N; v0 += w.width) {
     const uint32_t n = static_cast<uint32_t>(p.N - v0 < w.width ? p.N - v0 : w.width);
     o.B = static_cast<const uint16_t*>(p.B) + v0 * p.ldb;

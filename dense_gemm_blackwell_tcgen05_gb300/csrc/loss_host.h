@@ -99,9 +99,10 @@ int launch_loss_logits_forward(const LossOperands& o, LossArgs a, const LaunchCt
 int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, cudaStream_t stream);
 
 // The products with a piece of the logits' gradient (loss_products.cuh).
+struct LossDeal;
 struct LossProduct {
   uint32_t M, n, K, width;     // rows at most, the piece's columns, the width, the first piece's columns
-  const uint32_t* count;
+  const LossDeal* deal;        // of the items, found by an earlier kernel (nullptr: no row is left out)
   const void *g, *B;           // [M, n], B's rows of the piece
   const void *A, *compact;     // all rows of A, for where none is left out, and those that count
   uint64_t ldg, ldb, lda, ld_compact;

@@ -109,7 +109,7 @@ LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& p
   a.M = p.M;
   a.n = p.n;
   a.K = p.K;
-  a.count = p.count;
+  a.deal = p.deal;
   a.nt = plan.nt;
   a.width = p.width;
   a.most = p.most;

@@ -30,9 +30,10 @@
 
 namespace gb300 {
 
+struct LossDeal;
 struct LossProductArgs {
   uint32_t M, n, K;            // rows at most, columns of the piece, width
-  const uint32_t* count;       // rows that count (nullptr: all of them)
+  const LossDeal* deal;        // the deal for the rows that count (nullptr: all of them do, it is found here)
   uint32_t nt;                 // columns of a tile, a multiple of 64
   uint32_t width;              // of the first piece, by which the parts are chosen
   uint32_t most;               // parts at most
@@ -77,8 +78,7 @@ struct LossDeal {
 
 // The deal that ends first, of `kt` stages a tile over `tiles` tiles of Rows and `others`
 // items of Matrix, `cost` stages each; each part costs its sums' way to memory and back
-// (`extra` stages over all clusters).  The 32 lanes try a number of parts each; every warp
-// of every block, of the kernel that joins the sums too, finds the same.
+// (`extra` stages over all clusters).  The 32 lanes try a number of parts each.
 __device__ __forceinline__ void loss_parts(LossDeal& d, uint32_t tiles, uint32_t others, uint32_t kt, uint32_t cost,
                                            uint32_t extra, uint32_t G, uint32_t most) {
   constexpr uint32_t kEnds = 5;                          // an item's first loads and last store, in stages
@@ -108,20 +108,29 @@ __device__ __forceinline__ void loss_parts(LossDeal& d, uint32_t tiles, uint32_t
   d.n0 = __shfl_sync(0xffffffffu, n0, lane);
 }
 
-template <int CG>
-__device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t G) {
-  constexpr uint32_t LT = 128 * CG;
+// For `count` rows, tiles of `lt` rows and G clusters.
+__device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t count, uint32_t lt, uint32_t G) {
   LossDeal d;
-  d.count = a.count != nullptr ? min(*a.count, a.M) : a.M;
+  d.count = count;
   d.cb = (a.K + a.nt - 1) / a.nt;
-  d.rb_x = a.rows ? (d.count + LT - 1) / LT : 0u;
-  d.rb_y = a.matrix ? (a.n + LT - 1) / LT : 0u;
+  d.rb_x = a.rows ? (d.count + lt - 1) / lt : 0u;
+  d.rb_y = a.matrix ? (a.n + lt - 1) / lt : 0u;
   // (by the first piece: later ones, which may be narrower, add to the same parts)
-  const uint32_t others = a.matrix ? (a.width + LT - 1) / LT * d.cb : 0u;
+  const uint32_t others = a.matrix ? (a.width + lt - 1) / lt * d.cb : 0u;
   // 4 bytes written and read of each sum at 5 TB/s; 0.3 us a stage
   const uint32_t extra = static_cast<uint32_t>(static_cast<uint64_t>(d.count) * a.K * 8 / 1500000);
   loss_parts(d, d.rb_x * d.cb, others, (a.width + 63) / 64, max((d.count + 63) / 64 + 3, a.db_cost), extra, G, a.most);
   d.direct = a.direct != 0u && d.parts == 1 && d.count == a.M;
+  return d;
+}
+
+// The same, once the kernels before the product's have ended: found ahead where rows may be left out.
+template <int CG>
+__device__ __forceinline__ LossDeal loss_deal_of(const LossProductArgs& a, uint32_t G) {
+  constexpr uint32_t LT = 128 * CG;
+  if (a.deal == nullptr) return loss_deal(a, a.M, LT, G);
+  LossDeal d = *a.deal;
+  d.rb_y = a.matrix ? (a.n + LT - 1) / LT : 0u;          // (by this piece)
   return d;
 }
 
@@ -153,8 +162,9 @@ __device__ __forceinline__ bool loss_item(const LossProductArgs& a, const LossDe
   w.l0 = rb * 128 * CG;
   w.c0 = cb * a.nt;
   const uint32_t kt = ((w.matrix ? d.count : a.n) + 63) / 64, parts = w.matrix ? 1u : d.parts;
-  w.k0 = static_cast<uint32_t>(static_cast<uint64_t>(kt) * w.s / parts);
-  w.k1 = static_cast<uint32_t>(static_cast<uint64_t>(kt) * (w.s + 1) / parts);
+  // (several parts: kt is at most 0x4000)
+  w.k0 = parts == 1 ? 0u : kt * w.s / parts;
+  w.k1 = parts == 1 ? kt : kt * (w.s + 1) / parts;
   return true;
 }
 
@@ -218,8 +228,8 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
   const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // (every thread: g is an earlier kernel's; the number of rows only where some may be left out,
   // else the items are dealt ahead)
-  if (args.count != nullptr) grid_dependency_wait();
-  const LossDeal deal = loss_deal<CG>(args, G);
+  if (args.deal != nullptr) grid_dependency_wait();
+  const LossDeal deal = loss_deal_of<CG>(args, G);
   static_assert(sizeof(LossItem) == 24 && C::ITEM_BYTES == kLossAhead * sizeof(LossItem), "the items' table");
   LossItem* const ahead = reinterpret_cast<LossItem*>(base_ptr + (bar0 - base) + C::BAR_BYTES);
   if (threadIdx.x < kLossAhead) {
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     ahead[threadIdx.x] = w;
   }
   __syncthreads();
-  if (args.count == nullptr) grid_dependency_wait();
+  if (args.deal == nullptr) grid_dependency_wait();
   const auto item = [&](uint32_t i, LossItem& w) {
     if (i >= kLossAhead) return loss_item<CG>(args, deal, cluster_id, G, i, w);
     w = ahead[i];
