@@ -50,9 +50,9 @@ bool bucketed(uint64_t M, uint64_t top) { return M > kInPlace && top > 8; }
 constexpr uint64_t kTwoHalves = 128;
 
 struct Layout {
-  uint64_t count, deal, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums;
+  uint64_t count, deal, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums, sums_db;
   uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
-  uint32_t parts;                                        // of dA's sums at most
+  uint32_t parts, parts_db;                              // of dA's and dB's sums at most
   uint64_t lo, rows;                                     // where g's lower halves follow (0: none), rows of g
 };
 
@@ -89,6 +89,8 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     w.stride_sums = w.rows * w.ld_sums;
     w.parts = loss_most_parts(w.rows, w.width < N ? w.width : N, K);
     w.sums = take(4 * w.stride_sums * w.parts);
+    w.parts_db = M > kInPlace && w.width >= N ? loss_most_parts_db(M, N, K) : 1;
+    if (w.parts_db > 1) w.sums_db = take(4 * N * w.ld_sums * w.parts_db);
   } else {
     if (M > kInPlace) w.compact = take(2 * M * w.ld_compact);
     w.entry_z = take(4 * M * (top > 0 ? top : 1));
@@ -469,80 +471,113 @@ struct SpreadArgs {
   const void* targets;
   bool target64;
   const uint32_t* len;
-  void* dA;
+  void* dA;                    // (nullptr: not wanted)
   uint64_t ldo;
+  bool da_f32;
+  // the matrix's rows dealt in parts
+  const float* sums_db;        // (nullptr: never)
+  uint64_t stride_db;
+  uint32_t N;
+  void* dB;
+  uint64_t ld_db;
+  bool db_f32, add_db;
 };
 
-// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros; nothing where the
-// products have stored it themselves.  A block per 128 columns
+// Four columns of a row from c on, rounded once (add: fp32, to what is there).
+__device__ __forceinline__ void store_joined(void* out, uint64_t ld, bool f32, bool add, uint32_t K, uint64_t r, uint32_t c,
+                                             float4 x) {
+  const uint64_t size = f32 ? 4 : 2;
+  const bool vec = ((reinterpret_cast<uintptr_t>(out) | (ld * size)) & (4 * size - 1)) == 0 && c + 4 <= K;
+  if (!f32) {
+    uint16_t* const to = static_cast<uint16_t*>(out) + r * ld + c;
+    const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    if (vec) {
+      *reinterpret_cast<uint2*>(to) = h;
+    } else {
+      const uint32_t v[2] = {h.x, h.y};
+      for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e % 2)));
+    }
+    return;
+  }
+  float* const to = static_cast<float*>(out) + r * ld + c;
+  if (vec) {
+    if (add) {
+      const float4 had = *reinterpret_cast<const float4*>(to);
+      x = make_float4(had.x + x.x, had.y + x.y, had.z + x.z, had.w + x.w);
+    }
+    *reinterpret_cast<float4*>(to) = x;
+  } else {
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[e] = add ? to[e] + v[e] : v[e];
+  }
+}
+
+// dA[r] = the parts' sums[pos[r]] in order, rounded once, or zeros, and dB (+)= its parts'
+// sums; nothing where the products have stored it themselves.  A block per 128 columns
 // of a row where there are many parts, which its warps share; a warp where there are few.
-template <int CG, class T>
+// DB: Matrix's rows may have been dealt in parts.
+template <int CG, bool DB>
 __global__ void __launch_bounds__(256) loss_spread_kernel(const SpreadArgs a) {
   __shared__ float4 joined[8][32];
   if (a.pos != nullptr) grid_dependency_wait();          // (in place the deal needs no earlier kernel's count)
   const uint32_t lane = lane_idx(), warp = threadIdx.x / 32;
-  const uint32_t M = a.M, K = a.products.K;
+  const uint32_t K = a.products.K;
   const LossDeal deal = loss_deal_of<CG>(a.products, a.clusters);
-  if (deal.direct) return;
+  const uint32_t M = a.dA == nullptr || deal.direct ? 0u : a.M, N = !DB || deal.parts_db == 1 ? 0u : a.N;
+  if (M + N == 0) return;
   if (a.pos == nullptr) grid_dependency_wait();
-  const uint32_t parts = deal.parts;
-  const uint32_t share = parts > 4 ? 8u : 1u;            // warps a piece
-  const bool vec = ((reinterpret_cast<uintptr_t>(a.dA) | (a.ldo * sizeof(T))) & (4 * sizeof(T) - 1)) == 0;
   const uint32_t pieces = (K + 127) / 128;
-  const uint64_t units = static_cast<uint64_t>(M) * pieces, step = static_cast<uint64_t>(gridDim.x) * (8 / share);
-  // (a block's warps take the same turns)
-  for (uint64_t u0 = blockIdx.x * static_cast<uint64_t>(8 / share); u0 < units; u0 += step) {
-    const uint64_t u = u0 + (share == 1 ? warp : 0u);
-    const uint32_t r = static_cast<uint32_t>(u / pieces), c = static_cast<uint32_t>(u % pieces) * 128 + 4 * lane;
-    const bool in = u < units;
-    int32_t i = -1;
-    if (in && a.pos != nullptr) i = a.pos[r];
-    else if (in && (a.len != nullptr ? a.len[r] > 0 : loss_index_at(a.targets, a.target64, r) >= 0)) i = static_cast<int32_t>(r);
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (i >= 0 && c < K) {
-      const float* const from = a.sums + static_cast<uint32_t>(i) * a.ld_sums + c;
+  // `rows` rows; where(r): where row r's sums lie (nullptr: zeros)
+  const auto join = [&](uint32_t rows, uint32_t parts, uint64_t stride, uint64_t lo, const auto& where, const auto& store) {
+    const uint32_t share = parts > 4 ? 8u : 1u;          // warps a piece
+    const uint64_t units = static_cast<uint64_t>(rows) * pieces, step = static_cast<uint64_t>(gridDim.x) * (8 / share);
+    // (a block's warps take the same turns)
+    for (uint64_t u0 = blockIdx.x * static_cast<uint64_t>(8 / share); u0 < units; u0 += step) {
+      const uint64_t u = u0 + (share == 1 ? warp : 0u);
+      const uint32_t r = static_cast<uint32_t>(u / pieces), c = static_cast<uint32_t>(u % pieces) * 128 + 4 * lane;
+      const bool in = u < units && c < K;
+      const float* from = in ? where(r) : nullptr;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (from != nullptr) {
+        from += c;
 #pragma unroll 4
-      for (uint32_t p = share == 1 ? 0u : warp; p < parts; p += share) {
-        const float4 y = *reinterpret_cast<const float4*>(from + p * a.stride_sums);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-        if (a.lo != 0) {
-          const float4 z = *reinterpret_cast<const float4*>(from + p * a.stride_sums + a.lo * a.ld_sums);
-          x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
-        }
-      }
-    }
-    if (share > 1) {
-      joined[warp][lane] = x;
-      __syncthreads();
-      if (warp == 0) {
-#pragma unroll
-        for (uint32_t w = 1; w < 8; ++w) {
-          const float4 y = joined[w][lane];
+        for (uint32_t p = share == 1 ? 0u : warp; p < parts; p += share) {
+          const float4 y = *reinterpret_cast<const float4*>(from + p * stride);
           x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          if (lo != 0) {
+            const float4 z = *reinterpret_cast<const float4*>(from + p * stride + lo);
+            x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
+          }
         }
       }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    if (!in || c >= K) continue;
-    T* const to = static_cast<T*>(a.dA) + r * a.ldo;
-    if constexpr (sizeof(T) == 2) {
-      const uint2 h = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-      if (vec && c + 4 <= K) {
-        *reinterpret_cast<uint2*>(to + c) = h;
-      } else {
-        const uint32_t v[2] = {h.x, h.y};
-        for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[c + e] = static_cast<T>(v[e / 2] >> (16 * (e % 2)));
+      if (share > 1) {
+        joined[warp][lane] = x;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (uint32_t w = 1; w < 8; ++w) {
+            const float4 y = joined[w][lane];
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+        }
+        __syncthreads();
+        if (warp != 0) continue;
       }
-    } else {
-      if (vec && c + 4 <= K) {
-        *reinterpret_cast<float4*>(to + c) = x;
-      } else {
-        const float v[4] = {x.x, x.y, x.z, x.w};
-        for (uint32_t e = 0; e < 4 && c + e < K; ++e) to[c + e] = v[e];
-      }
+      if (in) store(r, c, x);
     }
-  }
+  };
+  join(M, deal.parts, a.stride_sums, a.lo * a.ld_sums,
+       [&](uint32_t r) -> const float* {
+         int32_t i = -1;
+         if (a.pos != nullptr) i = a.pos[r];
+         else if (a.len != nullptr ? a.len[r] > 0 : loss_index_at(a.targets, a.target64, r) >= 0) i = static_cast<int32_t>(r);
+         return i >= 0 ? a.sums + static_cast<uint32_t>(i) * a.ld_sums : nullptr;
+       },
+       [&](uint32_t r, uint32_t c, const float4& x) { store_joined(a.dA, a.ldo, a.da_f32, false, K, r, c, x); });
+  if constexpr (DB)
+    join(N, deal.parts_db, a.stride_db, 0,
+         [&](uint32_t v) -> const float* { return a.sums_db + v * a.ld_sums; },
+         [&](uint32_t v, uint32_t c, const float4& x) { store_joined(a.dB, a.ld_db, a.db_f32, a.add_db, K, v, c, x); });
 }
 
 template <class... P, class... A>
@@ -734,6 +769,11 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   g.ld_db = p.ld_db;
   g.db_f32 = p.db_f32;
   g.add_db = p.accumulate;
+  if (whole && w.parts_db > 1) {
+    g.sums_db = reinterpret_cast<float*>(ws + w.sums_db);
+    g.stride_db = static_cast<uint64_t>(p.N) * w.ld_sums;
+    g.most_db = w.parts_db;
+  }
   LossProductPlan plan = {};
   if ((g.sums != nullptr || whole) && (rc = loss_product_plan(g, ctx, &plan)) != GEMM_OK) return rc;
   if (in_place) {
@@ -796,7 +836,7 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
       if ((rc = launch_grouped_wgrad(d, ctx, stream)) != GEMM_OK) return rc;
     }
   }
-  if (p.dA == nullptr) return GEMM_OK;
+  if (p.dA == nullptr && g.sums_db == nullptr) return GEMM_OK;
   g.n = g.width;
   SpreadArgs d = {};
   d.products = loss_product_args(g, plan, ctx);
@@ -812,13 +852,22 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
   d.len = a.len;
   d.dA = p.dA;
   d.ldo = p.ld_da;
-  const uint64_t units = static_cast<uint64_t>(p.M) * ((p.K + 127) / 128), most = 16ull * static_cast<uint64_t>(ctx.num_sms);
+  d.da_f32 = p.da_f32;
+  d.sums_db = g.sums_db;
+  d.stride_db = g.stride_db;
+  d.N = p.N;
+  d.dB = p.dB;
+  d.ld_db = p.ld_db;
+  d.db_f32 = p.db_f32;
+  d.add_db = p.accumulate;
+  const uint64_t rows = (p.dA != nullptr ? p.M : 0ull) + (g.sums_db != nullptr ? p.N : 0ull);
+  const uint64_t units = rows * ((p.K + 127) / 128), most = 16ull * static_cast<uint64_t>(ctx.num_sms);
   const unsigned blocks = static_cast<unsigned>(units < most ? units : most);
-  if (plan.cg == 2)
-    return p.da_f32 ? launch(loss_spread_kernel<2, float>, blocks, 256, true, stream, d)
-                    : launch(loss_spread_kernel<2, uint16_t>, blocks, 256, true, stream, d);
-  return p.da_f32 ? launch(loss_spread_kernel<1, float>, blocks, 256, true, stream, d)
-                  : launch(loss_spread_kernel<1, uint16_t>, blocks, 256, true, stream, d);
+  if (g.sums_db != nullptr)
+    return plan.cg == 2 ? launch(loss_spread_kernel<2, true>, blocks, 256, true, stream, d)
+                        : launch(loss_spread_kernel<1, true>, blocks, 256, true, stream, d);
+  return plan.cg == 2 ? launch(loss_spread_kernel<2, false>, blocks, 256, true, stream, d)
+                      : launch(loss_spread_kernel<1, false>, blocks, 256, true, stream, d);
 }
 
 }  // namespace gb300

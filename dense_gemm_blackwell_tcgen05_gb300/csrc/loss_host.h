@@ -110,6 +110,9 @@ struct LossProduct {
   uint64_t ld_sums, stride_sums;
   uint32_t most;
   bool add_sums;
+  float* sums_db;              // (nullptr: the rows are not to be dealt in parts) [most_db][n][K], rows of ld_sums
+  uint64_t stride_db;
+  uint32_t most_db;
   void* dA;                    // (nullptr: not wanted) instead of sums where they need no joining
   uint64_t ld_da;
   bool da_f32;
@@ -119,6 +122,8 @@ struct LossProduct {
 };
 // Parts that the sums' reduction over a piece may be dealt in, at most.
 uint32_t loss_most_parts(uint64_t M, uint64_t width, uint64_t K);
+// Parts that the product to a matrix of few tiles may deal its rows in, at most.
+uint32_t loss_most_parts_db(uint64_t M, uint64_t N, uint64_t K);
 // Whether the product to the matrix can be stored at `out`: TMA takes rows that start and
 // end on 16 bytes.
 bool loss_matrix_ok(const void* out, uint64_t ldo, uint64_t K, bool out_f32, bool add);

@@ -40,12 +40,13 @@ int launch(const LossProduct& p, const LossProductPlan& plan, const LaunchCtx& c
       !operand_map(&m.B, p.B, p.K, p.n, 1, p.ldb, 0, 64) || !operand_map(&m.A, p.A, p.K, p.M, 1, p.lda, 0, 64) ||
       !operand_map(&m.compact, p.compact, p.K, p.M, 1, p.ld_compact, 0, 64) ||
       (p.sums != nullptr && !output_map(&m.sums, p.sums, true, p.K, p.M, p.most, p.ld_sums, p.stride_sums)) ||
+      (p.sums_db != nullptr && !output_map(&m.sums_db, p.sums_db, true, p.K, p.n, p.most_db, p.ld_sums, p.stride_db)) ||
       (p.dA != nullptr && !output_map(&m.dA, p.dA, p.da_f32, p.K, p.M, 1, p.ld_da, 0)) ||
       (p.dB != nullptr && !output_map(&m.dB, p.dB, p.db_f32, p.K, p.n, 1, p.ld_db, 0)))
     return GEMM_ERR_LAUNCH;
   const uint64_t columns = ceil_div_u64(p.K, plan.nt);
   const uint64_t tiles = (p.sums != nullptr ? ceil_div_u64(p.M, C::LT) * p.most : 0) * columns +
-                         (p.dB != nullptr ? ceil_div_u64(p.n, C::LT) : 0) * columns;
+                         (p.dB != nullptr ? ceil_div_u64(p.n, C::LT) * (p.sums_db != nullptr ? p.most_db : 1) : 0) * columns;
   if (tiles > 0x7FFFFFFFull) return GEMM_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(plan.clusters * CG);
@@ -71,6 +72,12 @@ uint32_t loss_most_parts(uint64_t M, uint64_t width, uint64_t K) {
   const uint64_t by_size = kMostSums / (4 * M * (K > 0 ? K : 1)), by_length = ceil_div_u64(width, 4 * 64);
   const uint64_t n = by_size < by_length ? by_size : by_length;
   return static_cast<uint32_t>(n < 1 ? 1 : n > 32 ? 32 : n);
+}
+
+uint32_t loss_most_parts_db(uint64_t M, uint64_t N, uint64_t K) {
+  const uint64_t tiles = ceil_div_u64(N, 128) * ceil_div_u64(K > 0 ? K : 1, 128), by_length = ceil_div_u64(M, 64) / 8;
+  const uint64_t n = kLossSms / tiles < by_length ? kLossSms / tiles : by_length;
+  return static_cast<uint32_t>(n < 1 ? 1 : n);
 }
 
 bool loss_matrix_ok(const void* out, uint64_t ldo, uint64_t K, bool out_f32, bool add) {
@@ -113,6 +120,7 @@ LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& p
   a.nt = plan.nt;
   a.width = p.width;
   a.most = p.most;
+  a.most_db = p.sums_db != nullptr ? p.most_db : 1u;
   a.rows = p.sums != nullptr ? 1u : 0u;
   a.direct = p.dA == nullptr ? 0u : p.da_f32 ? 2u : 1u;
   a.matrix = p.dB != nullptr ? 1u : 0u;

@@ -8,11 +8,12 @@
 // that fills no tile costs what it holds, in steps of 32 (16 on one CTA).  A warp stages
 // 32 rows of 128 bytes in shared memory and stores them by TMA, which leaves out what lies
 // past the output's ends and adds in L2 what is to be added in fp32 (129 rows, 32768 tokens
-// of width 2048, both gradients: 100 us; stored from registers, each lane its own row in
-// whole sectors, 103).  Rows has few tiles and a long reduction,
+// of width 2048, both gradients: 3 us of 100 less than from registers, each lane its own row
+// in whole sectors).  Rows has few tiles and a long reduction,
 // so it is dealt to the clusters in parts, whose sums lie apart and are joined in order:
-// the same bits every time.  Matrix has many tiles.  One launch takes the items of both
-// in turn, so that one last round is ragged instead of two.
+// the same bits every time.  Matrix has many tiles, or, of a small matrix and many rows, goes in
+// parts too.  One launch takes the items of both in turn, so that one last round is ragged
+// instead of two.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
 // 1113 us for both, 1.98 PFLOP/s, tensor pipes 97.6 % busy), few by B's read and dB's write
@@ -36,7 +37,7 @@ struct LossProductArgs {
   const LossDeal* deal;        // the deal for the rows that count (nullptr: all of them do, it is found here)
   uint32_t nt;                 // columns of a tile, a multiple of 64
   uint32_t width;              // of the first piece, by which the parts are chosen
-  uint32_t most;               // parts at most
+  uint32_t most, most_db;      // parts at most, of Rows and of Matrix
   uint32_t rows, matrix;       // which of them are wanted
   uint32_t direct;             // Rows to dA, bf16 (1) or fp32 (2), where there is nothing to join (0: never)
   uint32_t add_sums, add_db;   // added to what is there
@@ -67,12 +68,13 @@ struct LossProductCfg {
   static constexpr uint32_t ACC_COLS = 256;
 };
 
-// How the items are dealt.  Rows' reduction over the piece goes in `parts`, and its items
+// How the items are dealt.  Matrix's reduction to the rows goes in `parts_db` where it has so few
+// tiles that clusters would idle.  Rows' reduction over the piece goes in `parts`, and its items
 // in turn to the G clusters, so that the first `r` have one more than the others' x; Matrix's
 // follow, n1 at most to each of those and n0 to each of the others, who end no later for it.
 struct LossDeal {
   uint32_t count, rb_x, rb_y, cb;      // rows that count; tiles down, of either, and across
-  uint32_t parts, x, r, n1, n0;
+  uint32_t parts, parts_db, x, r, n1, n0;
   bool direct;                         // Rows go to dA: one part, and no row left out
 };
 
@@ -116,10 +118,20 @@ __device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t
   d.rb_x = a.rows ? (d.count + lt - 1) / lt : 0u;
   d.rb_y = a.matrix ? (a.n + lt - 1) / lt : 0u;
   // (by the first piece: later ones, which may be narrower, add to the same parts)
-  const uint32_t others = a.matrix ? (a.width + lt - 1) / lt * d.cb : 0u;
-  // 4 bytes written and read of each sum at 5 TB/s; 0.3 us a stage
+  const uint32_t tiles = a.matrix ? (a.width + lt - 1) / lt * d.cb : 0u, stages = (d.count + 63) / 64;
+  // Matrix in parts of at least 8 stages, where that saves more than the sums' way to memory and
+  // back (4 bytes at 5 TB/s, 0.3 us a stage) and the joining take: 4000 rows, 512 tokens of width
+  // 256, 8 tiles of 63 stages, 19.5 us in parts and 28.3 whole; 1500, 512, 128, 4 of 24, 19.0 and 17.0
+  d.parts_db = 1;
+  if (tiles > 0 && a.most_db > 1 && stages <= 0x1000000u) {
+    const uint32_t n = min(min(G / tiles, stages / 8), a.most_db);
+    const uint32_t way = static_cast<uint32_t>(static_cast<uint64_t>(a.width) * a.K * n * 8 / 1500000);
+    if (n > 1 && stages - (stages + n - 1) / n > way + 24) d.parts_db = n;
+  }
+  const uint32_t others = tiles * d.parts_db, each = (stages + d.parts_db - 1) / d.parts_db + 3;
+  // (Rows' sums, the same)
   const uint32_t extra = static_cast<uint32_t>(static_cast<uint64_t>(d.count) * a.K * 8 / 1500000);
-  loss_parts(d, d.rb_x * d.cb, others, (a.width + 63) / 64, max((d.count + 63) / 64 + 3, a.db_cost), extra, G, a.most);
+  loss_parts(d, d.rb_x * d.cb, others, (a.width + 63) / 64, max(each, a.db_cost), extra, G, a.most);
   d.direct = a.direct != 0u && d.parts == 1 && d.count == a.M;
   return d;
 }
@@ -134,7 +146,7 @@ __device__ __forceinline__ LossDeal loss_deal_of(const LossProductArgs& a, uint3
   return d;
 }
 
-// Cluster c's i-th item: rows l0.., columns c0.., stages k0 .. k1 - 1; part s of Rows, or
+// Cluster c's i-th item: rows l0.., columns c0.., stages k0 .. k1 - 1; part s of Rows or of
 // Matrix.  False past the last.
 struct LossItem {
   uint32_t l0, c0, k0, k1, s;
@@ -154,25 +166,25 @@ __device__ __forceinline__ bool loss_item(const LossProductArgs& a, const LossDe
     i -= mine;
     if (i >= (c < d.r ? d.n1 : d.n0)) return false;
     t = i < d.n1 ? c + i * G : d.n1 * G + (i - d.n1) * (G - d.r) + (c - d.r);
-    if (t >= per) return false;
+    if (t >= per * d.parts_db) return false;
   }
-  w.s = t / per;                                         // (Matrix: 0)
+  w.s = t / per;
   uint32_t rb, cb;
   tile_coords(t - w.s * per, rb_n, d.cb, 8u, rb, cb);
   w.l0 = rb * 128 * CG;
   w.c0 = cb * a.nt;
-  const uint32_t kt = ((w.matrix ? d.count : a.n) + 63) / 64, parts = w.matrix ? 1u : d.parts;
-  // (several parts: kt is at most 0x4000)
+  const uint32_t kt = ((w.matrix ? d.count : a.n) + 63) / 64, parts = w.matrix ? d.parts_db : d.parts;
+  // (several parts: at most 32 of 0x4000 stages, or 152 of 0x1000000)
   w.k0 = parts == 1 ? 0u : kt * w.s / parts;
   w.k1 = parts == 1 ? kt : kt * (w.s + 1) / parts;
   return true;
 }
 
 // g by its rows (boxes of 128) and by its columns, B's piece and the rows of A, all and those
-// that count (boxes of 64 x 64); the sums [parts][M][K], dA and dB's rows of the piece (boxes
-// of 128 bytes x 32).
+// that count (boxes of 64 x 64); the sums [parts][M][K] and [parts_db][n][K], dA and dB's rows
+// of the piece (boxes of 128 bytes x 32).
 struct LossMaps {
-  CUtensorMap g_rows, g_columns, B, A, compact, sums, dA, dB;
+  CUtensorMap g_rows, g_columns, B, A, compact, sums, sums_db, dA, dB;
 };
 
 // T: dB's elements, uint32_t (fp32) or uint16_t (bf16).
@@ -350,17 +362,18 @@ __global__ void __launch_bounds__(LossProductCfg<CG>::kThreads, 1)
     LossItem w;
     for (uint32_t i = 0; item(i, w); ++i) {
       // columns of a box: 128 bytes a row
-      const bool bf16 = w.matrix ? sizeof(T) == 2 : deal.direct && args.direct == 1u;
+      const bool apart = w.matrix && deal.parts_db > 1;   // Matrix's sums are joined later
+      const bool bf16 = w.matrix ? sizeof(T) == 2 && !apart : deal.direct && args.direct == 1u;
       const uint32_t wide = bf16 ? 64u : 32u;
       const uint32_t nch = (min(args.nt, args.K - w.c0) + wide - 1) / wide;
       const int32_t row = static_cast<int32_t>(w.l0 + rank * 128 + q * 32);
-      const bool add = w.matrix ? args.add_db != 0u : args.add_sums != 0u;
+      const bool add = w.matrix ? args.add_db != 0u && !apart : args.add_sums != 0u;
       // a box on its way: rows past the output's are nobody's
       const auto send = [&](uint32_t ch) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && row < static_cast<int32_t>(w.matrix ? args.n : deal.count)) {
-          const CUtensorMap* const out = w.matrix ? &maps.dB : deal.direct ? &maps.dA : &maps.sums;
+          const CUtensorMap* const out = apart ? &maps.sums_db : w.matrix ? &maps.dB : deal.direct ? &maps.dA : &maps.sums;
           const int32_t x = static_cast<int32_t>(w.c0 + ch * wide), z = static_cast<int32_t>(w.s);
           if (add) tma_add_3d(out, box, x, row, z);
           else tma_store_3d(out, box, x, row, z);

@@ -138,6 +138,36 @@ def test_pieces(M, N, K, wide, listed):
     ref.check(dB, rb, tb + (more.T @ A.double().abs() if listed else 0.0), "dB")
 
 
+@pytest.mark.parametrize("db, accumulate", [(BF16, False), (F32, False), (F32, True)])
+@pytest.mark.parametrize("M, N, K", [(4000, 512, 256), (2100, 130, 520), (9000, 600, 72), (2048, 40, 1000), (2500, 1000, 64),
+                                     (20000, 300, 136)])
+def test_matrices_of_few_tiles(M, N, K, db, accumulate):
+    """Many rows, a small matrix: its product is dealt in parts of the rows.  With most rows left
+    out it is not."""
+    A, B, targets, dloss, scale = problem(M, N, K)
+    for some in (targets, torch.where(torch.arange(M, device="cuda") % 50 == 0, targets, -1)):
+        t, live = ref.target_matrix(some, N, 0.0), some >= 0
+        loss, lse = g.matmul_cross_entropy(A, B, some, scale=scale)
+        old = torch.linspace(-1.0, 1.0, N * K, device="cuda").view(N, K).to(db)
+        buf = torch.full((N, K + 8), 7.0, dtype=db, device="cuda")
+        for need_dA in (True, False):
+            dB = buf[:, :K]
+            dB.copy_(old)
+            dA, got = g.matmul_cross_entropy_grad(dloss, A, B, some, lse, scale=scale, dB=dB, accumulate=accumulate,
+                                                  need_dA=need_dA)
+            assert got is dB and status() == g.GEMM_OK and (buf[:, K:] == 7.0).all()
+            (ra, ta), (rb, tb) = ref.gradients(A, B, t, live, dloss, lse, scale, dB=db, exact=True)
+            # up to 152 parts' sums are added up with a rounding each
+            steps = 152 * 2.0 ** -24 * (ref.dlogits(A, B, t, live, dloss, lse, scale)[0].abs().T @ A.double().abs())
+            if accumulate:
+                rb, tb = rb + old.double(), tb + 2.0 ** -23 * (rb.abs() + old.double().abs())
+            ref.check(dB, rb, tb + steps, "dB")
+            if need_dA:
+                ref.check(dA, ra, ta, "dA")
+            else:
+                assert dA is None
+
+
 def test_a_long_width():
     M, N, K = 40, 300, 1 << 17
     A, B, targets, dloss, scale = problem(M, N, K)
