@@ -7,7 +7,7 @@
 //              rows     which rows count, and a compact copy of them where some are left
 //                       out (more than kInPlace rows only)
 //              product  per tile the largest logit, the sum of exponentials and the
-//                       entries' logits (loss_kernel)
+//                       entries' products (loss_kernel)
 //              finish   the tiles' results joined, losses and lse
 //   backward   list, rows as above, with each row's factors; then for each piece of the
 //              vocabulary
@@ -50,7 +50,7 @@ bool bucketed(uint64_t M, uint64_t top) { return M > kInPlace && top > 8; }
 constexpr uint64_t kTwoHalves = 128;
 
 struct Layout {
-  uint64_t count, deal, index, pos, start, ids, prob, len, entropy, entry_z, part, part_sum, compact, row, piece, sums, sums_db;
+  uint64_t count, deal, index, pos, start, ids, prob, len, entropy, entry, part, part_sum, compact, row, piece, sums, sums_db;
   uint64_t ld_compact, ld_part, ld_sums, stride_sums, width, bytes;   // width: of a piece
   uint32_t parts, parts_db;                              // of dA's and dB's sums at most
   uint64_t lo, rows;                                     // where g's lower halves follow (0: none), rows of g
@@ -93,7 +93,7 @@ Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
     if (w.parts_db > 1) w.sums_db = take(4 * N * w.ld_sums * w.parts_db);
   } else {
     if (M > kInPlace) w.compact = take(2 * M * w.ld_compact);
-    w.entry_z = take(4 * M * (top > 0 ? top : 1));
+    w.entry = take(4 * M * (top > 0 ? top : 1));
     const uint64_t slots = loss_tiles(M, N, K).slots(M, N);
     w.ld_part = up(M, 32);
     w.part = take(16 * slots * w.ld_part);
@@ -345,10 +345,10 @@ struct FinishArgs {
   const float2* part;
   const float* part_sum;
   uint64_t ld_part;
-  float scale, smoothing, z_coef;
+  float c, smoothing, z_coef;  // c: exp(z) = 2^(c a.b)
   const void* targets;
   bool target64;
-  const float *entry_z, *prob, *entropy;
+  const float *entry, *prob, *entropy;   // entry: the entries' products with B
   const uint32_t* len;
   float *loss, *lse;
 };
@@ -380,11 +380,15 @@ __device__ __forceinline__ void join_warp(RowPart& r) {
   r.top = top;
 }
 
-// Row r's loss and lse, by one warp.
+// Row r's loss and lse, by one warp.  lse - z of an entry is taken in base 2, its product with B
+// subtracted from the largest in one fused multiply-add: what all of a row's logits share cancels
+// before anything is rounded (8192 in every logit: losses off by 9e-4 where lse and z are rounded
+// first, by 9e-6 so).  What is never below 0 is not let below it by roundings either.
 __device__ __forceinline__ void finish_row(const FinishArgs& a, uint32_t r, RowPart p) {
   const uint32_t lane = lane_idx();
   if (a.slots == 0) p = RowPart{0.0f, static_cast<float>(a.N), 0.0f};   // no width: all logits are 0
-  const float lse = kLn2 * (p.top + log2f(p.sum));
+  const float log_sum = log2f(p.sum), lse = kLn2 * (p.top + log_sum);
+  const auto behind = [&](float product) { return kLn2 * (fmaf(-a.c, product, p.top) + log_sum); };
   float loss;
   bool counts;
   if (a.top > 0) {
@@ -392,15 +396,17 @@ __device__ __forceinline__ void finish_row(const FinishArgs& a, uint32_t r, RowP
     const uint32_t len = a.len[r];
     const uint64_t at = static_cast<uint64_t>(r) * a.top;
     float x = 0.0f;
-    for (uint32_t e = lane; e < len; e += 32) x += a.prob[at + e] * (lse - (a.slots == 0 ? 0.0f : a.entry_z[at + e]));
+    for (uint32_t e = lane; e < len; e += 32) x += a.prob[at + e] * behind(a.slots == 0 ? 0.0f : a.entry[at + e]);
     loss = a.entropy[r] + warp_all(x, false);
+    if (loss < 0.0f) loss = 0.0f;
     counts = len > 0;
   } else {
     const int64_t t = loss_index_at(a.targets, a.target64, r);
     counts = t >= 0;
-    const float z = a.slots != 0 && counts && t < a.N ? a.entry_z[r] : 0.0f;
-    loss = (1.0f - a.smoothing) * (lse - z) + a.z_coef * lse * lse;
-    if (a.smoothing > 0.0f) loss += a.smoothing * (lse - a.scale * p.products / static_cast<float>(a.N));
+    loss = (1.0f - a.smoothing) * behind(a.slots != 0 && counts && t < a.N ? a.entry[r] : 0.0f);
+    if (a.smoothing > 0.0f) loss += a.smoothing * behind(p.products / static_cast<float>(a.N));
+    if (loss < 0.0f) loss = 0.0f;
+    loss += a.z_coef * lse * lse;
     if (t >= a.N) loss = NAN;
   }
   if (lane == 0) {
@@ -627,7 +633,6 @@ LossArgs logits_args(const LossProblem& p, const Layout& w, uint8_t* ws) {
   a.N = p.N;
   a.K = p.K;
   a.c = p.scale * kLog2e;
-  a.scale = p.scale;
   a.target = p.targets;
   a.target64 = p.target64 ? 1u : 0u;
   a.top = p.top;
@@ -703,7 +708,7 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   a.part = reinterpret_cast<float2*>(ws + w.part);
   a.part_sum = p.smoothing > 0.0f ? reinterpret_cast<float*>(ws + w.part_sum) : nullptr;
   a.ld_part = w.ld_part;
-  a.entry_z = reinterpret_cast<float*>(ws + w.entry_z);
+  a.entry = reinterpret_cast<float*>(ws + w.entry);
   uint32_t slots = 0;
   if (p.K > 0 && (rc = launch_loss_logits_forward(o, a, ctx, &slots, stream)) != GEMM_OK) return rc;
   FinishArgs f = {};
@@ -716,12 +721,12 @@ int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t
   f.part = a.part;
   f.part_sum = a.part_sum;
   f.ld_part = a.ld_part;
-  f.scale = p.scale;
+  f.c = a.c;
   f.smoothing = p.smoothing;
   f.z_coef = p.z_coef;
   f.targets = p.targets;
   f.target64 = p.target64;
-  f.entry_z = a.entry_z;
+  f.entry = a.entry;
   f.prob = a.prob;
   f.len = a.len;
   f.entropy = reinterpret_cast<const float*>(ws + w.entropy);

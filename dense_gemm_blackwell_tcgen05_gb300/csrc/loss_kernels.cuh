@@ -61,7 +61,6 @@ struct LossArgs {
   const uint32_t* count;       // rows that count (nullptr: all of them, in place)
   const uint32_t* index;       // [count] where each of them lies among all rows (nullptr: in place)
   float c;                     // scale log2(e): exp(z) = 2^(c a.b)
-  float scale;
   uint32_t first;              // number of this piece's first token
   // entries: a target per row, or a sorted list
   const void* target;          // [M] int32 or int64, by all rows
@@ -77,7 +76,7 @@ struct LossArgs {
   float* part_sum;             // [slots][2][ld_part] sum of a.b (nullptr: not wanted)
   uint64_t ld_part;
   uint32_t runs;               // one block of rows: a slot for each cluster, else for each tile of columns
-  float* entry_z;              // [M] or [M][top], by all rows: the entries' logits
+  float* entry;                // [M] or [M][top], by all rows: the entries' a.b
   // backward
   const float4* row;           // [count] (lse log2(e), gq, gs, gt) (nullptr: in place, from `factors`)
   LossFactors factors;
@@ -436,14 +435,14 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         }
         if (!ok) break;
         if (any) {
-          // the entries' logits
+          // the entries' products
 #pragma unroll
           for (uint32_t i = 0; i < C::NCH; ++i) {
             if (i >= chunks) break;
             while (__any_sync(0xffffffffu, next - 32 * i < 32u)) {
               const bool here = next - 32 * i < 32u;
-              const float z = args.scale * select32(acc[i], (next - 32 * i) & 31u);
-              if (here && next < cols) args.entry_z[LIST ? static_cast<uint64_t>(at) * args.top + cur : at] = z;
+              const float x = select32(acc[i], (next - 32 * i) & 31u);
+              if (here && next < cols) args.entry[LIST ? static_cast<uint64_t>(at) * args.top + cur : at] = x;
               if (here) {
                 ++cur;
                 if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
