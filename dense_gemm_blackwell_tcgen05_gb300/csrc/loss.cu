@@ -126,7 +126,8 @@ __device__ __forceinline__ float all_of(float v, bool largest, float* slots) {
 
 // T threads per row: p = softmax(teacher scale) over the entries that are there (id >= 0,
 // logit not -Inf), sorted by id, and sum p log p, which is NaN where an id lies past the
-// vocabulary or a logit is NaN or +Inf.  The place of an entry is the number of entries
+// vocabulary or a logit is NaN or +Inf.  The scale is applied to differences of halves, which
+// finite logits do not leave fp32 in: the type's lowest value is a logit like any other.  The place of an entry is the number of entries
 // before it: top^2 / T comparisons from shared memory.  A warp has room for 128 entries.
 constexpr uint32_t kWarpTop = 128;
 struct ListArgs {
@@ -162,8 +163,8 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
   for (uint32_t i = me; i < top; i += T) {
     const int64_t id = loss_index_at(a.ids, a.ids64, r * a.ld_ids + i);
     const uint64_t at = r * a.ld_teacher + i;
-    const float t = a.scale * (a.f32 ? static_cast<const float*>(a.teacher)[at]
-                                     : bf16_bits_to_f32(static_cast<const uint16_t*>(a.teacher)[at]));
+    const float t = 0.5f * (a.f32 ? static_cast<const float*>(a.teacher)[at]
+                                  : bf16_bits_to_f32(static_cast<const uint16_t*>(a.teacher)[at]));
     const bool there = id >= 0 && t != -INFINITY;
     wrong |= there && id >= a.N;
     s_id[i] = there ? static_cast<int32_t>(min(id, static_cast<int64_t>(0x7FFFFFFF))) : -1;
@@ -174,9 +175,10 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
     }
   }
   most = all_of<T>(most, true, slots);
+  const auto behind = [&](uint32_t i) { return 2.0f * (a.scale * (s_t[i] - most)); };   // the largest, scaled
   float sum = 0.0f;
   for (uint32_t i = me; i < top; i += T) {
-    if (s_id[i] >= 0) sum += expf(s_t[i] - most);
+    if (s_id[i] >= 0) sum += expf(behind(i));
   }
   sum = all_of<T>(sum, false, slots);
   const float log_sum = logf(sum);
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(256) loss_list_kernel(const ListArgs a) {
   for (uint32_t j = 0; j < kMine; ++j) {
     const uint32_t i = me + j * T;
     if (static_cast<int32_t>(id_of[j]) < 0) continue;
-    const float d = s_t[i] - most, p = expf(d) / sum;
+    const float d = behind(i), p = expf(d) / sum;
     a.out_ids[r * top + place[j]] = static_cast<int32_t>(id_of[j]);
     a.out_prob[r * top + place[j]] = p;
     h += p == 0.0f ? 0.0f : p * (d - log_sum);

@@ -1,4 +1,5 @@
-"""Losses over a vocabulary where rounding shows: large logits, sure tokens."""
+"""Losses over a vocabulary where rounding shows: large logits, sure tokens, a
+teacher's extreme logits."""
 import pytest
 import torch
 
@@ -92,3 +93,39 @@ def test_a_sure_token_loses_what_is_left(M, N):
             for got in (loss, kd):
                 assert (got >= 0).all()
                 ref.check(got, want, 2.0 ** -19 + 2.0 ** -21 * want, "loss")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("temperature", [0.25, 0.5, 1.0, 4.0])
+@pytest.mark.parametrize("M, top", [(40, 5), (300, 5), (300, 200)])
+def test_a_teachers_extreme_logits(M, top, temperature, dtype):
+    """Finite logits are entries, the type's lowest value and what leaves fp32 once it is divided by
+    the temperature too; only a logit of -Inf is not there."""
+    N, K = 500, 64
+    r, A, B = shifted(M, N, K, 0.0, 2)
+    lowest = torch.finfo(dtype).min
+    ids = torch.randint(0, N, (M, top), generator=r, device="cuda", dtype=torch.int32)
+    teacher = torch.randn(M, top, generator=r, device="cuda").to(dtype)
+    teacher[0::4, 1:] = lowest               # masked entries beside one that is not
+    teacher[1::4] = lowest                   # nothing but them: they are alike
+    teacher[2::4, 0] = -lowest               # one that is far ahead
+    teacher[3::4, :2] = -lowest              # two
+    teacher[5, :] = -torch.inf
+    teacher[9, 1:] = -torch.inf
+    t, entropy, live = ref.teacher_matrix(teacher.double(), ids, N, temperature)
+    assert live.sum() == M - 1
+    f = 1.0 / temperature
+    want, want_lse = ref.forward(A, B, t, entropy, live, f)
+    loss, lse = g.matmul_distill(A, B, teacher, ids, temperature=temperature)
+    dloss = torch.rand(M, generator=r, device="cuda")
+    dA, _ = g.matmul_distill_grad(dloss, A, B, teacher, ids, want_lse.float(), temperature=temperature, out_dtype=F32)
+    ok()
+    e_loss, e_lse = ref.forward_bounds(A, B, t, f, want_lse, 0.0, True)
+    ref.check(lse, want_lse, torch.where(live, e_lse, 0.0), "lse")
+    # p is off by 2^-21 (1 + the difference to the largest) of itself: under 2^-18 where it counts
+    size = ref.logits(A, B, f).abs().max(1)[0] + want_lse.abs() + entropy.abs() + 1.0
+    ref.check(loss, want, torch.where(live, e_loss + 2.0 ** -17 * size, 0.0), "loss")
+    (ra, ta), _ = ref.gradients(A, B, t, live, dloss, want_lse.float(), f, dA=F32, dB=F32, exact=True)
+    more = 2.0 ** -17 * torch.where(live, dloss.double() * f, 0.0)[:, None] * t
+    # what lies below fp32's 2^-126 becomes 0: 500 terms of it, times 2 of B and 4 of dloss / temperature
+    ref.check(dA, ra, ta + more @ B.double().abs() + 2.0 ** -114, "dA")
