@@ -46,6 +46,12 @@ int loss_room(const LaunchCtx& ctx, uint64_t* room) {
       cudaGetLastError();
       return GEMM_ERR_LAUNCH;
     }
+    // (a split of the registers that asked for more than the launch's would be waited for without end)
+    cudaFuncAttributes as_built = {};
+    if (cudaFuncGetAttributes(&as_built, kern) != cudaSuccess || as_built.numRegs < static_cast<int>(C::kLeastRegs)) {
+      cudaGetLastError();
+      return GEMM_ERR_LAUNCH;
+    }
     int clusters = ctx.num_sms / CG;
     if (CG > 1) {
       cudaLaunchConfig_t cfg = {};
@@ -71,19 +77,27 @@ int loss_room(const LaunchCtx& ctx, uint64_t* room) {
 
 // Launches on min(tiles, room) clusters.  A launch over one block of rows writes a slot
 // of partial results for each cluster, any other one for each tile of columns.
-template <int CG, uint32_t NT, bool BACK, bool LIST>
+template <int CG, uint32_t NT, bool BACK, bool LIST, bool SEG>
 int launch_loss(const LossOperands& o, LossArgs a, const LossTiles& tile, const LaunchCtx& ctx, uint32_t* slots,
                 cudaStream_t stream) {
-  using C = LossCfg<CG, NT, BACK, LIST>;
-  const auto kern = loss_kernel<CG, NT, BACK, LIST>;
+  using C = LossCfg<CG, NT, BACK, SEG>;
+  const auto kern = loss_kernel<CG, NT, BACK, LIST, SEG>;
   uint64_t room = 0;
-  if (const int rc = loss_room<C, loss_kernel<CG, NT, BACK, LIST>, CG>(ctx, &room); rc != GEMM_OK) return rc;
+  if (const int rc = loss_room<C, loss_kernel<CG, NT, BACK, LIST, SEG>, CG>(ctx, &room); rc != GEMM_OK) return rc;
   CUtensorMap all, compact, q;
   if (!operand_map(&all, o.A, a.K, a.M, 1, o.lda, 0, C::P_BOX) || !operand_map(&q, o.B, a.K, a.N, 1, o.ldb, 0, tile.nt / CG))
     return GEMM_ERR_LAUNCH;
   compact = all;
   if (o.compact != nullptr && !operand_map(&compact, o.compact, a.K, a.M, 1, o.ld_compact, 0, C::P_BOX))
     return GEMM_ERR_LAUNCH;
+  CUtensorMap out = all;
+  if constexpr (BACK) {
+    // (whole chunks of 32 columns: the pitch has room for them)
+    const uint64_t dims[3] = {o.ld_out, o.out_rows, 1}, strides[2] = {2 * o.ld_out, 2 * o.ld_out};
+    const uint32_t box[3] = {32, 32, 1};
+    if (!encode_map_3d(&out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
+      return GEMM_ERR_LAUNCH;
+  }
   a.nt = tile.nt;
   const uint64_t blocks = ceil_div_u64(a.M, C::LT), columns = ceil_div_u64(a.N, a.nt);
   if (blocks > 0x7FFFFFFFull / columns) return GEMM_ERR_INVALID_ARG;
@@ -105,7 +119,7 @@ int launch_loss(const LossOperands& o, LossArgs a, const LossTiles& tile, const 
   a.status = ctx.status;
   a.timeout_ns = ctx.timeout_ns;
   note_schedule(cfg.gridDim.x / CG, CG, static_cast<uint32_t>(tiles), 0u, 0u, 0u, 0u);
-  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, all, compact, q, a); e != cudaSuccess) {
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, all, compact, q, out, a); e != cudaSuccess) {
     note_cuda_error(e);
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
@@ -113,11 +127,11 @@ int launch_loss(const LossOperands& o, LossArgs a, const LossTiles& tile, const 
   return GEMM_OK;
 }
 
-template <bool BACK, bool LIST>
+template <bool BACK, bool LIST, bool SEG>
 int loss_pick(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, uint32_t* slots, cudaStream_t stream) {
   const LossTiles t = loss_tiles(a.M, a.N, a.K);
-  return t.cg == 2 ? launch_loss<2, 256, BACK, LIST>(o, a, t, ctx, slots, stream)
-                   : launch_loss<1, 128, BACK, LIST>(o, a, t, ctx, slots, stream);
+  return t.cg == 2 ? launch_loss<2, 256, BACK, LIST, SEG>(o, a, t, ctx, slots, stream)
+                   : launch_loss<1, 128, BACK, LIST, SEG>(o, a, t, ctx, slots, stream);
 }
 
 }  // namespace gb300

@@ -4,8 +4,11 @@
 namespace gb300 {
 
 int launch_loss_logits_backward(const LossOperands& o, const LossArgs& a, const LaunchCtx& ctx, cudaStream_t stream) {
-  return a.ids != nullptr ? loss_pick<true, true>(o, a, ctx, nullptr, stream)
-                          : loss_pick<true, false>(o, a, ctx, nullptr, stream);
+  if (a.K > 64 * kLossSegment)
+    return a.ids != nullptr ? loss_pick<true, true, true>(o, a, ctx, nullptr, stream)
+                            : loss_pick<true, false, true>(o, a, ctx, nullptr, stream);
+  return a.ids != nullptr ? loss_pick<true, true, false>(o, a, ctx, nullptr, stream)
+                          : loss_pick<true, false, false>(o, a, ctx, nullptr, stream);
 }
 
 }  // namespace gb300

@@ -5,8 +5,8 @@ namespace gb300 {
 
 int launch_loss_logits_forward(const LossOperands& o, LossArgs a, const LaunchCtx& ctx, uint32_t* slots,
                                cudaStream_t stream) {
-  return a.ids != nullptr ? loss_pick<false, true>(o, a, ctx, slots, stream)
-                          : loss_pick<false, false>(o, a, ctx, slots, stream);
+  return a.ids != nullptr ? loss_pick<false, true, true>(o, a, ctx, slots, stream)
+                          : loss_pick<false, false, true>(o, a, ctx, slots, stream);
 }
 
 }  // namespace gb300

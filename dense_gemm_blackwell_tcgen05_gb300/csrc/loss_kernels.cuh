@@ -15,15 +15,20 @@
 //
 // Persistent, warp-specialised like the grouped products: a TMA producer, an MMA
 // issuer with two accumulators, eight epilogue warps, two per lane quarter, each with
-// half of the tile's columns.  Rows left out of the loss are left out of the product:
-// the rows that count lie compact, and their number is read on the GPU.
+// half of the tile's columns.  The gradient leaves through shared memory by TMA (4096 rows,
+// 32768 tokens of width 2048: 11 us of 285 less than from registers, each lane its own row in
+// whole sectors).  Rows left out of the loss are left out of the product: the rows that count lie
+// compact, and their number is read on the GPU.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
 // 520 us forward, 2.11 PFLOP/s, tensor pipes 98.8 % busy; 541 backward), few by the read of B
 // (48 rows, 131072 tokens: 156 us, 6.9 TB/s), a few thousand tokens by latency.
 //
-// Precision.  The tensor core's additions truncate (1.1e-9 of the result a term), so
-// the forward pass, whose losses are fp32, adds up segments of 512 terms in registers.
+// Precision.  The tensor core's additions truncate (1.1e-9 of the result a term), so both
+// passes add up segments of 512 terms in registers: a row's loss is the difference of its
+// logits, and where it is sure of its target its gradient is that of two numbers near 1
+// (1 - exp(z - lse) of 2.2e-4 at a logit of 16, width 8192: 4.1e-4 off in one sum, 5e-6 in
+// segments; on pairs, shorter ones would be paid in time: 256 terms 3 to 6 %).
 // exp is 2^x of the multiprocessor's special function unit (2 units in the last place)
 // on arguments in fp32.  The gradient g is rounded to bf16 for the products with it, at
 // 2^-9 of itself: over many rows as much as rounding the products' bf16 results adds (2.4e-3
@@ -85,16 +90,17 @@ struct LossArgs {
   uint16_t* clean;
   uint64_t ld_clean;
   int32_t* offsets;            //   and {0, M}, as one group's offsets
-  uint16_t* out;               // [count][ld_out] the gradient's piece; zeros up to a multiple of 64 rows
-  uint32_t lo_row;             // where what that rounding left follows, row by row (0: it is dropped)
-  uint64_t ld_out;
+  uint32_t lo_row;             // the piece's row from which on what rounding left follows (0: it is dropped)
   unsigned long long* status;
   unsigned long long timeout_ns;
   uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
 };
 
-// NT: columns of a tile at most.  LIST: a list of entries per row, else one target.
-template <int CG, uint32_t NT, bool BACK, bool LIST>
+// Stages in a sum of the tensor core's: 512 terms.
+constexpr uint32_t kLossSegment = 8;
+
+// NT: columns of a tile at most.  BACK, SEG: as loss_kernel's.
+template <int CG, uint32_t NT, bool BACK, bool SEG>
 struct LossCfg {
   static_assert(CG == 1 || CG == 2, "cta_group is 1 or 2");
   static constexpr uint32_t BK = 64;                     // k per stage: one 128-byte row
@@ -106,15 +112,23 @@ struct LossCfg {
   static constexpr uint32_t Q_BYTES = NT / CG * 128;     // vocabulary rows staged by one CTA
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
   static constexpr uint32_t kEpiWarps = 8;
-  static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps);
-  static constexpr uint32_t SEG_TILES = BACK ? 0xFFFFFFFFu : 8u;
+  static constexpr uint32_t kThreads = 32 * (4 + kEpiWarps);   // producer, MMA issuer, two that idle; the epilogue
+  // A pair's epilogue holds 128 columns' sums a thread between segments: it takes registers that the
+  // other four warps leave (without, 64 bytes a thread are spilled: backward, 4096 lists of 64 over
+  // 32768 tokens of width 2048, 304 us instead of 278).
+  static constexpr bool kSplit = CG == 2 && SEG;
+  static constexpr uint32_t kFewRegs = 56, kManyRegs = 224, kLeastRegs = kSplit ? 168 : 0;   // least: of a launch
+  static_assert(!kSplit || 128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * kLeastRegs, "more than the launch's");
+  static constexpr uint32_t SEG_TILES = kLossSegment;
   static constexpr uint32_t NCH = NT / 64;               // 32-column chunks per epilogue warp at most
   static constexpr uint32_t BAR_BYTES = 512;
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;
-  static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES) / STAGE_BYTES;
+  static constexpr uint32_t BOX_BYTES = 32 * 64;         // a warp's 32 rows of a chunk on their way out
+  static constexpr uint32_t OUT_BYTES = BACK ? kEpiWarps * 2 * BOX_BYTES : 0;
+  static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - OUT_BYTES) / STAGE_BYTES;
   static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
-  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + BAR_BYTES;
+  static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + OUT_BYTES + BAR_BYTES;
   static_assert((2 * STAGES + 5) * 8 + 16 <= BAR_BYTES, "barrier area");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t ACC_COLS = 256;              // second accumulator's first column
@@ -149,22 +163,20 @@ __device__ __forceinline__ float4 loss_row_factors(const LossFactors& f, const v
                      g * f.smoothing / static_cast<float>(f.N), g * (1.0f - f.smoothing));
 }
 
-// A row's target as an offset from `first`; 0xFFFFFFFF where it lies before it or has none.
-__device__ __forceinline__ uint32_t target_offset(const LossArgs& a, uint32_t row) {
-  const int64_t d = loss_index_at(a.target, a.target64, row) - a.first;
-  return d >= 0 && d < 0x7FFFFFFF ? static_cast<uint32_t>(d) : 0xFFFFFFFFu;
-}
-
-template <int CG, uint32_t NT, bool BACK, bool LIST>
-__global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
+// LIST: a list of entries per row, else one target.  SEG: several segments of the width, else one,
+// whose sums a backward pass takes a chunk at a time.
+template <int CG, uint32_t NT, bool BACK, bool LIST, bool SEG>
+__global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
     loss_kernel(const __grid_constant__ CUtensorMap tmAll, const __grid_constant__ CUtensorMap tmCompact,
-                const __grid_constant__ CUtensorMap tmQ, const LossArgs args) {
-  using C = LossCfg<CG, NT, BACK, LIST>;
+                const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmOut, const LossArgs args) {
+  using C = LossCfg<CG, NT, BACK, SEG>;
+  static_assert(BACK || SEG, "a forward pass takes any width");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bar0 = base + C::STAGES * C::STAGE_BYTES;
+  const uint32_t out0 = base + C::STAGES * C::STAGE_BYTES;
+  const uint32_t bar0 = out0 + C::OUT_BYTES;
   const auto full_bar = [&](uint32_t s) { return bar0 + 8 * s; };
   const auto empty_bar = [&](uint32_t s) { return bar0 + 8 * (C::STAGES + s); };
   constexpr uint32_t kAccBar0 = 2 * C::STAGES;
@@ -188,6 +200,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
       tma_prefetch_desc(&tmAll);
       tma_prefetch_desc(&tmCompact);
       tma_prefetch_desc(&tmQ);
+      if constexpr (BACK) tma_prefetch_desc(&tmOut);
       *abort_flag = 0u;
     }
     for (uint32_t i = lane; i < kAccBar0 + 5; i += 32)
@@ -215,114 +228,118 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
   const uint32_t tiles = rbs * vts;
   const uint32_t kt_n = (args.K + C::BK - 1) / C::BK;
 
-  if (warp == 0) {
-    // ==================== TMA producer: one thread issues =======================
-    const uint64_t pol = l2_policy_evict_last();
-    const uint32_t q_rows = args.nt / CG, q_bytes = q_rows * 128;
-    const CUtensorMap* const tmP = args.index != nullptr && count < args.M ? &tmCompact : &tmAll;
-    RingStage r;
-    uint32_t it = 0;
-    bool ok = true;
-    for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
-      uint32_t rb, vt;
-      tile_coords(t, rbs, vts, kLossRaster, rb, vt);
-      // boxes of A that a CTA of the tile loads (one without rows loads one: its stage is waited for)
-      const auto boxes = [&](uint32_t p) {
-        const uint32_t live = count > p ? min(128u, count - p) : 1u;
-        return (live + C::P_BOX - 1) / C::P_BOX;
-      };
-      const uint32_t p0 = rb * C::LT + rank * 128, p_boxes = boxes(p0);
-      const uint32_t tx = CG * q_bytes + (CG == 2 ? boxes(rb * C::LT) + boxes(rb * C::LT + 128) : p_boxes) * C::P_BOX * 128;
-      const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * args.nt + rank * q_rows);
-      for (uint32_t kt = 0; kt < kt_n; ++kt, ++it, r.next<C::STAGES>()) {
-        if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
-        if (!uniform_wait(empty_bar(r.s), r.round ^ 1u, wd, kSiteProducerEmpty, lane)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t sb = base + r.s * C::STAGE_BYTES;
-          const int32_t k0 = static_cast<int32_t>(kt * C::BK);
-          uint32_t bar = full_bar(r.s);
-          if constexpr (CG == 2) bar = mapa_shared(full_bar(r.s), 0);
-          if (leader) mbar_arrive_expect_tx(full_bar(r.s), tx);
-          const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t y) {
-            if (CG == 2) tma_load_3d_pair(dst, m, bar, k0, y, 0, pol);
-            else tma_load_3d(dst, m, bar, k0, y, 0, pol);
-          };
-          for (uint32_t i = 0; i < (CG == 2 ? 1u : p_boxes); ++i)
-            load(sb + i * C::P_BOX * 128, tmP, px + static_cast<int32_t>(i * C::P_BOX));
-          load(sb + C::P_BYTES, &tmQ, qy);
-        }
-        __syncwarp();
-      }
-    }
-    // Exit path after a give-up: let this CTA's issued loads land first.
-    if (lane == 0 && leader && *abort_flag) {
-      const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
-      for (uint32_t i = first; i < it; ++i) {
-        if (i == args.stall_iter) continue;
-        drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
-      }
-    }
-  } else if (warp == 1) {
-    // ==================== MMA issuer: the leader CTA's, one thread issues ========
-    if (leader) {
-      const uint32_t idesc = idesc_f16(C::LT, args.nt, 1u, false, false);
-      const uint64_t pd0 = smem_desc_sw128(base), qd0 = smem_desc_sw128(base + C::P_BYTES);
+  if (warp < 4) {
+    if constexpr (C::kSplit) regs_dec<C::kFewRegs>();
+    if (warp == 0) {
+      // ==================== TMA producer: one thread issues =======================
+      const uint64_t pol = l2_policy_evict_last();
+      const uint32_t q_rows = args.nt / CG, q_bytes = q_rows * 128;
+      const CUtensorMap* const tmP = args.index != nullptr && count < args.M ? &tmCompact : &tmAll;
       RingStage r;
-      uint32_t j = 0;
-      bool ok = true, issued = false;
+      uint32_t it = 0;
+      bool ok = true;
       for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
-        for (uint32_t k_begin = 0; ok && k_begin < kt_n; ++j) {
-          const uint32_t k_end = kt_n - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : kt_n;
-          const uint32_t b = j & 1u;
-          // accumulator b must have been drained by every epilogue warp
-          if (!uniform_wait(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty, lane)) {
+        uint32_t rb, vt;
+        tile_coords(t, rbs, vts, kLossRaster, rb, vt);
+        // boxes of A that a CTA of the tile loads (one without rows loads one: its stage is waited for)
+        const auto boxes = [&](uint32_t p) {
+          const uint32_t live = count > p ? min(128u, count - p) : 1u;
+          return (live + C::P_BOX - 1) / C::P_BOX;
+        };
+        const uint32_t p0 = rb * C::LT + rank * 128, p_boxes = boxes(p0);
+        const uint32_t tx = CG * q_bytes + (CG == 2 ? boxes(rb * C::LT) + boxes(rb * C::LT + 128) : p_boxes) * C::P_BOX * 128;
+        const int32_t px = static_cast<int32_t>(p0), qy = static_cast<int32_t>(vt * args.nt + rank * q_rows);
+        for (uint32_t kt = 0; kt < kt_n; ++kt, ++it, r.next<C::STAGES>()) {
+          if (it == args.stall_iter) continue;   // watchdog test: this stage never fills
+          if (!uniform_wait(empty_bar(r.s), r.round ^ 1u, wd, kSiteProducerEmpty, lane)) {
             ok = false;
             break;
           }
-          tc_fence_after_sync();
-          const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
-          for (uint32_t kt = k_begin; kt < k_end; ++kt) {
-            if (!uniform_wait(full_bar(r.s), r.round, wd, kSiteMmaFull, lane)) {
+          if (lane == 0) {
+            const uint32_t sb = base + r.s * C::STAGE_BYTES;
+            const int32_t k0 = static_cast<int32_t>(kt * C::BK);
+            uint32_t bar = full_bar(r.s);
+            if constexpr (CG == 2) bar = mapa_shared(full_bar(r.s), 0);
+            if (leader) mbar_arrive_expect_tx(full_bar(r.s), tx);
+            const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t y) {
+              if (CG == 2) tma_load_3d_pair(dst, m, bar, k0, y, 0, pol);
+              else tma_load_3d(dst, m, bar, k0, y, 0, pol);
+            };
+            for (uint32_t i = 0; i < (CG == 2 ? 1u : p_boxes); ++i)
+              load(sb + i * C::P_BOX * 128, tmP, px + static_cast<int32_t>(i * C::P_BOX));
+            load(sb + C::P_BYTES, &tmQ, qy);
+          }
+          __syncwarp();
+        }
+      }
+      // Exit path after a give-up: let this CTA's issued loads land first.
+      if (lane == 0 && leader && *abort_flag) {
+        const uint32_t first = it > C::STAGES ? it - C::STAGES : 0u;
+        for (uint32_t i = first; i < it; ++i) {
+          if (i == args.stall_iter) continue;
+          drain_wait(full_bar(i % C::STAGES), (i / C::STAGES) & 1u, wd, kSiteProducerDrain);
+        }
+      }
+    } else if (warp == 1) {
+      // ==================== MMA issuer: the leader CTA's, one thread issues ========
+      if (leader) {
+        const uint32_t idesc = idesc_f16(C::LT, args.nt, 1u, false, false);
+        const uint64_t pd0 = smem_desc_sw128(base), qd0 = smem_desc_sw128(base + C::P_BYTES);
+        RingStage r;
+        uint32_t j = 0;
+        bool ok = true, issued = false;
+        for (uint32_t t = cluster_id; ok && t < tiles; t += G) {
+          for (uint32_t k_begin = 0; ok && k_begin < kt_n; ++j) {
+            const uint32_t k_end = kt_n - k_begin > C::SEG_TILES ? k_begin + C::SEG_TILES : kt_n;
+            const uint32_t b = j & 1u;
+            // accumulator b must have been drained by every epilogue warp
+            if (!uniform_wait(acce_bar(b), ((j >> 1) & 1u) ^ 1u, wd, kSiteMmaAccEmpty, lane)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const uint64_t step = static_cast<uint64_t>(r.s * (C::STAGE_BYTES / 16));
-            const uint32_t left = args.K - kt * C::BK;   // (no MMAs over nothing but the zeros past the width)
-            if (lane == 0) {
+            const uint32_t d_tmem = tmem_base + b * C::ACC_COLS;
+            for (uint32_t kt = k_begin; kt < k_end; ++kt) {
+              if (!uniform_wait(full_bar(r.s), r.round, wd, kSiteMmaFull, lane)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+              const uint64_t step = static_cast<uint64_t>(r.s * (C::STAGE_BYTES / 16));
+              const uint32_t left = args.K - kt * C::BK;   // (no MMAs over nothing but the zeros past the width)
+              if (lane == 0) {
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)   // 16 k per MMA: 32 bytes along a row
-                if (16 * k < left)
-                  mma_bf16<CG>(d_tmem, pd0 + step + 2 * k, qd0 + step + 2 * k, idesc, (kt != k_begin || k != 0u));
-              commit_to<CG>(empty_bar(r.s));     // frees the stage once these MMAs finish
+                for (uint32_t k = 0; k < 4; ++k)   // 16 k per MMA: 32 bytes along a row
+                  if (16 * k < left)
+                    mma_bf16<CG>(d_tmem, pd0 + step + 2 * k, qd0 + step + 2 * k, idesc, (kt != k_begin || k != 0u));
+                commit_to<CG>(empty_bar(r.s));     // frees the stage once these MMAs finish
+              }
+              __syncwarp();
+              issued = true;
+              r.next<C::STAGES>();
             }
-            __syncwarp();
-            issued = true;
-            r.next<C::STAGES>();
+            if (!ok) break;
+            if (lane == 0) commit_to<CG>(accf_bar(b));
+            k_begin = k_end;
           }
-          if (!ok) break;
-          if (lane == 0) commit_to<CG>(accf_bar(b));
-          k_begin = k_end;
         }
-      }
-      // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
-      if (issued && lane == 0) {
-        if constexpr (CG == 1)
-          tc_commit(drain_bar);
-        else
-          tc_commit_pair_multicast(drain_bar, 0x1);
-        drain_wait(drain_bar, 0, wd, kSiteMmaDrain);
+        // Exit path: every tcgen05 op this thread issued completes before TMEM is released.
+        if (issued && lane == 0) {
+          if constexpr (CG == 1)
+            tc_commit(drain_bar);
+          else
+            tc_commit_pair_multicast(drain_bar, 0x1);
+          drain_wait(drain_bar, 0, wd, kSiteMmaDrain);
+        }
       }
     }
   } else {
     // ==================== epilogue: eight warps, two per TMEM lane quarter =======
+    if constexpr (C::kSplit) regs_inc<C::kManyRegs>();
     const uint32_t q = warp & 3u;              // TMEM lanes 32q .. 32q + 31
-    const uint32_t eg = (warp - 2u) / 4u;      // this warp's half of the tile's chunks of 32 columns
+    const uint32_t eg = (warp - 4u) / 4u;      // this warp's half of the tile's chunks of 32 columns
     const uint32_t ch0 = eg == 0 ? 0u : (args.nt / 32 + 1) / 2, chunks = eg == 0 ? (args.nt / 32 + 1) / 2 : args.nt / 32 - ch0;
-    uint32_t j = 0;
+    uint32_t j = 0, sent = 0;
     bool ok = true;
     const auto counts = [&](uint32_t r) {      // in place: whether row r does
       return LIST ? args.len[r] > 0 : loss_index_at(args.target, args.target64, r) >= 0;
@@ -332,8 +349,8 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
       const uint32_t rows = args.lo_row + args.M;
       const uint32_t per = (args.K + 7) / 8;
       const uint64_t n = static_cast<uint64_t>(rows) * per;      // (few rows, of any width)
-      if (blockIdx.x == 0 && threadIdx.x == 64) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(rows);
-      for (uint64_t i = blockIdx.x * 256u + threadIdx.x - 64u; i < n; i += gridDim.x * 256u) {
+      if (blockIdx.x == 0 && threadIdx.x == 128) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(rows);
+      for (uint64_t i = blockIdx.x * 256u + threadIdx.x - 128u; i < n; i += gridDim.x * 256u) {
         const uint32_t to_row = static_cast<uint32_t>(n >> 32 ? i / per : static_cast<uint32_t>(i) / per);
         const uint32_t e = static_cast<uint32_t>(i - static_cast<uint64_t>(to_row) * per) * 8;
         const uint32_t r = args.lo_row != 0 && to_row >= args.lo_row ? to_row - args.lo_row : to_row;
@@ -364,41 +381,72 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
       const bool any = row - lane < count;               // some lane of the warp has a row
       const uint32_t n0 = vt * args.nt + ch0 * 32;       // this warp's first column
       const uint32_t cols = args.N > n0 ? min(chunks * 32, args.N - n0) : 0u;
-      // the first entry at or behind n0: its offset from n0, 0xFFFFFFFF where there is none
-      uint32_t next = 0xFFFFFFFFu, cur = 0, len = 0;
-      float p_next = 1.0f;
-      const int32_t* ids = nullptr;
-      const float* prob = nullptr;
-      const uint32_t from = args.first + n0;
-      const auto take = [&]() {
-        next = 0xFFFFFFFFu;
-        if (cur < len) {
-          next = static_cast<uint32_t>(ids[cur]) - from;
-          if constexpr (BACK) p_next = prob[cur];
-        }
-      };
-      if constexpr (LIST) {
-        if (live) {
-          const uint64_t o = static_cast<uint64_t>(at) * args.top;
-          ids = args.ids + o;
-          prob = args.prob + o;
+      // The first entry in this warp's columns: its offset from n0, 0xFFFFFFFF where there is none; a
+      // list's next one is known ahead.  Three loads that wait for each other, of a target one: where the
+      // sums have segments, each is on its way while a segment is added up.
+      const uint32_t here = chunks * 32, from = args.first + n0;
+      uint32_t next = 0xFFFFFFFFu, ahead = 0xFFFFFFFFu;
+      uint32_t cur = 0, end = 0xFFFFFFFFu, len = 0, id[3];
+      float p_next = 0.0f, p_ahead = 0.0f;
+      int64_t target = -1;
+      float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // backward: the row's factors
+      const uint64_t list = LIST ? static_cast<uint64_t>(at) * args.top : 0ull;
+      const auto look_up = [&]() {
+        if (!live) return;
+        if constexpr (LIST) {
           len = args.len[at];
-          uint32_t hi = len;
           if (args.start != nullptr) {
             const uint64_t bucket = min(from / args.bucket, kLossBuckets - 1);
             cur = args.start[bucket * args.M + at];
-            hi = args.start[(bucket + 1) * args.M + at];
+            end = args.start[(bucket + 1) * args.M + at];
           }
-          while (cur < hi) {
-            const uint32_t mid = (cur + hi) / 2;
-            if (static_cast<uint32_t>(ids[mid]) < from) cur = mid + 1; else hi = mid;
-          }
-          take();
+        } else {
+          target = loss_index_at(args.target, args.target64, at);
         }
-      } else if (live) {
-        const uint32_t d = target_offset(args, at);
-        next = d != 0xFFFFFFFFu && d >= n0 ? d - n0 : 0xFFFFFFFFu;
-      }
+      };
+      const auto search = [&]() {
+        if (!live) return;
+        if constexpr (BACK) r = args.row != nullptr ? args.row[row] : loss_row_factors(args.factors, args.target, args.target64, row);
+        if constexpr (LIST) {
+          end = min(end, len);
+          while (end - cur > 2) {
+            const uint32_t mid = (cur + end) / 2;
+            if (static_cast<uint32_t>(args.ids[list + mid]) < from) cur = mid + 1; else end = mid;
+          }
+#pragma unroll
+          for (uint32_t e = 0; e < 3; ++e) id[e] = cur + e < len ? static_cast<uint32_t>(args.ids[list + cur + e]) : 0xFFFFFFFFu;
+        } else {
+          const int64_t d = target - from;
+          next = d >= 0 && d < here ? static_cast<uint32_t>(d) : 0xFFFFFFFFu;
+        }
+      };
+      // (an offset's probability: only where the offset is this tile's)
+      const auto entry = [&](uint32_t e, uint32_t token, float& p) {
+        if (token == 0xFFFFFFFFu || token - from >= here) return 0xFFFFFFFFu;
+        if constexpr (BACK) p = args.prob[list + e];
+        return token - from;
+      };
+      const auto settle = [&]() {
+        if (!LIST || !live) return;
+#pragma unroll
+        for (uint32_t e = 0; e < 2; ++e)
+          if (id[0] < from) {
+            ++cur;
+            id[0] = id[1];
+            id[1] = id[2];
+            id[2] = 0u;   // not loaded
+          }
+        if (id[1] < from && cur + 1 < len) id[1] = static_cast<uint32_t>(args.ids[list + cur + 1]);
+        next = entry(cur, id[0], p_next);
+        ahead = entry(cur + 1, id[1], p_ahead);
+      };
+      const auto take = [&]() {
+        ++cur;
+        next = ahead;
+        p_next = p_ahead;
+        ahead = 0xFFFFFFFFu;
+        if (next != 0xFFFFFFFFu && cur + 1 < len) ahead = entry(cur + 1, static_cast<uint32_t>(args.ids[list + cur + 1]), p_ahead);
+      };
       look(t + G);
       // The hand-back of an accumulator whose reads are complete: it publishes nothing.
       const auto release = [&](uint32_t b) {
@@ -417,22 +465,41 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
         tc_fence_after_sync();
         return ok;
       };
-      if constexpr (!BACK) {
-        float acc[C::NCH][32];
+      look_up();
+      if (!SEG || kt_n <= C::SEG_TILES) {
+        search();
+        settle();
+      }
+      // the tile's sums, by segments of the width
+      float acc[C::NCH][32];
+      const auto add_up = [&]() {
         for (uint32_t k = 0; k < kt_n; k += C::SEG_TILES, ++j) {
-          if (!acc_wait()) break;
+          if (!acc_wait()) return;
           if (any) {
 #pragma unroll
             for (uint32_t i = 0; i < C::NCH; ++i) {
               if (i >= chunks) break;
               uint32_t v[32];
               tmem_ld_32x32b_x32_sync(t_addr(i), v);
+              if (k == 0) {
 #pragma unroll
-              for (uint32_t e = 0; e < 32; ++e) acc[i][e] = k == 0 ? __uint_as_float(v[e]) : acc[i][e] + __uint_as_float(v[e]);
+                for (uint32_t e = 0; e < 32; ++e) acc[i][e] = __uint_as_float(v[e]);
+              } else {
+#pragma unroll
+                for (uint32_t e = 0; e < 32; e += 2)
+                  add_pair(acc[i][e], acc[i][e + 1], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              }
             }
           }
           release(j & 1u);
+          if (kt_n > C::SEG_TILES) {
+            if (k == 0) search();
+            if (k == C::SEG_TILES) settle();
+          }
         }
+      };
+      if constexpr (!BACK) {
+        add_up();
         if (!ok) break;
         if (any) {
           // the entries' products
@@ -444,7 +511,6 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
               const float x = select32(acc[i], (next - 32 * i) & 31u);
               if (here && next < cols) args.entry[LIST ? static_cast<uint64_t>(at) * args.top + cur : at] = x;
               if (here) {
-                ++cur;
                 if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
               }
             }
@@ -496,60 +562,92 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, LIST>::kThreads, 1)
           }
         }
       } else {
-        float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (live) r = args.row != nullptr ? args.row[row] : loss_row_factors(args.factors, args.target, args.target64, row);
-        uint16_t* const o = args.out + static_cast<uint64_t>(row) * args.ld_out + n0;
         // the product that sums over rows takes 64 at a time
         const uint32_t padded = args.lo_row != 0 ? args.lo_row : min((count + 63) / 64 * 64, args.M);
-        const bool stored = row < padded;
-        if (!acc_wait()) break;
-        const uint32_t b = j & 1u;
-        if (row - lane < padded && chunks > 0) {
-#pragma unroll 1
-          for (uint32_t i = 0; i < chunks; ++i) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32_sync(t_addr(i), v);
-            if (i + 1 == chunks) release(b);
-            float g[32];
+        // chunk i's gradient from its sums
+        const auto finish = [&](uint32_t i, float(&g)[32], bool all_live) {
 #pragma unroll
-            for (uint32_t e = 0; e < 32; ++e)
-              g[e] = fmaf(r.y, exp2_approx(fmaf(args.c, __uint_as_float(v[e]), -r.x)), -r.z);
-            while (__any_sync(0xffffffffu, next - 32 * i < 32u)) {
-              const uint32_t w = next - 32 * i;
-              const float x = r.w * p_next;
+          for (uint32_t e = 0; e < 32; e += 2) {
+            fma_pair(args.c, g[e], g[e + 1], -r.x);
+            g[e] = exp2_approx(g[e]);
+            g[e + 1] = exp2_approx(g[e + 1]);
+            fma_pair(r.y, g[e], g[e + 1], -r.z);
+          }
+          while (__any_sync(0xffffffffu, next - 32 * i < 32u)) {
+            const uint32_t w = next - 32 * i;
+            const float x = LIST ? r.w * p_next : r.w;
+            float xs[4];
 #pragma unroll
-              for (uint32_t e = 0; e < 32; ++e) g[e] = w == e ? g[e] - x : g[e];
-              if (w < 32u) {
-                ++cur;
-                if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
-              }
-            }
-            if (stored && 32 * i < cols) {   // (the pitch has room for whole chunks)
-              uint16_t* const lo = o + static_cast<uint64_t>(args.lo_row) * args.ld_out;
+            for (uint32_t k = 0; k < 4; ++k) xs[k] = (w & 3u) == k ? x : 0.0f;
 #pragma unroll
-              for (uint32_t h = 0; h < 2; ++h) {
-                uint32_t x[8];
-                // (a padding row's accumulator is whatever its operand's rows held)
-#pragma unroll
-                for (uint32_t e = 0; e < 8; ++e) x[e] = live ? pack_bf16x2(g[16 * h + 2 * e], g[16 * h + 2 * e + 1]) : 0u;
-                st_global_v8(o + 32 * i + 16 * h, x);
-                if (args.lo_row != 0 && row < args.M) {
-#pragma unroll
-                  for (uint32_t e = 0; e < 8; ++e)
-                    x[e] = live ? pack_bf16x2(g[16 * h + 2 * e] - bf16_bits_to_f32(x[e] & 0xFFFFu),
-                                              g[16 * h + 2 * e + 1] - bf16_bits_to_f32(x[e] >> 16))
-                                : 0u;
-                  st_global_v8(lo + 32 * i + 16 * h, x);
-                }
-              }
+            for (uint32_t e = 0; e < 32; ++e) g[e] = w / 4 == e / 4 ? g[e] - xs[e % 4] : g[e];
+            if (w < 32u) {
+              if constexpr (LIST) take(); else next = 0xFFFFFFFFu;
             }
           }
+          if (!all_live) {   // (a padding row's accumulator is whatever its operand's rows held)
+#pragma unroll
+            for (uint32_t e = 0; e < 32; ++e) g[e] = live ? g[e] : 0.0f;
+          }
+          if (32 * i >= cols) return;
+          // a box of 32 rows, which no multiple of 64 divides: rows past the buffer's are left out
+          const auto send = [&](const uint32_t(&x)[16], uint32_t at_row) {
+            const uint32_t box = out0 + ((warp - 4u) * 2 + (sent & 1u)) * C::BOX_BYTES;
+            ++sent;
+            if (lane == 0) bulk_wait_group_read<1>();      // the store before the last has read it
+            __syncwarp();
+            stage_half_row(box, lane, x);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&tmOut, box, static_cast<int32_t>(n0 + 32 * i), static_cast<int32_t>(at_row), 0);
+              bulk_commit_group();
+            }
+          };
+          uint32_t x[16];
+#pragma unroll
+          for (uint32_t e = 0; e < 16; ++e) x[e] = pack_bf16x2(g[2 * e], g[2 * e + 1]);
+          send(x, row - lane);
+          if (args.lo_row != 0 && row - lane < args.M) {
+#pragma unroll
+            for (uint32_t e = 0; e < 16; ++e)
+              x[e] = pack_bf16x2(g[2 * e] - bf16_bits_to_f32(x[e] & 0xFFFFu), g[2 * e + 1] - bf16_bits_to_f32(x[e] >> 16));
+            send(x, args.lo_row + row - lane);
+          }
+        };
+        if constexpr (SEG) {
+          add_up();
+          if (!ok) break;
+          if (row - lane < padded) {
+            const bool all_live = __all_sync(0xffffffffu, live);
+#pragma unroll
+            for (uint32_t i = 0; i < C::NCH; ++i)
+              if (i < chunks) finish(i, acc[i], all_live);
+          }
         } else {
-          release(b);
+          if (!acc_wait()) break;
+          const uint32_t b = j & 1u;
+          if (row - lane < padded && chunks > 0) {
+            const bool all_live = __all_sync(0xffffffffu, live);
+#pragma unroll 1
+            for (uint32_t i = 0; i < chunks; ++i) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32_sync(t_addr(i), v);
+              if (i + 1 == chunks) release(b);
+              float g[32];
+#pragma unroll
+              for (uint32_t e = 0; e < 32; ++e) g[e] = __uint_as_float(v[e]);
+              finish(i, g, all_live);
+            }
+          } else {
+            release(b);
+          }
+          ++j;
         }
-        ++j;
       }
     }
+    if (BACK && lane == 0) bulk_wait_group<0>();
+    __syncwarp();
   }
 
   // ---- teardown: every role is done with TMEM and with the peer's barriers ----

@@ -55,6 +55,7 @@ struct LossProductCfg {
   static constexpr uint32_t STAGE_BYTES = P_BYTES + Q_BYTES;
   static constexpr uint32_t kEpiWarps = 8;
   static constexpr uint32_t kThreads = 32 * (2 + kEpiWarps);
+  static constexpr uint32_t kLeastRegs = 0;              // (any number will do)
   static constexpr uint32_t BAR_BYTES = 512;
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;

@@ -26,6 +26,31 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// A warpgroup's registers a thread from here on, within what the block was launched with.
+template <uint32_t N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two fp32 operations in one instruction, each rounded as it would be alone: a += b, and
+// x = a x + b with a and b for both.
+__device__ __forceinline__ void add_pair(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma_pair(float a, float& x0, float& x1, float b) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, y, x, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(a), "f"(b));
+}
+
 // A warp's box of 32 rows of 128 bytes for a store with 128-byte swizzle: pieces `first` ..
 // of 16 bytes of this lane's row, N words.
 template <uint32_t N>
@@ -33,6 +58,13 @@ __device__ __forceinline__ void stage_row(uint32_t box, uint32_t lane, uint32_t 
 #pragma unroll
   for (uint32_t i = 0; i < N / 4; ++i)
     st_shared_v4(box + lane * 128 + (((first + i) ^ (lane & 7u)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// The same of 32 rows of 64 bytes with 64-byte swizzle, a whole row.
+__device__ __forceinline__ void stage_half_row(uint32_t box, uint32_t lane, const uint32_t (&v)[16]) {
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i)
+    st_shared_v4(box + lane * 64 + ((i ^ ((lane >> 1) & 3u)) << 4), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 // warp_wait for a warp that walks its loop together: every lane probes, and all decide alike,

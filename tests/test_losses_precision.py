@@ -1,5 +1,5 @@
 """Losses over a vocabulary where rounding shows: large logits, sure tokens, a
-teacher's extreme logits."""
+teacher's extreme logits, gradients of sure rows over wide products."""
 import pytest
 import torch
 
@@ -129,3 +129,42 @@ def test_a_teachers_extreme_logits(M, top, temperature, dtype):
     more = 2.0 ** -17 * torch.where(live, dloss.double() * f, 0.0)[:, None] * t
     # what lies below fp32's 2^-126 becomes 0: 500 terms of it, times 2 of B and 4 of dloss / temperature
     ref.check(dA, ra, ta + more @ B.double().abs() + 2.0 ** -114, "dA")
+
+
+@pytest.mark.parametrize("M", [1, 130, 300])
+@pytest.mark.parametrize("K", [504, 1040, 4096, 8192])
+def test_a_sure_rows_gradient_over_a_wide_product(M, K):
+    """Rows that leave 5e-3 to 1e-5 to the other tokens: 1 - exp(z - lse) is what the logits' error
+    must not reach.  dB's row of a target, along the row of A, is that row's dz.
+
+    Logits are added up over 512 terms (1.1e-9 of the result a term, cut off; twice that allowed) and
+    then with a rounding a segment; exp takes 2^-21 (1 + |lse|) of its own; dz is rounded to bf16
+    (up to 128 rows, twice); the product to dB costs 2^-17 of what it adds up."""
+    N = 2000
+    r = gen(M + K)
+    A = ((torch.rand(M, K, generator=r, device="cuda") + 0.5) * torch.randn(M, K, generator=r, device="cuda").sign()).to(BF16)
+    a = A.double()
+    length = a.square().sum(1)
+    z_want = 16.0 + 1.5 * (torch.arange(M, device="cuda") % 5 - 2)
+    B = torch.zeros(N, K, device="cuda")
+    B[:M] = (a / length[:, None] * z_want[:, None]).float()
+    B = B.to(BF16)
+    targets = torch.arange(M, device="cuda")
+    z = ref.logits(A, B, 1.0)
+    lse = torch.logsumexp(z, 1).float()
+    t, live = ref.target_matrix(targets, N, 0.0), targets >= 0
+    one = torch.ones(M, device="cuda")
+    want, _ = ref.dlogits(A, B, t, live, one, lse, 1.0)
+    left = -want[torch.arange(M), targets]
+    assert (left > 3e-6).all() and (left < 2e-2).all()
+    bound = (2 * 512 * 1.1e-9 + ((K + 511) // 512) * 2.0 ** -24) * z.max(1)[0] + 2.0 ** -21 * (lse.double() + 1.0)
+    rounding = 2.0 ** -16 if M <= 128 else 2.0 ** -8
+    for own in (False, True):
+        at = g.matmul_cross_entropy(A, B, targets)[1] if own else lse
+        exact = 1.0 - torch.exp(z[torch.arange(M), targets] - at.double())
+        _, dB = g.matmul_cross_entropy_grad(one, A, B, targets, at, out_dtype=F32, need_dA=False)
+        ok()
+        got = -(dB[:M].double() * a).sum(1) / length
+        # (other rows' dz at this target, of 1e-8, along directions that are nearly orthogonal)
+        cross = ((torch.where(t[:, :M] > 0, 0.0, want[:, :M].abs())) * (a @ a.T).abs()).sum(0) / length
+        ref.check(got, exact, bound + (rounding + 2.0 ** -17) * exact.abs() + 2.0 ** -17 * cross + cross, "1 - p")
