@@ -91,11 +91,11 @@ int launch_loss(const LossOperands& o, LossArgs a, const LossTiles& tile, const 
   if (o.compact != nullptr && !operand_map(&compact, o.compact, a.K, a.M, 1, o.ld_compact, 0, C::P_BOX))
     return GEMM_ERR_LAUNCH;
   CUtensorMap out = all;
-  if constexpr (BACK) {
+  if constexpr (C::kBoxes) {
     // (whole chunks of 32 columns: the pitch has room for them)
-    const uint64_t dims[3] = {o.ld_out, o.out_rows, 1}, strides[2] = {2 * o.ld_out, 2 * o.ld_out};
+    const uint64_t dims[3] = {a.ld_out, o.out_rows, 1}, strides[2] = {2 * a.ld_out, 2 * a.ld_out};
     const uint32_t box[3] = {32, 32, 1};
-    if (!encode_map_3d(&out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!encode_map_3d(&out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
       return GEMM_ERR_LAUNCH;
   }
   a.nt = tile.nt;

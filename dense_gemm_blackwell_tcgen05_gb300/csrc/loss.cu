@@ -803,9 +803,9 @@ int launch_loss_backward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_
     if ((rc = launch_rows(p, w, ws, a, r, true, p.dB != nullptr && !whole, stream)) != GEMM_OK) return rc;
     a.row = reinterpret_cast<const float4*>(ws + w.row);
   }
-  o.out = ws + w.piece;
+  a.out = reinterpret_cast<uint16_t*>(ws + w.piece);
+  a.ld_out = w.width;
   o.out_rows = w.rows;
-  o.ld_out = w.width;
   a.lo_row = static_cast<uint32_t>(w.lo);
 
   for (uint64_t v0 = 0; v0 < p.N; v0 += w.width) {

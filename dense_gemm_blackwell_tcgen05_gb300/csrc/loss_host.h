@@ -58,8 +58,7 @@ struct LossOperands {
   const void* B;
   uint64_t ldb;
   bool chained;                // the launch follows another kernel of its call
-  void* out;                   // backward: the piece of the gradient [rows][ld_out], bf16
-  uint64_t out_rows, ld_out;
+  uint64_t out_rows;           // backward: of the piece of the gradient
 };
 // A GB300's SMs, not the current device's: a workspace is sized without a device.
 constexpr uint64_t kLossSms = 152;

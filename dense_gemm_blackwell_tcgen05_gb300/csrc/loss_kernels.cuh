@@ -15,9 +15,10 @@
 //
 // Persistent, warp-specialised like the grouped products: a TMA producer, an MMA
 // issuer with two accumulators, eight epilogue warps, two per lane quarter, each with
-// half of the tile's columns.  The gradient leaves through shared memory by TMA (4096 rows,
+// half of the tile's columns.  A pair's gradient leaves through shared memory by TMA (4096 rows,
 // 32768 tokens of width 2048: 11 us of 285 less than from registers, each lane its own row in
-// whole sectors).  Rows left out of the loss are left out of the product: the rows that count lie
+// whole sectors); one CTA's, bound by loads of B, does not, for another stage of them (64 rows,
+// 131072 tokens of width 4096: 164 us, 170 with boxes).  Rows left out of the loss are left out of the product: the rows that count lie
 // compact, and their number is read on the GPU.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
@@ -90,7 +91,9 @@ struct LossArgs {
   uint16_t* clean;
   uint64_t ld_clean;
   int32_t* offsets;            //   and {0, M}, as one group's offsets
-  uint32_t lo_row;             // the piece's row from which on what rounding left follows (0: it is dropped)
+  uint16_t* out;               // [count][ld_out] the gradient's piece; zeros up to a multiple of 64 rows
+  uint64_t ld_out;
+  uint32_t lo_row;             // its row from which on what rounding left follows (0: it is dropped)
   unsigned long long* status;
   unsigned long long timeout_ns;
   uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
@@ -125,7 +128,8 @@ struct LossCfg {
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;
   static constexpr uint32_t BOX_BYTES = 32 * 64;         // a warp's 32 rows of a chunk on their way out
-  static constexpr uint32_t OUT_BYTES = BACK ? kEpiWarps * 2 * BOX_BYTES : 0;
+  static constexpr bool kBoxes = BACK && CG == 2;        // the gradient leaves through them
+  static constexpr uint32_t OUT_BYTES = kBoxes ? kEpiWarps * 2 * BOX_BYTES : 0;
   static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - OUT_BYTES) / STAGE_BYTES;
   static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
   static constexpr uint32_t SMEM_BYTES = ALIGN_SLACK + STAGES * STAGE_BYTES + OUT_BYTES + BAR_BYTES;
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
       tma_prefetch_desc(&tmAll);
       tma_prefetch_desc(&tmCompact);
       tma_prefetch_desc(&tmQ);
-      if constexpr (BACK) tma_prefetch_desc(&tmOut);
+      if constexpr (C::kBoxes) tma_prefetch_desc(&tmOut);
       *abort_flag = 0u;
     }
     for (uint32_t i = lane; i < kAccBar0 + 5; i += 32)
@@ -590,18 +594,24 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
             for (uint32_t e = 0; e < 32; ++e) g[e] = live ? g[e] : 0.0f;
           }
           if (32 * i >= cols) return;
-          // a box of 32 rows, which no multiple of 64 divides: rows past the buffer's are left out
+          // 32 rows of the piece from at_row on, which no multiple of 64 divides
           const auto send = [&](const uint32_t(&x)[16], uint32_t at_row) {
-            const uint32_t box = out0 + ((warp - 4u) * 2 + (sent & 1u)) * C::BOX_BYTES;
-            ++sent;
-            if (lane == 0) bulk_wait_group_read<1>();      // the store before the last has read it
-            __syncwarp();
-            stage_half_row(box, lane, x);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_3d(&tmOut, box, static_cast<int32_t>(n0 + 32 * i), static_cast<int32_t>(at_row), 0);
-              bulk_commit_group();
+            if constexpr (C::kBoxes) {                     // (rows past the buffer's are left out)
+              const uint32_t box = out0 + ((warp - 4u) * 2 + (sent & 1u)) * C::BOX_BYTES;
+              ++sent;
+              if (lane == 0) bulk_wait_group_read<1>();    // the store before the last has read it
+              __syncwarp();
+              stage_half_row(box, lane, x);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&tmOut, box, static_cast<int32_t>(n0 + 32 * i), static_cast<int32_t>(at_row), 0);
+                bulk_commit_group();
+              }
+            } else if (row < (at_row >= padded ? args.M : padded)) {
+              uint16_t* const o = args.out + static_cast<uint64_t>(at_row + lane) * args.ld_out + n0 + 32 * i;
+              st_global_v8(o, x);
+              st_global_v8(o + 16, x + 8);
             }
           };
           uint32_t x[16];
@@ -646,7 +656,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
         }
       }
     }
-    if (BACK && lane == 0) bulk_wait_group<0>();
+    if (C::kBoxes && lane == 0) bulk_wait_group<0>();
     __syncwarp();
   }
 
