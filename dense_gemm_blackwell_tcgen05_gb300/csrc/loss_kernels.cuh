@@ -15,11 +15,12 @@
 //
 // Persistent, warp-specialised like the grouped products: a TMA producer, an MMA
 // issuer with two accumulators, eight epilogue warps, two per lane quarter, each with
-// half of the tile's columns.  A pair's gradient leaves through shared memory by TMA (4096 rows,
+// half of the tile's columns.  The gradient leaves through shared memory by TMA (4096 rows,
 // 32768 tokens of width 2048: 11 us of 285 less than from registers, each lane its own row in
-// whole sectors); one CTA's, bound by loads of B, does not, for another stage of them (64 rows,
-// 131072 tokens of width 4096: 164 us, 170 with boxes).  Rows left out of the loss are left out of the product: the rows that count lie
-// compact, and their number is read on the GPU.
+// whole sectors; 128 rows, a million tokens of width 64: 393 for 499, both gradients), but a single
+// CTA's over a long width, which the loads of B bound: there another stage of them is worth more
+// (64 rows, 131072 tokens of width 4096: 164 us, 170 with boxes).  Rows left out of the loss are
+// left out of the product: the rows that count lie compact, and their number is read on the GPU.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
 // 520 us forward, 2.11 PFLOP/s, tensor pipes 98.8 % busy; 541 backward), few by the read of B
@@ -128,7 +129,7 @@ struct LossCfg {
   static constexpr uint32_t SMEM_LIMIT = 232448;
   static constexpr uint32_t ALIGN_SLACK = 1024;
   static constexpr uint32_t BOX_BYTES = 32 * 64;         // a warp's 32 rows of a chunk on their way out
-  static constexpr bool kBoxes = BACK && CG == 2;        // the gradient leaves through them
+  static constexpr bool kBoxes = BACK && (CG == 2 || !SEG);   // the gradient leaves through them
   static constexpr uint32_t OUT_BYTES = kBoxes ? kEpiWarps * 2 * BOX_BYTES : 0;
   static constexpr uint32_t FIT = (SMEM_LIMIT - ALIGN_SLACK - BAR_BYTES - OUT_BYTES) / STAGE_BYTES;
   static constexpr uint32_t STAGES = FIT > 12 ? 12 : FIT;
