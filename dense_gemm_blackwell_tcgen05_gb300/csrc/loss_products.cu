@@ -127,6 +127,7 @@ LossProductArgs loss_product_args(const LossProduct& p, const LossProductPlan& p
   a.add_sums = p.add_sums ? 1u : 0u;
   a.add_db = p.add_db ? 1u : 0u;
   a.db_cost = p.db_f32 ? 10u : 6u;
+  a.unit = loss_unit(a, 128u * plan.cg);
   a.status = ctx.status;
   a.timeout_ns = ctx.timeout_ns;
   return a;

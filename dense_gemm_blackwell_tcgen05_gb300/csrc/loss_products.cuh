@@ -26,25 +26,11 @@
 
 #include "gemm_kernels.cuh"
 #include "grouped_kernels.cuh"
+#include "loss_deal.h"
 #include "ptx_grouped.cuh"
 #include "ptx_loss.cuh"
 
 namespace gb300 {
-
-struct LossDeal;
-struct LossProductArgs {
-  uint32_t M, n, K;            // rows at most, columns of the piece, width
-  const LossDeal* deal;        // the deal for the rows that count (nullptr: all of them do, it is found here)
-  uint32_t nt;                 // columns of a tile, a multiple of 64
-  uint32_t width;              // of the first piece, by which the parts are chosen
-  uint32_t most, most_db;      // parts at most, of Rows and of Matrix
-  uint32_t rows, matrix;       // which of them are wanted
-  uint32_t direct;             // Rows to dA, bf16 (1) or fp32 (2), where there is nothing to join (0: never)
-  uint32_t add_sums, add_db;   // added to what is there
-  uint32_t db_cost;            // a tile of dB's store in stages
-  unsigned long long* status;
-  unsigned long long timeout_ns;
-};
 
 template <int CG>
 struct LossProductCfg {
@@ -69,72 +55,22 @@ struct LossProductCfg {
   static constexpr uint32_t ACC_COLS = 256;
 };
 
-// How the items are dealt.  Matrix's reduction to the rows goes in `parts_db` where it has so few
-// tiles that clusters would idle.  Rows' reduction over the piece goes in `parts`, and its items
-// in turn to the G clusters, so that the first `r` have one more than the others' x; Matrix's
-// follow, n1 at most to each of those and n0 to each of the others, who end no later for it.
-struct LossDeal {
-  uint32_t count, rb_x, rb_y, cb;      // rows that count; tiles down, of either, and across
-  uint32_t parts, parts_db, x, r, n1, n0;
-  bool direct;                         // Rows go to dA: one part, and no row left out
+// The deal that ends first: the 32 lanes try a number of parts each.
+struct LossPick {
+  __device__ __forceinline__ void operator()(LossDeal& d, const LossWork& w, uint32_t G, uint32_t most) const {
+    const uint32_t s = lane_idx() + 1, found = loss_shares(w, s, G, d), time = s <= most ? found : 0xFFFFFFFFu;
+    const uint32_t best = __reduce_min_sync(0xffffffffu, time);
+    const int lane = __ffs(__ballot_sync(0xffffffffu, time == best)) - 1;
+    d.parts = static_cast<uint32_t>(lane) + 1;
+    d.x = __shfl_sync(0xffffffffu, d.x, lane);
+    d.r = __shfl_sync(0xffffffffu, d.r, lane);
+    d.n1 = __shfl_sync(0xffffffffu, d.n1, lane);
+    d.n0 = __shfl_sync(0xffffffffu, d.n0, lane);
+  }
 };
 
-// The deal that ends first, of `kt` stages a tile over `tiles` tiles of Rows and `others`
-// items of Matrix, `cost` stages each; each part costs its sums' way to memory and back
-// (`extra` stages over all clusters).  The 32 lanes try a number of parts each.
-__device__ __forceinline__ void loss_parts(LossDeal& d, uint32_t tiles, uint32_t others, uint32_t kt, uint32_t cost,
-                                           uint32_t extra, uint32_t G, uint32_t most) {
-  constexpr uint32_t kEnds = 5;                          // an item's first loads and last store, in stages
-  const uint32_t s = lane_idx() + 1;
-  // (what is beyond these needs no parts, and would leave 32 bits)
-  const bool few = tiles <= 0x4000u && others <= 0x100000u && kt <= 0x4000u && cost <= 0x4000u && extra <= 0x10000u;
-  const uint32_t items = tiles * (few ? s : 1u), x = items / G, r = items - x * G;
-  uint32_t n1 = others / G, n0 = n1, time = s == 1 ? 0xFFFFFFFEu : 0xFFFFFFFFu;
-  if (s <= most && few) {
-    const uint32_t each = (kt + s - 1) / s + kEnds, l0 = x * each, l1 = r > 0 ? l0 + each : l0;
-    uint32_t t = max((r * l1 + (G - r) * l0 + others * cost + G - 1) / G, l1);
-    for (uint32_t i = 0; i < 4; ++i) {
-      n1 = (t - l1) / cost;
-      n0 = (t - l0) / cost;
-      if (r * n1 + (G - r) * n0 >= others) break;
-      t = min(l0 + (n0 + 1) * cost, l1 + (n1 + 1) * cost);
-    }
-    time = t + s * extra;
-  }
-  if (r * n1 < others) n0 = max(n0, (others - r * n1 + G - r - 1) / (G - r));
-  const uint32_t best = __reduce_min_sync(0xffffffffu, time);
-  const int lane = __ffs(__ballot_sync(0xffffffffu, time == best)) - 1;
-  d.parts = static_cast<uint32_t>(lane) + 1;
-  d.x = __shfl_sync(0xffffffffu, x, lane);
-  d.r = __shfl_sync(0xffffffffu, r, lane);
-  d.n1 = __shfl_sync(0xffffffffu, n1, lane);
-  d.n0 = __shfl_sync(0xffffffffu, n0, lane);
-}
-
-// For `count` rows, tiles of `lt` rows and G clusters.
 __device__ __forceinline__ LossDeal loss_deal(const LossProductArgs& a, uint32_t count, uint32_t lt, uint32_t G) {
-  LossDeal d;
-  d.count = count;
-  d.cb = (a.K + a.nt - 1) / a.nt;
-  d.rb_x = a.rows ? (d.count + lt - 1) / lt : 0u;
-  d.rb_y = a.matrix ? (a.n + lt - 1) / lt : 0u;
-  // (by the first piece: later ones, which may be narrower, add to the same parts)
-  const uint32_t tiles = a.matrix ? (a.width + lt - 1) / lt * d.cb : 0u, stages = (d.count + 63) / 64;
-  // Matrix in parts of at least 8 stages, where that saves more than the sums' way to memory and
-  // back (4 bytes at 5 TB/s, 0.3 us a stage) and the joining take: 4000 rows, 512 tokens of width
-  // 256, 8 tiles of 63 stages, 19.5 us in parts and 28.3 whole; 1500, 512, 128, 4 of 24, 19.0 and 17.0
-  d.parts_db = 1;
-  if (tiles > 0 && a.most_db > 1 && stages <= 0x1000000u) {
-    const uint32_t n = min(min(G / tiles, stages / 8), a.most_db);
-    const uint32_t way = static_cast<uint32_t>(static_cast<uint64_t>(a.width) * a.K * n * 8 / 1500000);
-    if (n > 1 && stages - (stages + n - 1) / n > way + 24) d.parts_db = n;
-  }
-  const uint32_t others = tiles * d.parts_db, each = (stages + d.parts_db - 1) / d.parts_db + 3;
-  // (Rows' sums, the same)
-  const uint32_t extra = static_cast<uint32_t>(static_cast<uint64_t>(d.count) * a.K * 8 / 1500000);
-  loss_parts(d, d.rb_x * d.cb, others, (a.width + 63) / 64, max(each, a.db_cost), extra, G, a.most);
-  d.direct = a.direct != 0u && d.parts == 1 && d.count == a.M;
-  return d;
+  return loss_deal_by(a, count, lt, G, LossPick{});
 }
 
 // The same, once the kernels before the product's have ended: found ahead where rows may be left out.
@@ -159,23 +95,15 @@ constexpr uint32_t kLossAhead = 64;
 template <int CG>
 __device__ __forceinline__ bool loss_item(const LossProductArgs& a, const LossDeal& d, uint32_t c, uint32_t G, uint32_t i,
                                           LossItem& w) {
-  const uint32_t mine = d.x + (c < d.r ? 1u : 0u);
-  w.matrix = i >= mine ? 1 : 0;
-  const uint32_t rb_n = w.matrix ? d.rb_y : d.rb_x, per = rb_n * d.cb;
-  uint32_t t = c + i * G;
-  if (w.matrix) {
-    i -= mine;
-    if (i >= (c < d.r ? d.n1 : d.n0)) return false;
-    t = i < d.n1 ? c + i * G : d.n1 * G + (i - d.n1) * (G - d.r) + (c - d.r);
-    if (t >= per * d.parts_db) return false;
-  }
-  w.s = t / per;
-  uint32_t rb, cb;
-  tile_coords(t - w.s * per, rb_n, d.cb, 8u, rb, cb);
+  bool matrix;
+  uint32_t t, rb, cb;
+  if (!loss_item_at(d, c, G, i, matrix, t, w.s)) return false;
+  w.matrix = matrix ? 1 : 0;
+  tile_coords(t, matrix ? d.rb_y : d.rb_x, d.cb, 8u, rb, cb);
   w.l0 = rb * 128 * CG;
   w.c0 = cb * a.nt;
-  const uint32_t kt = ((w.matrix ? d.count : a.n) + 63) / 64, parts = w.matrix ? d.parts_db : d.parts;
-  // (several parts: at most 32 of 0x4000 stages, or 152 of 0x1000000)
+  const uint32_t kt = ((matrix ? d.count : a.n) + 63) / 64, parts = matrix ? d.parts_db : d.parts;
+  // (several parts: 32 of at most 2^25 stages, or 152 of 2^24)
   w.k0 = parts == 1 ? 0u : kt * w.s / parts;
   w.k1 = parts == 1 ? kt : kt * (w.s + 1) / parts;
   return true;
