@@ -38,6 +38,8 @@ constexpr uint64_t kPieceBytes = 512ull << 20;
 constexpr uint64_t kLeastPiece = 4096;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+constexpr uint64_t kMostWorkspace = 1ull << 62;
+
 uint64_t up(uint64_t n, uint64_t m) { return (n + m - 1) / m * m; }
 
 // Whether a list's entries are found by buckets.  Few rows have a tile or two a cluster, whose
@@ -58,46 +60,47 @@ struct Layout {
 
 Layout layout_of(uint64_t M, uint64_t N, uint64_t K, uint64_t top, bool back) {
   Layout w = {};
-  const auto take = [&](uint64_t bytes) {
+  // (sizes that no memory holds: kNoWorkspace)
+  const auto take = [&](uint64_t n, uint64_t size) {
     const uint64_t at = w.bytes;
-    w.bytes += up(bytes, 256);
+    w.bytes = at > kMostWorkspace || n > (kMostWorkspace - at) / size ? kNoWorkspace : at + up(n * size, 256);
     return at;
   };
-  w.count = take(8);
-  w.deal = back ? take(sizeof(LossDeal)) : 0;
-  w.index = take(4 * M);
-  w.pos = take(4 * M);
+  w.count = take(1, 8);
+  w.deal = back ? take(1, sizeof(LossDeal)) : 0;
+  w.index = take(M, 4);
+  w.pos = take(M, 4);
   if (top > 0) {
-    w.ids = take(4 * M * top);
-    w.prob = take(4 * M * top);
-    w.len = take(4 * M);
-    if (bucketed(M, top)) w.start = take(2 * (kLossBuckets + 1) * M);
-    w.entropy = take(4 * M);
+    w.ids = take(M * top, 4);
+    w.prob = take(M * top, 4);
+    w.len = take(M, 4);
+    if (bucketed(M, top)) w.start = take((kLossBuckets + 1) * M, 2);
+    w.entropy = take(M, 4);
   }
   w.ld_compact = up(K, 64);
   if (back) {
     w.lo = M <= kTwoHalves ? up(M, 64) : 0;
     w.rows = w.lo + M;
-    w.compact = take(2 * w.rows * w.ld_compact);
-    w.row = take(16 * M);
+    w.compact = take(w.rows * w.ld_compact, 2);
+    w.row = take(M, 16);
     uint64_t width = kPieceBytes / 2 / (w.rows > 0 ? w.rows : 1);
     width = width < kLeastPiece ? kLeastPiece : width;
     const uint64_t pieces = (N + width - 1) / width;
     w.width = up((N + pieces - 1) / (pieces > 0 ? pieces : 1), 256);
-    w.piece = take(2 * w.rows * w.width);
+    w.piece = take(w.rows * w.width, 2);
     w.ld_sums = up(K, 32);
     w.stride_sums = w.rows * w.ld_sums;
     w.parts = loss_most_parts(w.rows, w.width < N ? w.width : N, K);
-    w.sums = take(4 * w.stride_sums * w.parts);
+    w.sums = take(w.stride_sums * w.parts, 4);
     w.parts_db = M > kInPlace && w.width >= N ? loss_most_parts_db(M, N, K) : 1;
-    if (w.parts_db > 1) w.sums_db = take(4 * N * w.ld_sums * w.parts_db);
+    if (w.parts_db > 1) w.sums_db = take(N * w.ld_sums * w.parts_db, 4);
   } else {
-    if (M > kInPlace) w.compact = take(2 * M * w.ld_compact);
-    w.entry = take(4 * M * (top > 0 ? top : 1));
+    if (M > kInPlace) w.compact = take(M * w.ld_compact, 2);
+    w.entry = take(M * (top > 0 ? top : 1), 4);
     const uint64_t slots = loss_tiles(M, N, K).slots(M, N);
     w.ld_part = up(M, 32);
-    w.part = take(16 * slots * w.ld_part);
-    w.part_sum = take(8 * slots * w.ld_part);
+    w.part = take(slots * w.ld_part, 16);
+    w.part_sum = take(slots * w.ld_part, 8);
   }
   return w;
 }

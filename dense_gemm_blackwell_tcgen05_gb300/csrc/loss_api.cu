@@ -41,7 +41,8 @@ int64_t workspace_bytes(const Sizes& z, int grad) {
   if (z.M == 0 || z.N == 0) return 0;
   const uint64_t M = static_cast<uint64_t>(z.M), N = static_cast<uint64_t>(z.N), K = static_cast<uint64_t>(z.K),
                  top = static_cast<uint64_t>(z.top);
-  return static_cast<int64_t>(grad ? loss_backward_bytes(M, N, K, top) : loss_forward_bytes(M, N, K, top));
+  const uint64_t n = grad ? loss_backward_bytes(M, N, K, top) : loss_forward_bytes(M, N, K, top);
+  return n == kNoWorkspace ? static_cast<int64_t>(GEMM_ERR_INVALID_ARG) : static_cast<int64_t>(n);
 }
 
 // Sizes, operands and workspace shared by all four calls; the rest of `p` is the caller's.
@@ -50,7 +51,8 @@ int check_common(const Sizes& z, const void* A, const void* B, int64_t lda, int6
   int rc;
   if (z.K > 0 && ((rc = check_matrix(A, z.K, lda, 2, 8)) != GEMM_OK || (rc = check_matrix(B, z.K, ldb, 2, 8)) != GEMM_OK))
     return rc;
-  if (ws == nullptr || ws_bytes < workspace_bytes(z, grad)) return GEMM_ERR_INVALID_ARG;
+  const int64_t need = workspace_bytes(z, grad);
+  if (ws == nullptr || need < 0 || ws_bytes < need) return GEMM_ERR_INVALID_ARG;
   return aligned(ws, 256) ? GEMM_OK : GEMM_ERR_ALIGNMENT;
 }
 

@@ -42,6 +42,7 @@ struct LossProblem {
   uint32_t stall_iter;
 };
 
+constexpr uint64_t kNoWorkspace = ~0ull;   // for sizes that no memory holds
 uint64_t loss_forward_bytes(uint64_t M, uint64_t N, uint64_t K, uint64_t top);
 uint64_t loss_backward_bytes(uint64_t M, uint64_t N, uint64_t K, uint64_t top);
 int launch_loss_forward(const LossProblem& p, const LaunchCtx& ctx, cudaStream_t stream);

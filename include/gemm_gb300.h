@@ -449,8 +449,13 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * workspace: 256-byte aligned device memory of at least the number of bytes that
  * the _workspace_bytes call gives for these sizes (grad: 0 for the forward call,
  * 1 for the gradient), uninitialised; calls that share one must not overlap on
- * the GPU.  Large calls need, forward, 2 MK + MN / 10 bytes, and for the gradient
- * 6 MK (at least 6 * 64 K) and a piece of dz, 512 MiB or 4096 columns.  Calls are asynchronous on `stream`, allocate
+ * the GPU.  K rounded up to 64, the forward call takes 2 MK bytes (none up to 256 rows) and 24
+ * for each row and tile of columns, of which there are N / 256 in large calls.  The gradient,
+ * with R = M rows (up to 128: twice as many, M rounded up to 64 of them), takes 2 RK; 4 RK p for
+ * dA's sums in p parts, as many as 32 while they stay within 128 MiB; 2 RN for dz up to 512 MiB,
+ * beyond which it goes by pieces of 512 MiB or, where that is more, 4096 columns; and up to 10 MiB
+ * for dB's sums.  Lists take 12 bytes an entry and 150 a row.  Sizes that would need 2^62 bytes
+ * are refused.  Calls are asynchronous on `stream`, allocate
  * nothing and can be captured; the same call gives the same bits.  Errors as
  * gemm_bf16.
  */
