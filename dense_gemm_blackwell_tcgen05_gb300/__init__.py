@@ -1003,7 +1003,12 @@ def matmul_cross_entropy_grad(dloss, A, B, targets, lse, scale: float = 1.0, lab
     returned; returns (dA [M,K], dB [N,K]), into dA and dB if given (bfloat16 or
     float32 each), else of out_dtype; None for one that is neither given nor
     needed.  With accumulate, adds to dB.  Rows left out get zeros in dA and add
-    nothing to dB, whatever A holds there."""
+    nothing to dB, whatever A holds there.  The logits' gradient is rounded to
+    bfloat16 before the products with it (up to 128 rows keep a second term), so
+    float32 gradients of more rows are about 1.5e-3 off, as bfloat16 ones are
+    2.4e-3.  Without `workspace` (from cross_entropy_workspace with grad=True)
+    one is allocated for the call: 512 MiB of the logits' gradient at most, or
+    4096 of its columns, and a few times A's size."""
     import torch
     bf16, f32 = torch.bfloat16, torch.float32
     if accumulate and dB is None:

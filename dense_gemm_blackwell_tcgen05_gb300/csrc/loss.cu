@@ -19,8 +19,10 @@
 //                       others
 //
 // Every kernel but a call's first is launched while the one before it runs, and waits for
-// it before it touches memory.  Only a piece's g is held: kPieceBytes, or a piece of
-// kLeastPiece columns.
+// it before it touches memory.  Two exceptions: in place, the first logits' kernel loads A and
+// B, which no kernel of the call writes, before that wait; and the product that stores rows
+// TMA cannot, the grouped one, is launched when the one before it has ended.  Only a piece's g
+// is held: kPieceBytes, or a piece of kLeastPiece columns.
 #include <cuda_bf16.h>
 
 #include "gemm_gb300.h"

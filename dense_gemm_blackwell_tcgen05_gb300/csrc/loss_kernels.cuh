@@ -27,10 +27,10 @@
 // (48 rows, 131072 tokens: 156 us, 6.9 TB/s), a few thousand tokens by latency.
 //
 // Precision.  The tensor core's additions truncate (1.1e-9 of the result a term), so both
-// passes add up segments of 512 terms in registers: a row's loss is the difference of its
+// passes add up segments of 256 or 512 terms in registers: a row's loss is the difference of its
 // logits, and where it is sure of its target its gradient is that of two numbers near 1
 // (1 - exp(z - lse) of 2.2e-4 at a logit of 16, width 8192: 4.1e-4 off in one sum, 5e-6 in
-// segments; on pairs, shorter ones would be paid in time: 256 terms 3 to 6 %).
+// segments).
 // exp is 2^x of the multiprocessor's special function unit (2 units in the last place)
 // on arguments in fp32.  The gradient g is rounded to bf16 for the products with it, at
 // 2^-9 of itself: over many rows as much as rounding the products' bf16 results adds (2.4e-3
@@ -100,8 +100,10 @@ struct LossArgs {
   uint32_t stall_iter;         // watchdog test hook (0xFFFFFFFF: none)
 };
 
-// Stages in a sum of the tensor core's: 512 terms.
-constexpr uint32_t kLossSegment = 8;
+// Stages in a sum of the tensor core's: 512 terms, and 256 forward on one CTA, whose epilogue has the
+// time (48 rows, 131072 tokens of width 4096: 161.1 us for 160.5, losses 3.2e-6 off for 5.2e-6; on
+// pairs 3 to 6 % of the time, and of a gradient of 128 rows 3 % at a width of 512).
+constexpr uint32_t loss_segment(uint32_t cg, bool back) { return cg == 1 && !back ? 4 : 8; }
 
 // NT: columns of a tile at most.  BACK, SEG: as loss_kernel's.
 template <int CG, uint32_t NT, bool BACK, bool SEG>
@@ -123,7 +125,7 @@ struct LossCfg {
   static constexpr bool kSplit = CG == 2 && SEG;
   static constexpr uint32_t kFewRegs = 56, kManyRegs = 224, kLeastRegs = kSplit ? 168 : 0;   // least: of a launch
   static_assert(!kSplit || 128 * kFewRegs + 32 * kEpiWarps * kManyRegs <= kThreads * kLeastRegs, "more than the launch's");
-  static constexpr uint32_t SEG_TILES = kLossSegment;
+  static constexpr uint32_t SEG_TILES = loss_segment(CG, BACK);
   static constexpr uint32_t NCH = NT / 64;               // 32-column chunks per epilogue warp at most
   static constexpr uint32_t BAR_BYTES = 512;
   static constexpr uint32_t SMEM_LIMIT = 232448;

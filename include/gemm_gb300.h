@@ -439,12 +439,15 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  * M == 0 is a no-op (dB is zeroed unless accumulate); N == 0 with rows is
  * refused; K == 0 gives logits of 0.
  *
- * Precision: the forward pass adds up its logits from sums over 512 terms and
- * joins maxima and sums in fp32.  The gradient goes by pieces of the vocabulary:
- * a piece's logits are computed again, their dz is rounded to bf16 for the two
- * products with it (its target's and its list's terms are taken off before
- * that; for up to 128 rows dz keeps what is left in a second bf16 term), and
- * the pieces' dA are added up in fp32.
+ * Precision: logits are added up from sums over 512 terms (few rows', forward,
+ * over 256), maxima and sums joined in fp32; a loss is off by what its logits'
+ * differences are, not by their size.  The gradient goes by pieces of the
+ * vocabulary: a piece's logits are computed again, their dz is rounded to bf16
+ * for the two products with it (its target's and its list's terms are taken off
+ * before that; for up to 128 rows dz keeps what is left in a second bf16 term),
+ * whatever the type of dA and dB: of more rows an fp32 gradient too is 1.5e-3
+ * off.  The pieces' dA are added up in fp32.  The products' own sums truncate,
+ * 1.1e-9 of the result a term: 1e-3 for dB of a million rows.
  *
  * workspace: 256-byte aligned device memory of at least the number of bytes that
  * the _workspace_bytes call gives for these sizes (grad: 0 for the forward call,
