@@ -91,7 +91,8 @@ int launch_loss(const LossOperands& o, LossArgs a, const LossTiles& tile, const 
   if (o.compact != nullptr && !operand_map(&compact, o.compact, a.K, a.M, 1, o.ld_compact, 0, C::P_BOX))
     return GEMM_ERR_LAUNCH;
   CUtensorMap out = all;
-  if constexpr (C::kBoxes) {
+  a.boxes = C::kBoxes && (CG == 2 || a.M > 64);   // (loss_kernels.cuh: what either takes)
+  if (a.boxes) {
     // (whole chunks of 32 columns: the pitch has room for them)
     const uint64_t dims[3] = {a.ld_out, o.out_rows, 1}, strides[2] = {2 * a.ld_out, 2 * a.ld_out};
     const uint32_t box[3] = {32, 32, 1};

@@ -17,10 +17,12 @@
 // issuer with two accumulators, eight epilogue warps, two per lane quarter, each with
 // half of the tile's columns.  The gradient leaves through shared memory by TMA (4096 rows,
 // 32768 tokens of width 2048: 11 us of 285 less than from registers, each lane its own row in
-// whole sectors; 128 rows, a million tokens of width 64: 393 for 499, both gradients), but a single
-// CTA's over a long width, which the loads of B bound: there another stage of them is worth more
-// (64 rows, 131072 tokens of width 4096: 164 us, 170 with boxes).  Rows left out of the loss are
-// left out of the product: the rows that count lie compact, and their number is read on the GPU.
+// whole sectors; 128 rows, a million tokens of width 64: 393 for 508, both gradients), but for
+// single CTAs' up to 64 rows, whose boxes would be half empty (64 rows, 200000 tokens of width 256:
+// 87 us, 91 with boxes), or over a long width, which the loads of B bound: there another stage of
+// them is worth more (64 rows, 131072 tokens of width 4096: 164 us, 170 with boxes).  Rows left out
+// of the loss are left out of the product: the rows that count lie compact, and their number is
+// read on the GPU.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
 // 520 us forward, 2.11 PFLOP/s, tensor pipes 98.8 % busy; 541 backward), few by the read of B
@@ -94,6 +96,7 @@ struct LossArgs {
   int32_t* offsets;            //   and {0, M}, as one group's offsets
   uint16_t* out;               // [count][ld_out] the gradient's piece; zeros up to a multiple of 64 rows
   uint64_t ld_out;
+  bool boxes;                  // it leaves by TMA, where the kernel can
   uint32_t lo_row;             // its row from which on what rounding left follows (0: it is dropped)
   unsigned long long* status;
   unsigned long long timeout_ns;
@@ -351,25 +354,45 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
     const auto counts = [&](uint32_t r) {      // in place: whether row r does
       return LIST ? args.len[r] > 0 : loss_index_at(args.target, args.target64, r) >= 0;
     };
-    if (BACK && args.clean != nullptr) {
-      // rows in pieces of 8 elements, the last of them element by element
-      const uint32_t rows = args.lo_row + args.M;
-      const uint32_t per = (args.K + 7) / 8;
-      const uint64_t n = static_cast<uint64_t>(rows) * per;      // (few rows, of any width)
-      if (blockIdx.x == 0 && threadIdx.x == 128) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(rows);
-      for (uint64_t i = blockIdx.x * 256u + threadIdx.x - 128u; i < n; i += gridDim.x * 256u) {
-        const uint32_t to_row = static_cast<uint32_t>(n >> 32 ? i / per : static_cast<uint32_t>(i) / per);
-        const uint32_t e = static_cast<uint32_t>(i - static_cast<uint64_t>(to_row) * per) * 8;
-        const uint32_t r = args.lo_row != 0 && to_row >= args.lo_row ? to_row - args.lo_row : to_row;
-        const uint16_t* const from = args.A + r * args.lda + e;
-        uint16_t* const to = args.clean + to_row * args.ld_clean + e;
-        const bool in = r < args.M && counts(r);
-        if (e + 8 <= args.K) {
-          *reinterpret_cast<uint4*>(to) = in ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
-        } else {
-          for (uint32_t k = 0; e + k < args.K; ++k) to[k] = in ? from[k] : uint16_t(0);
+    // Backward, in place: A's rows copied without those left out, in pieces of 8 elements, the last of a
+    // row element by element.  Between segments, whose sums would else wait for it (105 rows, 1598
+    // tokens of width 6488: 26.2 us for 31.1); ahead of everything where there is one.
+    const uint32_t rows = args.lo_row + args.M, per = (args.K + 7) / 8;
+    const uint64_t pieces = BACK && args.clean != nullptr ? static_cast<uint64_t>(rows) * per : 0ull;   // (few rows, of any width)
+    uint64_t piece = blockIdx.x * 256u + threadIdx.x - 128u;
+    const auto copy = [&]() {                  // four of them
+      uint4 v[4];
+      uint32_t to_row[4], e[4];
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k, piece += gridDim.x * 256u) {
+        to_row[k] = 0xFFFFFFFFu;
+        if (piece >= pieces) continue;
+        to_row[k] = static_cast<uint32_t>(pieces >> 32 ? piece / per : static_cast<uint32_t>(piece) / per);
+        e[k] = static_cast<uint32_t>(piece - static_cast<uint64_t>(to_row[k]) * per) * 8;
+        const uint32_t r = args.lo_row != 0 && to_row[k] >= args.lo_row ? to_row[k] - args.lo_row : to_row[k];
+        const uint16_t* const from = args.A + r * args.lda + e[k];
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (r < args.M && counts(r)) {
+          if (e[k] + 8 <= args.K) {
+            v[k] = __ldg(reinterpret_cast<const uint4*>(from));
+          } else {
+            uint16_t x[8] = {};
+#pragma unroll
+            for (uint32_t i = 0; i < 7; ++i)
+              if (e[k] + i < args.K) x[i] = from[i];
+            v[k] = make_uint4(x[0] | static_cast<uint32_t>(x[1]) << 16, x[2] | static_cast<uint32_t>(x[3]) << 16,
+                              x[4] | static_cast<uint32_t>(x[5]) << 16, x[6]);
+          }
         }
       }
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)         // (the pitch has room for whole pieces)
+        if (to_row[k] != 0xFFFFFFFFu) *reinterpret_cast<uint4*>(args.clean + to_row[k] * args.ld_clean + e[k]) = v[k];
+    };
+    if constexpr (BACK) {
+      if (blockIdx.x == 0 && threadIdx.x == 128 && pieces > 0) args.offsets[0] = 0, args.offsets[1] = static_cast<int32_t>(rows);
+      if constexpr (!SEG)
+        while (piece < pieces) copy();
     }
     // forward, `runs`: largest and sums over this cluster's tiles so far
     float run_m = -INFINITY, run_s = 0.0f, run_z = 0.0f;
@@ -503,6 +526,8 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
             if (k == 0) search();
             if (k == C::SEG_TILES) settle();
           }
+          if constexpr (BACK)
+            if (piece < pieces) copy();
         }
       };
       if constexpr (!BACK) {
@@ -599,7 +624,7 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
           if (32 * i >= cols) return;
           // 32 rows of the piece from at_row on, which no multiple of 64 divides
           const auto send = [&](const uint32_t(&x)[16], uint32_t at_row) {
-            if constexpr (C::kBoxes) {                     // (rows past the buffer's are left out)
+            if (C::kBoxes && args.boxes) {                 // (rows past the buffer's are left out)
               const uint32_t box = out0 + ((warp - 4u) * 2 + (sent & 1u)) * C::BOX_BYTES;
               ++sent;
               if (lane == 0) bulk_wait_group_read<1>();    // the store before the last has read it
@@ -659,6 +684,8 @@ __global__ void __launch_bounds__(LossCfg<CG, NT, BACK, SEG>::kThreads, 1)
         }
       }
     }
+    if constexpr (BACK)
+      while (piece < pieces) copy();
     if (C::kBoxes && lane == 0) bulk_wait_group<0>();
     __syncwarp();
   }
