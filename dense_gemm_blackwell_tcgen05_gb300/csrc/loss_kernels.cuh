@@ -25,8 +25,8 @@
 // read on the GPU.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
-// 520 us forward, 2.11 PFLOP/s, tensor pipes 98.8 % busy; 541 backward), few by the read of B
-// (48 rows, 131072 tokens: 156 us, 6.9 TB/s), a few thousand tokens by latency.
+// 523 us forward, 2.10 PFLOP/s, tensor pipes 98.8 % busy; 549 backward), few by the read of B
+// (48 rows, 131072 tokens: 159 us, 6.8 TB/s), a few thousand tokens by latency.
 //
 // Precision.  The tensor core's additions truncate (1.1e-9 of the result a term), so both
 // passes add up segments of 256 or 512 terms in registers: a row's loss is the difference of its

@@ -16,8 +16,8 @@
 // instead of two.
 //
 // Bounds.  Thousands of rows are bound by the MMAs (4096 rows, 32768 tokens of width 4096:
-// 1113 us for both, 1.98 PFLOP/s, tensor pipes 97.6 % busy), few by B's read and dB's write
-// (48 rows, 131072 tokens: 406 us, 5.4 TB/s; the write alone goes at 5.9, a fill at 4.0).
+// 1134 us for both, 1.94 PFLOP/s, tensor pipes 97.8 % busy), few by B's read and dB's write
+// (48 rows, 131072 tokens: 402 us, 5.4 TB/s; the write alone goes at 5.9, a fill at 4.0).
 //
 // Persistent, warp-specialised like the other products: a TMA producer, an MMA issuer with
 // two accumulators, eight epilogue warps (two per lane quarter, alternating 32-column
