@@ -441,7 +441,8 @@ int gemm_newton_schulz(const void* G, void* O, int64_t batch, int64_t rows, int6
  *
  * Precision: logits are added up from sums over 512 terms (few rows', forward,
  * over 256), maxima and sums joined in fp32; a loss is off by what its logits'
- * differences are, not by their size.  The gradient goes by pieces of the
+ * differences are, not by their size (but for the mean that smoothing takes, a
+ * plain fp32 sum: 2^-21 of the logits' size).  The gradient goes by pieces of the
  * vocabulary: a piece's logits are computed again, their dz is rounded to bf16
  * for the two products with it (its target's and its list's terms are taken off
  * before that; for up to 128 rows dz keeps what is left in a second bf16 term),
